@@ -87,6 +87,7 @@ typedef enum pa_status_t {
 #define PA_DEVERR_TIMEOUT 4u /* a pipeline wait ran past its time limit; output invalid */
 #define PA_DEVERR_QUERY_START 8u /* pa_prefill: query offsets decreasing, past total_tokens,
                                    or more new tokens than context */
+#define PA_DEVERR_POSITION 16u /* pa_append_rope: a rotation position outside the table */
 
 /* How work is split across the GPU. */
 typedef enum pa_schedule_t {
@@ -277,6 +278,61 @@ pa_status_t pa_split_kv_combine(const pa_problem_t *problem, int32_t num_splits,
 pa_status_t pa_append_kv(const pa_problem_t *problem, const void *new_key, const void *new_value,
                          const int32_t *block_tables, const int32_t *context_lengths,
                          void *key_cache, void *value_cache, void *stream);
+
+/* How a head's elements pair up for the position rotation (pa_append_rope). */
+typedef enum pa_rope_style_t {
+  PA_ROPE_HALF = 0,       /* element i pairs with element i + rotary_dim / 2 */
+  PA_ROPE_INTERLEAVED = 1 /* element 2 i pairs with element 2 i + 1 */
+} pa_rope_style_t;
+
+/* The position rotation of pa_append_rope. The first rotary_dim elements of a head turn
+ * pair by pair, pair i of a row at position p by the angle whose cosine and sine are
+ * table[p][0][i] and table[p][1][i]:
+ *     (x, y) -> (x cos - y sin, x sin + y cos)
+ * in fp32, rounded once to fp16; the other elements are copied. Computing the table is the
+ * caller's (once, in 64 bits where positions are far), so any frequency scaling fits. */
+typedef struct pa_rope_t {
+  int32_t rotary_dim; /* 0 (no rotation) or a multiple of 16, <= head_dim */
+  int32_t style;      /* pa_rope_style_t */
+  int32_t table_rows; /* positions the table covers, >= 1 */
+  int32_t reserved;   /* 0 */
+  const float *table; /* device, fp32 [table_rows][2][rotary_dim / 2], 16-byte aligned */
+  const int32_t *positions; /* device, int32 [total_tokens]: the position a row turns by; NULL:
+                               its token index in the sequence */
+} pa_rope_t;
+
+/* Write several new tokens per sequence into the paged caches, keys rotated on the way, and
+ * rotate their queries: what precedes pa_prefill (or, with one new token per sequence,
+ * pa_decode) in a layer whose attention turns queries and keys by position -- the bulk form
+ * of pa_append_kv ("[TIL] Optimizing paged attention", section "Paged Attention": the K and
+ * V of earlier tokens are kept and reused). Sequences, offsets and lengths are pa_prefill's:
+ * sequence b's n_b = query_start[b + 1] - query_start[b] new tokens are the LAST n_b of its
+ * context_lengths[b] tokens (lengths after the append; pa_append_kv takes them before it),
+ * so one set of arrays drives the append and the attention after it. Row query_start[b] + j
+ * is written at token index t = context_lengths[b] - n_b + j, in physical page
+ * block_tables[b][t / page_size], slot t % page_size, in the problem's cache_layout.
+ *   rope         host struct; NULL or rotary_dim 0: rows are copied unrotated
+ *   query        fp16 rows [total_tokens] of [query_heads][head_dim], query_stride elements
+ *                from row to row, or NULL (then query_out is NULL too)
+ *   new_key, new_value  fp16 rows [total_tokens] of [kv_heads][head_dim], key_stride and
+ *                value_stride elements from row to row. A stride of 0 means packed rows; a
+ *                larger one takes the rows straight from a fused projection's output. Strides
+ *                are multiples of 8 and cover a row; pointers are 16-byte aligned
+ *   query_start  int32 [batch + 1], device, as for pa_prefill
+ *   query_out    fp16 [total_tokens][query_heads][head_dim], packed; may be `query` itself
+ *                when its rows are packed, and may overlap nothing else
+ * Rows before query_start[0] and from query_start[batch] on are left alone, in query_out too.
+ * A sequence with inconsistent offsets is skipped and flagged (PA_DEVERR_QUERY_START), one
+ * with a length out of range likewise (PA_DEVERR_CONTEXT). A token whose page id is outside
+ * the pool (PA_DEVERR_PAGE_ID) or whose position is outside the table (PA_DEVERR_POSITION) is
+ * flagged and nothing of it is written. Two tokens written to the same (page, slot) race.
+ * Runs asynchronously on `stream`; allocates nothing, keeps nothing between calls. */
+pa_status_t pa_append_rope(const pa_problem_t *problem, const pa_rope_t *rope, const void *query,
+                           int64_t query_stride, const void *new_key, int64_t key_stride,
+                           const void *new_value, int64_t value_stride,
+                           const int32_t *query_start, int64_t total_tokens,
+                           const int32_t *block_tables, const int32_t *context_lengths,
+                           void *query_out, void *key_cache, void *value_cache, void *stream);
 
 /* Causal multi-token (prefill) attention over the paged caches: the decode step of
  * section "Paged Attention" extended to several new tokens per sequence, computed

@@ -24,14 +24,16 @@ PA_DEVERR_PAGE_ID = 1
 PA_DEVERR_CONTEXT = 2
 PA_DEVERR_TIMEOUT = 4
 PA_DEVERR_QUERY_START = 8
+PA_DEVERR_POSITION = 16
 PA_TEST_EXPIRE_WAITS = 1
 SCHEDULE = {"auto": 0, "single": 1, "balanced": 2}
 MATH = {"auto": 0, "simt": 1, "mma": 2}
 COMBINE = {"auto": 0, "fused": 1, "kernel": 2}
+ROPE_STYLE = {"half": 0, "interleaved": 1}
 
 # Every entry point include/pagedattn.h declares.
 EXPORTS = ("pa_plan", "pa_workspace_size", "pa_workspace_init", "pa_decode", "pa_decode_ex",
-           "pa_decode_noalloc", "pa_append_kv", "pa_prefill",
+           "pa_decode_noalloc", "pa_append_kv", "pa_append_rope", "pa_prefill",
            "pa_split_kv_partial", "pa_split_kv_combine", "pa_get_device_error",
            "pa_status_string", "pa_version")
 
@@ -66,6 +68,12 @@ class pa_plan_t(ctypes.Structure):
                 ("smem_bytes", ctypes.c_int64), ("workspace_bytes", ctypes.c_int64)]
 
 
+class pa_rope_t(ctypes.Structure):
+    _fields_ = [("rotary_dim", ctypes.c_int32), ("style", ctypes.c_int32),
+                ("table_rows", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("table", ctypes.c_void_p), ("positions", ctypes.c_void_p)]
+
+
 _lib = None
 _lock = threading.Lock()
 
@@ -92,6 +100,9 @@ def load(path: Optional[str] = None):
                                      vp, ctypes.c_size_t, vp]
         lib.pa_decode_noalloc.argtypes = [P(pa_problem_t), vp, vp, vp, vp, vp, f32, vp, vp]
         lib.pa_append_kv.argtypes = [P(pa_problem_t), vp, vp, vp, vp, vp, vp, vp]
+        i64 = ctypes.c_int64
+        lib.pa_append_rope.argtypes = [P(pa_problem_t), P(pa_rope_t), vp, i64, vp, i64, vp, i64, vp,
+                                       i64, vp, vp, vp, vp, vp, vp]
         lib.pa_prefill.argtypes = [P(pa_problem_t), vp, vp, ctypes.c_int64, i32, vp, vp, vp, vp,
                                    f32, vp, P(pa_options_t), vp]
         lib.pa_split_kv_partial.argtypes = [P(pa_problem_t), vp, vp, vp, vp, vp, f32, i32, i32, vp,
@@ -135,12 +146,55 @@ def options(schedule="auto", math="auto", combine="auto", workers=0, stages=0,
     return o
 
 
+def rope(rotary_dim, style="half", table=None, positions=None, table_rows=None) -> pa_rope_t:
+    """pa_rope_t: the position rotation of pa_append_rope. ``table`` is fp32
+    [table_rows][2][rotary_dim / 2] (cosines, sines); ``positions`` int32, one per row, or None
+    for the token indices. The struct keeps the tensors it points to."""
+    _tensors("rope", table, positions)
+    r = pa_rope_t()
+    r.rotary_dim = int(rotary_dim)
+    r.style = ROPE_STYLE[style] if isinstance(style, str) else int(style)
+    r.table, r.positions = _ptr(table), _ptr(positions)
+    if table_rows is None:
+        table_rows = 0 if table is None or isinstance(table, int) else table.shape[0]
+    r.table_rows = int(table_rows)
+    r.keep = (table, positions)
+    return r
+
+
 def _ptr(x):
     if x is None:
         return None
     if isinstance(x, int):
         return x
     return x.data_ptr()
+
+
+def _tensors(where, *xs):
+    """Tensor arguments must be whole and on the current device (addresses pass unseen)."""
+    dev = None
+    for x in xs:
+        if x is None or isinstance(x, int):
+            continue
+        if dev is None:
+            import torch
+
+            dev = torch.cuda.current_device() if torch.cuda.is_available() else 0
+        if x.get_device() != dev or not x.is_contiguous():
+            raise PagedAttnError(1, where)
+
+
+def _rows(where, x, heads, head_dim, stride):
+    """(address, row stride in elements) of [tokens][heads][head_dim] rows whose tokens may be
+    apart, as slices of a fused projection's output are. An address takes ``stride`` as given
+    (0: packed)."""
+    if x is None or isinstance(x, int):
+        return x, int(stride)
+    n, h, d = x.stride()
+    if tuple(x.shape[1:]) != (heads, head_dim) or d != 1 or (h != head_dim and heads > 1):
+        raise PagedAttnError(1, where)
+    # one row has no next one: any stride says the same
+    return x.data_ptr(), n if x.shape[0] > 1 else 0
 
 
 def _stream(s):
@@ -218,6 +272,25 @@ def pa_append_kv(prob, new_key, new_value, block_tables, context_lengths, key_ca
     _check(load().pa_append_kv(ctypes.byref(prob), _ptr(new_key), _ptr(new_value),
                                _ptr(block_tables), _ptr(context_lengths), _ptr(key_cache),
                                _ptr(value_cache), _stream(stream)), "pa_append_kv")
+
+
+def pa_append_rope(prob, rope, query, new_key, new_value, query_start, total_tokens, block_tables,
+                   context_lengths, query_out, key_cache, value_cache, query_stride=0,
+                   key_stride=0, value_stride=0, stream=None):
+    """Write each sequence's last n_b tokens (rows query_start[b] .. query_start[b + 1]) into the
+    caches, keys turned by position, and their turned queries into query_out. query, new_key and
+    new_value may be slices of one fused projection's output (their row strides are taken from
+    the tensors); query and query_out may both be None."""
+    _tensors("pa_append_rope", query_start, block_tables, context_lengths, query_out, key_cache,
+             value_cache)
+    q, qs = _rows("pa_append_rope", query, prob.query_heads, prob.head_dim, query_stride)
+    k, ks = _rows("pa_append_rope", new_key, prob.kv_heads, prob.head_dim, key_stride)
+    v, vs = _rows("pa_append_rope", new_value, prob.kv_heads, prob.head_dim, value_stride)
+    _check(load().pa_append_rope(ctypes.byref(prob), ctypes.byref(rope) if rope is not None else None,
+                                 q, qs, k, ks, v, vs, _ptr(query_start), int(total_tokens),
+                                 _ptr(block_tables), _ptr(context_lengths), _ptr(query_out),
+                                 _ptr(key_cache), _ptr(value_cache), _stream(stream)),
+           "pa_append_rope")
 
 
 def pa_prefill(prob, query, query_start, total_tokens, max_query_len, key_cache, value_cache,
