@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import sys
 import threading
 from typing import Optional
 
@@ -150,11 +151,10 @@ def rope(rotary_dim, style="half", table=None, positions=None, table_rows=None) 
     """pa_rope_t: the position rotation of pa_append_rope. ``table`` is fp32
     [table_rows][2][rotary_dim / 2] (cosines, sines); ``positions`` int32, one per row, or None
     for the token indices. The struct keeps the tensors it points to."""
-    _tensors("rope", table, positions)
     r = pa_rope_t()
     r.rotary_dim = int(rotary_dim)
     r.style = ROPE_STYLE[style] if isinstance(style, str) else int(style)
-    r.table, r.positions = _ptr(table), _ptr(positions)
+    r.table, r.positions = _addresses("rope", table, positions)
     if table_rows is None:
         table_rows = 0 if table is None or isinstance(table, int) else table.shape[0]
     r.table_rows = int(table_rows)
@@ -170,18 +170,26 @@ def _ptr(x):
     return x.data_ptr()
 
 
-def _tensors(where, *xs):
-    """Tensor arguments must be whole and on the current device (addresses pass unseen)."""
-    dev = None
-    for x in xs:
-        if x is None or isinstance(x, int):
-            continue
-        if dev is None:
-            import torch
+def _torch_on_gpu():
+    """torch, if the process uses it on a GPU (then there is a current device and stream)."""
+    t = sys.modules.get("torch")
+    return t if t is not None and t.cuda.is_initialized() else None
 
-            dev = torch.cuda.current_device() if torch.cuda.is_available() else 0
-        if x.get_device() != dev or not x.is_contiguous():
-            raise PagedAttnError(1, where)
+
+def _addresses(where, *xs):
+    """Addresses of tensor arguments, which must be whole and on the current device (an address
+    passes unseen)."""
+    dev, out = None, []
+    for x in xs:
+        if x is not None and not isinstance(x, int):
+            if dev is None:
+                t = _torch_on_gpu()
+                dev = t._C._cuda_getDevice() if t is not None else 0
+            if x.get_device() != dev or not x.is_contiguous():
+                raise PagedAttnError(1, where)
+            x = x.data_ptr()
+        out.append(x)
+    return out
 
 
 def _rows(where, x, heads, head_dim, stride):
@@ -189,24 +197,21 @@ def _rows(where, x, heads, head_dim, stride):
     apart, as slices of a fused projection's output are. An address takes ``stride`` as given
     (0: packed)."""
     if x is None or isinstance(x, int):
-        return x, int(stride)
+        return x, stride
     n, h, d = x.stride()
-    if tuple(x.shape[1:]) != (heads, head_dim) or d != 1 or (h != head_dim and heads > 1):
+    rows, nh, nd = x.shape
+    if nh != heads or nd != head_dim or d != 1 or (h != head_dim and heads > 1):
         raise PagedAttnError(1, where)
     # one row has no next one: any stride says the same
-    return x.data_ptr(), n if x.shape[0] > 1 else 0
+    return x.data_ptr(), n if rows > 1 else 0
 
 
 def _stream(s):
+    """The stream's handle; None: torch's current stream (the default one without torch). Read
+    through the raw accessor: building the stream object costs more than a small launch."""
     if s is None:
-        try:
-            import torch
-
-            if torch.cuda.is_available():
-                return torch.cuda.current_stream().cuda_stream
-        except ImportError:
-            pass
-        return None
+        t = _torch_on_gpu()
+        return t._C._cuda_getCurrentRawStream(t._C._cuda_getDevice()) if t is not None else None
     if isinstance(s, int):
         return s
     return s.cuda_stream
@@ -281,16 +286,14 @@ def pa_append_rope(prob, rope, query, new_key, new_value, query_start, total_tok
     caches, keys turned by position, and their turned queries into query_out. query, new_key and
     new_value may be slices of one fused projection's output (their row strides are taken from
     the tensors); query and query_out may both be None."""
-    _tensors("pa_append_rope", query_start, block_tables, context_lengths, query_out, key_cache,
-             value_cache)
-    q, qs = _rows("pa_append_rope", query, prob.query_heads, prob.head_dim, query_stride)
-    k, ks = _rows("pa_append_rope", new_key, prob.kv_heads, prob.head_dim, key_stride)
-    v, vs = _rows("pa_append_rope", new_value, prob.kv_heads, prob.head_dim, value_stride)
-    _check(load().pa_append_rope(ctypes.byref(prob), ctypes.byref(rope) if rope is not None else None,
-                                 q, qs, k, ks, v, vs, _ptr(query_start), int(total_tokens),
-                                 _ptr(block_tables), _ptr(context_lengths), _ptr(query_out),
-                                 _ptr(key_cache), _ptr(value_cache), _stream(stream)),
-           "pa_append_rope")
+    where, heads, kv_heads, hd = "pa_append_rope", prob.query_heads, prob.kv_heads, prob.head_dim
+    q, qs = _rows(where, query, heads, hd, query_stride)
+    k, ks = _rows(where, new_key, kv_heads, hd, key_stride)
+    v, vs = _rows(where, new_value, kv_heads, hd, value_stride)
+    starts, bt, ctx, q_out, kc, vc = _addresses(where, query_start, block_tables, context_lengths,
+                                                query_out, key_cache, value_cache)
+    _check(load().pa_append_rope(prob, rope, q, qs, k, ks, v, vs, starts, total_tokens, bt, ctx,
+                                 q_out, kc, vc, _stream(stream)), where)
 
 
 def pa_prefill(prob, query, query_start, total_tokens, max_query_len, key_cache, value_cache,
