@@ -362,6 +362,61 @@ pa_status_t pa_prefill(const pa_problem_t *problem, const void *query, const int
                        const int32_t *context_lengths, float scale, float *out,
                        const pa_options_t *options, void *stream);
 
+/* Output element type of the calls that take a score rule. */
+typedef enum pa_out_t {
+  PA_OUT_FP32 = 0,
+  PA_OUT_FP16 = 1 /* rounded once from fp32 */
+} pa_out_t;
+
+/* A score rule: how pa_decode_scored and pa_prefill_scored turn the dot products of a query
+ * at position p of its sequence into weights. In this order, for query head h and token t:
+ *     s = scale * dot(q, K_t)
+ *     s = softcap * tanh(s / softcap)          if softcap > 0
+ *     s = s - slopes[h] * |p - t|              if slopes
+ * and the softmax runs over the tokens that the query sees:
+ *     max(0, first_tokens[row], p - window + 1) <= t <= p
+ * (without the window's term for window 0, without the first token's for first_tokens NULL).
+ * With prefix_lengths a query inside its sequence's prefix (p < prefix_lengths[b]) sees on to
+ * the prefix's end, t < min(prefix_lengths[b], context_lengths[b]), instead of to p; the
+ * window and the first token bound it as before. A query that sees nothing gives a zero row.
+ * The fields of a zeroed struct change nothing: softmax(scale q K) over t <= p, fp32 out.
+ * Tokens that no query of a call sees are not read, nor are block-table entries of pages
+ * that hold only such tokens (a local layer's freed pages may be anything). Cached keys and
+ * values that some query of a call sees must be finite: a non-finite value may also reach the
+ * call's other queries of its sequence and K/V head. */
+typedef struct pa_score_t {
+  float softcap;     /* 0: no cap; else positive and finite */
+  int32_t window;    /* 0: no window; else >= 1 */
+  int32_t out_type;  /* pa_out_t */
+  int32_t reserved;  /* 0 */
+  const float *slopes;           /* device, fp32 [query_heads], or NULL */
+  const int32_t *first_tokens;   /* device, int32 [query rows] (batch rows for a decode step,
+                                    total_tokens for several tokens), or NULL: where the row's
+                                    document starts; values below 0 mean 0 */
+  const int32_t *prefix_lengths; /* device, int32 [batch], or NULL; values outside
+                                    [0, context] are clamped to it. A decode step's query is
+                                    past or at the end of any prefix: not read there */
+} pa_score_t;
+
+/* One decode step under a score rule: pa_decode_ex's operation ("[TIL] Optimizing paged
+ * attention", sections "Paged Attention" and "V4 (Context-axis parallelism)") with the
+ * scores and the seen tokens of `score` (host struct; NULL: no rule, fp32 out), in the
+ * plan that pa_plan gives for `options` with two differences: the arithmetic is always the
+ * tensor-core form (PA_MATH_SIMT: PA_ERR_UNSUPPORTED) and a shared unit is always merged by
+ * the separate combine kernel (PA_COMBINE_FUSED: PA_ERR_UNSUPPORTED), so that a captured call
+ * can be replayed as it is. Probabilities are kept to 22 bits and sums in fp32.
+ *   out        fp32 or fp16 (score->out_type) [batch][query_heads][head_dim], 16-byte aligned,
+ *              fully overwritten
+ *   workspace  caller-owned device memory of workspace_bytes >= pa_workspace_size(problem,
+ *              options), 256-byte aligned (PA_ERR_WORKSPACE, PA_ERR_MISALIGNED); NULL if that
+ *              is 0. It needs no initialisation and nothing is kept in it between calls;
+ *              calls that may overlap in time need one each. */
+pa_status_t pa_decode_scored(const pa_problem_t *problem, const pa_score_t *score,
+                             const void *query, const void *key_cache, const void *value_cache,
+                             const int32_t *block_tables, const int32_t *context_lengths,
+                             float scale, void *out, const pa_options_t *options, void *workspace,
+                             size_t workspace_bytes, void *stream);
+
 /* Read and clear the device error word of the current device (PA_DEVERR_* bits) after
  * the work queued on `stream` finishes. Synchronises `stream`. The word records the
  * preconditions of "[TIL] Optimizing paged attention", section "Paged Attention" (a

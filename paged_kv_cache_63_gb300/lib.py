@@ -30,11 +30,13 @@ PA_TEST_EXPIRE_WAITS = 1
 SCHEDULE = {"auto": 0, "single": 1, "balanced": 2}
 MATH = {"auto": 0, "simt": 1, "mma": 2}
 COMBINE = {"auto": 0, "fused": 1, "kernel": 2}
+OUT = {"fp32": 0, "fp16": 1}
 ROPE_STYLE = {"half": 0, "interleaved": 1}
 
 # Every entry point include/pagedattn.h declares.
 EXPORTS = ("pa_plan", "pa_workspace_size", "pa_workspace_init", "pa_decode", "pa_decode_ex",
            "pa_decode_noalloc", "pa_append_kv", "pa_append_rope", "pa_prefill",
+           "pa_decode_scored",
            "pa_split_kv_partial", "pa_split_kv_combine", "pa_get_device_error",
            "pa_status_string", "pa_version")
 
@@ -75,6 +77,13 @@ class pa_rope_t(ctypes.Structure):
                 ("table", ctypes.c_void_p), ("positions", ctypes.c_void_p)]
 
 
+class pa_score_t(ctypes.Structure):
+    _fields_ = [("softcap", ctypes.c_float), ("window", ctypes.c_int32),
+                ("out_type", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("slopes", ctypes.c_void_p), ("first_tokens", ctypes.c_void_p),
+                ("prefix_lengths", ctypes.c_void_p)]
+
+
 _lib = None
 _lock = threading.Lock()
 
@@ -104,6 +113,8 @@ def load(path: Optional[str] = None):
         i64 = ctypes.c_int64
         lib.pa_append_rope.argtypes = [P(pa_problem_t), P(pa_rope_t), vp, i64, vp, i64, vp, i64, vp,
                                        i64, vp, vp, vp, vp, vp, vp]
+        lib.pa_decode_scored.argtypes = [P(pa_problem_t), P(pa_score_t), vp, vp, vp, vp, vp, f32, vp,
+                                         P(pa_options_t), vp, ctypes.c_size_t, vp]
         lib.pa_prefill.argtypes = [P(pa_problem_t), vp, vp, ctypes.c_int64, i32, vp, vp, vp, vp,
                                    f32, vp, P(pa_options_t), vp]
         lib.pa_split_kv_partial.argtypes = [P(pa_problem_t), vp, vp, vp, vp, vp, f32, i32, i32, vp,
@@ -160,6 +171,20 @@ def rope(rotary_dim, style="half", table=None, positions=None, table_rows=None) 
     r.table_rows = int(table_rows)
     r.keep = (table, positions)
     return r
+
+
+def score(softcap=0.0, window=0, slopes=None, first_tokens=None, prefix_lengths=None,
+          out="fp32") -> pa_score_t:
+    """pa_score_t: the score rule of pa_decode_scored and pa_prefill_scored. ``slopes`` is fp32
+    [query_heads], ``first_tokens`` int32 [query rows], ``prefix_lengths`` int32 [batch]. The
+    struct keeps the tensors it points to."""
+    s = pa_score_t()
+    s.softcap, s.window = float(softcap), int(window)
+    s.out_type = OUT[out] if isinstance(out, str) else int(out)
+    s.slopes, s.first_tokens, s.prefix_lengths = _addresses("score", slopes, first_tokens,
+                                                            prefix_lengths)
+    s.keep = (slopes, first_tokens, prefix_lengths)
+    return s
 
 
 def _ptr(x):
@@ -307,6 +332,17 @@ def pa_prefill(prob, query, query_start, total_tokens, max_query_len, key_cache,
                              float(scale), _ptr(out),
                              ctypes.byref(opts) if opts is not None else None,
                              _stream(stream)), "pa_prefill")
+
+
+def pa_decode_scored(prob, score, query, key_cache, value_cache, block_tables, context_lengths,
+                     scale, out, opts: Optional[pa_options_t] = None, workspace=None,
+                     workspace_bytes: int = 0, stream=None):
+    """A decode step under a score rule (``score()`` or None); out fp32 or fp16 as the rule says.
+    The workspace (pa_workspace_size) needs no initialisation."""
+    q, k, v, bt, ctx, o, ws = _addresses("pa_decode_scored", query, key_cache, value_cache,
+                                         block_tables, context_lengths, out, workspace)
+    _check(load().pa_decode_scored(prob, score, q, k, v, bt, ctx, scale, o, opts, ws,
+                                   workspace_bytes, _stream(stream)), "pa_decode_scored")
 
 
 def pa_split_kv_partial(prob, query, key_cache, value_cache, block_tables, context_lengths, scale,
