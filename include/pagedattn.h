@@ -417,6 +417,24 @@ pa_status_t pa_decode_scored(const pa_problem_t *problem, const pa_score_t *scor
                              float scale, void *out, const pa_options_t *options, void *workspace,
                              size_t workspace_bytes, void *stream);
 
+/* Attention of several new tokens per sequence under a score rule: pa_prefill's operation,
+ * arguments and checks ("[TIL] Optimizing paged attention", section "Flash Attention" over
+ * the paged cache) with the scores and the seen tokens of `score` (host struct, not NULL). The
+ * rows of first_tokens are the query's ([total_tokens]; rows of no new token are not read).
+ * Key tiles that none of a query tile's tokens sees are skipped.
+ *   out        fp16 [total_tokens][query_heads][head_dim], 16-byte aligned; rows of new tokens
+ *              are written, other rows are left untouched. score->out_type must be PA_OUT_FP16
+ *              (PA_ERR_UNSUPPORTED): the probabilities meet V rounded to fp16, so a wider output
+ *              would hold no more
+ * A prefix reaches past a query only as far as the cache does: the keys of a prefix whose
+ * later part comes with a later call are not there yet, so a prefix goes into one call. */
+pa_status_t pa_prefill_scored(const pa_problem_t *problem, const pa_score_t *score,
+                              const void *query, const int32_t *query_start,
+                              int64_t total_tokens, int32_t max_query_len, const void *key_cache,
+                              const void *value_cache, const int32_t *block_tables,
+                              const int32_t *context_lengths, float scale, void *out,
+                              const pa_options_t *options, void *stream);
+
 /* Read and clear the device error word of the current device (PA_DEVERR_* bits) after
  * the work queued on `stream` finishes. Synchronises `stream`. The word records the
  * preconditions of "[TIL] Optimizing paged attention", section "Paged Attention" (a

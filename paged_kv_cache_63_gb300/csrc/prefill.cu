@@ -1,70 +1,24 @@
-// prefill.cu -- host entry point of the causal multi-token (prefill) kernel: argument
-// checks, tensor maps and the launch.
+// prefill.cu -- host entry point of the causal multi-token (prefill) kernels, and the argument
+// checks and tensor maps that it shares with the one under a score rule.
 #include <cmath>
 
-#include "internal.h"
-#include "pagedattn.h"
-#include "prefill2_kernel.cuh"
-#include "prefill_kernel.cuh"
+#include "prefill_launch.cuh"
 
 namespace pa {
 
 namespace {
 
-constexpr int kMaxDevicesPrefill = 64;
-
-template <int HD>
-cudaError_t launch_prefill_hd(const PrefillArgs &a, const CUtensorMap &tq, const CUtensorMap &tk,
-                              const CUtensorMap &tv, dim3 grid, cudaStream_t stream) {
-  using C = PrefillCfg<HD>;
-  auto kern = prefill_kernel<HD>;
-  constexpr int smem = C::kSmem + 1024;
-  static bool set[kMaxDevicesPrefill] = {false};
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= kMaxDevicesPrefill || !set[dev]) {
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-    if (dev >= 0 && dev < kMaxDevicesPrefill) set[dev] = true;
-  }
-  kern<<<grid, kPrefillThreads, smem, stream>>>(a, tq, tk, tv);
-  return cudaGetLastError();
-}
-
-// head_dim 64 / 128: two query tiles per CTA (a.n_qtiles counts pairs, grid.z too)
-template <int HD>
-cudaError_t launch_prefill2_hd(const PrefillArgs &a, const CUtensorMap &tq, const CUtensorMap &tk,
-                               const CUtensorMap &tv, dim3 grid, cudaStream_t stream) {
-  using C = Prefill2Cfg<HD>;
-  auto kern = prefill2_kernel<HD>;
-  constexpr int smem = C::kSmem + 1024;
-  static bool set[kMaxDevicesPrefill] = {false};
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= kMaxDevicesPrefill || !set[dev]) {
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-    if (dev >= 0 && dev < kMaxDevicesPrefill) set[dev] = true;
-  }
-  kern<<<grid, kPrefill2Threads, smem, stream>>>(a, tq, tk, tv);
-  return cudaGetLastError();
-}
-
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 }  // namespace
 
-}  // namespace pa
-
-extern "C" pa_status_t pa_prefill(const pa_problem_t *problem, const void *query,
-                                  const int32_t *query_start, int64_t total_tokens,
-                                  int32_t max_query_len, const void *key_cache,
-                                  const void *value_cache, const int32_t *block_tables,
-                                  const int32_t *context_lengths, float scale, float *out,
-                                  const pa_options_t *options, void *stream) {
-  using namespace pa;
+pa_status_t setup_prefill(const pa_problem_t *problem, const void *query,
+                          const int32_t *query_start, int64_t total_tokens, int32_t max_query_len,
+                          const void *key_cache, const void *value_cache,
+                          const int32_t *block_tables, const int32_t *context_lengths, float scale,
+                          const void *out, const pa_options_t *options, PrefillLaunch *l,
+                          PrefillArgs *args) {
+  l->grid = dim3(0, 0, 0);
   pa_status_t st = check_problem_public(problem);
   if (st != PA_OK) return st;
   if (options && (options->schedule || options->math || options->combine || options->workers ||
@@ -83,9 +37,9 @@ extern "C" pa_status_t pa_prefill(const pa_problem_t *problem, const void *query
     return PA_ERR_MISALIGNED;
   const int g = problem->query_heads / problem->kv_heads;
   if (g > 128) return PA_ERR_UNSUPPORTED;
-  if (problem->batch == 0 || total_tokens == 0 || max_query_len == 0) return PA_OK;
+  if (problem->batch == 0 || total_tokens == 0 || max_query_len == 0) return PA_OK;  // empty grid
   if (problem->batch > 65535 || problem->kv_heads > 65535) return PA_ERR_UNSUPPORTED;
-  int smem_optin = 0;
+  int smem_optin = 0;  // only the device check matters: both kernels fit any sm_103
   st = current_device_smem(&smem_optin);
   if (st != PA_OK) return st;
 
@@ -95,11 +49,10 @@ extern "C" pa_status_t pa_prefill(const pa_problem_t *problem, const void *query
   const long long n_qtiles = (static_cast<long long>(max_query_len) + qt - 1) / qt;
   if (n_qtiles > 65535) return PA_ERR_UNSUPPORTED;
 
-  PrefillArgs a = {};
+  PrefillArgs &a = *args;
   a.qs = query_start;
   a.bt = block_tables;
   a.ctx = context_lengths;
-  a.out = out;
   a.err = device_error_word();
   if (!a.err) return PA_ERR_CUDA;
   a.total = total_tokens;
@@ -119,32 +72,34 @@ extern "C" pa_status_t pa_prefill(const pa_problem_t *problem, const void *query
   a.expire = (options && (options->test_flags & PA_TEST_EXPIRE_WAITS)) ? 1 : 0;
   a.out_v8 = (reinterpret_cast<uintptr_t>(out) & 31u) == 0 ? 1 : 0;
 
-  CUtensorMap tq, tk, tv;
   const int rows = a.ps < tn ? a.ps : tn;
-  st = encode_query_map(&tq, query, total_tokens, a.qh, hd, g, qt);
+  st = encode_query_map(&l->tq, query, total_tokens, a.qh, hd, g, qt);
   if (st != PA_OK) return st;
-  st = encode_cache_map_rows(&tk, key_cache, problem, rows);
+  st = encode_cache_map_rows(&l->tk, key_cache, problem, rows);
   if (st != PA_OK) return st;
-  st = encode_cache_map_rows(&tv, value_cache, problem, rows);
+  st = encode_cache_map_rows(&l->tv, value_cache, problem, rows);
   if (st != PA_OK) return st;
 
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  cudaError_t e;
   if (hd != 256) a.n_qtiles = (a.n_qtiles + 1) / 2;  // pairs of query tiles
-  const dim3 grid(a.kvh, a.batch, a.n_qtiles);
-  switch (hd) {
-    case 64:
-      e = launch_prefill2_hd<64>(a, tq, tk, tv, grid, s);
-      break;
-    case 128:
-      e = launch_prefill2_hd<128>(a, tq, tk, tv, grid, s);
-      break;
-    case 256:
-      e = launch_prefill_hd<256>(a, tq, tk, tv, grid, s);
-      break;
-    default:
-      return PA_ERR_UNSUPPORTED;
-  }
-  (void)smem_optin;
-  return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+  l->grid = dim3(a.kvh, a.batch, a.n_qtiles);
+  return PA_OK;
+}
+
+}  // namespace pa
+
+extern "C" pa_status_t pa_prefill(const pa_problem_t *problem, const void *query,
+                                  const int32_t *query_start, int64_t total_tokens,
+                                  int32_t max_query_len, const void *key_cache,
+                                  const void *value_cache, const int32_t *block_tables,
+                                  const int32_t *context_lengths, float scale, float *out,
+                                  const pa_options_t *options, void *stream) {
+  using namespace pa;
+  PrefillLaunch l;
+  PrefillArgs a = {};
+  pa_status_t st = setup_prefill(problem, query, query_start, total_tokens, max_query_len,
+                                 key_cache, value_cache, block_tables, context_lengths, scale, out,
+                                 options, &l, &a);
+  if (st != PA_OK || l.grid.x == 0) return st;
+  a.out = out;
+  return launch_prefill<false>(problem->head_dim, a, l, static_cast<cudaStream_t>(stream));
 }

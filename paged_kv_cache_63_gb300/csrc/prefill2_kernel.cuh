@@ -121,6 +121,57 @@ __device__ __forceinline__ Item2 item2_of(const PrefillArgs &a, int kv, int b, i
   return it;
 }
 
+// Under a score rule (kScored) an item also knows where its keys start: tiles are counted from
+// j0, the tile of the first token that some row of the pair sees (kv_lo), and end at the last
+// one (nt_a, nt_b, nt_max, max_pos_a, max_pos_b and kv_len follow what the rows see). Warp-collective.
+struct ScoredItem2 : Item2 {
+  int j0, kv_lo, prefix;
+};
+
+template <int TN>
+__device__ __forceinline__ ScoredItem2 scored_item2_of(const PrefillScoredArgs &a, int kv, int b,
+                                                       int pair) {
+  ScoredItem2 it;
+  it.kv = kv;
+  it.b = b;
+  it.live = 0;
+  it.stop = 0;
+  it.nt_a = it.nt_b = it.nt_max = 0;
+  const int q0 = __ldg(a.qs + b), q1 = __ldg(a.qs + b + 1), ctx = __ldg(a.ctx + b);
+  const int n = q1 - q0;
+  it.q0 = q0;
+  it.n = n;
+  it.ctx = ctx;
+  unsigned bad = 0;
+  if (ctx < 0 || static_cast<long long>(ctx) > static_cast<long long>(a.maxp) << a.ps_shift)
+    bad = PA_DEVERR_CONTEXT;
+  else if (q0 < 0 || n < 0 || static_cast<long long>(q1) > a.total || n > ctx)
+    bad = PA_DEVERR_QUERY_START;
+  if (bad) {
+    if ((threadIdx.x & 31) == 0) atomicOr(a.err, bad);
+    return it;
+  }
+  it.tok0_a = 2 * pair * a.qt;
+  it.tok0_b = it.tok0_a + a.qt;
+  if (it.tok0_a >= n) return it;
+  it.prefix = prefix_of(a.s, b, ctx);
+  int lo_a, lo_b;
+  seen_range(a.s, q0, ctx - n, it.tok0_a, min(it.tok0_b, n), it.prefix, lo_a, it.max_pos_a);
+  it.max_pos_b = -1;
+  it.kv_lo = lo_a;
+  if (it.tok0_b < n) {
+    seen_range(a.s, q0, ctx - n, it.tok0_b, min(it.tok0_b + a.qt, n), it.prefix, lo_b, it.max_pos_b);
+    it.kv_lo = min(lo_a, lo_b);
+  }
+  it.j0 = it.kv_lo / TN;
+  it.nt_a = (it.max_pos_a + TN) / TN - it.j0;
+  it.nt_b = it.tok0_b < n ? (it.max_pos_b + TN) / TN - it.j0 : 0;
+  it.nt_max = max(it.nt_a, it.nt_b);
+  it.kv_len = max(it.max_pos_a, it.max_pos_b) + 1;
+  it.live = 1;
+  return it;
+}
+
 // P = exp2(s * sl2 + nm) over a row of TN scores, written as fp16 pairs over the first TN / 2
 // TMEM columns at ts, with the row's partial sums in rp. With kMasked keys past lim give
 // exactly 0; without, packed fp32 pairs do two exponent arguments per FFMA2 and two sum terms
@@ -157,16 +208,18 @@ __device__ __forceinline__ void exps_row(const float (&v)[TN], float sl2, float 
   }
 }
 
-template <int HD>
+// kScored: under a score rule (scored_softmax.cuh), with fp16 output.
+template <int HD, bool kScored>
 __global__ void __launch_bounds__(kPrefill2Threads, 1)
-    prefill2_kernel(const __grid_constant__ PrefillArgs a, const __grid_constant__ CUtensorMap tq,
-                    const __grid_constant__ CUtensorMap tk,
+    prefill2_kernel(const __grid_constant__ PrefillArgsOf<kScored> a,
+                    const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                     const __grid_constant__ CUtensorMap tv) {
   using C = Prefill2Cfg<HD>;
+  using Item = std::conditional_t<kScored, ScoredItem2, Item2>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t bars[kNumBars2];
   __shared__ __align__(16) uint4 clc_answer;
-  __shared__ Item2 items[2];
+  __shared__ Item items[2];
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_word;
   __shared__ int drain_last[2];
@@ -211,8 +264,16 @@ __global__ void __launch_bounds__(kPrefill2Threads, 1)
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
 
+  // first token of tile j of an item
+  auto tile_token = [](const Item &it, int j) {
+    if constexpr (kScored)
+      return (it.j0 + j) * C::TN;
+    else
+      return j * C::TN;
+  };
+
   // Reader side of the item ring: item k sits in entry k & 1. Returns false on abort.
-  auto take_item = [&](int k, Item2 &it) {
+  auto take_item = [&](int k, Item &it) {
     if (!pipe_wait(bar(kB2ItemFull + (k & 1)), (k >> 1) & 1, abort_flag, a.err)) return false;
     it = items[k & 1];
     __syncwarp();
@@ -232,7 +293,16 @@ __global__ void __launch_bounds__(kPrefill2Threads, 1)
       // publish item k once every reader has taken item k - 2 from the same entry
       if (k >= 2 && !pipe_wait(bar(kB2ItemEmpty + (k & 1)), ((k >> 1) - 1) & 1, abort_flag, a.err))
         break;
-      if (lane == 0) {
+      if constexpr (kScored) {
+        Item it;
+        it.stop = 1;
+        it.live = 0;
+        if (!stop) it = scored_item2_of<C::TN>(a, kv, b, a.n_qtiles - 1 - z);
+        if (lane == 0) {
+          items[k & 1] = it;
+          mbar_arrive(bar(kB2ItemFull + (k & 1)));
+        }
+      } else if (lane == 0) {
         Item2 it;
         if (stop) {
           it.stop = 1;
@@ -286,7 +356,7 @@ __global__ void __launch_bounds__(kPrefill2Threads, 1)
     int q_loads = 0;
     bool ok = true;
     for (int k = 0; ok; ++k) {
-      Item2 it;
+      Item it;
       ok = take_item(k, it);
       if (!ok || it.stop) break;
       if (!is_v && lane == 0) mbar_arrive(bar(kB2ProdStart));
@@ -307,20 +377,25 @@ __global__ void __launch_bounds__(kPrefill2Threads, 1)
         ++q_loads;
       }
       const int32_t *bt_row = a.bt + static_cast<size_t>(it.b) * a.maxp;
+      // whether this lane's box, at token tok, holds a token that some row sees
+      auto needed = [&](int tok) {
+        if constexpr (kScored)
+          return lane < boxes && tok < it.kv_len && tok + rows_per_box > it.kv_lo;
+        else
+          return lane < boxes && tok < it.kv_len;
+      };
       auto page_of = [&](int j) {
-        const int tok = j * C::TN + lane * rows_per_box;
-        return (j < it.nt_max && lane < boxes && tok < it.kv_len)
-                   ? __ldg(bt_row + (tok >> a.ps_shift))
-                   : -1;
+        const int tok = tile_token(it, j) + lane * rows_per_box;
+        return (j < it.nt_max && needed(tok)) ? __ldg(bt_row + (tok >> a.ps_shift)) : -1;
       };
       int page_next = page_of(0);
       for (int j = 0; j < it.nt_max && ok; ++j) {
         const int item = 2 * (gt + j) + (is_v ? 1 : 0);
         const int s = item % C::kSlots;
-        const int tok = j * C::TN + lane * rows_per_box;
+        const int tok = tile_token(it, j) + lane * rows_per_box;
         int page = page_next;
         page_next = page_of(j + 1);
-        if (lane < boxes && tok < it.kv_len && (page < 0 || page >= a.num_pages)) {
+        if (needed(tok) && (page < 0 || page >= a.num_pages)) {
           if (!is_v) atomicOr(a.err, PA_DEVERR_PAGE_ID);
           page = -1;
         }
@@ -382,7 +457,7 @@ __global__ void __launch_bounds__(kPrefill2Threads, 1)
     int gt = 0;
     uint32_t phase = 0;  // parities of the next waits: bit 0 QFull, bit 1 + x PFull[x]
     for (int k = 0; ok; ++k) {
-      Item2 it;
+      Item it;
       ok = take_item(k, it);
       if (!ok || it.stop) break;
       if (!it.live) continue;
@@ -422,7 +497,7 @@ __global__ void __launch_bounds__(kPrefill2Threads, 1)
         // V rows past the last needed token hold unread cache slots (possibly never
         // written): P is zero there, but 0 * NaN is not, so clear them before the first P.V
         // of that tile.
-        const int rows_last = it.kv_len - j * C::TN;
+        const int rows_last = it.kv_len - tile_token(it, j);
         if (j != it.nt_max - 1 || rows_last >= C::TN) return;
         const int per_block = (C::TN - rows_last) * 8;
         uint8_t *vg = sgen + C::kRingOff + ((2 * (gt + j) + 1) % C::kSlots) * C::kSlotBytes;
@@ -433,6 +508,21 @@ __global__ void __launch_bounds__(kPrefill2Threads, 1)
         }
         fence_proxy_async();
         __syncwarp();
+      };
+      auto clear_v_head = [&](int j) {
+        // likewise the rows before the first token that some row sees
+        if constexpr (kScored) {
+          const int rows_first = it.kv_lo - tile_token(it, j);
+          if (j != 0 || rows_first <= 0) return;
+          const int per_block = rows_first * 8;
+          uint8_t *vg = sgen + C::kRingOff + ((2 * gt + 1) % C::kSlots) * C::kSlotBytes;
+          for (int c = lane; c < C::KB * per_block; c += 32) {
+            const int kb = c / per_block, r = c % per_block;
+            *reinterpret_cast<uint4 *>(vg + kb * (C::TN * 128) + r * 16) = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async();
+          __syncwarp();
+        }
       };
       ok = pipe_wait(bar(kB2QFull), phase & 1u, abort_flag, a.err);
       phase ^= 1u;
@@ -454,7 +544,10 @@ __global__ void __launch_bounds__(kPrefill2Threads, 1)
           if (!ok) break;
           phase ^= 2u << x;
           tc_fence_after();
-          if (x == 0 || j >= it.nt_a) clear_v_tail(j);
+          if (x == 0 || j >= it.nt_a) {
+            clear_v_head(j);
+            clear_v_tail(j);
+          }
           issue_pv(x, j);
           const bool last_v_user = (x == 1) || (j >= it.nt_b);
           if (last_v_user) release(2 * (gt + j) + 1);
@@ -486,9 +579,11 @@ __global__ void __launch_bounds__(kPrefill2Threads, 1)
     bool ok = true;
     for (int k = 0; ok; ++k) {
       int my_nt, pos, gt0, out_row0, out_head0;
+      int tile0 = 0;  // first token of the item's first tile
+      ScoredRow sr = {};
       bool valid;
       {
-        Item2 it;
+        Item it;
         ok = take_item(k, it);
         if (!ok || it.stop) break;
         if (!it.live) continue;
@@ -496,6 +591,13 @@ __global__ void __launch_bounds__(kPrefill2Threads, 1)
         my_nt = x ? it.nt_b : it.nt_a;
         valid = row < q_rows && my_tok0 + t < it.n;
         pos = min(it.ctx - it.n + my_tok0 + t, x ? it.max_pos_b : it.max_pos_a);
+        if constexpr (kScored) {
+          // rows past the tile's last token repeat it (and are not stored)
+          tile0 = it.j0 * C::TN;
+          if (my_nt > 0)
+            sr = scored_row(a.s, it.q0, it.ctx - it.n, min(my_tok0 + min(t, a.qt - 1), it.n - 1),
+                            it.kv * a.g + h, it.prefix);
+        }
         out_row0 = it.q0 + my_tok0;  // output row of the tile's first token
         out_head0 = it.kv * a.g;
         gt0 = gt;
@@ -527,6 +629,35 @@ __global__ void __launch_bounds__(kPrefill2Threads, 1)
           if (ok && j + 1 < my_nt)
             ok = pipe_wait(bar(kB2Full + ik % C::kSlots), (ik / C::kSlots) & 1, abort_flag, a.err);
           if (!ok) break;
+        }
+        if constexpr (kScored) {
+          auto reload = [&]() { tmem_ld128(ts, v); };
+          auto rescale = [&](float f) {
+            // S_X(j) completed, so PV_X(j - 1) has too: O_X is stable until P_X(j) is released
+#pragma unroll
+            for (int c = 0; c < HD / 32; ++c) {
+              float o[32];
+              tmem_ld32(to + c * 32, o);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] *= f;
+              tmem_st32(to + c * 32, o);
+            }
+            return true;
+          };
+          scored_weights<C::TN>(v, a.s, sl2, sr, tile0 + j * C::TN, j > 0, reload, rescale);
+          // P as fp16 pairs over the first 64 columns of S
+#pragma unroll
+          for (int h2 = 0; h2 < C::TN / 64; ++h2) {
+            float pk[32];
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              pk[e] = __uint_as_float(pack_half2(v[h2 * 64 + 2 * e], v[h2 * 64 + 2 * e + 1]));
+            tmem_st32(ts + h2 * 32, pk);
+          }
+          tmem_wait_st();
+          tc_fence_before();
+          mbar_arrive(bar(kB2PFull + x));
+          continue;
         }
         const int lim = pos - j * C::TN;
         // warp-uniform: the exponent passes hold tcgen05.st, which the whole warp executes
@@ -613,6 +744,7 @@ __global__ void __launch_bounds__(kPrefill2Threads, 1)
       }
       if (ok && my_nt > 0) {
         tc_fence_after();
+        if constexpr (kScored) l = sr.l;
         const float inv = l > 0.f ? 1.f / l : 0.f;
         // Each thread writes its row straight from TMEM, 32 columns at a time: 32-byte stores
         // fill whole sectors, so L2 never reads a partly written sector from DRAM first, and
@@ -628,19 +760,26 @@ __global__ void __launch_bounds__(kPrefill2Threads, 1)
         for (int c = 0; c < HD / 32; ++c) {
           float o[32];
           tmem_ld32(to + c * 32, o);
+          if constexpr (kScored) {
+            if (valid)
+              store_half32(a.out16 + (static_cast<size_t>(out_row0 + t) * a.qh + out_head0 + h) * HD +
+                               c * 32,
+                           o, inv, a.out_v8, pol);
+          } else {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] *= inv;
-          if (valid) {
-            if (a.out_v8) {
+            for (int e = 0; e < 32; ++e) o[e] *= inv;
+            if (valid) {
+              if (a.out_v8) {
 #pragma unroll
-              for (int e = 0; e < 32; e += 8)
-                st_global_v8(dst + c * 32 + e, o[e], o[e + 1], o[e + 2], o[e + 3], o[e + 4],
-                             o[e + 5], o[e + 6], o[e + 7], pol);
-            } else {
+                for (int e = 0; e < 32; e += 8)
+                  st_global_v8(dst + c * 32 + e, o[e], o[e + 1], o[e + 2], o[e + 3], o[e + 4],
+                               o[e + 5], o[e + 6], o[e + 7], pol);
+              } else {
 #pragma unroll
-              for (int e = 0; e < 32; e += 4)
-                *reinterpret_cast<float4 *>(dst + c * 32 + e) =
-                    make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                for (int e = 0; e < 32; e += 4)
+                  *reinterpret_cast<float4 *>(dst + c * 32 + e) =
+                      make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+              }
             }
           }
         }

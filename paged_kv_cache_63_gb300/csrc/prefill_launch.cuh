@@ -1,0 +1,82 @@
+// prefill_launch.cuh -- host-side set-up and launch of the multi-token kernels: the two-tile
+// kernel for head_dim 64 and 128, the single-tile kernel for 256, plain or under a score rule.
+#pragma once
+
+#include <atomic>
+
+#include "internal.h"
+#include "pagedattn.h"
+#include "prefill2_kernel.cuh"
+#include "prefill_kernel.cuh"
+
+namespace pa {
+
+struct PrefillLaunch {
+  CUtensorMap tq, tk, tv;
+  dim3 grid;  // x = 0: nothing to do
+};
+
+// Checks the arguments of a multi-token call and fills its tensor maps, grid and kernel
+// arguments but the output (defined in prefill.cu). `args` comes in zeroed.
+pa_status_t setup_prefill(const pa_problem_t *problem, const void *query,
+                          const int32_t *query_start, int64_t total_tokens, int32_t max_query_len,
+                          const void *key_cache, const void *value_cache,
+                          const int32_t *block_tables, const int32_t *context_lengths, float scale,
+                          const void *out, const pa_options_t *options, PrefillLaunch *l,
+                          PrefillArgs *args);
+
+constexpr int kMaxDevicesPrefill = 64;
+
+// Raises a kernel's shared-memory limit once per device.
+template <typename Kernel>
+cudaError_t allow_smem(Kernel kern, int smem, std::atomic<bool> (&set)[kMaxDevicesPrefill]) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= kMaxDevicesPrefill || !set[dev].load(std::memory_order_relaxed)) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < kMaxDevicesPrefill) set[dev].store(true, std::memory_order_relaxed);
+  }
+  return cudaSuccess;
+}
+
+// head_dim 64 / 128: two query tiles per CTA (a.n_qtiles counts pairs, grid.z too)
+template <int HD, bool kScored>
+cudaError_t launch_prefill2_hd(const PrefillArgsOf<kScored> &a, const PrefillLaunch &l,
+                               cudaStream_t stream) {
+  static std::atomic<bool> set[kMaxDevicesPrefill];
+  constexpr int smem = Prefill2Cfg<HD>::kSmem + 1024;
+  auto kern = prefill2_kernel<HD, kScored>;
+  const cudaError_t e = allow_smem(kern, smem, set);
+  if (e != cudaSuccess) return e;
+  kern<<<l.grid, kPrefill2Threads, smem, stream>>>(a, l.tq, l.tk, l.tv);
+  return cudaGetLastError();
+}
+
+template <int HD, bool kScored>
+cudaError_t launch_prefill_hd(const PrefillArgsOf<kScored> &a, const PrefillLaunch &l,
+                              cudaStream_t stream) {
+  static std::atomic<bool> set[kMaxDevicesPrefill];
+  constexpr int smem = PrefillCfg<HD>::kSmem + 1024;
+  auto kern = prefill_kernel<HD, kScored>;
+  const cudaError_t e = allow_smem(kern, smem, set);
+  if (e != cudaSuccess) return e;
+  kern<<<l.grid, kPrefillThreads, smem, stream>>>(a, l.tq, l.tk, l.tv);
+  return cudaGetLastError();
+}
+
+template <bool kScored>
+pa_status_t launch_prefill(int head_dim, const PrefillArgsOf<kScored> &a, const PrefillLaunch &l,
+                           cudaStream_t stream) {
+  cudaError_t e;
+  switch (head_dim) {
+    case 64: e = launch_prefill2_hd<64, kScored>(a, l, stream); break;
+    case 128: e = launch_prefill2_hd<128, kScored>(a, l, stream); break;
+    case 256: e = launch_prefill_hd<256, kScored>(a, l, stream); break;
+    default: return PA_ERR_UNSUPPORTED;
+  }
+  return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+}  // namespace pa

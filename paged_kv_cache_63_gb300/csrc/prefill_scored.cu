@@ -1,0 +1,25 @@
+// prefill_scored.cu -- host entry point of multi-token attention under a score rule.
+#include "prefill_launch.cuh"
+
+extern "C" pa_status_t pa_prefill_scored(const pa_problem_t *problem, const pa_score_t *score,
+                                         const void *query, const int32_t *query_start,
+                                         int64_t total_tokens, int32_t max_query_len,
+                                         const void *key_cache, const void *value_cache,
+                                         const int32_t *block_tables,
+                                         const int32_t *context_lengths, float scale, void *out,
+                                         const pa_options_t *options, void *stream) {
+  using namespace pa;
+  PrefillScoredArgs a = {};
+  pa_status_t st = check_problem_public(problem);
+  if (st != PA_OK) return st;
+  if (!score) return PA_ERR_INVALID_ARG;
+  st = resolve_score(score, scale, &a.s);
+  if (st != PA_OK) return st;
+  if (!a.s.out_half) return PA_ERR_UNSUPPORTED;
+  PrefillLaunch l;
+  st = setup_prefill(problem, query, query_start, total_tokens, max_query_len, key_cache,
+                     value_cache, block_tables, context_lengths, scale, out, options, &l, &a);
+  if (st != PA_OK || l.grid.x == 0) return st;
+  a.out16 = static_cast<uint16_t *>(out);
+  return launch_prefill<true>(problem->head_dim, a, l, static_cast<cudaStream_t>(stream));
+}

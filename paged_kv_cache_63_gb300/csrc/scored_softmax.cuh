@@ -1,0 +1,272 @@
+// scored_softmax.cuh -- the softmax of one key tile under a score rule, for the multi-token
+// kernels: one query row per thread, the tile's raw dot products in registers.
+//
+// What bounds it is instructions per score (the special-function pipe and the fp32 pipe share
+// the softmax warps' issue slots with the tensor-memory traffic), so:
+//  * tanh is a polynomial on the fp32 pipe in packed pairs wherever a warp's arguments allow:
+//    tanh t = t P(t^2) with P of degree 4, fitted to the least relative error for |t| <= 0.75
+//    (6.3e-7 evaluated in fp32; weighted least squares on Chebyshev nodes, weights iterated
+//    towards the equal-ripple fit). A score is then off by at most 0.64 cap * 6.3e-7, 2e-5 for
+//    a cap of 50, against the 2^-11 by which the fp16 probability is rounded. A warp with a
+//    larger argument takes 1 - 2 / (1 + e^2t) for its tile.
+//  * The bias is linear in the key's column wherever no key of the tile lies past its query:
+//    slope * column joins the score in the instruction that scales it, the rest of the bias
+//    is one number per row and tile.
+//  * The mask is compared per score only in tiles where some row of the warp needs it, and a
+//    tile that none of the warp's rows sees is not computed at all.
+#pragma once
+
+#include <type_traits>
+
+#include "prefill_common.cuh"
+#include "score_rule.cuh"
+
+namespace pa {
+
+struct PrefillScoredArgs : PrefillArgs {
+  ScoreArgs s;
+  uint16_t *out16;  // [total][qh][hd], fp16 bits
+};
+
+template <bool kScored>
+using PrefillArgsOf = std::conditional_t<kScored, PrefillScoredArgs, PrefillArgs>;
+
+// A query row: its position, the tokens [lo, hi] it sees, its head's slope * log2 e, and the
+// softmax so far (reference maximum in base 2, sum).
+struct ScoredRow {
+  int pos, lo, hi;
+  float slope2, m, l;
+};
+
+constexpr float kTanhPolyMax = 0.75f;
+
+__device__ __forceinline__ float2 fmul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 ra, rb, rd;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+      "mul.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+      : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+
+__device__ __forceinline__ float fast_rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// v = cap_out * tanh(v * cap_in). Warp-collective.
+template <int TN>
+__device__ __forceinline__ void cap_scores(float (&v)[TN], float cap_in, float cap_out) {
+  float big[4] = {0.f, 0.f, 0.f, 0.f};
+  const float2 in = make_float2(cap_in, cap_in);
+#pragma unroll
+  for (int c = 0; c < TN; c += 2) {
+    const float2 t = fmul2(make_float2(v[c], v[c + 1]), in);
+    v[c] = t.x;
+    v[c + 1] = t.y;
+    big[c & 2] = fmaxf(big[c & 2], fabsf(t.x));
+    big[(c & 2) + 1] = fmaxf(big[(c & 2) + 1], fabsf(t.y));
+  }
+  const float top = fmaxf(fmaxf(big[0], big[1]), fmaxf(big[2], big[3]));
+  if (__all_sync(0xffffffffu, top <= kTanhPolyMax)) {
+    // coefficients of P, times cap_out
+    const float k0 = 0.999999463558197f * cap_out, k1 = -0.3332825303077698f * cap_out,
+                k2 = 0.13258983194828033f * cap_out, k3 = -0.05005630478262901f * cap_out,
+                k4 = 0.012929633259773254f * cap_out;
+    const float2 c0 = make_float2(k0, k0), c1 = make_float2(k1, k1), c2 = make_float2(k2, k2),
+                 c3 = make_float2(k3, k3), c4 = make_float2(k4, k4);
+#pragma unroll
+    for (int c = 0; c < TN; c += 2) {
+      const float2 t = make_float2(v[c], v[c + 1]);
+      const float2 z = fmul2(t, t);
+      float2 p = ffma2(c4, z, c3);
+      p = ffma2(p, z, c2);
+      p = ffma2(p, z, c1);
+      p = ffma2(p, z, c0);
+      p = fmul2(p, t);
+      v[c] = p.x;
+      v[c + 1] = p.y;
+    }
+  } else {
+    // e^2t overflows to infinity and underflows to 0 where tanh is +-1
+#pragma unroll
+    for (int c = 0; c < TN; ++c) {
+      const float e = prefill_exp2(v[c] * (2.f * kLog2e));
+      v[c] = fmaf(-2.f * cap_out, fast_rcp(1.f + e), cap_out);
+    }
+  }
+}
+
+// From raw dot products to base-2 scores: afterwards the score of column c is
+// v[c] * mult + offset. `base` is the tile's first token.
+template <int TN>
+__device__ __forceinline__ void rule_scores(float (&v)[TN], const ScoreArgs &s, float scale_log2,
+                                            const ScoredRow &row, int base, float &mult,
+                                            float &offset) {
+  mult = scale_log2;
+  offset = 0.f;
+  if (s.cap_in != 0.f) {
+    cap_scores<TN>(v, s.cap_in, s.cap_out);
+    mult = 1.f;
+  }
+  if (s.slopes) {
+    const int rel = base - row.pos;
+    const float2 m2 = make_float2(mult, mult);
+    if (__all_sync(0xffffffffu, rel + TN - 1 <= 0)) {
+      const float2 slope = make_float2(row.slope2, row.slope2);
+#pragma unroll
+      for (int c = 0; c < TN; c += 2) {
+        const float2 bias = fmul2(slope, make_float2(static_cast<float>(c), static_cast<float>(c + 1)));
+        const float2 x = ffma2(make_float2(v[c], v[c + 1]), m2, bias);
+        v[c] = x.x;
+        v[c + 1] = x.y;
+      }
+      offset = row.slope2 * static_cast<float>(rel);
+    } else {
+      // keys on both sides of the query: the distance of each
+      const float first = static_cast<float>(rel);
+#pragma unroll
+      for (int c = 0; c < TN; ++c)
+        v[c] = fmaf(-row.slope2, fabsf(first + static_cast<float>(c)), v[c] * mult);
+    }
+    mult = 1.f;
+  }
+}
+
+// v = 2^(v * mult + nm), 0 for columns outside [lo, hi] where kMasked; partial sums in rp.
+template <int TN, bool kMasked>
+__device__ __forceinline__ void exps_in_place(float (&v)[TN], float mult, float nm, int lo, int hi,
+                                              float (&rp)[8]) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) rp[e] = 0.f;
+#pragma unroll
+  for (int c = 0; c < TN; c += 2) {
+    const float2 x = ffma2(make_float2(v[c], v[c + 1]), make_float2(mult, mult), make_float2(nm, nm));
+    float p0 = prefill_exp2(x.x), p1 = prefill_exp2(x.y);
+    if (kMasked) {
+      p0 = c >= lo && c <= hi ? p0 : 0.f;
+      p1 = c + 1 >= lo && c + 1 <= hi ? p1 : 0.f;
+    }
+    const float2 acc = fadd2(make_float2(rp[c & 7], rp[(c + 1) & 7]), make_float2(p0, p1));
+    rp[c & 7] = acc.x;
+    rp[(c + 1) & 7] = acc.y;
+    v[c] = p0;
+    v[c + 1] = p1;
+  }
+}
+
+// One tile: v goes from raw dot products to weights relative to row.m, whose running sum row.l
+// follows. Warp-collective. `reload()` puts the raw dot products back into v; `rescale(f)`
+// multiplies the row's accumulated output by f (only called when `later`, a tile after the
+// row's first; false from it means a wait gave up). As in the causal kernels a later tile takes
+// its exponents with the maximum as it stands and checks them by their sum. A row that has
+// seen nothing yet has m = -inf: its exponents are masked away, or infinite and redone.
+template <int TN, class Reload, class Rescale>
+__device__ __forceinline__ bool scored_weights(float (&v)[TN], const ScoreArgs &s,
+                                               float scale_log2, ScoredRow &row, int base,
+                                               bool later, Reload reload, Rescale rescale) {
+  const int lo = row.lo - base, hi = row.hi - base;
+  if (__all_sync(0xffffffffu, hi < 0 || lo >= TN || hi < lo)) {
+#pragma unroll
+    for (int c = 0; c < TN; ++c) v[c] = 0.f;
+    return true;
+  }
+  const bool full = __all_sync(0xffffffffu, lo <= 0 && hi >= TN - 1);
+  float mult, offset, rp[8];
+  rule_scores<TN>(v, s, scale_log2, row, base, mult, offset);
+  auto exps = [&](float nm) {
+    if (full)
+      exps_in_place<TN, false>(v, mult, nm, lo, hi, rp);
+    else
+      exps_in_place<TN, true>(v, mult, nm, lo, hi, rp);
+    return ((rp[0] + rp[1]) + (rp[2] + rp[3])) + ((rp[4] + rp[5]) + (rp[6] + rp[7]));
+  };
+  if (later) {
+    const float sum = exps(offset - row.m);
+    if (!__any_sync(0xffffffffu, !(sum <= kPrefillSlackBound))) {
+      row.l += sum;
+      return true;
+    }
+    reload();
+    rule_scores<TN>(v, s, scale_log2, row, base, mult, offset);
+  }
+  // the maximum of the scores is the extreme of v times mult (the maximum for mult >= 0)
+  float mp[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) mp[e] = -INFINITY;
+  const float sign = mult >= 0.f ? 1.f : -1.f;
+#pragma unroll
+  for (int c = 0; c < TN; ++c)
+    mp[c & 7] = fmaxf(mp[c & 7], full || (c >= lo && c <= hi) ? v[c] * sign : -INFINITY);
+  const float ext = fmaxf(fmaxf(fmaxf(mp[0], mp[1]), fmaxf(mp[2], mp[3])),
+                          fmaxf(fmaxf(mp[4], mp[5]), fmaxf(mp[6], mp[7])));
+  const float mx = ext == -INFINITY ? ext : fmaf(ext, mult * sign, offset);
+  const bool grow = mx > row.m + kPrefillRescaleSlack;
+  if (__any_sync(0xffffffffu, grow)) {
+    const float mnew = grow ? mx : row.m;
+    const float f = mnew == -INFINITY ? 1.f : prefill_exp2(row.m - mnew);
+    row.l *= f;
+    if (later && !rescale(f)) return false;
+    row.m = mnew;
+  }
+  row.l += exps(offset - row.m);
+  return true;
+}
+
+// The tokens that the new tokens [t0, t1) of sequence b see (t0 < t1; the sequence's query rows
+// start at q0, its new tokens at position p0), as the range its key tiles are taken from:
+// lowest first token and highest last one. A token that sees nothing counts as seeing itself,
+// so that its tile still writes its zero row. Warp-collective; a lane takes every 32nd token.
+__device__ __forceinline__ void seen_range(const ScoreArgs &s, int q0, int p0, int t0, int t1,
+                                           int prefix, int &lo, int &last) {
+  const int p_last = p0 + t1 - 1;
+  last = p0 + t0 < prefix ? max(p_last, prefix - 1) : p_last;
+  if (!s.first) {
+    lo = min(first_seen(s, 0, p0 + t0), p0 + t0);  // the window's start grows with the position
+    return;
+  }
+  int mine = 0x7fffffff;
+  for (int t = t0 + (threadIdx.x & 31); t < t1; t += 32)
+    mine = min(mine, min(first_seen(s, static_cast<long long>(q0) + t, p0 + t), p0 + t));
+  lo = __reduce_min_sync(0xffffffffu, mine);
+}
+
+// Length of sequence b's prefix within its context.
+__device__ __forceinline__ int prefix_of(const ScoreArgs &s, int b, int ctx) {
+  return s.prefix ? min(__ldg(s.prefix + b), ctx) : 0;
+}
+
+// The thread's row: new token t of sequence b (position p0 + t).
+__device__ __forceinline__ ScoredRow scored_row(const ScoreArgs &s, int q0, int p0, int t, int head,
+                                                int prefix) {
+  ScoredRow r;
+  r.pos = p0 + t;
+  r.lo = first_seen(s, static_cast<long long>(q0) + t, r.pos);
+  r.hi = r.pos < prefix ? prefix - 1 : r.pos;
+  r.slope2 = s.slopes ? __ldg(s.slopes + head) * kLog2e : 0.f;
+  r.m = -INFINITY;
+  r.l = 0.f;
+  return r;
+}
+
+// 32 consecutive fp32 outputs of a row, scaled and written as fp16.
+__device__ __forceinline__ void store_half32(uint16_t *dst, const float (&o)[32], float inv,
+                                             bool v8, uint64_t pol) {
+  uint32_t w[16];
+#pragma unroll
+  for (int e = 0; e < 16; ++e) w[e] = pack_half2(o[2 * e] * inv, o[2 * e + 1] * inv);
+  if (v8) {
+#pragma unroll
+    for (int e = 0; e < 16; e += 8)
+      st_global_v8(reinterpret_cast<float *>(dst + 2 * e), __uint_as_float(w[e]),
+                   __uint_as_float(w[e + 1]), __uint_as_float(w[e + 2]), __uint_as_float(w[e + 3]),
+                   __uint_as_float(w[e + 4]), __uint_as_float(w[e + 5]), __uint_as_float(w[e + 6]),
+                   __uint_as_float(w[e + 7]), pol);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 16; e += 4)
+      *reinterpret_cast<uint4 *>(dst + 2 * e) = make_uint4(w[e], w[e + 1], w[e + 2], w[e + 3]);
+  }
+}
+
+}  // namespace pa

@@ -36,7 +36,7 @@ ROPE_STYLE = {"half": 0, "interleaved": 1}
 # Every entry point include/pagedattn.h declares.
 EXPORTS = ("pa_plan", "pa_workspace_size", "pa_workspace_init", "pa_decode", "pa_decode_ex",
            "pa_decode_noalloc", "pa_append_kv", "pa_append_rope", "pa_prefill",
-           "pa_decode_scored",
+           "pa_decode_scored", "pa_prefill_scored",
            "pa_split_kv_partial", "pa_split_kv_combine", "pa_get_device_error",
            "pa_status_string", "pa_version")
 
@@ -115,6 +115,8 @@ def load(path: Optional[str] = None):
                                        i64, vp, vp, vp, vp, vp, vp]
         lib.pa_decode_scored.argtypes = [P(pa_problem_t), P(pa_score_t), vp, vp, vp, vp, vp, f32, vp,
                                          P(pa_options_t), vp, ctypes.c_size_t, vp]
+        lib.pa_prefill_scored.argtypes = [P(pa_problem_t), P(pa_score_t), vp, vp, i64, i32, vp, vp,
+                                          vp, vp, f32, vp, P(pa_options_t), vp]
         lib.pa_prefill.argtypes = [P(pa_problem_t), vp, vp, ctypes.c_int64, i32, vp, vp, vp, vp,
                                    f32, vp, P(pa_options_t), vp]
         lib.pa_split_kv_partial.argtypes = [P(pa_problem_t), vp, vp, vp, vp, vp, f32, i32, i32, vp,
@@ -343,6 +345,16 @@ def pa_decode_scored(prob, score, query, key_cache, value_cache, block_tables, c
                                          block_tables, context_lengths, out, workspace)
     _check(load().pa_decode_scored(prob, score, q, k, v, bt, ctx, scale, o, opts, ws,
                                    workspace_bytes, _stream(stream)), "pa_decode_scored")
+
+
+def pa_prefill_scored(prob, score, query, query_start, total_tokens, max_query_len, key_cache,
+                      value_cache, block_tables, context_lengths, scale, out,
+                      opts: Optional[pa_options_t] = None, stream=None):
+    """pa_prefill under a score rule (``score(out="fp16", ...)``); fp16 out."""
+    q, qs, k, v, bt, ctx, o = _addresses("pa_prefill_scored", query, query_start, key_cache,
+                                         value_cache, block_tables, context_lengths, out)
+    _check(load().pa_prefill_scored(prob, score, q, qs, total_tokens, max_query_len, k, v, bt, ctx,
+                                    scale, o, opts, _stream(stream)), "pa_prefill_scored")
 
 
 def pa_split_kv_partial(prob, query, key_cache, value_cache, block_tables, context_lengths, scale,

@@ -29,14 +29,15 @@ def seen(rule, b, row, pos, ctx):
     return lo, max(end, lo)
 
 
-def attend(case, rule, probability_error, weight_floor):
+def attend(case, rule, probability_error, weight_floor, cap_error=2.0 ** -22, span=0):
     """(out, bound) in 64 bits over case's query rows; rows that are no new token's stay NaN.
 
     A kernel's weight of token t carries a relative error e_t: the dot product's accumulation
     (the products are exact in fp32; at most head_dim / 16 + 2 additions, each off by 2^-23 of
     the terms' absolute sum), the roundings of the scaled, capped and biased score (2^-22 of
     each, tanhf's two last places among them), the exponential (2^-22, and 2^-24 of its
-    argument), and `probability_error`, the rounding of the probabilities that meet V. The
+    argument), `cap_error` of a capped score, a bias formed in two parts of up to `span` tokens
+    each, and `probability_error`, the rounding of the probabilities that meet V. The
     weighted mean out = sum w v / sum w is then off by at most sum w e (|v| + |out|), plus the
     fp32 sums over the tiles (2^-24 of sum w |v| for each of n additions), plus
     `weight_floor`, the smallest weight the probability's type tells from 0, on every token."""
@@ -60,11 +61,11 @@ def attend(case, rule, probability_error, weight_floor):
                 e += np.abs(s) * 2.0 ** -22
                 if rule.softcap:
                     s = rule.softcap * np.tanh(s / rule.softcap)
-                    e += np.abs(s) * 2.0 ** -22
+                    e += np.abs(s) * cap_error
                 if rule.slopes is not None:
                     bias = float(rule.slopes[h]) * np.abs(pos - np.arange(lo, end))
                     s = s - bias
-                    e += np.abs(bias) * 2.0 ** -22
+                    e += (np.abs(bias) + abs(float(rule.slopes[h])) * span) * 2.0 ** -22
                 e += (np.abs(s) + np.abs(s.max())) * 2.0 ** -23 + 2.0 ** -22 + probability_error
                 p = np.exp(s - s.max())
                 p /= p.sum()
