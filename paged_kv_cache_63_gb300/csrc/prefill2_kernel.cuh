@@ -623,7 +623,7 @@ __global__ void __launch_bounds__(kPrefill2Threads, 1)
           kv_ready = rv && rk;
         }
         float v[C::TN];
-        tmem_ld128(ts, v);
+        if constexpr (!kScored) tmem_ld128(ts, v);
         if (rg == 0 && !__all_sync(0xffffffffu, kv_ready)) {
           ok = pipe_wait(bar(kB2Full + iv % C::kSlots), (iv / C::kSlots) & 1, abort_flag, a.err);
           if (ok && j + 1 < my_nt)
@@ -631,7 +631,9 @@ __global__ void __launch_bounds__(kPrefill2Threads, 1)
           if (!ok) break;
         }
         if constexpr (kScored) {
-          auto reload = [&]() { tmem_ld128(ts, v); };
+          auto load = [&](int part, float (&c)[64]) { tmem_ld64(ts + part * 64, c); };
+          // P as fp16 pairs over the first 64 columns of S
+          auto emit = [&](int part, const float (&pk)[32]) { tmem_st32(ts + part * 32, pk); };
           auto rescale = [&](float f) {
             // S_X(j) completed, so PV_X(j - 1) has too: O_X is stable until P_X(j) is released
 #pragma unroll
@@ -644,96 +646,84 @@ __global__ void __launch_bounds__(kPrefill2Threads, 1)
             }
             return true;
           };
-          scored_weights<C::TN>(v, a.s, sl2, sr, tile0 + j * C::TN, j > 0, reload, rescale);
-          // P as fp16 pairs over the first 64 columns of S
-#pragma unroll
-          for (int h2 = 0; h2 < C::TN / 64; ++h2) {
-            float pk[32];
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              pk[e] = __uint_as_float(pack_half2(v[h2 * 64 + 2 * e], v[h2 * 64 + 2 * e + 1]));
-            tmem_st32(ts + h2 * 32, pk);
+          scored_weights<C::TN>(a.s, sl2, sr, tile0 + j * C::TN, j > 0, load, emit, rescale);
+        } else {
+          const int lim = pos - j * C::TN;
+          // warp-uniform: the exponent passes hold tcgen05.st, which the whole warp executes
+          const bool full = __all_sync(0xffffffffu, lim >= C::TN - 1);
+          float rp[8];
+          // After a row's first tile its running maximum m seldom grows by more than the slack,
+          // so a tile first takes its exponents with m as it stands and no maximum pass: the
+          // terms are non-negative (masked keys give 0), so the tile's row sum bounds each of
+          // them, and a sum of at most 2^slack shows that no score passed m + slack. Only a warp
+          // in which some row's sum is larger (or not a number) takes the tile again in the
+          // plain order: maximum, rescale, exponents.
+          bool redo = true;
+          if (j > 0) {
+            if (full)
+              exps_row<C::TN, false>(v, sl2, -m, lim, ts, rp);
+            else
+              exps_row<C::TN, true>(v, sl2, -m, lim, ts, rp);
+            const float tsum =
+                ((rp[0] + rp[1]) + (rp[2] + rp[3])) + ((rp[4] + rp[5]) + (rp[6] + rp[7]));
+            redo = __any_sync(0xffffffffu, !(tsum <= kPrefillSlackBound));
+            if (redo) tmem_wait_st();  // the plain pass below rewrites the same columns
           }
-          tmem_wait_st();
-          tc_fence_before();
-          mbar_arrive(bar(kB2PFull + x));
-          continue;
-        }
-        const int lim = pos - j * C::TN;
-        // warp-uniform: the exponent passes hold tcgen05.st, which the whole warp executes
-        const bool full = __all_sync(0xffffffffu, lim >= C::TN - 1);
-        float rp[8];
-        // After a row's first tile its running maximum m seldom grows by more than the slack,
-        // so a tile first takes its exponents with m as it stands and no maximum pass: the
-        // terms are non-negative (masked keys give 0), so the tile's row sum bounds each of
-        // them, and a sum of at most 2^slack shows that no score passed m + slack. Only a warp
-        // in which some row's sum is larger (or not a number) takes the tile again in the
-        // plain order: maximum, rescale, exponents.
-        bool redo = true;
-        if (j > 0) {
-          if (full)
-            exps_row<C::TN, false>(v, sl2, -m, lim, ts, rp);
-          else
-            exps_row<C::TN, true>(v, sl2, -m, lim, ts, rp);
-          const float tsum =
-              ((rp[0] + rp[1]) + (rp[2] + rp[3])) + ((rp[4] + rp[5]) + (rp[6] + rp[7]));
-          redo = __any_sync(0xffffffffu, !(tsum <= kPrefillSlackBound));
-          if (redo) tmem_wait_st();  // the plain pass below rewrites the same columns
-        }
-        if (redo) {
-          // keys past this row's position are masked out (on tiles that reach the diagonal);
-          // the row maximum of the scaled scores is the extreme raw score times the scale (the
-          // maximum for a non-negative scale, else the minimum), which saves a multiply per score
-          float mp[8];
+          if (redo) {
+            // keys past this row's position are masked out (on tiles that reach the diagonal);
+            // the row maximum of the scaled scores is the extreme raw score times the scale (the
+            // maximum for a non-negative scale, else the minimum), which saves a multiply per score
+            float mp[8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) mp[e] = -INFINITY;
-          float ext;
-          if (sl2 >= 0.f) {
-            if (full) {
+            for (int e = 0; e < 8; ++e) mp[e] = -INFINITY;
+            float ext;
+            if (sl2 >= 0.f) {
+              if (full) {
 #pragma unroll
-              for (int c = 0; c < C::TN; ++c) mp[c & 7] = fmaxf(mp[c & 7], v[c]);
+                for (int c = 0; c < C::TN; ++c) mp[c & 7] = fmaxf(mp[c & 7], v[c]);
+              } else {
+#pragma unroll
+                for (int c = 0; c < C::TN; ++c) mp[c & 7] = fmaxf(mp[c & 7], c <= lim ? v[c] : -INFINITY);
+              }
+              ext = fmaxf(fmaxf(fmaxf(mp[0], mp[1]), fmaxf(mp[2], mp[3])),
+                          fmaxf(fmaxf(mp[4], mp[5]), fmaxf(mp[6], mp[7])));
             } else {
 #pragma unroll
-              for (int c = 0; c < C::TN; ++c) mp[c & 7] = fmaxf(mp[c & 7], c <= lim ? v[c] : -INFINITY);
+              for (int e = 0; e < 8; ++e) mp[e] = INFINITY;
+#pragma unroll
+              for (int c = 0; c < C::TN; ++c) mp[c & 7] = fminf(mp[c & 7], (full || c <= lim) ? v[c] : INFINITY);
+              ext = fminf(fminf(fminf(mp[0], mp[1]), fminf(mp[2], mp[3])),
+                          fminf(fminf(mp[4], mp[5]), fminf(mp[6], mp[7])));
             }
-            ext = fmaxf(fmaxf(fmaxf(mp[0], mp[1]), fmaxf(mp[2], mp[3])),
-                        fmaxf(fmaxf(mp[4], mp[5]), fmaxf(mp[6], mp[7])));
-          } else {
+            const float mx = ext * sl2;
+            const bool grow = mx > m + kPrefillRescaleSlack;
+            if (__any_sync(0xffffffffu, grow)) {
+              const float mnew = grow ? mx : m;
+              const float f = mnew == -INFINITY ? 1.f : prefill_exp2(m - mnew);
+              l *= f;
+              if (j > 0) {
+                // S_X(j) completed, so PV_X(j - 1) has too: O_X is stable until P_X(j) is released
 #pragma unroll
-            for (int e = 0; e < 8; ++e) mp[e] = INFINITY;
+                for (int c = 0; c < HD / 32; ++c) {
+                  float o[32];
+                  tmem_ld32(to + c * 32, o);
 #pragma unroll
-            for (int c = 0; c < C::TN; ++c) mp[c & 7] = fminf(mp[c & 7], (full || c <= lim) ? v[c] : INFINITY);
-            ext = fminf(fminf(fminf(mp[0], mp[1]), fminf(mp[2], mp[3])),
-                        fminf(fminf(mp[4], mp[5]), fminf(mp[6], mp[7])));
-          }
-          const float mx = ext * sl2;
-          const bool grow = mx > m + kPrefillRescaleSlack;
-          if (__any_sync(0xffffffffu, grow)) {
-            const float mnew = grow ? mx : m;
-            const float f = mnew == -INFINITY ? 1.f : prefill_exp2(m - mnew);
-            l *= f;
-            if (j > 0) {
-              // S_X(j) completed, so PV_X(j - 1) has too: O_X is stable until P_X(j) is released
-#pragma unroll
-              for (int c = 0; c < HD / 32; ++c) {
-                float o[32];
-                tmem_ld32(to + c * 32, o);
-#pragma unroll
-                for (int e = 0; e < 32; ++e) o[e] *= f;
-                tmem_st32(to + c * 32, o);
+                  for (int e = 0; e < 32; ++e) o[e] *= f;
+                  tmem_st32(to + c * 32, o);
+                }
               }
+              m = mnew;
             }
-            m = mnew;
+            // P = exp2(s * scale * log2e - m) as fp16 pairs over the first 64 columns of S (the
+            // scale is folded into one FFMA per score; masked keys give exactly 0)
+            const float nm = -m;
+            if (full)
+              exps_row<C::TN, false>(v, sl2, nm, lim, ts, rp);
+            else
+              exps_row<C::TN, true>(v, sl2, nm, lim, ts, rp);
           }
-          // P = exp2(s * scale * log2e - m) as fp16 pairs over the first 64 columns of S (the
-          // scale is folded into one FFMA per score; masked keys give exactly 0)
-          const float nm = -m;
-          if (full)
-            exps_row<C::TN, false>(v, sl2, nm, lim, ts, rp);
-          else
-            exps_row<C::TN, true>(v, sl2, nm, lim, ts, rp);
+          l += ((rp[0] + rp[1]) + (rp[2] + rp[3])) + ((rp[4] + rp[5]) + (rp[6] + rp[7]));
         }
-        l += ((rp[0] + rp[1]) + (rp[2] + rp[3])) + ((rp[4] + rp[5]) + (rp[6] + rp[7]));
         tmem_wait_st();
         tc_fence_before();
         mbar_arrive(bar(kB2PFull + x));

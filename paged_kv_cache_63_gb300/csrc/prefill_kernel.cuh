@@ -508,23 +508,19 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
         ok = pipe_wait(bar(kBarSFull + st), (gj >> 1) & 1, abort_flag, a.err);
         if (!ok) break;
         tc_fence_after();
-        float x[C::TN];
-#pragma unroll
-        for (int c = 0; c < C::TN / 32; ++c) {
-          float v[32];
-          tmem_ld32(trow + st * C::TN + c * 32, v);
-#pragma unroll
-          for (int e = 0; e < 32; ++e) x[c * 32 + e] = v[e];
-        }
         if constexpr (kScored) {
-          auto reload = [&]() {
+          // P buffer st was last read by the P.V of global tile gj - 2
+          if (gj >= 2) {
+            ok = pipe_wait(bar(kBarPV + st), ((gj >> 1) - 1) & 1, abort_flag, a.err);
+            if (!ok) break;
+          }
+          auto load = [&](int, float (&c)[64]) { tmem_ld64(trow + st * C::TN, c); };
+          auto emit = [&](int, const float (&pk)[32]) {
 #pragma unroll
-            for (int c = 0; c < C::TN / 32; ++c) {
-              float v[32];
-              tmem_ld32(trow + st * C::TN + c * 32, v);
-#pragma unroll
-              for (int e = 0; e < 32; ++e) x[c * 32 + e] = v[e];
-            }
+            for (int e = 0; e < 32; e += 4)
+              sts128(p_buf(st) + row * 128 + (((e >> 2) ^ (row & 7)) << 4),
+                     make_uint4(__float_as_uint(pk[e]), __float_as_uint(pk[e + 1]),
+                                __float_as_uint(pk[e + 2]), __float_as_uint(pk[e + 3])));
           };
           auto rescale = [&](float f) {
             // O holds tiles < j: wait for the last P.V, then scale this row of O in TMEM
@@ -542,9 +538,17 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
             tmem_wait_st();
             return true;
           };
-          ok = scored_weights<C::TN>(x, a.s, sl2, sr, tile_token(it, j), j > 0, reload, rescale);
+          ok = scored_weights<C::TN>(a.s, sl2, sr, tile_token(it, j), j > 0, load, emit, rescale);
           if (!ok) break;
         } else {
+          float x[C::TN];
+#pragma unroll
+          for (int c = 0; c < C::TN / 32; ++c) {
+            float v[32];
+            tmem_ld32(trow + st * C::TN + c * 32, v);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) x[c * 32 + e] = v[e];
+          }
           const int lim = pos - j * C::TN;
           const bool full = lim >= C::TN - 1;
           float rp[8];
@@ -624,21 +628,21 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
             exps_row<C::TN>(x, sl2, -m, full, lim, rp);
           }
           l += ((rp[0] + rp[1]) + (rp[2] + rp[3])) + ((rp[4] + rp[5]) + (rp[6] + rp[7]));
-        }
-        // P buffer st was last read by the P.V of global tile gj - 2
-        if (gj >= 2) {
-          ok = pipe_wait(bar(kBarPV + st), ((gj >> 1) - 1) & 1, abort_flag, a.err);
-          if (!ok) break;
-        }
-        const uint32_t prow = p_buf(st) + row * 128;
+          // P buffer st was last read by the P.V of global tile gj - 2
+          if (gj >= 2) {
+            ok = pipe_wait(bar(kBarPV + st), ((gj >> 1) - 1) & 1, abort_flag, a.err);
+            if (!ok) break;
+          }
+          const uint32_t prow = p_buf(st) + row * 128;
 #pragma unroll
-        for (int c8 = 0; c8 < C::TN / 8; ++c8) {
-          uint4 w;
-          w.x = pack_half2(x[c8 * 8 + 0], x[c8 * 8 + 1]);
-          w.y = pack_half2(x[c8 * 8 + 2], x[c8 * 8 + 3]);
-          w.z = pack_half2(x[c8 * 8 + 4], x[c8 * 8 + 5]);
-          w.w = pack_half2(x[c8 * 8 + 6], x[c8 * 8 + 7]);
-          sts128(prow + (c8 >> 3) * (C::kRows * 128) + (((c8 & 7) ^ (row & 7)) << 4), w);
+          for (int c8 = 0; c8 < C::TN / 8; ++c8) {
+            uint4 w;
+            w.x = pack_half2(x[c8 * 8 + 0], x[c8 * 8 + 1]);
+            w.y = pack_half2(x[c8 * 8 + 2], x[c8 * 8 + 3]);
+            w.z = pack_half2(x[c8 * 8 + 4], x[c8 * 8 + 5]);
+            w.w = pack_half2(x[c8 * 8 + 6], x[c8 * 8 + 7]);
+            sts128(prow + (c8 >> 3) * (C::kRows * 128) + (((c8 & 7) ^ (row & 7)) << 4), w);
+          }
         }
         fence_proxy_async();
         tc_fence_before();

@@ -20,6 +20,9 @@ extern "C" pa_status_t pa_prefill_scored(const pa_problem_t *problem, const pa_s
   st = setup_prefill(problem, query, query_start, total_tokens, max_query_len, key_cache,
                      value_cache, block_tables, context_lengths, scale, out, options, &l, &a);
   if (st != PA_OK || l.grid.x == 0) return st;
+  // a masked score is an infinity times the scale, so the scale is never 0: with this one every
+  // finite dot product (below 2^41) still scores 0 in fp32 next to the maximum
+  if (a.scale_log2 == 0.f) a.scale_log2 = 1e-30f;
   a.out16 = static_cast<uint16_t *>(out);
   return launch_prefill<true>(problem->head_dim, a, l, static_cast<cudaStream_t>(stream));
 }

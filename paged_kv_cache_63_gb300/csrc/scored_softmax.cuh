@@ -55,12 +55,11 @@ __device__ __forceinline__ float fast_rcp(float x) {
 }
 
 // v = cap_out * tanh(v * cap_in). Warp-collective.
-template <int TN>
-__device__ __forceinline__ void cap_scores(float (&v)[TN], float cap_in, float cap_out) {
+__device__ __forceinline__ void cap_scores(float (&v)[64], float cap_in, float cap_out) {
   float big[4] = {0.f, 0.f, 0.f, 0.f};
   const float2 in = make_float2(cap_in, cap_in);
 #pragma unroll
-  for (int c = 0; c < TN; c += 2) {
+  for (int c = 0; c < 64; c += 2) {
     const float2 t = fmul2(make_float2(v[c], v[c + 1]), in);
     v[c] = t.x;
     v[c + 1] = t.y;
@@ -68,7 +67,7 @@ __device__ __forceinline__ void cap_scores(float (&v)[TN], float cap_in, float c
     big[(c & 2) + 1] = fmaxf(big[(c & 2) + 1], fabsf(t.y));
   }
   const float top = fmaxf(fmaxf(big[0], big[1]), fmaxf(big[2], big[3]));
-  if (__all_sync(0xffffffffu, top <= kTanhPolyMax)) {
+  if (__builtin_expect(__all_sync(0xffffffffu, top <= kTanhPolyMax), 1)) {
     // coefficients of P, times cap_out
     const float k0 = 0.999999463558197f * cap_out, k1 = -0.3332825303077698f * cap_out,
                 k2 = 0.13258983194828033f * cap_out, k3 = -0.05005630478262901f * cap_out,
@@ -76,7 +75,7 @@ __device__ __forceinline__ void cap_scores(float (&v)[TN], float cap_in, float c
     const float2 c0 = make_float2(k0, k0), c1 = make_float2(k1, k1), c2 = make_float2(k2, k2),
                  c3 = make_float2(k3, k3), c4 = make_float2(k4, k4);
 #pragma unroll
-    for (int c = 0; c < TN; c += 2) {
+    for (int c = 0; c < 64; c += 2) {
       const float2 t = make_float2(v[c], v[c + 1]);
       const float2 z = fmul2(t, t);
       float2 p = ffma2(c4, z, c3);
@@ -90,7 +89,7 @@ __device__ __forceinline__ void cap_scores(float (&v)[TN], float cap_in, float c
   } else {
     // e^2t overflows to infinity and underflows to 0 where tanh is +-1
 #pragma unroll
-    for (int c = 0; c < TN; ++c) {
+    for (int c = 0; c < 64; ++c) {
       const float e = prefill_exp2(v[c] * (2.f * kLog2e));
       v[c] = fmaf(-2.f * cap_out, fast_rcp(1.f + e), cap_out);
     }
@@ -98,24 +97,27 @@ __device__ __forceinline__ void cap_scores(float (&v)[TN], float cap_in, float c
 }
 
 // From raw dot products to base-2 scores: afterwards the score of column c is
-// v[c] * mult + offset. `base` is the tile's first token.
-template <int TN>
-__device__ __forceinline__ void rule_scores(float (&v)[TN], const ScoreArgs &s, float scale_log2,
+// v[c] * mult + offset. `base` is the columns' first token. Warp-collective.
+__device__ __forceinline__ void rule_scores(float (&v)[64], const ScoreArgs &s, float scale_log2,
                                             const ScoredRow &row, int base, float &mult,
                                             float &offset) {
   mult = scale_log2;
   offset = 0.f;
   if (s.cap_in != 0.f) {
-    cap_scores<TN>(v, s.cap_in, s.cap_out);
+    cap_scores(v, s.cap_in, s.cap_out);
     mult = 1.f;
   }
   if (s.slopes) {
     const int rel = base - row.pos;
     const float2 m2 = make_float2(mult, mult);
-    if (__all_sync(0xffffffffu, rel + TN - 1 <= 0)) {
-      const float2 slope = make_float2(row.slope2, row.slope2);
+    if (__builtin_expect(__all_sync(0xffffffffu, rel + 63 <= 0), 1)) {
+      // the empty asm keeps the biases of all columns, the same for every tile, from being
+      // kept in registers across tiles
+      float sl = row.slope2;
+      asm volatile("" : "+f"(sl));
+      const float2 slope = make_float2(sl, sl);
 #pragma unroll
-      for (int c = 0; c < TN; c += 2) {
+      for (int c = 0; c < 64; c += 2) {
         const float2 bias = fmul2(slope, make_float2(static_cast<float>(c), static_cast<float>(c + 1)));
         const float2 x = ffma2(make_float2(v[c], v[c + 1]), m2, bias);
         v[c] = x.x;
@@ -126,90 +128,112 @@ __device__ __forceinline__ void rule_scores(float (&v)[TN], const ScoreArgs &s, 
       // keys on both sides of the query: the distance of each
       const float first = static_cast<float>(rel);
 #pragma unroll
-      for (int c = 0; c < TN; ++c)
+      for (int c = 0; c < 64; ++c)
         v[c] = fmaf(-row.slope2, fabsf(first + static_cast<float>(c)), v[c] * mult);
     }
     mult = 1.f;
   }
 }
 
-// v = 2^(v * mult + nm), 0 for columns outside [lo, hi] where kMasked; partial sums in rp.
-template <int TN, bool kMasked>
-__device__ __forceinline__ void exps_in_place(float (&v)[TN], float mult, float nm, int lo, int hi,
-                                              float (&rp)[8]) {
-#pragma unroll
-  for (int e = 0; e < 8; ++e) rp[e] = 0.f;
-#pragma unroll
-  for (int c = 0; c < TN; c += 2) {
-    const float2 x = ffma2(make_float2(v[c], v[c + 1]), make_float2(mult, mult), make_float2(nm, nm));
-    float p0 = prefill_exp2(x.x), p1 = prefill_exp2(x.y);
-    if (kMasked) {
-      p0 = c >= lo && c <= hi ? p0 : 0.f;
-      p1 = c + 1 >= lo && c + 1 <= hi ? p1 : 0.f;
-    }
-    const float2 acc = fadd2(make_float2(rp[c & 7], rp[(c + 1) & 7]), make_float2(p0, p1));
-    rp[c & 7] = acc.x;
-    rp[(c + 1) & 7] = acc.y;
-    v[c] = p0;
-    v[c + 1] = p1;
-  }
-}
-
-// One tile: v goes from raw dot products to weights relative to row.m, whose running sum row.l
-// follows. Warp-collective. `reload()` puts the raw dot products back into v; `rescale(f)`
-// multiplies the row's accumulated output by f (only called when `later`, a tile after the
-// row's first; false from it means a wait gave up). As in the causal kernels a later tile takes
-// its exponents with the maximum as it stands and checks them by their sum. A row that has
-// seen nothing yet has m = -inf: its exponents are masked away, or infinite and redone.
-template <int TN, class Reload, class Rescale>
-__device__ __forceinline__ bool scored_weights(float (&v)[TN], const ScoreArgs &s,
-                                               float scale_log2, ScoredRow &row, int base,
-                                               bool later, Reload reload, Rescale rescale) {
+// One tile of TN keys from token `base`: raw dot products become weights relative to row.m,
+// row.l grows by their sum. Warp-collective. `load(h, v)` reads raw columns 64 h .. 64 h + 63,
+// again when asked again; `emit(h, pk)` takes their weights as fp16 pairs once they stand (all
+// loads come before the first emit); `rescale(f)` multiplies the row's accumulated output by f
+// (only called when `later`, a tile after the row's first; false from it: a wait gave up).
+//
+// As in the causal kernels a later tile takes its exponents with the maximum as it stands and
+// checks them by their sum; a first tile, and one whose check fails in some row of the warp,
+// is gone through for its maximum first. A row that has seen nothing yet (m = -inf) takes its
+// maximum as soon as a tile holds a token it sees.
+//
+// The columns are taken 64 at a time by one loop body that serves both walks. Whole rows of 128
+// scores beside their weights do not fit a thread's registers (a spilled word is an L2 access
+// here, the shared memory being full), and the body unrolled over both parts and both walks
+// outgrew the instruction cache: the softmax warps spent most of their time fetching (6900
+// cycles a tile against 2500 of the causal form's).
+template <int TN, class Load, class Emit, class Rescale>
+__device__ __forceinline__ bool scored_weights(const ScoreArgs &s, float scale_log2,
+                                               ScoredRow &row, int base, bool later, Load load,
+                                               Emit emit, Rescale rescale) {
+  constexpr int H = TN / 64;
   const int lo = row.lo - base, hi = row.hi - base;
-  if (__all_sync(0xffffffffu, hi < 0 || lo >= TN || hi < lo)) {
+  const bool some = hi >= 0 && lo < TN && lo <= hi;
+  float pk[H][32];
+  if (!__any_sync(0xffffffffu, some)) {
 #pragma unroll
-    for (int c = 0; c < TN; ++c) v[c] = 0.f;
+    for (int h = 0; h < H; ++h) {
+#pragma unroll
+      for (int e = 0; e < 32; ++e) pk[h][e] = 0.f;
+      emit(h, pk[h]);
+    }
     return true;
   }
   const bool full = __all_sync(0xffffffffu, lo <= 0 && hi >= TN - 1);
-  float mult, offset, rp[8];
-  rule_scores<TN>(v, s, scale_log2, row, base, mult, offset);
-  auto exps = [&](float nm) {
-    if (full)
-      exps_in_place<TN, false>(v, mult, nm, lo, hi, rp);
-    else
-      exps_in_place<TN, true>(v, mult, nm, lo, hi, rp);
-    return ((rp[0] + rp[1]) + (rp[2] + rp[3])) + ((rp[4] + rp[5]) + (rp[6] + rp[7]));
-  };
-  if (later) {
-    const float sum = exps(offset - row.m);
-    if (!__any_sync(0xffffffffu, !(sum <= kPrefillSlackBound))) {
-      row.l += sum;
-      return true;
+  bool find = !later;  // whether the next walk looks for the maximum
+  float sum;
+  for (bool last = find;;) {
+    const float nm = row.m == -INFINITY ? 0.f : -row.m;
+    float mx = -INFINITY;
+    float rp[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+    for (int h = 0; h < H; ++h) {
+      float v[64], mult, offset;
+      load(h, v);
+      rule_scores(v, s, scale_log2, row, base + 64 * h, mult, offset);
+      const float sign = mult >= 0.f ? 1.f : -1.f;
+      if (!full) {
+        const float none = -sign * INFINITY;
+        const int l = lo - 64 * h, r = hi - 64 * h;
+#pragma unroll
+        for (int c = 0; c < 64; ++c) v[c] = c >= l && c <= r ? v[c] : none;
+      }
+      if (find) {
+        // the maximum of the scores is the extreme of v times mult (the maximum for mult >= 0)
+        float mp[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int c = 0; c < 64; ++c) mp[c & 3] = fmaxf(mp[c & 3], v[c] * sign);
+        const float ext = fmaxf(fmaxf(mp[0], mp[1]), fmaxf(mp[2], mp[3]));
+        if (ext > -INFINITY) mx = fmaxf(mx, fmaf(ext, mult * sign, offset));
+      } else {
+        if (H > 1 && h > 0) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) pk[0][e] = pk[H - 1][e];
+        }
+        const float2 m2 = make_float2(mult, mult), n2 = make_float2(offset + nm, offset + nm);
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+          const int c = 2 * e;
+          const float2 x = ffma2(make_float2(v[c], v[c + 1]), m2, n2);
+          const float2 w = make_float2(prefill_exp2(x.x), prefill_exp2(x.y));
+          const float2 acc = fadd2(make_float2(rp[c & 2], rp[(c & 2) + 1]), w);
+          rp[c & 2] = acc.x;
+          rp[(c & 2) + 1] = acc.y;
+          pk[H - 1][e] = __uint_as_float(pack_half2(w.x, w.y));
+        }
+      }
     }
-    reload();
-    rule_scores<TN>(v, s, scale_log2, row, base, mult, offset);
+    if (find) {
+      const bool grow = mx > row.m + kPrefillRescaleSlack;
+      if (__any_sync(0xffffffffu, grow)) {
+        const float mnew = grow ? mx : row.m;
+        const float f = mnew == -INFINITY ? 1.f : prefill_exp2(row.m - mnew);
+        row.l *= f;
+        if (later && !rescale(f)) return false;
+        row.m = mnew;
+      }
+      find = false;
+      last = true;
+      continue;
+    }
+    sum = (rp[0] + rp[1]) + (rp[2] + rp[3]);
+    if (last || __all_sync(0xffffffffu, sum <= kPrefillSlackBound &&
+                                            !(some && row.m == -INFINITY)))
+      break;
+    find = true;
   }
-  // the maximum of the scores is the extreme of v times mult (the maximum for mult >= 0)
-  float mp[8];
+  row.l += sum;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) mp[e] = -INFINITY;
-  const float sign = mult >= 0.f ? 1.f : -1.f;
-#pragma unroll
-  for (int c = 0; c < TN; ++c)
-    mp[c & 7] = fmaxf(mp[c & 7], full || (c >= lo && c <= hi) ? v[c] * sign : -INFINITY);
-  const float ext = fmaxf(fmaxf(fmaxf(mp[0], mp[1]), fmaxf(mp[2], mp[3])),
-                          fmaxf(fmaxf(mp[4], mp[5]), fmaxf(mp[6], mp[7])));
-  const float mx = ext == -INFINITY ? ext : fmaf(ext, mult * sign, offset);
-  const bool grow = mx > row.m + kPrefillRescaleSlack;
-  if (__any_sync(0xffffffffu, grow)) {
-    const float mnew = grow ? mx : row.m;
-    const float f = mnew == -INFINITY ? 1.f : prefill_exp2(row.m - mnew);
-    row.l *= f;
-    if (later && !rescale(f)) return false;
-    row.m = mnew;
-  }
-  row.l += exps(offset - row.m);
+  for (int h = 0; h < H; ++h) emit(h, pk[h]);
   return true;
 }
 

@@ -139,6 +139,11 @@ def test_scores_far_past_the_cap_and_growing_maxima():
             w.k[page, slot] = (w.k[page, slot].astype(np.float32) * (1 + t / 40)).astype(np.float16)
     check(w, Rule())
     check(w, Rule(softcap=200.0, slopes=-0.01 * slopes_of(w.query_heads)))
+    w.scale = 0.0  # every seen token weighs the same
+    check(w, Rule(window=70, softcap=3.0))
+    check(w, Rule())
+    w.scale = -0.05
+    check(w, Rule(window=70, softcap=3.0))
 
 
 @gpu

@@ -169,6 +169,10 @@ def test_negative_scale_and_steep_biases():
     check(w, Rule())
     check(w, Rule(window=140))
     check(w, Rule(softcap=6.0, slopes=100.0 * slopes_of(w.query_heads)))
+    w.scale = 0.0  # every seen token weighs the same
+    check(w, Rule(window=70))
+    check(w, Rule(softcap=6.0))
+    check(w, Rule(slopes=slopes_of(w.query_heads)))
 
 
 @gpu
