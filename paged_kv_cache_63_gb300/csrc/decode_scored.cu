@@ -677,6 +677,18 @@ pa_status_t resolve_score(const pa_score_t *score, float scale, ScoreArgs *s) {
     // a cap so small or large against the scale that the quotient is no normal number
     if (scale != 0.f && !std::isnormal(s->cap_in)) return PA_ERR_INVALID_ARG;
     if (!std::isfinite(s->cap_out)) return PA_ERR_INVALID_ARG;
+    // tanh t = t P(t^2) for |t| <= 1/2 (scored_softmax.cuh), as a polynomial of the raw dot
+    // product v = t / cap_in; never taken where a coefficient leaves the normal floats
+    static const double fit[4] = {0.999999463558197, -0.33326318860054016, 0.13190296292304993,
+                                  -0.04440222680568695};
+    const double in = static_cast<double>(scale) / score->softcap;
+    double power = in * score->softcap * 1.4426950408889634;
+    s->cap_poly_max = static_cast<float>(0.25 / (in * in));
+    for (int k = 0; k < 4; ++k, power *= in * in) {
+      s->cap_poly[k] = static_cast<float>(fit[k] * power);
+      if (!std::isnormal(s->cap_poly[k])) s->cap_poly_max = -1.f;
+    }
+    if (!std::isnormal(s->cap_poly_max)) s->cap_poly_max = -1.f;
   }
   const uintptr_t ptrs = reinterpret_cast<uintptr_t>(score->slopes) |
                          reinterpret_cast<uintptr_t>(score->first_tokens) |

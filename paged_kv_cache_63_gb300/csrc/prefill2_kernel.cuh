@@ -121,11 +121,17 @@ __device__ __forceinline__ Item2 item2_of(const PrefillArgs &a, int kv, int b, i
   return it;
 }
 
-// Under a score rule (kScored) an item also knows where its keys start: tiles are counted from
-// j0, the tile of the first token that some row of the pair sees (kv_lo), and end at the last
-// one (nt_a, nt_b, nt_max, max_pos_a, max_pos_b and kv_len follow what the rows see). Warp-collective.
+// Under a score rule (kScored) an item's keys go from kv_lo, the first token that some row of
+// the pair sees, to kv_len. Its key tiles are taken last to first, tile j (0 .. nt_max - 1) being
+// the one j before the last: a bias by distance and most attention favour near keys, so a row
+// meets its largest scores first and rarely moves its maximum again (first to last, a steep
+// bias moved it, and rescaled O, on every tile: 7250 cycles a tile against 3600). Query tile X
+// takes part in tiles [from_X, to_X); the pair's other tile may see keys on either side of that.
+// Both spans are non-empty for a tile that has rows, overlap or touch, and cover all tiles.
+// Warp-collective.
 struct ScoredItem2 : Item2 {
-  int j0, kv_lo, prefix;
+  int kv_lo, prefix, last_tile;  // last_tile: index of the key tile taken first
+  int from_a, to_a, from_b, to_b;
 };
 
 template <int TN>
@@ -157,17 +163,24 @@ __device__ __forceinline__ ScoredItem2 scored_item2_of(const PrefillScoredArgs &
   it.prefix = prefix_of(a.s, b, ctx);
   int lo_a, lo_b;
   seen_range(a.s, q0, ctx - n, it.tok0_a, min(it.tok0_b, n), it.prefix, lo_a, it.max_pos_a);
-  it.max_pos_b = -1;
-  it.kv_lo = lo_a;
-  if (it.tok0_b < n) {
+  it.max_pos_b = it.max_pos_a;
+  it.kv_lo = lo_b = lo_a;
+  const bool b_rows = it.tok0_b < n;
+  if (b_rows) {
     seen_range(a.s, q0, ctx - n, it.tok0_b, min(it.tok0_b + a.qt, n), it.prefix, lo_b, it.max_pos_b);
     it.kv_lo = min(lo_a, lo_b);
   }
-  it.j0 = it.kv_lo / TN;
-  it.nt_a = (it.max_pos_a + TN) / TN - it.j0;
-  it.nt_b = it.tok0_b < n ? (it.max_pos_b + TN) / TN - it.j0 : 0;
-  it.nt_max = max(it.nt_a, it.nt_b);
-  it.kv_len = max(it.max_pos_a, it.max_pos_b) + 1;
+  // tile B's rows come after tile A's, so they see at least as far: max_pos_b >= max_pos_a, by
+  // less than a query tile's tokens (<= TN), so that from_a <= 1 <= to_b
+  it.last_tile = it.max_pos_b / TN;
+  it.from_a = it.last_tile - it.max_pos_a / TN;
+  it.from_b = 0;
+  it.to_a = it.last_tile - lo_a / TN + 1;
+  it.to_b = b_rows ? it.last_tile - lo_b / TN + 1 : 0;
+  it.nt_a = it.to_a - it.from_a;
+  it.nt_b = it.to_b;
+  it.nt_max = max(it.to_a, it.to_b);
+  it.kv_len = it.max_pos_b + 1;
   it.live = 1;
   return it;
 }
@@ -264,12 +277,24 @@ __global__ void __launch_bounds__(kPrefill2Threads, 1)
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
 
-  // first token of tile j of an item
+  // first token of tile j of an item, and the tiles [from, to) that query tile x takes part in
   auto tile_token = [](const Item &it, int j) {
     if constexpr (kScored)
-      return (it.j0 + j) * C::TN;
+      return (it.last_tile - j) * C::TN;
     else
       return j * C::TN;
+  };
+  auto from_of = [](const Item &it, int x) {
+    if constexpr (kScored)
+      return x ? it.from_b : it.from_a;
+    else
+      return 0;
+  };
+  auto to_of = [](const Item &it, int x) {
+    if constexpr (kScored)
+      return x ? it.to_b : it.to_a;
+    else
+      return x ? it.nt_b : it.nt_a;
   };
 
   // Reader side of the item ring: item k sits in entry k & 1. Returns false on abort.
@@ -461,8 +486,8 @@ __global__ void __launch_bounds__(kPrefill2Threads, 1)
       ok = take_item(k, it);
       if (!ok || it.stop) break;
       if (!it.live) continue;
-      auto nt_of = [&](int x) { return x ? it.nt_b : it.nt_a; };
-      const int last_s_x = it.nt_b == it.nt_max ? 1 : 0;  // tile of the item's last score MMA
+      const int from[2] = {from_of(it, 0), from_of(it, 1)}, to[2] = {to_of(it, 0), to_of(it, 1)};
+      const int last_s_x = to[1] == it.nt_max ? 1 : 0;  // tile of the item's last score MMA
       // MMAs and commits are issued warp-collectively (one elected lane), with operands every
       // lane computes identically
       // Descriptors of a K step are the tile's base descriptor plus the step's byte offset / 16
@@ -488,9 +513,9 @@ __global__ void __launch_bounds__(kPrefill2Threads, 1)
         for (int ks = 0; ks < C::TN / 16; ++ks) {
           const uint64_t bd = vd + ((ks * 2048) >> 4);
           mma_f16_ts_warp(tmem + 256u + 128u * x, tmem + 128u * x + ks * 8, bd, C::kIdescPV,
-                          (j > 0 || ks > 0) ? 1u : 0u);
+                          (j > from[x] || ks > 0) ? 1u : 0u);
         }
-        if (j == nt_of(x) - 1) mma_commit_warp(bar(kB2ODone + x));
+        if (j == to[x] - 1) mma_commit_warp(bar(kB2ODone + x));
       };
       auto release = [&](int item) { mma_commit_warp(bar(kB2Empty + item % C::kSlots)); };
       auto clear_v_tail = [&](int j) {
@@ -498,7 +523,7 @@ __global__ void __launch_bounds__(kPrefill2Threads, 1)
         // written): P is zero there, but 0 * NaN is not, so clear them before the first P.V
         // of that tile.
         const int rows_last = it.kv_len - tile_token(it, j);
-        if (j != it.nt_max - 1 || rows_last >= C::TN) return;
+        if (j != (kScored ? 0 : it.nt_max - 1) || rows_last >= C::TN) return;
         const int per_block = (C::TN - rows_last) * 8;
         uint8_t *vg = sgen + C::kRingOff + ((2 * (gt + j) + 1) % C::kSlots) * C::kSlotBytes;
         for (int c = lane; c < C::KB * per_block; c += 32) {
@@ -513,9 +538,9 @@ __global__ void __launch_bounds__(kPrefill2Threads, 1)
         // likewise the rows before the first token that some row sees
         if constexpr (kScored) {
           const int rows_first = it.kv_lo - tile_token(it, j);
-          if (j != 0 || rows_first <= 0) return;
+          if (j != it.nt_max - 1 || rows_first <= 0) return;
           const int per_block = rows_first * 8;
-          uint8_t *vg = sgen + C::kRingOff + ((2 * gt + 1) % C::kSlots) * C::kSlotBytes;
+          uint8_t *vg = sgen + C::kRingOff + ((2 * (gt + j) + 1) % C::kSlots) * C::kSlotBytes;
           for (int c = lane; c < C::KB * per_block; c += 32) {
             const int kb = c / per_block, r = c % per_block;
             *reinterpret_cast<uint4 *>(vg + kb * (C::TN * 128) + r * 16) = make_uint4(0, 0, 0, 0);
@@ -531,29 +556,41 @@ __global__ void __launch_bounds__(kPrefill2Threads, 1)
       if (ok) {
         // S_X(0) overwrites the columns from which the previous item's last P.V read P_X:
         // that MMA was issued earlier by this thread and so runs first
-        issue_s(0, 0);
-        if (it.nt_b > 0) issue_s(1, 0);
+        if (from[0] == 0) issue_s(0, 0);
+        if (to[1] > 0) issue_s(1, 0);
         release(2 * gt);
       }
       for (int j = 0; j < it.nt_max && ok; ++j) {
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          if (!ok || j >= nt_of(x)) continue;
+          if constexpr (kScored) {
+            if (x == 0 && ok && j + 1 == from[0]) {
+              // tile A joins at the next key tile: its first scores, whose keys no softmax has
+              // confirmed (tile B takes part in that tile too, or this is its last user)
+              ok = wait_item(2 * (gt + j + 1));
+              if (ok) {
+                issue_s(0, j + 1);
+                if (j + 1 >= to[1]) release(2 * (gt + j + 1));
+              }
+            }
+            if (j < from[x]) continue;
+          }
+          if (!ok || j >= to[x]) continue;
           // P_X(j) is released only after V(j) and K(j + 1) have landed (see the softmax)
           ok = pipe_wait(bar(kB2PFull + x), (phase >> (1 + x)) & 1u, abort_flag, a.err);
           if (!ok) break;
           phase ^= 2u << x;
           tc_fence_after();
-          if (x == 0 || j >= it.nt_a) {
+          if (x == 0 || j >= to[0] || j < from[0]) {
             clear_v_head(j);
             clear_v_tail(j);
           }
           issue_pv(x, j);
-          const bool last_v_user = (x == 1) || (j >= it.nt_b);
+          const bool last_v_user = (x == 1) || (j >= to[1]);
           if (last_v_user) release(2 * (gt + j) + 1);
-          if (j + 1 < nt_of(x)) {
+          if (j + 1 < to[x]) {
             issue_s(x, j + 1);
-            const bool last_k_user = (x == 1) || (j + 1 >= it.nt_b);
+            const bool last_k_user = (x == 1) || (j + 1 >= to[1]);
             if (last_k_user) release(2 * (gt + j + 1));
           }
         }
@@ -578,8 +615,8 @@ __global__ void __launch_bounds__(kPrefill2Threads, 1)
     uint32_t phase = 0;  // parities of the next waits: bit 0 SFull[x], bit 1 ODone[x]
     bool ok = true;
     for (int k = 0; ok; ++k) {
-      int my_nt, pos, gt0, out_row0, out_head0;
-      int tile0 = 0;  // first token of the item's first tile
+      int my_from, my_nt, pos, gt0, out_row0, out_head0;
+      int tile0 = 0;  // first token of the key tile taken first
       ScoredRow sr = {};
       bool valid;
       {
@@ -588,12 +625,13 @@ __global__ void __launch_bounds__(kPrefill2Threads, 1)
         if (!ok || it.stop) break;
         if (!it.live) continue;
         const int my_tok0 = x ? it.tok0_b : it.tok0_a;
-        my_nt = x ? it.nt_b : it.nt_a;
+        my_from = from_of(it, x);
+        my_nt = to_of(it, x);
         valid = row < q_rows && my_tok0 + t < it.n;
         pos = min(it.ctx - it.n + my_tok0 + t, x ? it.max_pos_b : it.max_pos_a);
         if constexpr (kScored) {
           // rows past the tile's last token repeat it (and are not stored)
-          tile0 = it.j0 * C::TN;
+          tile0 = it.last_tile * C::TN;
           if (my_nt > 0)
             sr = scored_row(a.s, it.q0, it.ctx - it.n, min(my_tok0 + min(t, a.qt - 1), it.n - 1),
                             it.kv * a.g + h, it.prefix);
@@ -604,7 +642,7 @@ __global__ void __launch_bounds__(kPrefill2Threads, 1)
         gt += it.nt_max;
       }
       float m = -INFINITY, l = 0.f;
-      for (int j = 0; j < my_nt; ++j) {
+      for (int j = my_from; j < my_nt; ++j) {
         ok = pipe_wait(bar(kB2SFull + x), phase & 1u, abort_flag, a.err);
         if (!ok) break;
         phase ^= 1u;
@@ -646,7 +684,8 @@ __global__ void __launch_bounds__(kPrefill2Threads, 1)
             }
             return true;
           };
-          scored_weights<C::TN>(a.s, sl2, sr, tile0 + j * C::TN, j > 0, load, emit, rescale);
+          scored_weights<C::TN>(a.s, sl2, sr, tile0 - j * C::TN, j > my_from, load, emit,
+                                rescale);
         } else {
           const int lim = pos - j * C::TN;
           // warp-uniform: the exponent passes hold tcgen05.st, which the whole warp executes

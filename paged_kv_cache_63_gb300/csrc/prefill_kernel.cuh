@@ -131,11 +131,11 @@ __device__ __forceinline__ Item1 item1_of(const PrefillArgs &a, int kv, int b, i
   return it;
 }
 
-// Under a score rule (kScored) an item also knows where its keys start: tiles are counted from
-// j0, the tile of the first token that some row sees (kv_lo), and end at the last one (ntiles,
-// max_pos and kv_len follow what the rows see). Warp-collective.
+// Under a score rule (kScored) an item's keys go from kv_lo, the first token that some row
+// sees, to kv_len, and its key tiles are taken last to first (as in prefill2_kernel.cuh): tile j
+// is the one j before last_tile. Warp-collective.
 struct ScoredItem1 : Item1 {
-  int j0, kv_lo, prefix;
+  int kv_lo, prefix, last_tile;
 };
 
 template <int TN>
@@ -165,9 +165,9 @@ __device__ __forceinline__ ScoredItem1 scored_item1_of(const PrefillScoredArgs &
   it.base_pos = ctx - n + it.tok0;
   it.prefix = prefix_of(a.s, b, ctx);
   seen_range(a.s, q0, ctx - n, it.tok0, min(it.tok0 + a.qt, n), it.prefix, it.kv_lo, it.max_pos);
-  it.j0 = it.kv_lo / TN;
   it.kv_len = it.max_pos + 1;
-  it.ntiles = (it.kv_len + TN - 1) / TN - it.j0;
+  it.last_tile = it.max_pos / TN;
+  it.ntiles = it.last_tile - it.kv_lo / TN + 1;
   it.live = 1;
   return it;
 }
@@ -232,7 +232,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
   // first token of tile j of an item
   auto tile_token = [](const Item &it, int j) {
     if constexpr (kScored)
-      return (it.j0 + j) * C::TN;
+      return (it.last_tile - j) * C::TN;
     else
       return j * C::TN;
   };
@@ -400,7 +400,9 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
       ++q_waits;
       if (!ok) break;
       tc_fence_after();
-      const int rows_last = it.kv_len - tile_token(it, it.ntiles - 1);  // valid rows of the last V tile
+      // the tile that holds the last needed token, and its valid rows
+      const int tail = kScored ? 0 : it.ntiles - 1;
+      const int rows_last = it.kv_len - tile_token(it, tail);
       for (int j = 0; j <= it.ntiles && ok; ++j) {
         if (j < it.ntiles) {
           const int t = g + j, st = t & 1;
@@ -434,8 +436,8 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
           tc_fence_after();
           if constexpr (kScored) {
             // likewise the rows before the first token that some row sees
-            const int rows_first = it.kv_lo - tile_token(it, 0);
-            if (i == 0 && rows_first > 0) {
+            const int rows_first = it.kv_lo - tile_token(it, i);
+            if (i == it.ntiles - 1 && rows_first > 0) {
               const int per_block = rows_first * 8;
               uint8_t *vg = sgen + C::kVOff + st * C::kKVBytes;
               for (int c = lane; c < C::KB * per_block; c += 32) {
@@ -446,7 +448,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
               __syncwarp();
             }
           }
-          if (i == it.ntiles - 1 && rows_last < C::TN) {
+          if (i == tail && rows_last < C::TN) {
             // V rows past the last needed token hold unread cache slots (possibly never
             // written); P is zero there, but 0 * NaN is not, so clear them.
             const int per_block = (C::TN - rows_last) * 8;

@@ -19,6 +19,8 @@ struct ScoreArgs {
   float cap_in;           // scale / softcap: a raw dot product times this is tanh's argument; 0:
                           // no cap
   float cap_out;          // softcap * log2 e
+  float cap_poly[4];      // cap_out tanh(v cap_in) ~ v (poly[0] + poly[1] v^2 + ...) for
+  float cap_poly_max;     // v^2 <= cap_poly_max (multi-token kernels)
   int window;             // 0: no limit
   int out_half;           // output in fp16
 };

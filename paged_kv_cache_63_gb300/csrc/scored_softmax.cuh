@@ -4,11 +4,12 @@
 // What bounds it is instructions per score (the special-function pipe and the fp32 pipe share
 // the softmax warps' issue slots with the tensor-memory traffic), so:
 //  * tanh is a polynomial on the fp32 pipe in packed pairs wherever a warp's arguments allow:
-//    tanh t = t P(t^2) with P of degree 4, fitted to the least relative error for |t| <= 0.75
-//    (6.3e-7 evaluated in fp32; weighted least squares on Chebyshev nodes, weights iterated
-//    towards the equal-ripple fit). A score is then off by at most 0.64 cap * 6.3e-7, 2e-5 for
-//    a cap of 50, against the 2^-11 by which the fp16 probability is rounded. A warp with a
-//    larger argument takes 1 - 2 / (1 + e^2t) for its tile.
+//    tanh t = t P(t^2) with P of degree 3, fitted to the least relative error for |t| <= 1/2
+//    (5.8e-7 evaluated in fp32; weighted least squares on Chebyshev nodes, weights iterated
+//    towards the equal-ripple fit), the scale and the cap folded into its coefficients. A score
+//    is then off by at most 0.47 cap * 5.8e-7, 1.4e-5 for a cap of 50, against the 2^-11 by
+//    which the fp16 probability is rounded. A warp with a larger argument among its 64 columns
+//    takes 1 - 2 / (1 + e^2t) for them.
 //  * The bias is linear in the key's column wherever no key of the tile lies past its query:
 //    slope * column joins the score in the instruction that scales it, the rest of the bias
 //    is one number per row and tile.
@@ -31,14 +32,18 @@ struct PrefillScoredArgs : PrefillArgs {
 template <bool kScored>
 using PrefillArgsOf = std::conditional_t<kScored, PrefillScoredArgs, PrefillArgs>;
 
+// A row's reference maximum moves only when a score passes it by more than 2^15: weights stay
+// below 2^15 until then, which fp16 holds as precisely as any, and a tile's row sum of at most
+// 2^15 shows that none passed.
+constexpr float kScoredSlack = 15.f;  // log2 units
+constexpr float kScoredSlackBound = 32768.f;
+
 // A query row: its position, the tokens [lo, hi] it sees, its head's slope * log2 e, and the
 // softmax so far (reference maximum in base 2, sum).
 struct ScoredRow {
   int pos, lo, hi;
   float slope2, m, l;
 };
-
-constexpr float kTanhPolyMax = 0.75f;
 
 __device__ __forceinline__ float2 fmul2(float2 a, float2 b) {
   float2 d;
@@ -54,57 +59,54 @@ __device__ __forceinline__ float fast_rcp(float x) {
   return y;
 }
 
-// v = cap_out * tanh(v * cap_in). Warp-collective.
-__device__ __forceinline__ void cap_scores(float (&v)[64], float cap_in, float cap_out) {
-  float big[4] = {0.f, 0.f, 0.f, 0.f};
-  const float2 in = make_float2(cap_in, cap_in);
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+// v = cap_out * tanh(v * cap_in); reload() puts the raw v back. Warp-collective.
+template <class Reload>
+__device__ __forceinline__ void cap_scores(float (&v)[64], const ScoreArgs &s, Reload reload) {
+  float top[4] = {0.f, 0.f, 0.f, 0.f};
+  const float2 c0 = make_float2(s.cap_poly[0], s.cap_poly[0]),
+               c1 = make_float2(s.cap_poly[1], s.cap_poly[1]),
+               c2 = make_float2(s.cap_poly[2], s.cap_poly[2]),
+               c3 = make_float2(s.cap_poly[3], s.cap_poly[3]);
 #pragma unroll
   for (int c = 0; c < 64; c += 2) {
-    const float2 t = fmul2(make_float2(v[c], v[c + 1]), in);
-    v[c] = t.x;
-    v[c + 1] = t.y;
-    big[c & 2] = fmaxf(big[c & 2], fabsf(t.x));
-    big[(c & 2) + 1] = fmaxf(big[(c & 2) + 1], fabsf(t.y));
+    const float2 x = make_float2(v[c], v[c + 1]);
+    const float2 z = fmul2(x, x);
+    top[(c >> 1) & 3] = max3(top[(c >> 1) & 3], z.x, z.y);
+    float2 p = ffma2(c3, z, c2);
+    p = ffma2(p, z, c1);
+    p = ffma2(p, z, c0);
+    p = fmul2(p, x);
+    v[c] = p.x;
+    v[c + 1] = p.y;
   }
-  const float top = fmaxf(fmaxf(big[0], big[1]), fmaxf(big[2], big[3]));
-  if (__builtin_expect(__all_sync(0xffffffffu, top <= kTanhPolyMax), 1)) {
-    // coefficients of P, times cap_out
-    const float k0 = 0.999999463558197f * cap_out, k1 = -0.3332825303077698f * cap_out,
-                k2 = 0.13258983194828033f * cap_out, k3 = -0.05005630478262901f * cap_out,
-                k4 = 0.012929633259773254f * cap_out;
-    const float2 c0 = make_float2(k0, k0), c1 = make_float2(k1, k1), c2 = make_float2(k2, k2),
-                 c3 = make_float2(k3, k3), c4 = make_float2(k4, k4);
-#pragma unroll
-    for (int c = 0; c < 64; c += 2) {
-      const float2 t = make_float2(v[c], v[c + 1]);
-      const float2 z = fmul2(t, t);
-      float2 p = ffma2(c4, z, c3);
-      p = ffma2(p, z, c2);
-      p = ffma2(p, z, c1);
-      p = ffma2(p, z, c0);
-      p = fmul2(p, t);
-      v[c] = p.x;
-      v[c + 1] = p.y;
-    }
-  } else {
+  const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+  if (__builtin_expect(__any_sync(0xffffffffu, !(most <= s.cap_poly_max)), 0)) {
+    reload();
     // e^2t overflows to infinity and underflows to 0 where tanh is +-1
 #pragma unroll
     for (int c = 0; c < 64; ++c) {
-      const float e = prefill_exp2(v[c] * (2.f * kLog2e));
-      v[c] = fmaf(-2.f * cap_out, fast_rcp(1.f + e), cap_out);
+      const float e = prefill_exp2(v[c] * (s.cap_in * (2.f * kLog2e)));
+      v[c] = fmaf(-2.f * s.cap_out, fast_rcp(1.f + e), s.cap_out);
     }
   }
 }
 
 // From raw dot products to base-2 scores: afterwards the score of column c is
 // v[c] * mult + offset. `base` is the columns' first token. Warp-collective.
+template <class Reload>
 __device__ __forceinline__ void rule_scores(float (&v)[64], const ScoreArgs &s, float scale_log2,
-                                            const ScoredRow &row, int base, float &mult,
-                                            float &offset) {
+                                            const ScoredRow &row, int base, Reload reload,
+                                            float &mult, float &offset) {
   mult = scale_log2;
   offset = 0.f;
   if (s.cap_in != 0.f) {
-    cap_scores(v, s.cap_in, s.cap_out);
+    cap_scores(v, s, reload);
     mult = 1.f;
   }
   if (s.slopes) {
@@ -179,7 +181,7 @@ __device__ __forceinline__ bool scored_weights(const ScoreArgs &s, float scale_l
     for (int h = 0; h < H; ++h) {
       float v[64], mult, offset;
       load(h, v);
-      rule_scores(v, s, scale_log2, row, base + 64 * h, mult, offset);
+      rule_scores(v, s, scale_log2, row, base + 64 * h, [&] { load(h, v); }, mult, offset);
       const float sign = mult >= 0.f ? 1.f : -1.f;
       if (!full) {
         const float none = -sign * INFINITY;
@@ -213,7 +215,7 @@ __device__ __forceinline__ bool scored_weights(const ScoreArgs &s, float scale_l
       }
     }
     if (find) {
-      const bool grow = mx > row.m + kPrefillRescaleSlack;
+      const bool grow = mx > row.m + kScoredSlack;
       if (__any_sync(0xffffffffu, grow)) {
         const float mnew = grow ? mx : row.m;
         const float f = mnew == -INFINITY ? 1.f : prefill_exp2(row.m - mnew);
@@ -226,7 +228,7 @@ __device__ __forceinline__ bool scored_weights(const ScoreArgs &s, float scale_l
       continue;
     }
     sum = (rp[0] + rp[1]) + (rp[2] + rp[3]);
-    if (last || __all_sync(0xffffffffu, sum <= kPrefillSlackBound &&
+    if (last || __all_sync(0xffffffffu, sum <= kScoredSlackBound &&
                                             !(some && row.m == -INFINITY)))
       break;
     find = true;
