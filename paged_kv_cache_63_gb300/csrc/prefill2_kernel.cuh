@@ -669,9 +669,9 @@ __global__ void __launch_bounds__(kPrefill2Threads, 1)
           if (!ok) break;
         }
         if constexpr (kScored) {
-          auto load = [&](int part, float (&c)[64]) { tmem_ld64(ts + part * 64, c); };
-          // P as fp16 pairs over the first 64 columns of S
-          auto emit = [&](int part, const float (&pk)[32]) { tmem_st32(ts + part * 32, pk); };
+          auto load = [&](int part, float (&c)[32]) { tmem_ld32(ts + part * 32, c); };
+          // P as fp16 pairs over the first 64 columns of S, behind the columns being read
+          auto emit = [&](int part, const float (&pk)[16]) { tmem_st16(ts + part * 16, pk); };
           auto rescale = [&](float f) {
             // S_X(j) completed, so PV_X(j - 1) has too: O_X is stable until P_X(j) is released
 #pragma unroll

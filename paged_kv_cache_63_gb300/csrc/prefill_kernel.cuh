@@ -516,11 +516,11 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
             ok = pipe_wait(bar(kBarPV + st), ((gj >> 1) - 1) & 1, abort_flag, a.err);
             if (!ok) break;
           }
-          auto load = [&](int, float (&c)[64]) { tmem_ld64(trow + st * C::TN, c); };
-          auto emit = [&](int, const float (&pk)[32]) {
+          auto load = [&](int part, float (&c)[32]) { tmem_ld32(trow + st * C::TN + part * 32, c); };
+          auto emit = [&](int part, const float (&pk)[16]) {
 #pragma unroll
-            for (int e = 0; e < 32; e += 4)
-              sts128(p_buf(st) + row * 128 + (((e >> 2) ^ (row & 7)) << 4),
+            for (int e = 0; e < 16; e += 4)
+              sts128(p_buf(st) + row * 128 + (((part * 4 + (e >> 2)) ^ (row & 7)) << 4),
                      make_uint4(__float_as_uint(pk[e]), __float_as_uint(pk[e + 1]),
                                 __float_as_uint(pk[e + 2]), __float_as_uint(pk[e + 3])));
           };
