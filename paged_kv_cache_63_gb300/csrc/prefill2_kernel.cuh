@@ -221,6 +221,31 @@ __device__ __forceinline__ void exps_row(const float (&v)[TN], float sl2, float 
   }
 }
 
+// A thread's row of a tile, for scored_weights: scores at TMEM address ts, accumulated output
+// at to.
+template <int HD>
+struct ScoredTile2 {
+  uint32_t ts, to;
+  __device__ __forceinline__ void load_all(float (&c)[128]) const { tmem_ld128(ts, c); }
+  __device__ __forceinline__ void load64(int h, float (&c)[64]) const { tmem_ld64(ts + h * 64, c); }
+  __device__ __forceinline__ void load32(int h, float (&c)[32]) const { tmem_ld32(ts + h * 32, c); }
+  // P as fp16 pairs over the first 64 columns of S, behind the columns being read
+  __device__ __forceinline__ void emit64(int h, const float (&pk)[32]) const { tmem_st32(ts + h * 32, pk); }
+  __device__ __forceinline__ void emit32(int h, const float (&pk)[16]) const { tmem_st16(ts + h * 16, pk); }
+  __device__ __forceinline__ bool rescale(float f) const {
+    // S_X(j) completed, so PV_X(j - 1) has too: O_X is stable until P_X(j) is released
+#pragma unroll
+    for (int c = 0; c < HD / 32; ++c) {
+      float o[32];
+      tmem_ld32(to + c * 32, o);
+#pragma unroll
+      for (int e = 0; e < 32; ++e) o[e] *= f;
+      tmem_st32(to + c * 32, o);
+    }
+    return true;
+  }
+};
+
 // kScored: under a score rule (scored_softmax.cuh), with fp16 output.
 template <int HD, bool kScored>
 __global__ void __launch_bounds__(kPrefill2Threads, 1)
@@ -669,23 +694,8 @@ __global__ void __launch_bounds__(kPrefill2Threads, 1)
           if (!ok) break;
         }
         if constexpr (kScored) {
-          auto load = [&](int part, float (&c)[32]) { tmem_ld32(ts + part * 32, c); };
-          // P as fp16 pairs over the first 64 columns of S, behind the columns being read
-          auto emit = [&](int part, const float (&pk)[16]) { tmem_st16(ts + part * 16, pk); };
-          auto rescale = [&](float f) {
-            // S_X(j) completed, so PV_X(j - 1) has too: O_X is stable until P_X(j) is released
-#pragma unroll
-            for (int c = 0; c < HD / 32; ++c) {
-              float o[32];
-              tmem_ld32(to + c * 32, o);
-#pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] *= f;
-              tmem_st32(to + c * 32, o);
-            }
-            return true;
-          };
-          scored_weights<C::TN>(a.s, sl2, sr, tile0 - j * C::TN, j > my_from, load, emit,
-                                rescale);
+          const ScoredTile2<HD> io = {ts, to};
+          scored_weights<C::TN>(a.s, sl2, sr, tile0 - j * C::TN, j > my_from, io);
         } else {
           const int lim = pos - j * C::TN;
           // warp-uniform: the exponent passes hold tcgen05.st, which the whole warp executes

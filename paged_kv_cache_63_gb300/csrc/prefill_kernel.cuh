@@ -172,6 +172,45 @@ __device__ __forceinline__ ScoredItem1 scored_item1_of(const PrefillScoredArgs &
   return it;
 }
 
+// A thread's row of a tile, for scored_weights: scores at TMEM address ts, weights to the
+// shared-memory row prow (16-byte chunks swizzled by xor7), accumulated output at TMEM address
+// to, stable once the barrier of the last P.V has completed.
+template <int HD>
+struct ScoredTile1 {
+  uint32_t ts, to, prow, xor7;
+  uint32_t pv_bar, pv_parity;
+  volatile int *abort_flag;
+  unsigned *err;
+  __device__ __forceinline__ void load_all(float (&c)[64]) const { tmem_ld64(ts, c); }
+  __device__ __forceinline__ void load64(int, float (&c)[64]) const { tmem_ld64(ts, c); }
+  __device__ __forceinline__ void load32(int h, float (&c)[32]) const { tmem_ld32(ts + h * 32, c); }
+  template <int N>
+  __device__ __forceinline__ void put(int chunk, const float (&pk)[N]) const {
+#pragma unroll
+    for (int e = 0; e < N; e += 4)
+      sts128(prow + (((chunk + (e >> 2)) ^ xor7) << 4),
+             make_uint4(__float_as_uint(pk[e]), __float_as_uint(pk[e + 1]),
+                        __float_as_uint(pk[e + 2]), __float_as_uint(pk[e + 3])));
+  }
+  __device__ __forceinline__ void emit64(int, const float (&pk)[32]) const { put(0, pk); }
+  __device__ __forceinline__ void emit32(int h, const float (&pk)[16]) const { put(4 * h, pk); }
+  __device__ __forceinline__ bool rescale(float f) const {
+    // O holds tiles < j: wait for the last P.V, then scale this row of O in TMEM
+    if (!pipe_wait(pv_bar, pv_parity, abort_flag, err)) return false;
+    tc_fence_after();
+#pragma unroll
+    for (int c = 0; c < HD / 32; ++c) {
+      float v[32];
+      tmem_ld32(to + c * 32, v);
+#pragma unroll
+      for (int e = 0; e < 32; ++e) v[e] *= f;
+      tmem_st32(to + c * 32, v);
+    }
+    tmem_wait_st();
+    return true;
+  }
+};
+
 // kScored: under a score rule (scored_softmax.cuh), with fp16 output.
 template <int HD, bool kScored>
 __global__ void __launch_bounds__(kPrefillThreads, 1)
@@ -516,31 +555,10 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
             ok = pipe_wait(bar(kBarPV + st), ((gj >> 1) - 1) & 1, abort_flag, a.err);
             if (!ok) break;
           }
-          auto load = [&](int part, float (&c)[32]) { tmem_ld32(trow + st * C::TN + part * 32, c); };
-          auto emit = [&](int part, const float (&pk)[16]) {
-#pragma unroll
-            for (int e = 0; e < 16; e += 4)
-              sts128(p_buf(st) + row * 128 + (((part * 4 + (e >> 2)) ^ (row & 7)) << 4),
-                     make_uint4(__float_as_uint(pk[e]), __float_as_uint(pk[e + 1]),
-                                __float_as_uint(pk[e + 2]), __float_as_uint(pk[e + 3])));
-          };
-          auto rescale = [&](float f) {
-            // O holds tiles < j: wait for the last P.V, then scale this row of O in TMEM
-            if (!pipe_wait(bar(kBarPV + ((gj - 1) & 1)), ((gj - 1) >> 1) & 1, abort_flag, a.err))
-              return false;
-            tc_fence_after();
-#pragma unroll
-            for (int c = 0; c < HD / 32; ++c) {
-              float v[32];
-              tmem_ld32(trow + C::kOCol + c * 32, v);
-#pragma unroll
-              for (int e = 0; e < 32; ++e) v[e] *= f;
-              tmem_st32(trow + C::kOCol + c * 32, v);
-            }
-            tmem_wait_st();
-            return true;
-          };
-          ok = scored_weights<C::TN>(a.s, sl2, sr, tile_token(it, j), j > 0, load, emit, rescale);
+          const ScoredTile1<HD> io = {trow + st * C::TN, trow + C::kOCol, p_buf(st) + row * 128,
+                  static_cast<uint32_t>(row & 7), bar(kBarPV + ((gj - 1) & 1)),
+                  static_cast<uint32_t>(((gj - 1) >> 1) & 1), abort_flag, a.err};
+          ok = scored_weights<C::TN>(a.s, sl2, sr, tile_token(it, j), j > 0, io);
           if (!ok) break;
         } else {
           float x[C::TN];

@@ -1,13 +1,13 @@
 // scored_softmax.cuh -- the softmax of one key tile under a score rule, for the multi-token
 // kernels: one query row per thread, the tile's raw dot products in registers.
 //
-// A tile's chain bounds the kernel (scores, weights, the two products, the next scores), in it
-// the instructions per score of a warp, and with them their fetching: so a tile is walked twice
-// by short loops of 32 columns that hold no more than 32 scores, the first for the maximum, the
-// second for the weights, each written to tensor memory as it stands. (One walk with the
-// maximum as it was, checked by the sum as in the causal kernels, has to keep a row's weights
-// until the check; its code spilled or outgrew the instruction cache: 6900 cycles a tile
-// unrolled and 4750 as a loop of 64 columns, on the capped rows of 2048-token prompts.)
+// A tile's chain bounds the kernel (scores, weights, the two products, the next scores), and in
+// it the instructions per score of one warp and their fetching. So a tile is walked twice, first
+// for the maximum, then for the weights, each part of them written as it stands, by loops short
+// enough for the instruction cache. (One walk with the maximum as it was, checked by the sum as
+// in the causal kernels, has to keep a row's weights until the check; its code spilled -- a
+// spilled word is an L2 access, the shared memory being full -- or outgrew the cache: 6900
+// cycles a tile unrolled, 4750 as a loop of 64 columns, on capped rows in a window.)
 //  * tanh is a polynomial on the fp32 pipe in packed pairs wherever a warp's arguments allow:
 //    tanh t = t P(t^2) with P of degree 3, fitted to the least relative error for |t| <= 1/2
 //    (5.8e-7 evaluated in fp32; weighted least squares on Chebyshev nodes, weights iterated
@@ -79,14 +79,16 @@ __device__ __forceinline__ float cap_exact(const ScoreArgs &s, float v) {
   return fmaf(-2.f * s.cap_out, fast_rcp(1.f + e), s.cap_out);
 }
 
-__device__ __forceinline__ void cap_scores(float (&v)[32], const ScoreArgs &s, bool poly) {
+// v = cap_out * tanh(v * cap_in), by the polynomial where `poly` (warp-uniform) says so.
+template <int N>
+__device__ __forceinline__ void cap_scores(float (&v)[N], const ScoreArgs &s, bool poly) {
   if (__builtin_expect(poly, 1)) {
     const float2 c0 = make_float2(s.cap_poly[0], s.cap_poly[0]),
                  c1 = make_float2(s.cap_poly[1], s.cap_poly[1]),
                  c2 = make_float2(s.cap_poly[2], s.cap_poly[2]),
                  c3 = make_float2(s.cap_poly[3], s.cap_poly[3]);
 #pragma unroll
-    for (int c = 0; c < 32; c += 2) {
+    for (int c = 0; c < N; c += 2) {
       const float2 x = make_float2(v[c], v[c + 1]);
       const float2 z = fmul2(x, x);
       float2 p = ffma2(c3, z, c2);
@@ -98,25 +100,30 @@ __device__ __forceinline__ void cap_scores(float (&v)[32], const ScoreArgs &s, b
     }
   } else {
 #pragma unroll
-    for (int c = 0; c < 32; ++c) v[c] = cap_exact(s, v[c]);
+    for (int c = 0; c < N; ++c) v[c] = cap_exact(s, v[c]);
+  }
+}
+
+// v = v * mult + slope2 * column, by steps of two columns, each off by a rounding (a table of
+// columns for the packed pairs would take a register each).
+template <int N>
+__device__ __forceinline__ void add_slope(float (&v)[N], float slope2, float mult) {
+  const float2 m2 = make_float2(mult, mult), step = make_float2(2.f * slope2, 2.f * slope2);
+  float2 bias = make_float2(0.f, slope2);
+#pragma unroll
+  for (int c = 0; c < N; c += 2) {
+    const float2 x = ffma2(make_float2(v[c], v[c + 1]), m2, bias);
+    v[c] = x.x;
+    v[c + 1] = x.y;
+    bias = fadd2(bias, step);
   }
 }
 
 // v * mult - slope2 * distance for 32 columns of which the first is `rel` past the query; the
 // part of the bias that the columns share is returned instead of added. Warp-collective.
 __device__ __forceinline__ float bias_scores(float (&v)[32], float slope2, int rel, float mult) {
-  if (__builtin_expect(__all_sync(0xffffffffu, rel + 31 <= 0), 1)) {
-    // slope * column by steps of two columns, each off by a rounding: a table of columns for
-    // the packed pairs would take 32 registers
-    const float2 m2 = make_float2(mult, mult), step = make_float2(2.f * slope2, 2.f * slope2);
-    float2 bias = make_float2(0.f, slope2);
-#pragma unroll
-    for (int c = 0; c < 32; c += 2) {
-      const float2 x = ffma2(make_float2(v[c], v[c + 1]), m2, bias);
-      v[c] = x.x;
-      v[c + 1] = x.y;
-      bias = fadd2(bias, step);
-    }
+  if (__all_sync(0xffffffffu, rel + 31 <= 0)) {
+    add_slope(v, slope2, mult);
     return slope2 * static_cast<float>(rel);
   }
   // keys on both sides of the query: the distance of each
@@ -127,61 +134,93 @@ __device__ __forceinline__ float bias_scores(float (&v)[32], float slope2, int r
   return 0.f;
 }
 
+// Extremes of N columns, joined into hi and lo.
+template <int N>
+__device__ __forceinline__ void extremes(const float (&v)[N], float &hi, float &lo) {
+  float mx[4] = {hi, v[0], v[0], v[0]}, mn[4] = {lo, v[0], v[0], v[0]};
+#pragma unroll
+  for (int c = 0; c < N; c += 2) {
+    mx[(c >> 1) & 3] = max3(mx[(c >> 1) & 3], v[c], v[c + 1]);
+    mn[(c >> 1) & 3] = min3(mn[(c >> 1) & 3], v[c], v[c + 1]);
+  }
+  hi = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
+  lo = min3(fminf(mn[0], mn[1]), mn[2], mn[3]);
+}
+
+// Weights 2^(v * mult + nm) of N columns, packed into pk and added to rp.
+template <int N>
+__device__ __forceinline__ void weigh(const float (&v)[N], float mult, float nm,
+                                      float (&pk)[N / 2], float (&rp)[4]) {
+  const float2 m2 = make_float2(mult, mult), n2 = make_float2(nm, nm);
+#pragma unroll
+  for (int e = 0; e < N / 2; ++e) {
+    const int c = 2 * e;
+    const float2 x = ffma2(make_float2(v[c], v[c + 1]), m2, n2);
+    const float2 w = make_float2(prefill_exp2(x.x), prefill_exp2(x.y));
+    const float2 acc = fadd2(make_float2(rp[c & 2], rp[(c & 2) + 1]), w);
+    rp[c & 2] = acc.x;
+    rp[(c & 2) + 1] = acc.y;
+    pk[e] = __uint_as_float(pack_half2(w.x, w.y));
+  }
+}
+
 // One tile of TN keys from token `base`: raw dot products become weights relative to row.m,
-// row.l grows by their sum. Warp-collective. `load(h, v)` reads raw columns 32 h .. 32 h + 31;
-// `emit(h, pk)` takes their weights as fp16 pairs (columns are emitted in order, those up to
-// 32 h + 31 having been read for the last time); `rescale(f)` multiplies the row's accumulated
-// output by f (only called when `later`, a tile after the row's first; false from it: a wait
-// gave up). A row that has seen nothing yet has m = -inf.
-template <int TN, class Load, class Emit, class Rescale>
+// row.l grows by their sum. Warp-collective. `Row` gives access to the row's scores and weights:
+// load_all(v) reads the TN raw columns, load64(h, v) and load32(h, v) a part of them, emit64(h,
+// pk) and emit32(h, pk) take a part's weights as fp16 pairs (parts are emitted in order, the
+// columns up to their end having been read for the last time), rescale(f) multiplies the row's
+// accumulated output by f (called when `later`, a tile after the row's first; false from it: a
+// wait gave up). A row that has seen nothing yet has m = -inf.
+//
+// A tile that every row sees whole is loaded at once for its maximum and 64 columns at a time
+// for its weights: a load costs ~180 cycles however wide it is. The other tiles are taken 32
+// columns at a time, without the parts that no row sees.
+template <int TN, class Row>
 __device__ __forceinline__ bool scored_weights(const ScoreArgs &s, float scale_log2,
-                                               ScoredRow &row, int base, bool later, Load load,
-                                               Emit emit, Rescale rescale) {
+                                               ScoredRow &row, int base, bool later, Row io) {
   constexpr int H = TN / 32;
   const int lo = row.lo - base, hi = row.hi - base;
   const bool some = hi >= 0 && lo < TN && lo <= hi;
-  if (!__any_sync(0xffffffffu, some)) {
-    float none[16];
-#pragma unroll
-    for (int e = 0; e < 16; ++e) none[e] = 0.f;
-#pragma unroll
-    for (int h = 0; h < H; ++h) emit(h, none);
-    return true;
-  }
-  const bool full = __all_sync(0xffffffffu, lo <= 0 && hi >= TN - 1);
   const bool cap = s.cap_in != 0.f, biased = s.slopes != nullptr;
+  const int rel = base - row.pos;
+  const bool straight = __all_sync(0xffffffffu, lo <= 0 && hi >= TN - 1 &&
+                                                    (!biased || (!cap && rel + TN - 1 <= 0)));
+  unsigned seen = 0;  // the parts of 32 columns that some row of the warp sees
 
-  // ---- the row's largest score
-  float top = -INFINITY, low = INFINITY;  // of the raw products; of the scores where biased
-  bool poly = true;
+  // ---- the row's largest score, from the extremes of the raw products (of the scores where
+  // biased)
+  float top = -INFINITY, low = INFINITY;
+  if (straight) {
+    float v[TN];
+    io.load_all(v);
+    if (biased) add_slope(v, row.slope2, scale_log2);
+    extremes(v, top, low);
+    if (biased) top = fmaf(row.slope2, static_cast<float>(rel), top);
+  } else {
 #pragma unroll 1
-  for (int h = 0; h < H; ++h) {
-    float v[32];
-    load(h, v);
-    float offset = 0.f;
-    if (biased) {
-      if (cap) cap_scores(v, s, false);
-      offset = bias_scores(v, row.slope2, base + 32 * h - row.pos, cap ? 1.f : scale_log2);
-    }
-    float mx[2] = {-INFINITY, -INFINITY}, mn[2] = {INFINITY, INFINITY};
-    if (full) {
-#pragma unroll
-      for (int c = 0; c < 32; c += 2) {
-        mx[(c >> 1) & 1] = max3(mx[(c >> 1) & 1], v[c], v[c + 1]);
-        mn[(c >> 1) & 1] = min3(mn[(c >> 1) & 1], v[c], v[c + 1]);
-      }
-    } else {
+    for (int h = 0; h < H; ++h) {
       const int l = lo - 32 * h, r = hi - 32 * h;
+      if (!__any_sync(0xffffffffu, some && r >= 0 && l < 32)) continue;
+      seen |= 1u << h;
+      float v[32];
+      io.load32(h, v);
+      float offset = 0.f;
+      if (biased) {
+        if (cap) cap_scores(v, s, false);
+        offset = bias_scores(v, row.slope2, rel + 32 * h, cap ? 1.f : scale_log2);
+      }
+      float mx[2] = {-INFINITY, -INFINITY}, mn[2] = {INFINITY, INFINITY};
 #pragma unroll
       for (int c = 0; c < 32; ++c) {
         const bool in = c >= l && c <= r;
         mx[c & 1] = fmaxf(mx[c & 1], in ? v[c] : -INFINITY);
         mn[c & 1] = fminf(mn[c & 1], in ? v[c] : INFINITY);
       }
+      top = max3(top, mx[0] + offset, mx[1] + offset);
+      low = min3(low, mn[0], mn[1]);
     }
-    top = max3(top, mx[0] + offset, mx[1] + offset);
-    low = min3(low, mn[0], mn[1]);
   }
+  bool poly = false;
   if (!biased) {
     // scores are monotonic in the raw products: growing with them for a positive scale
     const float ext = scale_log2 >= 0.f ? top : low;
@@ -192,53 +231,63 @@ __device__ __forceinline__ bool scored_weights(const ScoreArgs &s, float scale_l
     } else {
       top = some ? ext * scale_log2 : -INFINITY;
     }
-  } else {
-    poly = false;
   }
   const bool grow = top > row.m + kScoredSlack;
   if (__any_sync(0xffffffffu, grow)) {
     const float mnew = grow ? top : row.m;
     const float f = mnew == -INFINITY ? 1.f : prefill_exp2(row.m - mnew);
     row.l *= f;
-    if (later && !rescale(f)) return false;
+    if (later && !io.rescale(f)) return false;
     row.m = mnew;
   }
 
   // ---- the weights
   const float nm = row.m == -INFINITY ? 0.f : -row.m;
   float rp[4] = {0.f, 0.f, 0.f, 0.f};
+  if (straight) {
 #pragma unroll 1
-  for (int h = 0; h < H; ++h) {
-    float v[32], mult = scale_log2, offset = nm;
-    load(h, v);
-    if (cap) {
-      cap_scores(v, s, poly);
-      mult = 1.f;
+    for (int h = 0; h < TN / 64; ++h) {
+      float v[64], pk[32], mult = scale_log2, offset = nm;
+      io.load64(h, v);
+      if (cap) {
+        cap_scores(v, s, poly);
+        mult = 1.f;
+      }
+      if (biased) {
+        add_slope(v, row.slope2, mult);
+        offset = fmaf(row.slope2, static_cast<float>(rel + 64 * h), offset);
+        mult = 1.f;
+      }
+      weigh(v, mult, offset, pk, rp);
+      io.emit64(h, pk);
     }
-    if (biased) {
-      offset += bias_scores(v, row.slope2, base + 32 * h - row.pos, mult);
-      mult = 1.f;
-    }
-    if (!full) {
-      // the scale is never 0, so that the score of a masked column is -inf
-      const float none = mult >= 0.f ? -INFINITY : INFINITY;
-      const int l = lo - 32 * h, r = hi - 32 * h;
+  } else {
+#pragma unroll 1
+    for (int h = 0; h < H; ++h) {
+      float pk[16];
+      if (!(seen >> h & 1)) {
 #pragma unroll
-      for (int c = 0; c < 32; ++c) v[c] = c >= l && c <= r ? v[c] : none;
-    }
-    const float2 m2 = make_float2(mult, mult), n2 = make_float2(offset, offset);
-    float pk[16];
+        for (int e = 0; e < 16; ++e) pk[e] = 0.f;
+      } else {
+        float v[32], mult = scale_log2, offset = nm;
+        io.load32(h, v);
+        if (cap) {
+          cap_scores(v, s, poly);
+          mult = 1.f;
+        }
+        if (biased) {
+          offset += bias_scores(v, row.slope2, rel + 32 * h, mult);
+          mult = 1.f;
+        }
+        // the scale is never 0, so that the score of a masked column is -inf
+        const float none = mult >= 0.f ? -INFINITY : INFINITY;
+        const int l = lo - 32 * h, r = hi - 32 * h;
 #pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      const int c = 2 * e;
-      const float2 x = ffma2(make_float2(v[c], v[c + 1]), m2, n2);
-      const float2 w = make_float2(prefill_exp2(x.x), prefill_exp2(x.y));
-      const float2 acc = fadd2(make_float2(rp[c & 2], rp[(c & 2) + 1]), w);
-      rp[c & 2] = acc.x;
-      rp[(c & 2) + 1] = acc.y;
-      pk[e] = __uint_as_float(pack_half2(w.x, w.y));
+        for (int c = 0; c < 32; ++c) v[c] = c >= l && c <= r ? v[c] : none;
+        weigh(v, mult, offset, pk, rp);
+      }
+      io.emit32(h, pk);
     }
-    emit(h, pk);
   }
   row.l += (rp[0] + rp[1]) + (rp[2] + rp[3]);
   return true;
