@@ -121,70 +121,6 @@ __device__ __forceinline__ Item2 item2_of(const PrefillArgs &a, int kv, int b, i
   return it;
 }
 
-// Under a score rule (kScored) an item's keys go from kv_lo, the first token that some row of
-// the pair sees, to kv_len. Its key tiles are taken last to first, tile j (0 .. nt_max - 1) being
-// the one j before the last: a bias by distance and most attention favour near keys, so a row
-// meets its largest scores first and rarely moves its maximum again (first to last, a steep
-// bias moved it, and rescaled O, on every tile: 7250 cycles a tile against 3600). Query tile X
-// takes part in tiles [from_X, to_X); the pair's other tile may see keys on either side of that.
-// Both spans are non-empty for a tile that has rows, overlap or touch, and cover all tiles.
-// Warp-collective.
-struct ScoredItem2 : Item2 {
-  int kv_lo, prefix, last_tile;  // last_tile: index of the key tile taken first
-  int from_a, to_a, from_b, to_b;
-};
-
-template <int TN>
-__device__ __forceinline__ ScoredItem2 scored_item2_of(const PrefillScoredArgs &a, int kv, int b,
-                                                       int pair) {
-  ScoredItem2 it;
-  it.kv = kv;
-  it.b = b;
-  it.live = 0;
-  it.stop = 0;
-  it.nt_a = it.nt_b = it.nt_max = 0;
-  const int q0 = __ldg(a.qs + b), q1 = __ldg(a.qs + b + 1), ctx = __ldg(a.ctx + b);
-  const int n = q1 - q0;
-  it.q0 = q0;
-  it.n = n;
-  it.ctx = ctx;
-  unsigned bad = 0;
-  if (ctx < 0 || static_cast<long long>(ctx) > static_cast<long long>(a.maxp) << a.ps_shift)
-    bad = PA_DEVERR_CONTEXT;
-  else if (q0 < 0 || n < 0 || static_cast<long long>(q1) > a.total || n > ctx)
-    bad = PA_DEVERR_QUERY_START;
-  if (bad) {
-    if ((threadIdx.x & 31) == 0) atomicOr(a.err, bad);
-    return it;
-  }
-  it.tok0_a = 2 * pair * a.qt;
-  it.tok0_b = it.tok0_a + a.qt;
-  if (it.tok0_a >= n) return it;
-  it.prefix = prefix_of(a.s, b, ctx);
-  int lo_a, lo_b;
-  seen_range(a.s, q0, ctx - n, it.tok0_a, min(it.tok0_b, n), it.prefix, lo_a, it.max_pos_a);
-  it.max_pos_b = it.max_pos_a;
-  it.kv_lo = lo_b = lo_a;
-  const bool b_rows = it.tok0_b < n;
-  if (b_rows) {
-    seen_range(a.s, q0, ctx - n, it.tok0_b, min(it.tok0_b + a.qt, n), it.prefix, lo_b, it.max_pos_b);
-    it.kv_lo = min(lo_a, lo_b);
-  }
-  // tile B's rows come after tile A's, so they see at least as far: max_pos_b >= max_pos_a, by
-  // less than a query tile's tokens (<= TN), so that from_a <= 1 <= to_b
-  it.last_tile = it.max_pos_b / TN;
-  it.from_a = it.last_tile - it.max_pos_a / TN;
-  it.from_b = 0;
-  it.to_a = it.last_tile - lo_a / TN + 1;
-  it.to_b = b_rows ? it.last_tile - lo_b / TN + 1 : 0;
-  it.nt_a = it.to_a - it.from_a;
-  it.nt_b = it.to_b;
-  it.nt_max = max(it.to_a, it.to_b);
-  it.kv_len = it.max_pos_b + 1;
-  it.live = 1;
-  return it;
-}
-
 // P = exp2(s * sl2 + nm) over a row of TN scores, written as fp16 pairs over the first TN / 2
 // TMEM columns at ts, with the row's partial sums in rp. With kMasked keys past lim give
 // exactly 0; without, packed fp32 pairs do two exponent arguments per FFMA2 and two sum terms
@@ -221,43 +157,16 @@ __device__ __forceinline__ void exps_row(const float (&v)[TN], float sl2, float 
   }
 }
 
-// A thread's row of a tile, for scored_weights: scores at TMEM address ts, accumulated output
-// at to.
 template <int HD>
-struct ScoredTile2 {
-  uint32_t ts, to;
-  __device__ __forceinline__ void load_all(float (&c)[128]) const { tmem_ld128(ts, c); }
-  __device__ __forceinline__ void load64(int h, float (&c)[64]) const { tmem_ld64(ts + h * 64, c); }
-  __device__ __forceinline__ void load32(int h, float (&c)[32]) const { tmem_ld32(ts + h * 32, c); }
-  // P as fp16 pairs over the first 64 columns of S, behind the columns being read
-  __device__ __forceinline__ void emit64(int h, const float (&pk)[32]) const { tmem_st32(ts + h * 32, pk); }
-  __device__ __forceinline__ void emit32(int h, const float (&pk)[16]) const { tmem_st16(ts + h * 16, pk); }
-  __device__ __forceinline__ bool rescale(float f) const {
-    // S_X(j) completed, so PV_X(j - 1) has too: O_X is stable until P_X(j) is released
-#pragma unroll
-    for (int c = 0; c < HD / 32; ++c) {
-      float o[32];
-      tmem_ld32(to + c * 32, o);
-#pragma unroll
-      for (int e = 0; e < 32; ++e) o[e] *= f;
-      tmem_st32(to + c * 32, o);
-    }
-    return true;
-  }
-};
-
-// kScored: under a score rule (scored_softmax.cuh), with fp16 output.
-template <int HD, bool kScored>
 __global__ void __launch_bounds__(kPrefill2Threads, 1)
-    prefill2_kernel(const __grid_constant__ PrefillArgsOf<kScored> a,
-                    const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
+    prefill2_kernel(const __grid_constant__ PrefillArgs a, const __grid_constant__ CUtensorMap tq,
+                    const __grid_constant__ CUtensorMap tk,
                     const __grid_constant__ CUtensorMap tv) {
   using C = Prefill2Cfg<HD>;
-  using Item = std::conditional_t<kScored, ScoredItem2, Item2>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t bars[kNumBars2];
   __shared__ __align__(16) uint4 clc_answer;
-  __shared__ Item items[2];
+  __shared__ Item2 items[2];
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_word;
   __shared__ int drain_last[2];
@@ -302,28 +211,8 @@ __global__ void __launch_bounds__(kPrefill2Threads, 1)
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
 
-  // first token of tile j of an item, and the tiles [from, to) that query tile x takes part in
-  auto tile_token = [](const Item &it, int j) {
-    if constexpr (kScored)
-      return (it.last_tile - j) * C::TN;
-    else
-      return j * C::TN;
-  };
-  auto from_of = [](const Item &it, int x) {
-    if constexpr (kScored)
-      return x ? it.from_b : it.from_a;
-    else
-      return 0;
-  };
-  auto to_of = [](const Item &it, int x) {
-    if constexpr (kScored)
-      return x ? it.to_b : it.to_a;
-    else
-      return x ? it.nt_b : it.nt_a;
-  };
-
   // Reader side of the item ring: item k sits in entry k & 1. Returns false on abort.
-  auto take_item = [&](int k, Item &it) {
+  auto take_item = [&](int k, Item2 &it) {
     if (!pipe_wait(bar(kB2ItemFull + (k & 1)), (k >> 1) & 1, abort_flag, a.err)) return false;
     it = items[k & 1];
     __syncwarp();
@@ -343,16 +232,7 @@ __global__ void __launch_bounds__(kPrefill2Threads, 1)
       // publish item k once every reader has taken item k - 2 from the same entry
       if (k >= 2 && !pipe_wait(bar(kB2ItemEmpty + (k & 1)), ((k >> 1) - 1) & 1, abort_flag, a.err))
         break;
-      if constexpr (kScored) {
-        Item it;
-        it.stop = 1;
-        it.live = 0;
-        if (!stop) it = scored_item2_of<C::TN>(a, kv, b, a.n_qtiles - 1 - z);
-        if (lane == 0) {
-          items[k & 1] = it;
-          mbar_arrive(bar(kB2ItemFull + (k & 1)));
-        }
-      } else if (lane == 0) {
+      if (lane == 0) {
         Item2 it;
         if (stop) {
           it.stop = 1;
@@ -406,7 +286,7 @@ __global__ void __launch_bounds__(kPrefill2Threads, 1)
     int q_loads = 0;
     bool ok = true;
     for (int k = 0; ok; ++k) {
-      Item it;
+      Item2 it;
       ok = take_item(k, it);
       if (!ok || it.stop) break;
       if (!is_v && lane == 0) mbar_arrive(bar(kB2ProdStart));
@@ -427,25 +307,20 @@ __global__ void __launch_bounds__(kPrefill2Threads, 1)
         ++q_loads;
       }
       const int32_t *bt_row = a.bt + static_cast<size_t>(it.b) * a.maxp;
-      // whether this lane's box, at token tok, holds a token that some row sees
-      auto needed = [&](int tok) {
-        if constexpr (kScored)
-          return lane < boxes && tok < it.kv_len && tok + rows_per_box > it.kv_lo;
-        else
-          return lane < boxes && tok < it.kv_len;
-      };
       auto page_of = [&](int j) {
-        const int tok = tile_token(it, j) + lane * rows_per_box;
-        return (j < it.nt_max && needed(tok)) ? __ldg(bt_row + (tok >> a.ps_shift)) : -1;
+        const int tok = j * C::TN + lane * rows_per_box;
+        return (j < it.nt_max && lane < boxes && tok < it.kv_len)
+                   ? __ldg(bt_row + (tok >> a.ps_shift))
+                   : -1;
       };
       int page_next = page_of(0);
       for (int j = 0; j < it.nt_max && ok; ++j) {
         const int item = 2 * (gt + j) + (is_v ? 1 : 0);
         const int s = item % C::kSlots;
-        const int tok = tile_token(it, j) + lane * rows_per_box;
+        const int tok = j * C::TN + lane * rows_per_box;
         int page = page_next;
         page_next = page_of(j + 1);
-        if (needed(tok) && (page < 0 || page >= a.num_pages)) {
+        if (lane < boxes && tok < it.kv_len && (page < 0 || page >= a.num_pages)) {
           if (!is_v) atomicOr(a.err, PA_DEVERR_PAGE_ID);
           page = -1;
         }
@@ -507,12 +382,12 @@ __global__ void __launch_bounds__(kPrefill2Threads, 1)
     int gt = 0;
     uint32_t phase = 0;  // parities of the next waits: bit 0 QFull, bit 1 + x PFull[x]
     for (int k = 0; ok; ++k) {
-      Item it;
+      Item2 it;
       ok = take_item(k, it);
       if (!ok || it.stop) break;
       if (!it.live) continue;
-      const int from[2] = {from_of(it, 0), from_of(it, 1)}, to[2] = {to_of(it, 0), to_of(it, 1)};
-      const int last_s_x = to[1] == it.nt_max ? 1 : 0;  // tile of the item's last score MMA
+      auto nt_of = [&](int x) { return x ? it.nt_b : it.nt_a; };
+      const int last_s_x = it.nt_b == it.nt_max ? 1 : 0;  // tile of the item's last score MMA
       // MMAs and commits are issued warp-collectively (one elected lane), with operands every
       // lane computes identically
       // Descriptors of a K step are the tile's base descriptor plus the step's byte offset / 16
@@ -538,17 +413,17 @@ __global__ void __launch_bounds__(kPrefill2Threads, 1)
         for (int ks = 0; ks < C::TN / 16; ++ks) {
           const uint64_t bd = vd + ((ks * 2048) >> 4);
           mma_f16_ts_warp(tmem + 256u + 128u * x, tmem + 128u * x + ks * 8, bd, C::kIdescPV,
-                          (j > from[x] || ks > 0) ? 1u : 0u);
+                          (j > 0 || ks > 0) ? 1u : 0u);
         }
-        if (j == to[x] - 1) mma_commit_warp(bar(kB2ODone + x));
+        if (j == nt_of(x) - 1) mma_commit_warp(bar(kB2ODone + x));
       };
       auto release = [&](int item) { mma_commit_warp(bar(kB2Empty + item % C::kSlots)); };
       auto clear_v_tail = [&](int j) {
         // V rows past the last needed token hold unread cache slots (possibly never
         // written): P is zero there, but 0 * NaN is not, so clear them before the first P.V
         // of that tile.
-        const int rows_last = it.kv_len - tile_token(it, j);
-        if (j != (kScored ? 0 : it.nt_max - 1) || rows_last >= C::TN) return;
+        const int rows_last = it.kv_len - j * C::TN;
+        if (j != it.nt_max - 1 || rows_last >= C::TN) return;
         const int per_block = (C::TN - rows_last) * 8;
         uint8_t *vg = sgen + C::kRingOff + ((2 * (gt + j) + 1) % C::kSlots) * C::kSlotBytes;
         for (int c = lane; c < C::KB * per_block; c += 32) {
@@ -559,21 +434,6 @@ __global__ void __launch_bounds__(kPrefill2Threads, 1)
         fence_proxy_async();
         __syncwarp();
       };
-      auto clear_v_head = [&](int j) {
-        // likewise the rows before the first token that some row sees
-        if constexpr (kScored) {
-          const int rows_first = it.kv_lo - tile_token(it, j);
-          if (j != it.nt_max - 1 || rows_first <= 0) return;
-          const int per_block = rows_first * 8;
-          uint8_t *vg = sgen + C::kRingOff + ((2 * (gt + j) + 1) % C::kSlots) * C::kSlotBytes;
-          for (int c = lane; c < C::KB * per_block; c += 32) {
-            const int kb = c / per_block, r = c % per_block;
-            *reinterpret_cast<uint4 *>(vg + kb * (C::TN * 128) + r * 16) = make_uint4(0, 0, 0, 0);
-          }
-          fence_proxy_async();
-          __syncwarp();
-        }
-      };
       ok = pipe_wait(bar(kB2QFull), phase & 1u, abort_flag, a.err);
       phase ^= 1u;
       tc_fence_after();
@@ -581,41 +441,26 @@ __global__ void __launch_bounds__(kPrefill2Threads, 1)
       if (ok) {
         // S_X(0) overwrites the columns from which the previous item's last P.V read P_X:
         // that MMA was issued earlier by this thread and so runs first
-        if (from[0] == 0) issue_s(0, 0);
-        if (to[1] > 0) issue_s(1, 0);
+        issue_s(0, 0);
+        if (it.nt_b > 0) issue_s(1, 0);
         release(2 * gt);
       }
       for (int j = 0; j < it.nt_max && ok; ++j) {
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          if constexpr (kScored) {
-            if (x == 0 && ok && j + 1 == from[0]) {
-              // tile A joins at the next key tile: its first scores, whose keys no softmax has
-              // confirmed (tile B takes part in that tile too, or this is its last user)
-              ok = wait_item(2 * (gt + j + 1));
-              if (ok) {
-                issue_s(0, j + 1);
-                if (j + 1 >= to[1]) release(2 * (gt + j + 1));
-              }
-            }
-            if (j < from[x]) continue;
-          }
-          if (!ok || j >= to[x]) continue;
+          if (!ok || j >= nt_of(x)) continue;
           // P_X(j) is released only after V(j) and K(j + 1) have landed (see the softmax)
           ok = pipe_wait(bar(kB2PFull + x), (phase >> (1 + x)) & 1u, abort_flag, a.err);
           if (!ok) break;
           phase ^= 2u << x;
           tc_fence_after();
-          if (x == 0 || j >= to[0] || j < from[0]) {
-            clear_v_head(j);
-            clear_v_tail(j);
-          }
+          if (x == 0 || j >= it.nt_a) clear_v_tail(j);
           issue_pv(x, j);
-          const bool last_v_user = (x == 1) || (j >= to[1]);
+          const bool last_v_user = (x == 1) || (j >= it.nt_b);
           if (last_v_user) release(2 * (gt + j) + 1);
-          if (j + 1 < to[x]) {
+          if (j + 1 < nt_of(x)) {
             issue_s(x, j + 1);
-            const bool last_k_user = (x == 1) || (j + 1 >= to[1]);
+            const bool last_k_user = (x == 1) || (j + 1 >= it.nt_b);
             if (last_k_user) release(2 * (gt + j + 1));
           }
         }
@@ -640,34 +485,24 @@ __global__ void __launch_bounds__(kPrefill2Threads, 1)
     uint32_t phase = 0;  // parities of the next waits: bit 0 SFull[x], bit 1 ODone[x]
     bool ok = true;
     for (int k = 0; ok; ++k) {
-      int my_from, my_nt, pos, gt0, out_row0, out_head0;
-      int tile0 = 0;  // first token of the key tile taken first
-      ScoredRow sr = {};
+      int my_nt, pos, gt0, out_row0, out_head0;
       bool valid;
       {
-        Item it;
+        Item2 it;
         ok = take_item(k, it);
         if (!ok || it.stop) break;
         if (!it.live) continue;
         const int my_tok0 = x ? it.tok0_b : it.tok0_a;
-        my_from = from_of(it, x);
-        my_nt = to_of(it, x);
+        my_nt = x ? it.nt_b : it.nt_a;
         valid = row < q_rows && my_tok0 + t < it.n;
         pos = min(it.ctx - it.n + my_tok0 + t, x ? it.max_pos_b : it.max_pos_a);
-        if constexpr (kScored) {
-          // rows past the tile's last token repeat it (and are not stored)
-          tile0 = it.last_tile * C::TN;
-          if (my_nt > 0)
-            sr = scored_row(a.s, it.q0, it.ctx - it.n, min(my_tok0 + min(t, a.qt - 1), it.n - 1),
-                            it.kv * a.g + h, it.prefix);
-        }
         out_row0 = it.q0 + my_tok0;  // output row of the tile's first token
         out_head0 = it.kv * a.g;
         gt0 = gt;
         gt += it.nt_max;
       }
       float m = -INFINITY, l = 0.f;
-      for (int j = my_from; j < my_nt; ++j) {
+      for (int j = 0; j < my_nt; ++j) {
         ok = pipe_wait(bar(kB2SFull + x), phase & 1u, abort_flag, a.err);
         if (!ok) break;
         phase ^= 1u;
@@ -686,93 +521,88 @@ __global__ void __launch_bounds__(kPrefill2Threads, 1)
           kv_ready = rv && rk;
         }
         float v[C::TN];
-        if constexpr (!kScored) tmem_ld128(ts, v);
+        tmem_ld128(ts, v);
         if (rg == 0 && !__all_sync(0xffffffffu, kv_ready)) {
           ok = pipe_wait(bar(kB2Full + iv % C::kSlots), (iv / C::kSlots) & 1, abort_flag, a.err);
           if (ok && j + 1 < my_nt)
             ok = pipe_wait(bar(kB2Full + ik % C::kSlots), (ik / C::kSlots) & 1, abort_flag, a.err);
           if (!ok) break;
         }
-        if constexpr (kScored) {
-          const ScoredTile2<HD> io = {ts, to};
-          scored_weights<C::TN>(a.s, sl2, sr, tile0 - j * C::TN, j > my_from, io);
-        } else {
-          const int lim = pos - j * C::TN;
-          // warp-uniform: the exponent passes hold tcgen05.st, which the whole warp executes
-          const bool full = __all_sync(0xffffffffu, lim >= C::TN - 1);
-          float rp[8];
-          // After a row's first tile its running maximum m seldom grows by more than the slack,
-          // so a tile first takes its exponents with m as it stands and no maximum pass: the
-          // terms are non-negative (masked keys give 0), so the tile's row sum bounds each of
-          // them, and a sum of at most 2^slack shows that no score passed m + slack. Only a warp
-          // in which some row's sum is larger (or not a number) takes the tile again in the
-          // plain order: maximum, rescale, exponents.
-          bool redo = true;
-          if (j > 0) {
-            if (full)
-              exps_row<C::TN, false>(v, sl2, -m, lim, ts, rp);
-            else
-              exps_row<C::TN, true>(v, sl2, -m, lim, ts, rp);
-            const float tsum =
-                ((rp[0] + rp[1]) + (rp[2] + rp[3])) + ((rp[4] + rp[5]) + (rp[6] + rp[7]));
-            redo = __any_sync(0xffffffffu, !(tsum <= kPrefillSlackBound));
-            if (redo) tmem_wait_st();  // the plain pass below rewrites the same columns
-          }
-          if (redo) {
-            // keys past this row's position are masked out (on tiles that reach the diagonal);
-            // the row maximum of the scaled scores is the extreme raw score times the scale (the
-            // maximum for a non-negative scale, else the minimum), which saves a multiply per score
-            float mp[8];
+        const int lim = pos - j * C::TN;
+        // warp-uniform: the exponent passes hold tcgen05.st, which the whole warp executes
+        const bool full = __all_sync(0xffffffffu, lim >= C::TN - 1);
+        float rp[8];
+        // After a row's first tile its running maximum m seldom grows by more than the slack,
+        // so a tile first takes its exponents with m as it stands and no maximum pass: the
+        // terms are non-negative (masked keys give 0), so the tile's row sum bounds each of
+        // them, and a sum of at most 2^slack shows that no score passed m + slack. Only a warp
+        // in which some row's sum is larger (or not a number) takes the tile again in the
+        // plain order: maximum, rescale, exponents.
+        bool redo = true;
+        if (j > 0) {
+          if (full)
+            exps_row<C::TN, false>(v, sl2, -m, lim, ts, rp);
+          else
+            exps_row<C::TN, true>(v, sl2, -m, lim, ts, rp);
+          const float tsum =
+              ((rp[0] + rp[1]) + (rp[2] + rp[3])) + ((rp[4] + rp[5]) + (rp[6] + rp[7]));
+          redo = __any_sync(0xffffffffu, !(tsum <= kPrefillSlackBound));
+          if (redo) tmem_wait_st();  // the plain pass below rewrites the same columns
+        }
+        if (redo) {
+          // keys past this row's position are masked out (on tiles that reach the diagonal);
+          // the row maximum of the scaled scores is the extreme raw score times the scale (the
+          // maximum for a non-negative scale, else the minimum), which saves a multiply per score
+          float mp[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) mp[e] = -INFINITY;
-            float ext;
-            if (sl2 >= 0.f) {
-              if (full) {
+          for (int e = 0; e < 8; ++e) mp[e] = -INFINITY;
+          float ext;
+          if (sl2 >= 0.f) {
+            if (full) {
 #pragma unroll
-                for (int c = 0; c < C::TN; ++c) mp[c & 7] = fmaxf(mp[c & 7], v[c]);
-              } else {
-#pragma unroll
-                for (int c = 0; c < C::TN; ++c) mp[c & 7] = fmaxf(mp[c & 7], c <= lim ? v[c] : -INFINITY);
-              }
-              ext = fmaxf(fmaxf(fmaxf(mp[0], mp[1]), fmaxf(mp[2], mp[3])),
-                          fmaxf(fmaxf(mp[4], mp[5]), fmaxf(mp[6], mp[7])));
+              for (int c = 0; c < C::TN; ++c) mp[c & 7] = fmaxf(mp[c & 7], v[c]);
             } else {
 #pragma unroll
-              for (int e = 0; e < 8; ++e) mp[e] = INFINITY;
-#pragma unroll
-              for (int c = 0; c < C::TN; ++c) mp[c & 7] = fminf(mp[c & 7], (full || c <= lim) ? v[c] : INFINITY);
-              ext = fminf(fminf(fminf(mp[0], mp[1]), fminf(mp[2], mp[3])),
-                          fminf(fminf(mp[4], mp[5]), fminf(mp[6], mp[7])));
+              for (int c = 0; c < C::TN; ++c) mp[c & 7] = fmaxf(mp[c & 7], c <= lim ? v[c] : -INFINITY);
             }
-            const float mx = ext * sl2;
-            const bool grow = mx > m + kPrefillRescaleSlack;
-            if (__any_sync(0xffffffffu, grow)) {
-              const float mnew = grow ? mx : m;
-              const float f = mnew == -INFINITY ? 1.f : prefill_exp2(m - mnew);
-              l *= f;
-              if (j > 0) {
-                // S_X(j) completed, so PV_X(j - 1) has too: O_X is stable until P_X(j) is released
+            ext = fmaxf(fmaxf(fmaxf(mp[0], mp[1]), fmaxf(mp[2], mp[3])),
+                        fmaxf(fmaxf(mp[4], mp[5]), fmaxf(mp[6], mp[7])));
+          } else {
 #pragma unroll
-                for (int c = 0; c < HD / 32; ++c) {
-                  float o[32];
-                  tmem_ld32(to + c * 32, o);
+            for (int e = 0; e < 8; ++e) mp[e] = INFINITY;
 #pragma unroll
-                  for (int e = 0; e < 32; ++e) o[e] *= f;
-                  tmem_st32(to + c * 32, o);
-                }
-              }
-              m = mnew;
-            }
-            // P = exp2(s * scale * log2e - m) as fp16 pairs over the first 64 columns of S (the
-            // scale is folded into one FFMA per score; masked keys give exactly 0)
-            const float nm = -m;
-            if (full)
-              exps_row<C::TN, false>(v, sl2, nm, lim, ts, rp);
-            else
-              exps_row<C::TN, true>(v, sl2, nm, lim, ts, rp);
+            for (int c = 0; c < C::TN; ++c) mp[c & 7] = fminf(mp[c & 7], (full || c <= lim) ? v[c] : INFINITY);
+            ext = fminf(fminf(fminf(mp[0], mp[1]), fminf(mp[2], mp[3])),
+                        fminf(fminf(mp[4], mp[5]), fminf(mp[6], mp[7])));
           }
-          l += ((rp[0] + rp[1]) + (rp[2] + rp[3])) + ((rp[4] + rp[5]) + (rp[6] + rp[7]));
+          const float mx = ext * sl2;
+          const bool grow = mx > m + kPrefillRescaleSlack;
+          if (__any_sync(0xffffffffu, grow)) {
+            const float mnew = grow ? mx : m;
+            const float f = mnew == -INFINITY ? 1.f : prefill_exp2(m - mnew);
+            l *= f;
+            if (j > 0) {
+              // S_X(j) completed, so PV_X(j - 1) has too: O_X is stable until P_X(j) is released
+#pragma unroll
+              for (int c = 0; c < HD / 32; ++c) {
+                float o[32];
+                tmem_ld32(to + c * 32, o);
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] *= f;
+                tmem_st32(to + c * 32, o);
+              }
+            }
+            m = mnew;
+          }
+          // P = exp2(s * scale * log2e - m) as fp16 pairs over the first 64 columns of S (the
+          // scale is folded into one FFMA per score; masked keys give exactly 0)
+          const float nm = -m;
+          if (full)
+            exps_row<C::TN, false>(v, sl2, nm, lim, ts, rp);
+          else
+            exps_row<C::TN, true>(v, sl2, nm, lim, ts, rp);
         }
+        l += ((rp[0] + rp[1]) + (rp[2] + rp[3])) + ((rp[4] + rp[5]) + (rp[6] + rp[7]));
         tmem_wait_st();
         tc_fence_before();
         mbar_arrive(bar(kB2PFull + x));
@@ -783,7 +613,6 @@ __global__ void __launch_bounds__(kPrefill2Threads, 1)
       }
       if (ok && my_nt > 0) {
         tc_fence_after();
-        if constexpr (kScored) l = sr.l;
         const float inv = l > 0.f ? 1.f / l : 0.f;
         // Each thread writes its row straight from TMEM, 32 columns at a time: 32-byte stores
         // fill whole sectors, so L2 never reads a partly written sector from DRAM first, and
@@ -799,26 +628,19 @@ __global__ void __launch_bounds__(kPrefill2Threads, 1)
         for (int c = 0; c < HD / 32; ++c) {
           float o[32];
           tmem_ld32(to + c * 32, o);
-          if constexpr (kScored) {
-            if (valid)
-              store_half32(a.out16 + (static_cast<size_t>(out_row0 + t) * a.qh + out_head0 + h) * HD +
-                               c * 32,
-                           o, inv, a.out_v8, pol);
-          } else {
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] *= inv;
-            if (valid) {
-              if (a.out_v8) {
+          for (int e = 0; e < 32; ++e) o[e] *= inv;
+          if (valid) {
+            if (a.out_v8) {
 #pragma unroll
-                for (int e = 0; e < 32; e += 8)
-                  st_global_v8(dst + c * 32 + e, o[e], o[e + 1], o[e + 2], o[e + 3], o[e + 4],
-                               o[e + 5], o[e + 6], o[e + 7], pol);
-              } else {
+              for (int e = 0; e < 32; e += 8)
+                st_global_v8(dst + c * 32 + e, o[e], o[e + 1], o[e + 2], o[e + 3], o[e + 4],
+                             o[e + 5], o[e + 6], o[e + 7], pol);
+            } else {
 #pragma unroll
-                for (int e = 0; e < 32; e += 4)
-                  *reinterpret_cast<float4 *>(dst + c * 32 + e) =
-                      make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
-              }
+              for (int e = 0; e < 32; e += 4)
+                *reinterpret_cast<float4 *>(dst + c * 32 + e) =
+                    make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
             }
           }
         }

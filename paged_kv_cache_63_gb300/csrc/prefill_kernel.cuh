@@ -132,7 +132,7 @@ __device__ __forceinline__ Item1 item1_of(const PrefillArgs &a, int kv, int b, i
 }
 
 // Under a score rule (kScored) an item's keys go from kv_lo, the first token that some row
-// sees, to kv_len, and its key tiles are taken last to first (as in prefill2_kernel.cuh): tile j
+// sees, to kv_len, and its key tiles are taken last to first (as in prefill2_scored_kernel.cuh): tile j
 // is the one j before last_tile. Warp-collective.
 struct ScoredItem1 : Item1 {
   int kv_lo, prefix, last_tile;
@@ -181,19 +181,14 @@ struct ScoredTile1 {
   uint32_t pv_bar, pv_parity;
   volatile int *abort_flag;
   unsigned *err;
-  __device__ __forceinline__ void load_all(float (&c)[64]) const { tmem_ld64(ts, c); }
-  __device__ __forceinline__ void load64(int, float (&c)[64]) const { tmem_ld64(ts, c); }
-  __device__ __forceinline__ void load32(int h, float (&c)[32]) const { tmem_ld32(ts + h * 32, c); }
-  template <int N>
-  __device__ __forceinline__ void put(int chunk, const float (&pk)[N]) const {
+  __device__ __forceinline__ void load(float (&c)[64]) const { tmem_ld64(ts, c); }
+  __device__ __forceinline__ void emit(const float (&pk)[32]) const {
 #pragma unroll
-    for (int e = 0; e < N; e += 4)
-      sts128(prow + (((chunk + (e >> 2)) ^ xor7) << 4),
+    for (int e = 0; e < 32; e += 4)
+      sts128(prow + (((e >> 2) ^ xor7) << 4),
              make_uint4(__float_as_uint(pk[e]), __float_as_uint(pk[e + 1]),
                         __float_as_uint(pk[e + 2]), __float_as_uint(pk[e + 3])));
   }
-  __device__ __forceinline__ void emit64(int, const float (&pk)[32]) const { put(0, pk); }
-  __device__ __forceinline__ void emit32(int h, const float (&pk)[16]) const { put(4 * h, pk); }
   __device__ __forceinline__ bool rescale(float f) const {
     // O holds tiles < j: wait for the last P.V, then scale this row of O in TMEM
     if (!pipe_wait(pv_bar, pv_parity, abort_flag, err)) return false;
@@ -558,7 +553,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
           const ScoredTile1<HD> io = {trow + st * C::TN, trow + C::kOCol, p_buf(st) + row * 128,
                   static_cast<uint32_t>(row & 7), bar(kBarPV + ((gj - 1) & 1)),
                   static_cast<uint32_t>(((gj - 1) >> 1) & 1), abort_flag, a.err};
-          ok = scored_weights<C::TN>(a.s, sl2, sr, tile_token(it, j), j > 0, io);
+          ok = scored_weights(a.s, sl2, sr, tile_token(it, j), j > 0, io);
           if (!ok) break;
         } else {
           float x[C::TN];

@@ -6,7 +6,7 @@
 
 #include "internal.h"
 #include "pagedattn.h"
-#include "prefill2_kernel.cuh"
+#include "prefill2_scored_kernel.cuh"
 #include "prefill_kernel.cuh"
 
 namespace pa {
@@ -47,7 +47,11 @@ cudaError_t launch_prefill2_hd(const PrefillArgsOf<kScored> &a, const PrefillLau
                                cudaStream_t stream) {
   static std::atomic<bool> set[kMaxDevicesPrefill];
   constexpr int smem = Prefill2Cfg<HD>::kSmem + 1024;
-  auto kern = prefill2_kernel<HD, kScored>;
+  void (*kern)(PrefillArgsOf<kScored>, CUtensorMap, CUtensorMap, CUtensorMap);
+  if constexpr (kScored)
+    kern = prefill2_scored_kernel<HD>;
+  else
+    kern = prefill2_kernel<HD>;
   const cudaError_t e = allow_smem(kern, smem, set);
   if (e != cudaSuccess) return e;
   kern<<<l.grid, kPrefill2Threads, smem, stream>>>(a, l.tq, l.tk, l.tv);

@@ -80,15 +80,14 @@ __device__ __forceinline__ float cap_exact(const ScoreArgs &s, float v) {
 }
 
 // v = cap_out * tanh(v * cap_in), by the polynomial where `poly` (warp-uniform) says so.
-template <int N>
-__device__ __forceinline__ void cap_scores(float (&v)[N], const ScoreArgs &s, bool poly) {
+__device__ __forceinline__ void cap_scores(float (&v)[64], const ScoreArgs &s, bool poly) {
   if (__builtin_expect(poly, 1)) {
     const float2 c0 = make_float2(s.cap_poly[0], s.cap_poly[0]),
                  c1 = make_float2(s.cap_poly[1], s.cap_poly[1]),
                  c2 = make_float2(s.cap_poly[2], s.cap_poly[2]),
                  c3 = make_float2(s.cap_poly[3], s.cap_poly[3]);
 #pragma unroll
-    for (int c = 0; c < N; c += 2) {
+    for (int c = 0; c < 64; c += 2) {
       const float2 x = make_float2(v[c], v[c + 1]);
       const float2 z = fmul2(x, x);
       float2 p = ffma2(c3, z, c2);
@@ -100,18 +99,17 @@ __device__ __forceinline__ void cap_scores(float (&v)[N], const ScoreArgs &s, bo
     }
   } else {
 #pragma unroll
-    for (int c = 0; c < N; ++c) v[c] = cap_exact(s, v[c]);
+    for (int c = 0; c < 64; ++c) v[c] = cap_exact(s, v[c]);
   }
 }
 
 // v = v * mult + slope2 * column, by steps of two columns, each off by a rounding (a table of
 // columns for the packed pairs would take a register each).
-template <int N>
-__device__ __forceinline__ void add_slope(float (&v)[N], float slope2, float mult) {
+__device__ __forceinline__ void add_slope(float (&v)[64], float slope2, float mult) {
   const float2 m2 = make_float2(mult, mult), step = make_float2(2.f * slope2, 2.f * slope2);
   float2 bias = make_float2(0.f, slope2);
 #pragma unroll
-  for (int c = 0; c < N; c += 2) {
+  for (int c = 0; c < 64; c += 2) {
     const float2 x = ffma2(make_float2(v[c], v[c + 1]), m2, bias);
     v[c] = x.x;
     v[c + 1] = x.y;
@@ -119,27 +117,11 @@ __device__ __forceinline__ void add_slope(float (&v)[N], float slope2, float mul
   }
 }
 
-// v * mult - slope2 * distance for 32 columns of which the first is `rel` past the query; the
-// part of the bias that the columns share is returned instead of added. Warp-collective.
-__device__ __forceinline__ float bias_scores(float (&v)[32], float slope2, int rel, float mult) {
-  if (__all_sync(0xffffffffu, rel + 31 <= 0)) {
-    add_slope(v, slope2, mult);
-    return slope2 * static_cast<float>(rel);
-  }
-  // keys on both sides of the query: the distance of each
-  const float first = static_cast<float>(rel);
+// Extremes of 64 columns.
+__device__ __forceinline__ void extremes(const float (&v)[64], float &hi, float &lo) {
+  float mx[4] = {v[0], v[0], v[0], v[0]}, mn[4] = {v[0], v[0], v[0], v[0]};
 #pragma unroll
-  for (int c = 0; c < 32; ++c)
-    v[c] = fmaf(-slope2, fabsf(first + static_cast<float>(c)), v[c] * mult);
-  return 0.f;
-}
-
-// Extremes of N columns, joined into hi and lo.
-template <int N>
-__device__ __forceinline__ void extremes(const float (&v)[N], float &hi, float &lo) {
-  float mx[4] = {hi, v[0], v[0], v[0]}, mn[4] = {lo, v[0], v[0], v[0]};
-#pragma unroll
-  for (int c = 0; c < N; c += 2) {
+  for (int c = 0; c < 64; c += 2) {
     mx[(c >> 1) & 3] = max3(mx[(c >> 1) & 3], v[c], v[c + 1]);
     mn[(c >> 1) & 3] = min3(mn[(c >> 1) & 3], v[c], v[c + 1]);
   }
@@ -147,90 +129,63 @@ __device__ __forceinline__ void extremes(const float (&v)[N], float &hi, float &
   lo = min3(fminf(mn[0], mn[1]), mn[2], mn[3]);
 }
 
-// Weights 2^(v * mult + nm) of N columns, packed into pk and added to rp.
-template <int N>
-__device__ __forceinline__ void weigh(const float (&v)[N], float mult, float nm,
-                                      float (&pk)[N / 2], float (&rp)[4]) {
-  const float2 m2 = make_float2(mult, mult), n2 = make_float2(nm, nm);
-#pragma unroll
-  for (int e = 0; e < N / 2; ++e) {
-    const int c = 2 * e;
-    const float2 x = ffma2(make_float2(v[c], v[c + 1]), m2, n2);
-    const float2 w = make_float2(prefill_exp2(x.x), prefill_exp2(x.y));
-    const float2 acc = fadd2(make_float2(rp[c & 2], rp[(c & 2) + 1]), w);
-    rp[c & 2] = acc.x;
-    rp[(c & 2) + 1] = acc.y;
-    pk[e] = __uint_as_float(pack_half2(w.x, w.y));
-  }
-}
-
-// One tile of TN keys from token `base`: raw dot products become weights relative to row.m,
-// row.l grows by their sum. Warp-collective. `Row` gives access to the row's scores and weights:
-// load_all(v) reads the TN raw columns, load64(h, v) and load32(h, v) a part of them, emit64(h,
-// pk) and emit32(h, pk) take a part's weights as fp16 pairs (parts are emitted in order, the
-// columns up to their end having been read for the last time), rescale(f) multiplies the row's
-// accumulated output by f (called when `later`, a tile after the row's first; false from it: a
+// One unit of 64 keys from token `base`: raw dot products become weights relative to row.m,
+// row.l grows by their sum. Warp-collective. `io` gives access to the row: load(v) reads the raw
+// columns, emit(pk) takes their weights as fp16 pairs, rescale(f) multiplies the row's
+// accumulated output by f (called when `later`, a unit after the row's first; false from it: a
 // wait gave up). A row that has seen nothing yet has m = -inf.
-//
-// A tile that every row sees whole is loaded at once for its maximum and 64 columns at a time
-// for its weights: a load costs ~180 cycles however wide it is. The other tiles are taken 32
-// columns at a time, without the parts that no row sees.
-template <int TN, class Row>
+template <class Io>
 __device__ __forceinline__ bool scored_weights(const ScoreArgs &s, float scale_log2,
-                                               ScoredRow &row, int base, bool later, Row io) {
-  constexpr int H = TN / 32;
+                                               ScoredRow &row, int base, bool later,
+                                               const Io &io) {
   const int lo = row.lo - base, hi = row.hi - base;
-  const bool some = hi >= 0 && lo < TN && lo <= hi;
-  const bool cap = s.cap_in != 0.f, biased = s.slopes != nullptr;
-  const int rel = base - row.pos;
-  const bool straight = __all_sync(0xffffffffu, lo <= 0 && hi >= TN - 1 &&
-                                                    (!biased || (!cap && rel + TN - 1 <= 0)));
-  unsigned seen = 0;  // the parts of 32 columns that some row of the warp sees
-
-  // ---- the row's largest score, from the extremes of the raw products (of the scores where
-  // biased)
-  float top = -INFINITY, low = INFINITY;
-  if (straight) {
-    float v[TN];
-    io.load_all(v);
-    if (biased) add_slope(v, row.slope2, scale_log2);
-    extremes(v, top, low);
-    if (biased) top = fmaf(row.slope2, static_cast<float>(rel), top);
-  } else {
-#pragma unroll 1
-    for (int h = 0; h < H; ++h) {
-      const int l = lo - 32 * h, r = hi - 32 * h;
-      if (!__any_sync(0xffffffffu, some && r >= 0 && l < 32)) continue;
-      seen |= 1u << h;
-      float v[32];
-      io.load32(h, v);
-      float offset = 0.f;
-      if (biased) {
-        if (cap) cap_scores(v, s, false);
-        offset = bias_scores(v, row.slope2, rel + 32 * h, cap ? 1.f : scale_log2);
-      }
-      float mx[2] = {-INFINITY, -INFINITY}, mn[2] = {INFINITY, INFINITY};
+  float pk[32];
+  if (!__any_sync(0xffffffffu, hi >= 0 && lo < 64 && lo <= hi)) {
 #pragma unroll
-      for (int c = 0; c < 32; ++c) {
-        const bool in = c >= l && c <= r;
-        mx[c & 1] = fmaxf(mx[c & 1], in ? v[c] : -INFINITY);
-        mn[c & 1] = fminf(mn[c & 1], in ? v[c] : INFINITY);
-      }
-      top = max3(top, mx[0] + offset, mx[1] + offset);
-      low = min3(low, mn[0], mn[1]);
-    }
+    for (int e = 0; e < 32; ++e) pk[e] = 0.f;
+    io.emit(pk);
+    return true;
   }
-  bool poly = false;
-  if (!biased) {
-    // scores are monotonic in the raw products: growing with them for a positive scale
-    const float ext = scale_log2 >= 0.f ? top : low;
-    if (cap) {
-      const float far = fmaxf(fabsf(top), fabsf(low));
-      poly = __all_sync(0xffffffffu, !some || far * far <= s.cap_poly_max);
-      top = some ? cap_exact(s, ext) : -INFINITY;
-    } else {
-      top = some ? ext * scale_log2 : -INFINITY;
+  const bool masked = !__all_sync(0xffffffffu, lo <= 0 && hi >= 63);
+  float v[64], mult = scale_log2, offset = 0.f, high, low;
+  io.load(v);
+  float top = -INFINITY;
+  bool known = false;  // whether top is the row's largest score already
+  if (s.cap_in != 0.f) {
+    // columns nobody sees may widen the extremes, and so send the warp to the exact form
+    extremes(v, high, low);
+    const float far = fmaxf(fabsf(high), fabsf(low));
+    const bool poly = __all_sync(0xffffffffu, far * far <= s.cap_poly_max);
+    if (!masked && !s.slopes) {
+      // capped scores are monotonic in the raw products
+      top = cap_exact(s, scale_log2 >= 0.f ? high : low);
+      known = true;
     }
+    cap_scores(v, s, poly);
+    mult = 1.f;
+  }
+  if (s.slopes) {
+    const int rel = base - row.pos;
+    if (__all_sync(0xffffffffu, rel + 63 <= 0)) {
+      add_slope(v, row.slope2, mult);
+      offset = row.slope2 * static_cast<float>(rel);
+    } else {  // keys on both sides of the query: the distance of each
+      const float first = static_cast<float>(rel);
+#pragma unroll
+      for (int c = 0; c < 64; ++c)
+        v[c] = fmaf(-row.slope2, fabsf(first + static_cast<float>(c)), v[c] * mult);
+    }
+    mult = 1.f;
+  }
+  if (masked) {
+    // the scale is never 0, so that the score of a masked column is -inf
+    const float none = mult >= 0.f ? -INFINITY : INFINITY;
+#pragma unroll
+    for (int c = 0; c < 64; ++c) v[c] = c >= lo && c <= hi ? v[c] : none;
+  }
+  if (!known) {
+    extremes(v, high, low);
+    top = fmaf(mult >= 0.f ? high : low, mult, offset);
   }
   const bool grow = top > row.m + kScoredSlack;
   if (__any_sync(0xffffffffu, grow)) {
@@ -240,56 +195,21 @@ __device__ __forceinline__ bool scored_weights(const ScoreArgs &s, float scale_l
     if (later && !io.rescale(f)) return false;
     row.m = mnew;
   }
-
-  // ---- the weights
-  const float nm = row.m == -INFINITY ? 0.f : -row.m;
+  if (row.m != -INFINITY) offset -= row.m;
+  const float2 m2 = make_float2(mult, mult), n2 = make_float2(offset, offset);
   float rp[4] = {0.f, 0.f, 0.f, 0.f};
-  if (straight) {
-#pragma unroll 1
-    for (int h = 0; h < TN / 64; ++h) {
-      float v[64], pk[32], mult = scale_log2, offset = nm;
-      io.load64(h, v);
-      if (cap) {
-        cap_scores(v, s, poly);
-        mult = 1.f;
-      }
-      if (biased) {
-        add_slope(v, row.slope2, mult);
-        offset = fmaf(row.slope2, static_cast<float>(rel + 64 * h), offset);
-        mult = 1.f;
-      }
-      weigh(v, mult, offset, pk, rp);
-      io.emit64(h, pk);
-    }
-  } else {
-#pragma unroll 1
-    for (int h = 0; h < H; ++h) {
-      float pk[16];
-      if (!(seen >> h & 1)) {
 #pragma unroll
-        for (int e = 0; e < 16; ++e) pk[e] = 0.f;
-      } else {
-        float v[32], mult = scale_log2, offset = nm;
-        io.load32(h, v);
-        if (cap) {
-          cap_scores(v, s, poly);
-          mult = 1.f;
-        }
-        if (biased) {
-          offset += bias_scores(v, row.slope2, rel + 32 * h, mult);
-          mult = 1.f;
-        }
-        // the scale is never 0, so that the score of a masked column is -inf
-        const float none = mult >= 0.f ? -INFINITY : INFINITY;
-        const int l = lo - 32 * h, r = hi - 32 * h;
-#pragma unroll
-        for (int c = 0; c < 32; ++c) v[c] = c >= l && c <= r ? v[c] : none;
-        weigh(v, mult, offset, pk, rp);
-      }
-      io.emit32(h, pk);
-    }
+  for (int e = 0; e < 32; ++e) {
+    const int c = 2 * e;
+    const float2 x = ffma2(make_float2(v[c], v[c + 1]), m2, n2);
+    const float2 w = make_float2(prefill_exp2(x.x), prefill_exp2(x.y));
+    const float2 acc = fadd2(make_float2(rp[c & 2], rp[(c & 2) + 1]), w);
+    rp[c & 2] = acc.x;
+    rp[(c & 2) + 1] = acc.y;
+    pk[e] = __uint_as_float(pack_half2(w.x, w.y));
   }
   row.l += (rp[0] + rp[1]) + (rp[2] + rp[3]);
+  io.emit(pk);
   return true;
 }
 
