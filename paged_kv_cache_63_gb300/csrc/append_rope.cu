@@ -7,6 +7,7 @@
 // Bound: HBM. A token reads and writes (query_heads + 2 kv_heads) * head_dim fp16 and reads one
 // table row; there are ~1.5 fp32 operations a byte.
 #include "device_common.cuh"
+#include "early_launch.cuh"
 #include "internal.h"
 
 namespace pa {
@@ -76,6 +77,7 @@ constexpr int kRopeUnroll = 4;
 template <int HD, bool kInterleaved>
 __global__ void __launch_bounds__(256) append_rope_kernel(const __grid_constant__ RopeArgs a) {
   constexpr int IPR = HD / 16;  // items per head row
+  wait_for_stream();
   // every sequence is checked once, whichever rows it holds
   for (long long b = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; b < a.batch;
        b += static_cast<long long>(gridDim.x) * blockDim.x) {
@@ -168,16 +170,13 @@ namespace {
 bool misaligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) != 0; }
 
 template <int HD>
-void launch_append_rope(const RopeArgs &a, bool interleaved, cudaStream_t stream) {
+cudaError_t launch_append_rope(const RopeArgs &a, bool interleaved, cudaStream_t stream) {
   constexpr int IPR = HD / 16;
   const int heads = (a.q ? a.qh : 0) + 2 * a.kvh;
   const int want = (heads * IPR + kRopeUnroll - 1) / kRopeUnroll;  // one walk over the heads
   const int threads = want >= 256 ? 256 : (want + 31) / 32 * 32;
-  const unsigned rows = static_cast<unsigned>(a.total);
-  if (interleaved)
-    append_rope_kernel<HD, true><<<rows, threads, 0, stream>>>(a);
-  else
-    append_rope_kernel<HD, false><<<rows, threads, 0, stream>>>(a);
+  return launch_early(interleaved ? append_rope_kernel<HD, true> : append_rope_kernel<HD, false>,
+                      dim3(static_cast<unsigned>(a.total)), threads, 0, stream, a);
 }
 
 }  // namespace
@@ -257,11 +256,12 @@ extern "C" pa_status_t pa_append_rope(const pa_problem_t *problem, const pa_rope
   a.table_rows = rotary ? rope->table_rows : 0;
   const bool interleaved = rotary && rope->style == PA_ROPE_INTERLEAVED;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e;
   switch (problem->head_dim) {
-    case 64: launch_append_rope<64>(a, interleaved, s); break;
-    case 128: launch_append_rope<128>(a, interleaved, s); break;
-    case 256: launch_append_rope<256>(a, interleaved, s); break;
+    case 64: e = launch_append_rope<64>(a, interleaved, s); break;
+    case 128: e = launch_append_rope<128>(a, interleaved, s); break;
+    case 256: e = launch_append_rope<256>(a, interleaved, s); break;
     default: return PA_ERR_UNSUPPORTED;
   }
-  return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+  return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }

@@ -18,11 +18,14 @@
 //    take a probability rounded to fp16 and rows 8..15 the remainder, at no further tensor
 //    instruction; tile results are added to the output in fp32 registers, so a long context
 //    does not lose bits to the tensor cores' accumulator either.
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <cstring>
 
 #include "decode_kernel.cuh"
+#include "early_launch.cuh"
+#include "row_maps.h"
 #include "score_rule.cuh"
 
 namespace pa {
@@ -133,54 +136,80 @@ __device__ inline bool span_balanced_start(const ScoredArgs &a, int worker, int 
   return false;
 }
 
+// One elected lane of the converged warp announces the bytes a barrier waits for, or issues a
+// TMA load; the operands are the same in every lane. (In a branch of lane 0 alone the issue of a
+// 16-token tile of head_dim 128 took 1030 of the 2970 cycles that a worker spends on the tile.)
+__device__ __forceinline__ void expect_bytes_warp(uint32_t bar, uint32_t bytes) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}" ::"r"(bar),
+      "r"(bytes)
+      : "memory");
+}
+
+__device__ __forceinline__ void tma_rows_warp(uint32_t dst, const CUtensorMap *map, uint32_t bar,
+                                              int row, int head, int block, uint64_t policy) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      ".L2::cache_hint [%0], [%1, {%3, %4, %5, %6}], [%2], %7;\n\t}" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(0), "r"(row), "r"(head), "r"(block),
+      "l"(policy)
+      : "memory");
+}
+
 // Issue the TMA loads of the tile at cursor c into a stage (warp-uniform). Pieces (min(page
-// size, T) rows) that hold no seen token are not loaded.
+// size, T) rows) that hold no seen token are not loaded. A tile of one piece is one load each
+// for K and V; the column blocks of smaller pieces lie apart in the stage and are loaded alone.
 template <int HD, int T>
 __device__ __forceinline__ void issue_span_tile(const ScoredArgs &sa, const CUtensorMap *tk,
-                                                const CUtensorMap *tv, const SpanCursor &c,
-                                                int member, BtWindow &w, uint32_t stage,
-                                                uint32_t bar, uint64_t pol, uint32_t extra_tx) {
+                                                const CUtensorMap *tv, const SpanCursor &c, int kv,
+                                                BtWindow &w, uint32_t stage, uint32_t bar,
+                                                uint64_t pol, uint32_t extra_tx) {
   const KernelArgs &a = sa.k;
   constexpr int kMaxPieces = T / 8;
   const int R = a.ps < T ? a.ps : T;
-  const int pieces = T / R;
-  const int kv = (c.us * a.group + member) / a.sub;
   const int npages = (c.sp.end + a.ps - 1) >> a.ps_shift;
-  int yc[kMaxPieces], zc[kMaxPieces];  // TMA coordinates; z < 0 marks a piece not loaded
+  const bool hm = a.layout == PA_LAYOUT_HEAD_MAJOR;
+  auto place = [&](int tok, int &row, int &head) {  // false: the page id is outside the pool
+    const int page = bt_page(a, w, c.b, tok >> a.ps_shift, npages);
+    const int slot = tok & (a.ps - 1);
+    row = hm ? slot : (page << a.ps_shift) + slot;
+    head = hm ? page * a.kvh + kv : kv;
+    if (page >= 0 && page < a.num_pages) return true;
+    if ((threadIdx.x & 31) == 0) atomicOr(a.err, PA_DEVERR_PAGE_ID);
+    return false;
+  };
+  if (R == T) {
+    int row, head;
+    const bool good = place(c.tok, row, head);
+    expect_bytes_warp(bar, (good ? Geom<HD, T>::kStageBytes : 0u) + extra_tx);
+    if (good) {
+      tma_rows_warp(stage, tk, bar, row, head, 0, pol);
+      tma_rows_warp(stage + Geom<HD, T>::kHalfBytes, tv, bar, row, head, 0, pol);
+    }
+    return;
+  }
+  int row[kMaxPieces], head[kMaxPieces];  // row < 0 marks a piece not loaded
   uint32_t bytes = 0;
 #pragma unroll
   for (int p = 0; p < kMaxPieces; ++p) {
-    zc[p] = -1;
-    yc[p] = 0;
     const int tok = c.tok + p * R;
-    if (p < pieces && tok < c.sp.end && tok + R > c.sp.lo) {
-      const int page = bt_page(a, w, c.b, tok >> a.ps_shift, npages);
-      if (page < 0 || page >= a.num_pages) {
-        if ((threadIdx.x & 31) == 0) atomicOr(a.err, PA_DEVERR_PAGE_ID);
-      } else {
-        const int slot = tok & (a.ps - 1);
-        if (a.layout == PA_LAYOUT_HEAD_MAJOR) {
-          yc[p] = slot;
-          zc[p] = page * a.kvh + kv;
-        } else {
-          yc[p] = kv;
-          zc[p] = (page << a.ps_shift) + slot;
-        }
-        bytes += static_cast<uint32_t>(R * HD * 4);
-      }
-    }
+    head[p] = 0;
+    if (p * R < T && tok < c.sp.end && tok + R > c.sp.lo && place(tok, row[p], head[p]))
+      bytes += static_cast<uint32_t>(R * HD * 4);
+    else
+      row[p] = -1;
   }
-  if ((threadIdx.x & 31) == 0) {
-    mbar_arrive_expect_tx(bar, bytes + extra_tx);
+  expect_bytes_warp(bar, bytes + extra_tx);
 #pragma unroll
-    for (int p = 0; p < kMaxPieces; ++p) {
-      if (zc[p] < 0) continue;
+  for (int p = 0; p < kMaxPieces; ++p) {
+    if (row[p] < 0) continue;
 #pragma unroll
-      for (int blk = 0; blk < HD / 64; ++blk) {
-        const uint32_t dst = stage + blk * (T * 128) + p * R * 128;
-        tma_load_3d(dst, tk, bar, blk * 64, yc[p], zc[p], pol);
-        tma_load_3d(dst + Geom<HD, T>::kHalfBytes, tv, bar, blk * 64, yc[p], zc[p], pol);
-      }
+    for (int blk = 0; blk < HD / 64; ++blk) {
+      const uint32_t dst = stage + blk * (T * 128) + p * R * 128;
+      tma_rows_warp(dst, tk, bar, row[p], head[p], blk, pol);
+      tma_rows_warp(dst + Geom<HD, T>::kHalfBytes, tv, bar, row[p], head[p], blk, pol);
     }
   }
 }
@@ -371,6 +400,15 @@ __global__ void __launch_bounds__(kMaxWarpsPerCta * 32, 1)
       warp * a.warp_smem;
   const uint32_t bar0 = smem_addr(&bars[warp * kMaxStages]);
 
+  if (lane == 0) {
+    for (int s = 0; s < S; ++s) mbar_init(bar0 + 8 * s, 1);
+    fence_barrier_init();
+    prefetch_tensormap(&tk);
+    prefetch_tensormap(&tv);
+  }
+  __syncwarp();
+  wait_for_stream();
+
   {
     // warm L2 with the small inputs every warp reads first
     const long long nthreads = static_cast<long long>(gridDim.x) * blockDim.x;
@@ -423,14 +461,7 @@ __global__ void __launch_bounds__(kMaxWarpsPerCta * 32, 1)
     }
   }
 
-  // ---- pipeline set-up
-  if (lane == 0) {
-    for (int s = 0; s < S; ++s) mbar_init(bar0 + 8 * s, 1);
-    fence_barrier_init();
-    prefetch_tensormap(&tk);
-    prefetch_tensormap(&tv);
-  }
-  __syncwarp();
+  // ---- pipeline
   const uint64_t pol = l2_evict_first_policy();
 
   SpanCursor ic = c;
@@ -438,14 +469,27 @@ __global__ void __launch_bounds__(kMaxWarpsPerCta * 32, 1)
   win.b = -1;
   win.base = 0;
   win.cur = win.nxt = -1;
-  int issued = 0, consumed = 0;
-  for (; issued < S - 1 && ic.left > 0; ++issued) {
-    issue_span_tile<HD, T>(sa, &tk, &tv, ic, member, win, wbase + issued * G::kStageBytes,
-                           bar0 + 8 * issued, pol, issued == 0 ? a.tx_extra : 0u);
+  // ring positions: the stage and phase parity of the next tile to consume, the stage of the
+  // next one to issue, and the tiles in flight; divisions stay out of the loop (with them a
+  // tile's bookkeeping took 500 cycles more)
+  int cs = 0, is = 0, flying = 0;
+  uint32_t cphase = 0, extra = a.tx_extra;
+  int ius = ic.us, ikv = (ic.us * a.group + member) / a.sub;  // K/V head of the cursor's unit
+  auto issue = [&]() {
+    if (ic.us != ius) {
+      ius = ic.us;
+      ikv = (ic.us * a.group + member) / a.sub;
+    }
+    issue_span_tile<HD, T>(sa, &tk, &tv, ic, ikv, win, wbase + is * G::kStageBytes, bar0 + 8 * is,
+                           pol, extra);
+    extra = 0;
+    is = is + 1 == S ? 0 : is + 1;
+    ++flying;
     advance(sa, ic, T);
-  }
+  };
+  while (flying < S - 1 && ic.left > 0) issue();
 
-  SpanState<HD> st;
+  SpanState<HD> st = {};
   MmaLane<HD, T> lane_addr;
   lane_addr.init();
   UnitInfo cur;
@@ -495,30 +539,32 @@ __global__ void __launch_bounds__(kMaxWarpsPerCta * 32, 1)
       cur_tiles = span_tiles(c.sp, T);
       span_begin<HD>(st, sa, cur.b, cur.h0, cur.nh);
     }
-    if (ic.left > 0) {
-      const int s = issued % S;
-      issue_span_tile<HD, T>(sa, &tk, &tv, ic, member, win, wbase + s * G::kStageBytes,
-                             bar0 + 8 * s, pol, issued == 0 ? a.tx_extra : 0u);
-      ++issued;
-      advance(sa, ic, T);
-    }
-    const int s = consumed % S;
-    if (!mbar_wait(bar0 + 8 * s, static_cast<uint32_t>((consumed / S) & 1), a.err)) {
+    if (ic.left > 0) issue();
+    if (!mbar_wait(bar0 + 8 * cs, cphase, a.err)) {
       aborted = true;
       break;
     }
-    span_tile<HD, T>(st, lane_addr, wbase + s * G::kStageBytes, c, sa);
+    span_tile<HD, T>(st, lane_addr, wbase + cs * G::kStageBytes, c, sa);
     fence_proxy_async();
     __syncwarp();
-    ++consumed;
+    if (++cs == S) {
+      cs = 0;
+      cphase ^= 1u;
+    }
+    --flying;
     advance(sa, c, T);
   }
   // the joining kernel may come up now (it waits for this grid before it reads any state)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (aborted) {
     // let the copies still in flight land before the shared memory is given up
-    for (int i = consumed; i < issued; ++i)
-      mbar_wait(bar0 + 8 * (i % S), static_cast<uint32_t>((i / S) & 1), a.err);
+    for (; flying > 0; --flying) {
+      mbar_wait(bar0 + 8 * cs, cphase, a.err);
+      if (++cs == S) {
+        cs = 0;
+        cphase ^= 1u;
+      }
+    }
     return;
   }
   finish_unit();
@@ -526,8 +572,9 @@ __global__ void __launch_bounds__(kMaxWarpsPerCta * 32, 1)
 
 // Joins the states of units that several workers share: out = sum_k 2^(m_k - M) acc_k /
 // sum_k 2^(m_k - M) l_k, contributors in their order. W warps take one (unit, head) pair, a
-// CTA of eight warps 8 / W pairs; before griddepcontrol.wait a warp redoes the decode kernel's
-// split from the inputs alone, after it the pair costs about one memory round trip.
+// CTA of eight warps 8 / W pairs. Its CTAs come up when the decode kernel's have finished their
+// tiles, which had waited for everything before them in the stream: so a warp redoes the split
+// from the inputs before its own wait, and after it the pair costs about one memory round trip.
 template <int HD, int W>
 __global__ void __launch_bounds__(256)
     join_scored_kernel(const __grid_constant__ ScoredArgs sa, int heads, long long pairs, int T) {
@@ -569,7 +616,7 @@ __global__ void __launch_bounds__(256)
     // a unit with one worker was finished by it; heads past the unit's own do not exist
     if (n <= 1 || h >= u.nh) n = 0;
   }
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  wait_for_stream();
   if constexpr (W == 1) {
     if (n == 0) return;  // no barrier below for a warp per pair
   }
@@ -732,24 +779,16 @@ cudaError_t launch_scored(const ScoredArgs &a, const CUtensorMap &tk, const CUte
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < kMaxDev) set[dev].store(smem, std::memory_order_relaxed);
   }
-  kern<<<pl.ctas, pl.warps_per_cta * 32, smem, stream>>>(a, tk, tv);
-  return cudaGetLastError();
+  return launch_early(kern, dim3(pl.ctas), pl.warps_per_cta * 32, smem, stream, a, tk, tv);
 }
 
 template <int HD, int W>
 cudaError_t launch_join(const ScoredArgs &a, int units, int heads, int tile, cudaStream_t stream) {
   const long long pairs = static_cast<long long>(units) * heads;
   constexpr int P = 8 / W;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>((pairs + P - 1) / P), 1, 1);
-  cfg.blockDim = dim3(256, 1, 1);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, join_scored_kernel<HD, W>, a, heads, pairs, tile);
+  return launch_early(join_scored_kernel<HD, W>,
+                      dim3(static_cast<unsigned>((pairs + P - 1) / P)), 256, 0, stream, a, heads,
+                      pairs, tile);
 }
 
 template <int HD>
@@ -783,9 +822,23 @@ extern "C" pa_status_t pa_decode_scored(const pa_problem_t *problem, const pa_sc
   if (st != PA_OK) return st;
   if (options && (options->math == PA_MATH_SIMT || options->combine == PA_COMBINE_FUSED))
     return PA_ERR_UNSUPPORTED;
+  // With at most three tiles to a unit one worker walks them faster than several share and join
+  // them (head_dim 64, two sequences: 7.0 against 9.0 us; from four tiles on 9.7 against 9.4).
+  pa_options_t single = {};
   pa_plan_t pl;
   st = pa_plan(problem, options, 1, &pl);  // shapes and options the plan refuses
   if (st != PA_OK) return st;
+  if (!options || options->schedule == PA_SCHEDULE_AUTO) {
+    int64_t most = static_cast<int64_t>(problem->max_pages_per_sequence) * problem->page_size;
+    int64_t tiles = (most + pl.tile_tokens - 1) / pl.tile_tokens;
+    if (a.s.window > 0 && a.s.window < most)  // a window may start anywhere in a tile
+      tiles = std::min<int64_t>(tiles, (a.s.window + 2 * pl.tile_tokens - 2) / pl.tile_tokens);
+    if (tiles <= 3) {
+      if (options) single = *options;
+      single.schedule = PA_SCHEDULE_SINGLE;
+      options = &single;
+    }
+  }
   if (problem->batch == 0) return PA_OK;
   int smem_optin = 0;
   st = current_device_smem(&smem_optin);
@@ -799,13 +852,13 @@ extern "C" pa_status_t pa_decode_scored(const pa_problem_t *problem, const pa_sc
   }
 
   alignas(64) CUtensorMap tk, tv;
-  const int rows = problem->page_size < pl.tile_tokens ? problem->page_size : pl.tile_tokens;
-  st = encode_cache_map_rows(&tk, key_cache, problem, rows);
-  if (st != PA_OK) return st;
-  st = encode_cache_map_rows(&tv, value_cache, problem, rows);
-  if (st != PA_OK) return st;
-
   const int hd = problem->head_dim;
+  const int rows = problem->page_size < pl.tile_tokens ? problem->page_size : pl.tile_tokens;
+  const int blocks = rows == pl.tile_tokens ? hd / 64 : 1;
+  st = encode_row_map(&tk, key_cache, problem, rows, blocks);
+  if (st != PA_OK) return st;
+  st = encode_row_map(&tv, value_cache, problem, rows, blocks);
+  if (st != PA_OK) return st;
   const int g = problem->query_heads / problem->kv_heads;
   KernelArgs &k = a.k;
   k.q = static_cast<const uint16_t *>(query);

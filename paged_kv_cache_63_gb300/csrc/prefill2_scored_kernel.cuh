@@ -18,6 +18,7 @@
 // memory); 3 schedules; 4..7 are tile A's softmax, 8..11 tile B's.
 #pragma once
 
+#include "early_launch.cuh"
 #include "prefill2_kernel.cuh"
 #include "scored_softmax.cuh"
 
@@ -185,6 +186,7 @@ __global__ void __launch_bounds__(kPrefill2Threads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
+  wait_for_stream();
 
   // first token of K/V tile j of an item
   auto tile_token = [](const Item &it, int j) { return (it.last_tile - j) * C::TN; };

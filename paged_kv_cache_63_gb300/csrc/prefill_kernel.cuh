@@ -21,6 +21,7 @@
 // roles stop at their next wait, in-flight copies and MMAs are drained and TMEM is freed.
 #pragma once
 
+#include "early_launch.cuh"
 #include "prefill_common.cuh"
 #include "scored_softmax.cuh"
 
@@ -262,6 +263,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
+  if constexpr (kScored) wait_for_stream();
 
   // first token of tile j of an item
   auto tile_token = [](const Item &it, int j) {

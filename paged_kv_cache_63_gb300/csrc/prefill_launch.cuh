@@ -54,6 +54,8 @@ cudaError_t launch_prefill2_hd(const PrefillArgsOf<kScored> &a, const PrefillLau
     kern = prefill2_kernel<HD>;
   const cudaError_t e = allow_smem(kern, smem, set);
   if (e != cudaSuccess) return e;
+  if constexpr (kScored)
+    return launch_early(kern, l.grid, kPrefill2Threads, smem, stream, a, l.tq, l.tk, l.tv);
   kern<<<l.grid, kPrefill2Threads, smem, stream>>>(a, l.tq, l.tk, l.tv);
   return cudaGetLastError();
 }
@@ -66,6 +68,8 @@ cudaError_t launch_prefill_hd(const PrefillArgsOf<kScored> &a, const PrefillLaun
   auto kern = prefill_kernel<HD, kScored>;
   const cudaError_t e = allow_smem(kern, smem, set);
   if (e != cudaSuccess) return e;
+  if constexpr (kScored)
+    return launch_early(kern, l.grid, kPrefillThreads, smem, stream, a, l.tq, l.tk, l.tv);
   kern<<<l.grid, kPrefillThreads, smem, stream>>>(a, l.tq, l.tk, l.tv);
   return cudaGetLastError();
 }
