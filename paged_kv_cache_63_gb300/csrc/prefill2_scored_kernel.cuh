@@ -115,18 +115,20 @@ struct ScoredTile2 {
   unsigned *err;
   __device__ __forceinline__ void load(float (&c)[64]) const { tmem_ld64(ts, c); }
   __device__ __forceinline__ void emit(const float (&pk)[32]) const { tmem_st32(ts, pk); }
-  __device__ __forceinline__ bool rescale(float f) const {
-    if (!pipe_wait(pv_bar, pv_parity, abort_flag, err)) return false;
-    tc_fence_after();
+  __device__ __forceinline__ bool settle(ScoredRow &row, float top, bool later) const {
+    return settle_row(row, top, later, [&](float f) {
+      if (!pipe_wait(pv_bar, pv_parity, abort_flag, err)) return false;
+      tc_fence_after();
 #pragma unroll
-    for (int c = 0; c < HD / 32; ++c) {
-      float o[32];
-      tmem_ld32(to + c * 32, o);
+      for (int c = 0; c < HD / 32; ++c) {
+        float o[32];
+        tmem_ld32(to + c * 32, o);
 #pragma unroll
-      for (int e = 0; e < 32; ++e) o[e] *= f;
-      tmem_st32(to + c * 32, o);
-    }
-    return true;
+        for (int e = 0; e < 32; ++e) o[e] *= f;
+        tmem_st32(to + c * 32, o);
+      }
+      return true;
+    });
   }
 };
 

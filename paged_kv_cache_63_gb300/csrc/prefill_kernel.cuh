@@ -21,11 +21,28 @@
 // roles stop at their next wait, in-flight copies and MMAs are drained and TMEM is freed.
 #pragma once
 
-#include "early_launch.cuh"
-#include "prefill_common.cuh"
-#include "scored_softmax.cuh"
+#include "device_common.cuh"
+#include "internal.h"
+#include "tcgen05.cuh"
 
 namespace pa {
+
+struct PrefillArgs {
+  const int32_t *qs;   // [batch + 1] first query row of each sequence
+  const int32_t *bt;   // [batch][maxp]
+  const int32_t *ctx;  // [batch] tokens in the cache, the new ones included
+  float *out;          // [total][qh][hd]
+  unsigned *err;
+  long long total;  // rows of query and out
+  int batch, qh, kvh, ps, ps_shift, maxp, num_pages, layout;
+  int g;         // query heads per K/V head
+  int qt;        // new tokens per query tile (128 / g)
+  int n_qtiles;  // grid.z
+  float scale_log2;
+  int expire;  // PA_TEST_EXPIRE_WAITS: the MMA warp's first wait is on a barrier that
+               // completes only at the end, so it runs out
+  int out_v8;  // out is 32-byte aligned: the two-tile kernel writes rows in 32-byte stores
+};
 
 template <int HD>
 struct PrefillCfg {
@@ -52,6 +69,12 @@ constexpr int kPrefillVWarp = 6;
 constexpr int kPrefillSchedWarp = 7;
 // warps that read each published work item: 0, 1, the softmax warps 2..5 and 6
 constexpr int kItemReaders1 = 7;
+// O is rescaled only when a row's running maximum grows by more than 2^kPrefillSlackLog2;
+// until then every exponent term is at most kPrefillSlackBound, which a tile's row sum may
+// therefore be checked against.
+constexpr int kPrefillSlackLog2 = 8;
+constexpr float kPrefillRescaleSlack = static_cast<float>(kPrefillSlackLog2);  // log2 units
+constexpr float kPrefillSlackBound = static_cast<float>(1 << kPrefillSlackLog2);
 
 // Barrier slots.
 enum : int {
@@ -72,6 +95,36 @@ enum : int {
   kNumBars = 23
 };
 
+// L2 policy for bytes that other CTAs read again soon: keep them ahead of streamed data.
+__device__ __forceinline__ uint64_t l2_evict_last_policy() {
+  uint64_t pol;
+  asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(pol));
+  return pol;
+}
+
+__device__ __forceinline__ float prefill_exp2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Packed fp32 pairs (sm_100 family): one instruction does two FMAs or two adds.
+__device__ __forceinline__ float2 ffma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 ra, rb, rc, rd;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+      "mov.b64 rc, {%6, %7};\n\tfma.rn.f32x2 rd, ra, rb, rc;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+      : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+
+__device__ __forceinline__ float2 fadd2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 ra, rb, rd;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+      "add.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+      : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+
 // P = exp2(s * sl2 + nm) over a row of TN scores, in place, with keys past lim (when the row
 // is not full) giving exactly 0, and the row's partial sums in rp. Packed fp32 pairs: one
 // FFMA2 gives two exponent arguments and one FADD2 adds two terms to the sums.
@@ -91,6 +144,94 @@ __device__ __forceinline__ void exps_row(float (&x)[TN], float sl2, float nm, bo
     x[c] = p0;
     x[c + 1] = p1;
   }
+}
+
+// 32-byte store (one full sector) of 8 floats with an L2 eviction-priority policy.
+__device__ __forceinline__ void st_global_v8(float *p, float v0, float v1, float v2, float v3,
+                                             float v4, float v5, float v6, float v7, uint64_t pol) {
+  asm volatile(
+      "st.global.L2::cache_hint.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8}, %9;" ::"l"(p),
+      "f"(v0), "f"(v1), "f"(v2), "f"(v3), "f"(v4), "f"(v5), "f"(v6), "f"(v7), "l"(pol)
+      : "memory");
+}
+
+__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// Warp-collective bounded wait that also gives up when another role has aborted.
+__device__ __forceinline__ bool pipe_wait(uint32_t bar, uint32_t parity, volatile int *abort_flag,
+                                          unsigned *err) {
+  bool ok = mbar_try_wait(bar, parity);
+  bool expired = false;
+  if (!ok) {
+    const uint64_t t0 = global_ns();
+    for (uint32_t i = 1;; ++i) {
+      if (mbar_try_wait(bar, parity)) {
+        ok = true;
+        break;
+      }
+      if ((i & 31u) == 0) {
+        if (*abort_flag) break;
+        if (global_ns() - t0 > kWaitLimitNs) {
+          expired = true;
+          break;
+        }
+      }
+    }
+  }
+  ok = __all_sync(0xffffffffu, ok);
+  expired = __any_sync(0xffffffffu, expired);
+  if (!ok && (threadIdx.x & 31) == 0) {
+    if (expired) atomicOr(err, PA_DEVERR_TIMEOUT);
+    *abort_flag = 1;
+  }
+  return ok;
+}
+
+// Bounded wait used while draining (ignores the abort flag).
+__device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity, unsigned *err) {
+  bool ok = mbar_try_wait(bar, parity);
+  if (!ok) {
+    const uint64_t t0 = global_ns();
+    for (uint32_t i = 1;; ++i) {
+      if (mbar_try_wait(bar, parity)) {
+        ok = true;
+        break;
+      }
+      if ((i & 31u) == 0 && global_ns() - t0 > kWaitLimitNs) break;
+    }
+  }
+  if (!ok) atomicOr(err, PA_DEVERR_TIMEOUT);
+}
+
+// ---- cluster launch control -------------------------------------------------------------
+// Ask for one CTA of this grid that has not started to be cancelled so that the caller runs
+// its work; the 16-byte answer is written to shared memory and completes `bar` with 16 bytes
+// of transaction count.
+__device__ __forceinline__ void clc_try_cancel(uint32_t answer, uint32_t bar) {
+  asm volatile(
+      "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128"
+      " [%0], [%1];" ::"r"(answer), "r"(bar)
+      : "memory");
+}
+
+// Read an answer: true and the cancelled CTA's index if a CTA was cancelled, false when
+// every CTA of the grid has started (no work is left to take).
+__device__ __forceinline__ bool clc_query(uint32_t answer, int &x, int &y, int &z) {
+  uint32_t ok, cx = 0, cy = 0, cz = 0;
+  asm volatile(
+      "{\n\t.reg .b128 r;\n\t.reg .pred p;\n\tld.shared.b128 r, [%4];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+      "selp.u32 %3, 1, 0, p;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%0, %1, %2, _}, r;\n\t}"
+      : "+r"(cx), "+r"(cy), "+r"(cz), "=r"(ok)
+      : "r"(answer)
+      : "memory");
+  x = static_cast<int>(cx);
+  y = static_cast<int>(cy);
+  z = static_cast<int>(cz);
+  return ok != 0;
 }
 
 // Geometry of one work item (K/V head kv, sequence b, query tile), computed once by the
@@ -132,93 +273,15 @@ __device__ __forceinline__ Item1 item1_of(const PrefillArgs &a, int kv, int b, i
   return it;
 }
 
-// Under a score rule (kScored) an item's keys go from kv_lo, the first token that some row
-// sees, to kv_len, and its key tiles are taken last to first (as in prefill2_scored_kernel.cuh): tile j
-// is the one j before last_tile. Warp-collective.
-struct ScoredItem1 : Item1 {
-  int kv_lo, prefix, last_tile;
-};
-
-template <int TN>
-__device__ __forceinline__ ScoredItem1 scored_item1_of(const PrefillScoredArgs &a, int kv, int b,
-                                                       int qtile) {
-  ScoredItem1 it;
-  it.kv = kv;
-  it.b = b;
-  it.live = 0;
-  it.stop = 0;
-  it.ntiles = 0;
-  const int q0 = __ldg(a.qs + b), q1 = __ldg(a.qs + b + 1), ctx = __ldg(a.ctx + b);
-  const int n = q1 - q0;
-  it.q0 = q0;
-  it.n = n;
-  unsigned bad = 0;
-  if (ctx < 0 || static_cast<long long>(ctx) > static_cast<long long>(a.maxp) << a.ps_shift)
-    bad = PA_DEVERR_CONTEXT;
-  else if (q0 < 0 || n < 0 || static_cast<long long>(q1) > a.total || n > ctx)
-    bad = PA_DEVERR_QUERY_START;
-  if (bad) {
-    if ((threadIdx.x & 31) == 0) atomicOr(a.err, bad);
-    return it;
-  }
-  it.tok0 = qtile * a.qt;
-  if (it.tok0 >= n) return it;
-  it.base_pos = ctx - n + it.tok0;
-  it.prefix = prefix_of(a.s, b, ctx);
-  seen_range(a.s, q0, ctx - n, it.tok0, min(it.tok0 + a.qt, n), it.prefix, it.kv_lo, it.max_pos);
-  it.kv_len = it.max_pos + 1;
-  it.last_tile = it.max_pos / TN;
-  it.ntiles = it.last_tile - it.kv_lo / TN + 1;
-  it.live = 1;
-  return it;
-}
-
-// A thread's row of a tile, for scored_weights: scores at TMEM address ts, weights to the
-// shared-memory row prow (16-byte chunks swizzled by xor7), accumulated output at TMEM address
-// to, stable once the barrier of the last P.V has completed.
 template <int HD>
-struct ScoredTile1 {
-  uint32_t ts, to, prow, xor7;
-  uint32_t pv_bar, pv_parity;
-  volatile int *abort_flag;
-  unsigned *err;
-  __device__ __forceinline__ void load(float (&c)[64]) const { tmem_ld64(ts, c); }
-  __device__ __forceinline__ void emit(const float (&pk)[32]) const {
-#pragma unroll
-    for (int e = 0; e < 32; e += 4)
-      sts128(prow + (((e >> 2) ^ xor7) << 4),
-             make_uint4(__float_as_uint(pk[e]), __float_as_uint(pk[e + 1]),
-                        __float_as_uint(pk[e + 2]), __float_as_uint(pk[e + 3])));
-  }
-  __device__ __forceinline__ bool rescale(float f) const {
-    // O holds tiles < j: wait for the last P.V, then scale this row of O in TMEM
-    if (!pipe_wait(pv_bar, pv_parity, abort_flag, err)) return false;
-    tc_fence_after();
-#pragma unroll
-    for (int c = 0; c < HD / 32; ++c) {
-      float v[32];
-      tmem_ld32(to + c * 32, v);
-#pragma unroll
-      for (int e = 0; e < 32; ++e) v[e] *= f;
-      tmem_st32(to + c * 32, v);
-    }
-    tmem_wait_st();
-    return true;
-  }
-};
-
-// kScored: under a score rule (scored_softmax.cuh), with fp16 output.
-template <int HD, bool kScored>
 __global__ void __launch_bounds__(kPrefillThreads, 1)
-    prefill_kernel(const __grid_constant__ PrefillArgsOf<kScored> a,
-                   const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
-                   const __grid_constant__ CUtensorMap tv) {
+    prefill_kernel(const __grid_constant__ PrefillArgs a, const __grid_constant__ CUtensorMap tq,
+                   const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv) {
   using C = PrefillCfg<HD>;
-  using Item = std::conditional_t<kScored, ScoredItem1, Item1>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t bars[kNumBars];
   __shared__ __align__(16) uint4 clc_answer;
-  __shared__ Item items[2];
+  __shared__ Item1 items[2];
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_word;
   volatile int *abort_flag = &abort_word;
@@ -263,18 +326,9 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
-  if constexpr (kScored) wait_for_stream();
-
-  // first token of tile j of an item
-  auto tile_token = [](const Item &it, int j) {
-    if constexpr (kScored)
-      return (it.last_tile - j) * C::TN;
-    else
-      return j * C::TN;
-  };
 
   // Reader side of the item ring: item k sits in entry k & 1. Returns false on abort.
-  auto take_item = [&](int k, Item &it) {
+  auto take_item = [&](int k, Item1 &it) {
     if (!pipe_wait(bar(kBarItemFull + (k & 1)), (k >> 1) & 1, abort_flag, a.err)) return false;
     it = items[k & 1];
     __syncwarp();
@@ -292,16 +346,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
     for (int k = 0;; ++k) {
       if (k >= 2 && !pipe_wait(bar(kBarItemEmpty + (k & 1)), ((k >> 1) - 1) & 1, abort_flag, a.err))
         break;
-      if constexpr (kScored) {
-        Item it;
-        it.stop = 1;
-        it.live = 0;
-        if (!stop) it = scored_item1_of<C::TN>(a, kv, b, a.n_qtiles - 1 - z);
-        if (lane == 0) {
-          items[k & 1] = it;
-          mbar_arrive(bar(kBarItemFull + (k & 1)));
-        }
-      } else if (lane == 0) {
+      if (lane == 0) {
         if (stop) {
           items[k & 1].stop = 1;
           items[k & 1].live = 0;
@@ -351,7 +396,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
     int q_loads = 0;
     bool ok = true;
     for (int k = 0; ok; ++k) {
-      Item it;
+      Item1 it;
       ok = take_item(k, it);
       if (!ok || it.stop) break;
       if (!is_v && lane == 0) mbar_arrive(bar(kBarProdStart));
@@ -371,24 +416,20 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
       }
       const int32_t *bt_row = a.bt + static_cast<size_t>(it.b) * a.maxp;
       // page of this lane's box of tile j (lanes < boxes); -1 past the last needed token
-      auto needed = [&](int tok) {  // the box at token tok holds a token that some row sees
-        if constexpr (kScored)
-          return lane < boxes && tok < it.kv_len && tok + rows_per_box > it.kv_lo;
-        else
-          return lane < boxes && tok < it.kv_len;
-      };
       auto page_of = [&](int j) {
-        const int tok = tile_token(it, j) + lane * rows_per_box;
-        return (j < it.ntiles && needed(tok)) ? __ldg(bt_row + (tok >> a.ps_shift)) : -1;
+        const int tok = j * C::TN + lane * rows_per_box;
+        return (j < it.ntiles && lane < boxes && tok < it.kv_len)
+                   ? __ldg(bt_row + (tok >> a.ps_shift))
+                   : -1;
       };
       // the block-table read for tile j + 1 is issued before the waits of tile j
       int page_next = page_of(0);
       for (int j = 0; j < it.ntiles && ok; ++j, ++g) {
         const int st = g & 1;
-        const int tok = tile_token(it, j) + lane * rows_per_box;
+        const int tok = j * C::TN + lane * rows_per_box;
         int page = page_next;
         page_next = page_of(j + 1);
-        if (needed(tok) && (page < 0 || page >= a.num_pages)) {
+        if (lane < boxes && tok < it.kv_len && (page < 0 || page >= a.num_pages)) {
           if (!is_v) atomicOr(a.err, PA_DEVERR_PAGE_ID);
           page = -1;
         }
@@ -428,7 +469,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
     if (a.expire) ok = pipe_wait(bar(kBarDone), 0, abort_flag, a.err);
     int g = 0, q_waits = 0;
     for (int k = 0; ok; ++k) {
-      Item it;
+      Item1 it;
       ok = take_item(k, it);
       if (!ok || it.stop) break;
       if (!it.live) continue;
@@ -436,9 +477,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
       ++q_waits;
       if (!ok) break;
       tc_fence_after();
-      // the tile that holds the last needed token, and its valid rows
-      const int tail = kScored ? 0 : it.ntiles - 1;
-      const int rows_last = it.kv_len - tile_token(it, tail);
+      const int rows_last = it.kv_len - (it.ntiles - 1) * C::TN;  // valid rows of the last V tile
       for (int j = 0; j <= it.ntiles && ok; ++j) {
         if (j < it.ntiles) {
           const int t = g + j, st = t & 1;
@@ -470,21 +509,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
           if (ok) ok = pipe_wait(bar(kBarVFull + st), (t >> 1) & 1, abort_flag, a.err);
           if (!ok) break;
           tc_fence_after();
-          if constexpr (kScored) {
-            // likewise the rows before the first token that some row sees
-            const int rows_first = it.kv_lo - tile_token(it, i);
-            if (i == it.ntiles - 1 && rows_first > 0) {
-              const int per_block = rows_first * 8;
-              uint8_t *vg = sgen + C::kVOff + st * C::kKVBytes;
-              for (int c = lane; c < C::KB * per_block; c += 32) {
-                const int kb = c / per_block, r = c % per_block;
-                *reinterpret_cast<uint4 *>(vg + kb * (C::TN * 128) + r * 16) = make_uint4(0, 0, 0, 0);
-              }
-              fence_proxy_async();
-              __syncwarp();
-            }
-          }
-          if (i == tail && rows_last < C::TN) {
+          if (i == it.ntiles - 1 && rows_last < C::TN) {
             // V rows past the last needed token hold unread cache slots (possibly never
             // written); P is zero there, but 0 * NaN is not, so clear them.
             const int per_block = (C::TN - rows_last) * 8;
@@ -530,136 +555,119 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
     int g = 0;
     bool ok = true;
     for (int k = 0; ok; ++k) {
-      Item it;
+      Item1 it;
       ok = take_item(k, it);
       if (!ok || it.stop) break;
       if (!it.live) continue;
       const bool valid = row < q_rows && it.tok0 + t < it.n;
       const int pos = min(it.base_pos + t, it.max_pos);
       float m = -INFINITY, l = 0.f;
-      ScoredRow sr = {};
-      if constexpr (kScored)  // rows past the tile's last token repeat it (and are not stored)
-        sr = scored_row(a.s, it.q0, it.base_pos - it.tok0,
-                        min(it.tok0 + min(t, a.qt - 1), it.n - 1), it.kv * a.g + h, it.prefix);
       for (int j = 0; j < it.ntiles; ++j) {
         const int gj = g + j, st = gj & 1;
         ok = pipe_wait(bar(kBarSFull + st), (gj >> 1) & 1, abort_flag, a.err);
         if (!ok) break;
         tc_fence_after();
-        if constexpr (kScored) {
-          // P buffer st was last read by the P.V of global tile gj - 2
-          if (gj >= 2) {
-            ok = pipe_wait(bar(kBarPV + st), ((gj >> 1) - 1) & 1, abort_flag, a.err);
-            if (!ok) break;
-          }
-          const ScoredTile1<HD> io = {trow + st * C::TN, trow + C::kOCol, p_buf(st) + row * 128,
-                  static_cast<uint32_t>(row & 7), bar(kBarPV + ((gj - 1) & 1)),
-                  static_cast<uint32_t>(((gj - 1) >> 1) & 1), abort_flag, a.err};
-          ok = scored_weights(a.s, sl2, sr, tile_token(it, j), j > 0, io);
-          if (!ok) break;
-        } else {
-          float x[C::TN];
+        float x[C::TN];
 #pragma unroll
-          for (int c = 0; c < C::TN / 32; ++c) {
-            float v[32];
-            tmem_ld32(trow + st * C::TN + c * 32, v);
+        for (int c = 0; c < C::TN / 32; ++c) {
+          float v[32];
+          tmem_ld32(trow + st * C::TN + c * 32, v);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) x[c * 32 + e] = v[e];
-          }
-          const int lim = pos - j * C::TN;
-          const bool full = lim >= C::TN - 1;
-          float rp[8];
-          // After a row's first tile its running maximum m seldom grows by more than the slack,
-          // so a tile first takes its exponents with m as it stands and no maximum pass: the
-          // terms are non-negative (masked keys give 0), so the tile's row sum bounds each of
-          // them, and a sum of at most 2^slack shows that no score passed m + slack. Only a warp
-          // in which some row's sum is larger (or not a number) reloads the scores and takes
-          // the plain order: maximum, rescale, exponents.
-          bool redo = true;
-          if (j > 0) {
-            if (__all_sync(0xffffffffu, full))
-              exps_row<C::TN>(x, sl2, -m, true, lim, rp);  // no key of the warp's rows masked
-            else
-              exps_row<C::TN>(x, sl2, -m, full, lim, rp);
-            const float tsum =
-                ((rp[0] + rp[1]) + (rp[2] + rp[3])) + ((rp[4] + rp[5]) + (rp[6] + rp[7]));
-            redo = __any_sync(0xffffffffu, !(tsum <= kPrefillSlackBound));
-            if (redo) {
-#pragma unroll
-              for (int c = 0; c < C::TN / 32; ++c) {
-                float v[32];
-                tmem_ld32(trow + st * C::TN + c * 32, v);
-#pragma unroll
-                for (int e = 0; e < 32; ++e) x[c * 32 + e] = v[e];
-              }
-            }
-          }
-          if (redo) {
-            // keys past this row's position are masked out; the row maximum of the scaled scores
-            // (log2 units) is the extreme raw score times the scale (the maximum for a
-            // non-negative scale, else the minimum), which saves a multiply per score; eight
-            // independent partial extremes keep the reduction off one dependency chain
-            float mp[8];
-            float ext;
-            if (sl2 >= 0.f) {
-#pragma unroll
-              for (int e = 0; e < 8; ++e) mp[e] = -INFINITY;
-#pragma unroll
-              for (int c = 0; c < C::TN; ++c) mp[c & 7] = fmaxf(mp[c & 7], (full || c <= lim) ? x[c] : -INFINITY);
-              ext = fmaxf(fmaxf(fmaxf(mp[0], mp[1]), fmaxf(mp[2], mp[3])),
-                          fmaxf(fmaxf(mp[4], mp[5]), fmaxf(mp[6], mp[7])));
-            } else {
-#pragma unroll
-              for (int e = 0; e < 8; ++e) mp[e] = INFINITY;
-#pragma unroll
-              for (int c = 0; c < C::TN; ++c) mp[c & 7] = fminf(mp[c & 7], (full || c <= lim) ? x[c] : INFINITY);
-              ext = fminf(fminf(fminf(mp[0], mp[1]), fminf(mp[2], mp[3])),
-                          fminf(fminf(mp[4], mp[5]), fminf(mp[6], mp[7])));
-            }
-            const float mx = ext * sl2;
-            const bool grow = mx > m + kPrefillRescaleSlack;
-            if (__any_sync(0xffffffffu, grow)) {
-              const float mnew = grow ? mx : m;
-              // 0 on the first tile (m = -inf); 1 for rows whose maximum did not grow
-              const float f = mnew == -INFINITY ? 1.f : prefill_exp2(m - mnew);
-              l *= f;
-              if (j > 0) {
-                // O holds tiles < j: wait for the last P.V, then scale this row of O in TMEM
-                ok = pipe_wait(bar(kBarPV + ((gj - 1) & 1)), ((gj - 1) >> 1) & 1, abort_flag, a.err);
-                if (!ok) break;
-                tc_fence_after();
-#pragma unroll
-                for (int c = 0; c < HD / 32; ++c) {
-                  float v[32];
-                  tmem_ld32(trow + C::kOCol + c * 32, v);
-#pragma unroll
-                  for (int e = 0; e < 32; ++e) v[e] *= f;
-                  tmem_st32(trow + C::kOCol + c * 32, v);
-                }
-                tmem_wait_st();
-              }
-              m = mnew;
-            }
-            // P = exp2(s * scale * log2e - m): the scale is folded into one FMA per score (packed
-            // fp32 pairs: one FFMA2 for two exponents, one FADD2 for two sums); masked keys give 0
+          for (int e = 0; e < 32; ++e) x[c * 32 + e] = v[e];
+        }
+        const int lim = pos - j * C::TN;
+        const bool full = lim >= C::TN - 1;
+        float rp[8];
+        // After a row's first tile its running maximum m seldom grows by more than the slack,
+        // so a tile first takes its exponents with m as it stands and no maximum pass: the
+        // terms are non-negative (masked keys give 0), so the tile's row sum bounds each of
+        // them, and a sum of at most 2^slack shows that no score passed m + slack. Only a warp
+        // in which some row's sum is larger (or not a number) reloads the scores and takes
+        // the plain order: maximum, rescale, exponents.
+        bool redo = true;
+        if (j > 0) {
+          if (__all_sync(0xffffffffu, full))
+            exps_row<C::TN>(x, sl2, -m, true, lim, rp);  // no key of the warp's rows masked
+          else
             exps_row<C::TN>(x, sl2, -m, full, lim, rp);
-          }
-          l += ((rp[0] + rp[1]) + (rp[2] + rp[3])) + ((rp[4] + rp[5]) + (rp[6] + rp[7]));
-          // P buffer st was last read by the P.V of global tile gj - 2
-          if (gj >= 2) {
-            ok = pipe_wait(bar(kBarPV + st), ((gj >> 1) - 1) & 1, abort_flag, a.err);
-            if (!ok) break;
-          }
-          const uint32_t prow = p_buf(st) + row * 128;
+          const float tsum =
+              ((rp[0] + rp[1]) + (rp[2] + rp[3])) + ((rp[4] + rp[5]) + (rp[6] + rp[7]));
+          redo = __any_sync(0xffffffffu, !(tsum <= kPrefillSlackBound));
+          if (redo) {
 #pragma unroll
-          for (int c8 = 0; c8 < C::TN / 8; ++c8) {
-            uint4 w;
-            w.x = pack_half2(x[c8 * 8 + 0], x[c8 * 8 + 1]);
-            w.y = pack_half2(x[c8 * 8 + 2], x[c8 * 8 + 3]);
-            w.z = pack_half2(x[c8 * 8 + 4], x[c8 * 8 + 5]);
-            w.w = pack_half2(x[c8 * 8 + 6], x[c8 * 8 + 7]);
-            sts128(prow + (c8 >> 3) * (C::kRows * 128) + (((c8 & 7) ^ (row & 7)) << 4), w);
+            for (int c = 0; c < C::TN / 32; ++c) {
+              float v[32];
+              tmem_ld32(trow + st * C::TN + c * 32, v);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) x[c * 32 + e] = v[e];
+            }
           }
+        }
+        if (redo) {
+          // keys past this row's position are masked out; the row maximum of the scaled scores
+          // (log2 units) is the extreme raw score times the scale (the maximum for a
+          // non-negative scale, else the minimum), which saves a multiply per score; eight
+          // independent partial extremes keep the reduction off one dependency chain
+          float mp[8];
+          float ext;
+          if (sl2 >= 0.f) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) mp[e] = -INFINITY;
+#pragma unroll
+            for (int c = 0; c < C::TN; ++c) mp[c & 7] = fmaxf(mp[c & 7], (full || c <= lim) ? x[c] : -INFINITY);
+            ext = fmaxf(fmaxf(fmaxf(mp[0], mp[1]), fmaxf(mp[2], mp[3])),
+                        fmaxf(fmaxf(mp[4], mp[5]), fmaxf(mp[6], mp[7])));
+          } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) mp[e] = INFINITY;
+#pragma unroll
+            for (int c = 0; c < C::TN; ++c) mp[c & 7] = fminf(mp[c & 7], (full || c <= lim) ? x[c] : INFINITY);
+            ext = fminf(fminf(fminf(mp[0], mp[1]), fminf(mp[2], mp[3])),
+                        fminf(fminf(mp[4], mp[5]), fminf(mp[6], mp[7])));
+          }
+          const float mx = ext * sl2;
+          const bool grow = mx > m + kPrefillRescaleSlack;
+          if (__any_sync(0xffffffffu, grow)) {
+            const float mnew = grow ? mx : m;
+            // 0 on the first tile (m = -inf); 1 for rows whose maximum did not grow
+            const float f = mnew == -INFINITY ? 1.f : prefill_exp2(m - mnew);
+            l *= f;
+            if (j > 0) {
+              // O holds tiles < j: wait for the last P.V, then scale this row of O in TMEM
+              ok = pipe_wait(bar(kBarPV + ((gj - 1) & 1)), ((gj - 1) >> 1) & 1, abort_flag, a.err);
+              if (!ok) break;
+              tc_fence_after();
+#pragma unroll
+              for (int c = 0; c < HD / 32; ++c) {
+                float v[32];
+                tmem_ld32(trow + C::kOCol + c * 32, v);
+#pragma unroll
+                for (int e = 0; e < 32; ++e) v[e] *= f;
+                tmem_st32(trow + C::kOCol + c * 32, v);
+              }
+              tmem_wait_st();
+            }
+            m = mnew;
+          }
+          // P = exp2(s * scale * log2e - m): the scale is folded into one FMA per score (packed
+          // fp32 pairs: one FFMA2 for two exponents, one FADD2 for two sums); masked keys give 0
+          exps_row<C::TN>(x, sl2, -m, full, lim, rp);
+        }
+        l += ((rp[0] + rp[1]) + (rp[2] + rp[3])) + ((rp[4] + rp[5]) + (rp[6] + rp[7]));
+        // P buffer st was last read by the P.V of global tile gj - 2
+        if (gj >= 2) {
+          ok = pipe_wait(bar(kBarPV + st), ((gj >> 1) - 1) & 1, abort_flag, a.err);
+          if (!ok) break;
+        }
+        const uint32_t prow = p_buf(st) + row * 128;
+#pragma unroll
+        for (int c8 = 0; c8 < C::TN / 8; ++c8) {
+          uint4 w;
+          w.x = pack_half2(x[c8 * 8 + 0], x[c8 * 8 + 1]);
+          w.y = pack_half2(x[c8 * 8 + 2], x[c8 * 8 + 3]);
+          w.z = pack_half2(x[c8 * 8 + 4], x[c8 * 8 + 5]);
+          w.w = pack_half2(x[c8 * 8 + 6], x[c8 * 8 + 7]);
+          sts128(prow + (c8 >> 3) * (C::kRows * 128) + (((c8 & 7) ^ (row & 7)) << 4), w);
         }
         fence_proxy_async();
         tc_fence_before();
@@ -671,7 +679,6 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
       }
       if (ok) {
         tc_fence_after();
-        if constexpr (kScored) l = sr.l;
         const float inv = l > 0.f ? 1.f / l : 0.f;
         float *dst = a.out + (static_cast<size_t>(it.q0 + it.tok0 + t) * a.qh + it.kv * a.g + h) * HD;
         // whole 32-byte sectors where out allows (L2 then never fills a partly written sector
@@ -683,26 +690,19 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
         for (int c = 0; c < HD / 32; ++c) {
           float v[32];
           tmem_ld32(trow + C::kOCol + c * 32, v);
-          if constexpr (kScored) {
-            if (valid)
-              store_half32(a.out16 + (static_cast<size_t>(it.q0 + it.tok0 + t) * a.qh +
-                                      it.kv * a.g + h) * HD + c * 32,
-                           v, inv, a.out_v8, pol);
-          } else {
 #pragma unroll
-            for (int e = 0; e < 32; ++e) v[e] *= inv;
-            if (valid) {
-              if (a.out_v8) {
+          for (int e = 0; e < 32; ++e) v[e] *= inv;
+          if (valid) {
+            if (a.out_v8) {
 #pragma unroll
-                for (int e = 0; e < 32; e += 8)
-                  st_global_v8(dst + c * 32 + e, v[e], v[e + 1], v[e + 2], v[e + 3], v[e + 4],
-                               v[e + 5], v[e + 6], v[e + 7], pol);
-              } else {
+              for (int e = 0; e < 32; e += 8)
+                st_global_v8(dst + c * 32 + e, v[e], v[e + 1], v[e + 2], v[e + 3], v[e + 4],
+                             v[e + 5], v[e + 6], v[e + 7], pol);
+            } else {
 #pragma unroll
-                for (int e = 0; e < 32; e += 4)
-                  *reinterpret_cast<float4 *>(dst + c * 32 + e) =
-                      make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
-              }
+              for (int e = 0; e < 32; e += 4)
+                *reinterpret_cast<float4 *>(dst + c * 32 + e) =
+                    make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
             }
           }
         }

@@ -7,7 +7,7 @@
 #include "internal.h"
 #include "pagedattn.h"
 #include "prefill2_scored_kernel.cuh"
-#include "prefill_kernel.cuh"
+#include "prefill_scored_kernel.cuh"
 
 namespace pa {
 
@@ -65,11 +65,15 @@ cudaError_t launch_prefill_hd(const PrefillArgsOf<kScored> &a, const PrefillLaun
                               cudaStream_t stream) {
   static std::atomic<bool> set[kMaxDevicesPrefill];
   constexpr int smem = PrefillCfg<HD>::kSmem + 1024;
-  auto kern = prefill_kernel<HD, kScored>;
+  void (*kern)(PrefillArgsOf<kScored>, CUtensorMap, CUtensorMap, CUtensorMap);
+  if constexpr (kScored)
+    kern = prefill_scored_kernel<HD>;
+  else
+    kern = prefill_kernel<HD>;
   const cudaError_t e = allow_smem(kern, smem, set);
   if (e != cudaSuccess) return e;
   if constexpr (kScored)
-    return launch_early(kern, l.grid, kPrefillThreads, smem, stream, a, l.tq, l.tk, l.tv);
+    return launch_early(kern, l.grid, kScoredThreads, smem, stream, a, l.tq, l.tk, l.tv);
   kern<<<l.grid, kPrefillThreads, smem, stream>>>(a, l.tq, l.tk, l.tv);
   return cudaGetLastError();
 }

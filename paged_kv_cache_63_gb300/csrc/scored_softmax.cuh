@@ -23,7 +23,7 @@
 
 #include <type_traits>
 
-#include "prefill_common.cuh"
+#include "prefill_kernel.cuh"
 #include "score_rule.cuh"
 
 namespace pa {
@@ -129,11 +129,28 @@ __device__ __forceinline__ void extremes(const float (&v)[64], float &hi, float 
   lo = min3(fminf(mn[0], mn[1]), mn[2], mn[3]);
 }
 
+// Moves a row's reference to `top`, its largest score in the unit at hand, if that passes it by
+// more than the slack; rescale(f) then multiplies the accumulated output by f (where `later`;
+// false: a wait gave up). Warp-collective.
+template <class Rescale>
+__device__ __forceinline__ bool settle_row(ScoredRow &row, float top, bool later,
+                                           Rescale rescale) {
+  const bool grow = top > row.m + kScoredSlack;
+  if (__any_sync(0xffffffffu, grow)) {
+    const float mnew = grow ? top : row.m;
+    const float f = mnew == -INFINITY ? 1.f : prefill_exp2(row.m - mnew);
+    row.l *= f;
+    if (later && !rescale(f)) return false;
+    row.m = mnew;
+  }
+  return true;
+}
+
 // One unit of 64 keys from token `base`: raw dot products become weights relative to row.m,
 // row.l grows by their sum. Warp-collective. `io` gives access to the row: load(v) reads the raw
-// columns, emit(pk) takes their weights as fp16 pairs, rescale(f) multiplies the row's
-// accumulated output by f (called when `later`, a unit after the row's first; false from it: a
-// wait gave up). A row that has seen nothing yet has m = -inf.
+// columns, settle(row, top, later) brings row.m up to date for a largest score `top` (settle_row;
+// `later`: a unit after the row's first), emit(pk) takes the weights as fp16 pairs. False: a wait
+// gave up. A row that has seen nothing yet has m = -inf.
 template <class Io>
 __device__ __forceinline__ bool scored_weights(const ScoreArgs &s, float scale_log2,
                                                ScoredRow &row, int base, bool later,
@@ -141,6 +158,7 @@ __device__ __forceinline__ bool scored_weights(const ScoreArgs &s, float scale_l
   const int lo = row.lo - base, hi = row.hi - base;
   float pk[32];
   if (!__any_sync(0xffffffffu, hi >= 0 && lo < 64 && lo <= hi)) {
+    if (!io.settle(row, -INFINITY, later)) return false;
 #pragma unroll
     for (int e = 0; e < 32; ++e) pk[e] = 0.f;
     io.emit(pk);
@@ -187,14 +205,7 @@ __device__ __forceinline__ bool scored_weights(const ScoreArgs &s, float scale_l
     extremes(v, high, low);
     top = fmaf(mult >= 0.f ? high : low, mult, offset);
   }
-  const bool grow = top > row.m + kScoredSlack;
-  if (__any_sync(0xffffffffu, grow)) {
-    const float mnew = grow ? top : row.m;
-    const float f = mnew == -INFINITY ? 1.f : prefill_exp2(row.m - mnew);
-    row.l *= f;
-    if (later && !io.rescale(f)) return false;
-    row.m = mnew;
-  }
+  if (!io.settle(row, top, later)) return false;
   if (row.m != -INFINITY) offset -= row.m;
   const float2 m2 = make_float2(mult, mult), n2 = make_float2(offset, offset);
   float rp[4] = {0.f, 0.f, 0.f, 0.f};
