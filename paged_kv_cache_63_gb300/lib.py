@@ -197,10 +197,21 @@ def _ptr(x):
     return x.data_ptr()
 
 
-def _torch_on_gpu():
-    """torch, if the process uses it on a GPU (then there is a current device and stream)."""
+_raw_stream = _get_device = None  # torch's raw accessors, once the process uses a GPU
+
+
+def _torch_on_gpu() -> bool:
+    """Whether the process uses torch on a GPU: then there is a current device and stream, read
+    through torch's raw accessors (building the stream object costs more than a small launch)."""
+    global _raw_stream, _get_device
+    if _raw_stream is not None:
+        return True
     t = sys.modules.get("torch")
-    return t if t is not None and t.cuda.is_initialized() else None
+    if t is None or not t.cuda.is_initialized():
+        return False
+    _get_device = t._C._cuda_getDevice
+    _raw_stream = t._C._cuda_getCurrentRawStream
+    return True
 
 
 def _addresses(where, *xs):
@@ -208,10 +219,9 @@ def _addresses(where, *xs):
     passes unseen)."""
     dev, out = None, []
     for x in xs:
-        if x is not None and not isinstance(x, int):
+        if x is not None and x.__class__ is not int:
             if dev is None:
-                t = _torch_on_gpu()
-                dev = t._C._cuda_getDevice() if t is not None else 0
+                dev = _get_device() if _torch_on_gpu() else 0
             if x.get_device() != dev or not x.is_contiguous():
                 raise PagedAttnError(1, where)
             x = x.data_ptr()
@@ -223,22 +233,21 @@ def _rows(where, x, heads, head_dim, stride):
     """(address, row stride in elements) of [tokens][heads][head_dim] rows whose tokens may be
     apart, as slices of a fused projection's output are. An address takes ``stride`` as given
     (0: packed)."""
-    if x is None or isinstance(x, int):
+    if x is None or x.__class__ is int:
         return x, stride
     n, h, d = x.stride()
     rows, nh, nd = x.shape
-    if nh != heads or nd != head_dim or d != 1 or (h != head_dim and heads > 1):
+    if nh != heads or nd != head_dim or d != 1 or (h != head_dim and heads > 1) \
+            or x.get_device() != (_get_device() if _torch_on_gpu() else 0):
         raise PagedAttnError(1, where)
     # one row has no next one: any stride says the same
     return x.data_ptr(), n if rows > 1 else 0
 
 
 def _stream(s):
-    """The stream's handle; None: torch's current stream (the default one without torch). Read
-    through the raw accessor: building the stream object costs more than a small launch."""
+    """The stream's handle; None: torch's current stream (the default one without torch)."""
     if s is None:
-        t = _torch_on_gpu()
-        return t._C._cuda_getCurrentRawStream(t._C._cuda_getDevice()) if t is not None else None
+        return _raw_stream(_get_device()) if _torch_on_gpu() else None
     if isinstance(s, int):
         return s
     return s.cuda_stream
