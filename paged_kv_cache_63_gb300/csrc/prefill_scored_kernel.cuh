@@ -1,43 +1,26 @@
 // prefill_scored_kernel.cuh -- multi-token attention under a score rule (pa_prefill_scored) for
 // head_dim 256: one query tile per work item, CTAs that stay resident and take over work items
-// of CTAs that have not started, as in prefill_kernel.cuh (work items, K/V
-// stages, score and weight buffers).
+// of CTAs that have not started, as in prefill_kernel.cuh (work items, K/V stages, score
+// buffers).
 //
-// What differs:
-//  * Two groups of four softmax warps take turns, one the even key tiles, the other the odd ones,
-//    so that two tiles' softmax run at once (one group alone took 2440 cycles a tile of 64 keys).
-//    The weights of both go into one output, so a row has one reference maximum: a group settles
-//    it for its tile after the other has for the tile before (shared memory and a barrier a
-//    warp pair), which comes after the scores and before the exponents of each.
-//  * Q and the weights are tensor-memory operands of the products, which then read shared memory
-//    for K and V alone: 64 KB a tile beside the 64 KB that the loads write. With Q and P in
-//    shared memory 224 KB passed through it a tile, 1750 cycles at its 128 bytes a cycle, and two
-//    groups were no faster than one.
-//   TMEM (512 columns): S buffers at 0 and 64, the weights of a tile over the first 32 columns of
-//   its scores; Q at 128 (row = lane, two fp16 a column); O at 256.
+// What differs, beside the keys that an item sees: the weights are a tensor-memory operand of
+// their product (over the first 32 columns of their scores), so no shared memory is written for
+// them and no buffer waited for (472 -> 418 us on two 4096-token prompts of 24 / 4 heads with a
+// prefix and a cap). Q stays in shared memory: as a tensor-memory operand too, copied there by
+// the softmax warps at the start of an item, it took the same prompts to 337 us without a cap
+// (371) but to 438 us with one, where those warps are the bound. Two softmax groups taking turns
+// on the tiles gained nothing: one MMA warp's issue (1200 of 2150 cycles a tile) bound them.
 #pragma once
 
 #include "early_launch.cuh"
-#include "prefill2_kernel.cuh"
 #include "scored_softmax.cuh"
 
 namespace pa {
 
-// Barrier slots behind those of the plain kernel.
-enum : int {
-  kS1Settled = kNumBars,     // + row group: the reference is settled for another tile
-  kS1Handed = kNumBars + 4,  // + row group: the other group's part of the sums is handed over
-  kS1ORead = kNumBars + 8,   // the item's O has been read (4 arrivals)
-  kS1QReady = kNumBars + 9,  // the item's Q is in tensor memory, its shared copy free (4 arrivals)
-  kNumBarsS1 = kNumBars + 10
-};
-
-// Warps: 0 loads K, 2 Q and V; 1 owns TMEM and issues the MMAs; 3 schedules; 4..7 and 8..11 are
-// the softmax groups. Registers are split as in the two-tile kernels (384 threads).
-constexpr int kScoredThreads = 384;
+// Warps: 0 loads K, 2 Q and V; 1 owns TMEM and issues the MMAs; 3 schedules; 4..7 softmax.
+constexpr int kScoredThreads = 256;
 constexpr int kScoredVWarp = 2;
 constexpr int kScoredSchedWarp = 3;
-constexpr uint32_t kQCol = 128;  // Q's first tensor-memory column
 
 // An item's keys go from kv_lo, the first token that some row sees, to kv_len, and its key tiles
 // are taken last to first (as in prefill2_scored_kernel.cuh): tile j is the one j before last_tile.
@@ -84,24 +67,13 @@ __device__ __forceinline__ ScoredItem1 scored_item1_of(const PrefillScoredArgs &
 // to, stable once the barrier of the last P.V has completed.
 template <int HD>
 struct ScoredTile1 {
-  uint32_t ts, to, pv_bar, pv_parity, settled_bar;
-  int gj;  // the tile's global index
-  float *ref;
+  uint32_t ts, to, pv_bar, pv_parity;
   volatile int *abort_flag;
   unsigned *err;
   __device__ __forceinline__ void load(float (&c)[64]) const { tmem_ld64(ts, c); }
   __device__ __forceinline__ void emit(const float (&pk)[32]) const { tmem_st32(ts, pk); }
   __device__ __forceinline__ bool settle(ScoredRow &row, float top, bool later) const {
-    volatile float *shared = ref;
-    if (gj > 0 && !pipe_wait(settled_bar, (gj - 1) & 1, abort_flag, err)) return false;
-    if (later) {  // what the other group made of the reference since
-      const float m = *shared;
-      if (row.m != m) {
-        row.l = row.l > 0.f ? row.l * prefill_exp2(row.m - m) : 0.f;
-        row.m = m;
-      }
-    }
-    const bool ok = settle_row(row, top, later, [&](float f) {
+    return settle_row(row, top, later, [&](float f) {
       // O holds the tiles before: wait for the last P.V, then scale this row of O in TMEM
       if (!pipe_wait(pv_bar, pv_parity, abort_flag, err)) return false;
       tc_fence_after();
@@ -113,14 +85,8 @@ struct ScoredTile1 {
         for (int e = 0; e < 32; ++e) v[e] *= f;
         tmem_st32(to + c * 32, v);
       }
-      tmem_wait_st();
       return true;
     });
-    if (!ok) return false;
-    *shared = row.m;
-    __syncwarp();
-    if ((threadIdx.x & 31) == 0) mbar_arrive(settled_bar);
-    return true;
   }
 };
 
@@ -133,13 +99,11 @@ __global__ void __launch_bounds__(kScoredThreads, 1)
   using C = PrefillCfg<HD>;
   using Item = ScoredItem1;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t bars[kNumBarsS1];
+  __shared__ __align__(8) uint64_t bars[kNumBars];
   __shared__ __align__(16) uint4 clc_answer;
   __shared__ Item items[2];
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_word;
-  __shared__ float row_ref[4][32];     // a row's reference after the latest unit
-  __shared__ float other_sum[2][4][32];  // the other group's part of the rows' sums, by item parity
   volatile int *abort_flag = &abort_word;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -153,11 +117,10 @@ __global__ void __launch_bounds__(kScoredThreads, 1)
   auto bar = [&](int i) { return smem_addr(&bars[i]); };
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kNumBarsS1; ++i) {
+    for (int i = 0; i < kNumBars; ++i) {
       uint32_t count = 1;
       if (i == kBarPFull || i == kBarPFull + 1) count = 128;
-      if (i == kBarItemEmpty || i == kBarItemEmpty + 1) count = kItemReaders1 + 4;
-      if (i == kS1ORead || i == kS1QReady) count = 4;
+      if (i == kBarItemEmpty || i == kBarItemEmpty + 1) count = kItemReaders1;
       mbar_init(bar(i), count);
     }
     abort_word = 0;
@@ -198,7 +161,6 @@ __global__ void __launch_bounds__(kScoredThreads, 1)
 
   // K/V tiles, S and P buffers and their barrier phases are numbered across the work items
   // a CTA runs: tile t (global) uses stage / buffer t & 1 and phase (t >> 1) & 1.
-  if (warp < 4) regs_decrease<kPrefill2SmallRegs>();
   if (warp == kScoredSchedWarp) {
     // ================= scheduler: one request per item (as in prefill2_kernel) =================
     int kv = blockIdx.x, b = blockIdx.y, z = blockIdx.z;
@@ -262,8 +224,8 @@ __global__ void __launch_bounds__(kScoredThreads, 1)
       if (!is_v && lane == 0) mbar_arrive(bar(kBarProdStart));
       if (!it.live) continue;
       if (is_v) {
-        // Q of this item, once the previous item's has been copied out
-        if (q_loads > 0) ok = pipe_wait(bar(kS1QReady), (q_loads - 1) & 1, abort_flag, a.err);
+        // Q of this item, once the previous item's last score MMA has read the buffer
+        if (q_loads > 0) ok = pipe_wait(bar(kBarQEmpty), (q_loads - 1) & 1, abort_flag, a.err);
         if (!ok) break;
         if (lane == 0) {
           mbar_arrive_expect_tx(bar(kBarQ), C::KB * q_rows * 128);
@@ -334,7 +296,7 @@ __global__ void __launch_bounds__(kScoredThreads, 1)
       ok = take_item(k, it);
       if (!ok || it.stop) break;
       if (!it.live) continue;
-      ok = pipe_wait(bar(kS1QReady), q_waits & 1, abort_flag, a.err);
+      ok = pipe_wait(bar(kBarQ), q_waits & 1, abort_flag, a.err);
       ++q_waits;
       if (!ok) break;
       tc_fence_after();
@@ -351,12 +313,14 @@ __global__ void __launch_bounds__(kScoredThreads, 1)
             // descriptors = base descriptor + step offset / 16 (the empty asm keeps the
             // compiler from hoisting every step's descriptor into registers)
             const uint32_t d = tmem + st * C::TN;
+            uint64_t qd = smem_desc_sw128(sq, 16, 1024);
             uint64_t kd = smem_desc_sw128(k_stage(st), 16, 1024);
-            asm volatile("" : "+l"(kd));
+            asm volatile("" : "+l"(qd), "+l"(kd));
 #pragma unroll
             for (int ks = 0; ks < HD / 16; ++ks) {
+              const uint64_t ad = qd + (((ks >> 2) * (C::kRows * 128) + (ks & 3) * 32) >> 4);
               const uint64_t bd = kd + (((ks >> 2) * (C::TN * 128) + (ks & 3) * 32) >> 4);
-              mma_f16_ts_warp(d, tmem + kQCol + ks * 8, bd, C::kIdescS, ks > 0);
+              mma_f16_ss_warp(d, ad, bd, C::kIdescS, ks > 0);
             }
             mma_commit_warp(bar(kBarSFull + st));
             mma_commit_warp(bar(kBarKEmpty + st));
@@ -367,8 +331,6 @@ __global__ void __launch_bounds__(kScoredThreads, 1)
           const int i = j - 1, t = g + i, st = t & 1;
           ok = pipe_wait(bar(kBarPFull + st), (t >> 1) & 1, abort_flag, a.err);
           if (ok) ok = pipe_wait(bar(kBarVFull + st), (t >> 1) & 1, abort_flag, a.err);
-          if (ok && i == 0 && q_waits > 1)
-            ok = pipe_wait(bar(kS1ORead), (q_waits - 2) & 1, abort_flag, a.err);
           if (!ok) break;
           tc_fence_after();
           // likewise the rows before the first token that some row sees
@@ -397,7 +359,8 @@ __global__ void __launch_bounds__(kScoredThreads, 1)
             __syncwarp();
           }
           {
-            // the item's first P.V overwrites O, once the previous item's has been read
+            // the item's first P.V overwrites O: the softmax released this P only after it
+            // had read the previous item's O
             uint64_t vd = smem_desc_sw128(v_stage(st), C::TN * 128, 1024);
             asm volatile("" : "+l"(vd));
 #pragma unroll
@@ -418,111 +381,51 @@ __global__ void __launch_bounds__(kScoredThreads, 1)
     if (lane == 0) drain_wait(bar(kBarDone), 0, a.err);
     __syncwarp();
   } else {
-    regs_increase<kPrefill2BigRegs>();
-    // ====== softmax, one query row per thread: warps 4..7 take the tiles with even global index,
-    // 8..11 the odd ones ======
-    const int group = warp >= 8 ? 1 : 0;
+    // ================= softmax: one query row per thread =================
     const int rg = warp & 3;
     const int row = rg * 32 + lane;
     const int t = row / a.g, h = row - t * a.g;
     const uint32_t trow = tmem + (static_cast<uint32_t>(rg * 32) << 16);
-    int g = 0, live = 0;  // tiles and live items so far
+    int g = 0;  // tiles so far
     bool ok = true;
     for (int k = 0; ok; ++k) {
       Item it;
       ok = take_item(k, it);
       if (!ok || it.stop) break;
       if (!it.live) continue;
+      const bool valid = row < q_rows && it.tok0 + t < it.n;
       // rows past the tile's last token repeat it (and are not stored)
       ScoredRow sr = scored_row(a.s, it.q0, it.base_pos - it.tok0,
                                 min(it.tok0 + min(t, a.qt - 1), it.n - 1), it.kv * a.g + h,
                                 it.prefix);
-      if ((g & 1) == group) {
-        // the group of the first tile (free while the other finishes the item before) moves Q to
-        // tensor memory, once the last score MMA of that item has read the Q there
-        ok = pipe_wait(bar(kBarQ), live & 1, abort_flag, a.err);
-        if (ok && live > 0) ok = pipe_wait(bar(kBarQEmpty), (live - 1) & 1, abort_flag, a.err);
+      for (int j = 0; j < it.ntiles; ++j, ++g) {
+        const int st = g & 1;
+        ok = pipe_wait(bar(kBarSFull + st), (g >> 1) & 1, abort_flag, a.err);
         if (!ok) break;
         tc_fence_after();
-#pragma unroll
-        for (int kb = 0; kb < C::KB; ++kb) {
-          float q[32];
-#pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            const uint4 w =
-                lds128(sq + kb * (C::kRows * 128) + row * 128 + ((c ^ (row & 7)) << 4));
-            q[4 * c] = __uint_as_float(w.x);
-            q[4 * c + 1] = __uint_as_float(w.y);
-            q[4 * c + 2] = __uint_as_float(w.z);
-            q[4 * c + 3] = __uint_as_float(w.w);
-          }
-          tmem_st32(trow + kQCol + kb * 32, q);
-        }
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kS1QReady));
-      }
-      const int last = g + it.ntiles - 1;  // global index of the item's last tile
-      for (int gj = g + ((g ^ group) & 1); gj <= last; gj += 2) {
-        const int j = gj - g, st = group;
-        ok = pipe_wait(bar(kBarSFull + st), (gj >> 1) & 1, abort_flag, a.err);
-        if (!ok) break;
-        tc_fence_after();
-        const ScoredTile1<HD> io = {trow + st * C::TN,
-                                    trow + C::kOCol,
-                                    bar(kBarPV + (st ^ 1)),
-                                    static_cast<uint32_t>(((gj - 1) >> 1) & 1),
-                                    bar(kS1Settled + rg),
-                                    gj,
-                                    &row_ref[rg][lane],
-                                    abort_flag,
-                                    a.err};
+        const ScoredTile1<HD> io = {trow + st * C::TN, trow + C::kOCol, bar(kBarPV + (st ^ 1)),
+                                    static_cast<uint32_t>(((g - 1) >> 1) & 1), abort_flag, a.err};
         ok = scored_weights(a.s, a.scale_log2, sr, tile_token(it, j), j > 0, io);
         if (!ok) break;
         tmem_wait_st();
         tc_fence_before();
         mbar_arrive(bar(kBarPFull + st));
       }
+      if (ok) ok = pipe_wait(bar(kBarPV + ((g - 1) & 1)), ((g - 1) >> 1) & 1, abort_flag, a.err);
       if (!ok) break;
-      // The group of the last tile writes the rows; the other hands over its part of the sums,
-      // brought to the final reference.
-      float *handed = &other_sum[live & 1][rg][lane];
-      if ((last & 1) != group) {
-        if (it.ntiles > 1) {
-          ok = pipe_wait(bar(kS1Settled + rg), last & 1, abort_flag, a.err);
-          if (!ok) break;
-          const float m = *static_cast<volatile float *>(&row_ref[rg][lane]);
-          if (sr.m != m) sr.l = sr.l > 0.f ? sr.l * prefill_exp2(sr.m - m) : 0.f;
-        }
-        *static_cast<volatile float *>(handed) = sr.l;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kS1Handed + rg));
-      } else {
-        ok = pipe_wait(bar(kS1Handed + rg), live & 1, abort_flag, a.err);
-        if (ok) ok = pipe_wait(bar(kBarPV + (last & 1)), (last >> 1) & 1, abort_flag, a.err);
-        if (!ok) break;
-        tc_fence_after();
-        const float l = sr.l + *static_cast<volatile float *>(handed);
-        const float inv = l > 0.f ? 1.f / l : 0.f;
-        const bool valid = row < q_rows && it.tok0 + t < it.n;
-        const uint64_t pol = l2_evict_first_policy();
-        uint16_t *dst =
-            a.out16 + (static_cast<size_t>(it.q0 + it.tok0 + t) * a.qh + it.kv * a.g + h) * HD;
+      tc_fence_after();
+      // Once these loads have returned, O may be overwritten by the next item's first P.V, which
+      // waits for this warp's next P.
+      const float inv = sr.l > 0.f ? 1.f / sr.l : 0.f;
+      const uint64_t pol = l2_evict_first_policy();
+      uint16_t *dst =
+          a.out16 + (static_cast<size_t>(it.q0 + it.tok0 + t) * a.qh + it.kv * a.g + h) * HD;
 #pragma unroll
-        for (int c = 0; c < HD / 32; ++c) {
-          float v[32];
-          tmem_ld32(trow + C::kOCol + c * 32, v);
-          if (c == HD / 32 - 1) {  // O is read: the next item's first P.V may overwrite it
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(kS1ORead));
-          }
-          if (valid) store_half32(dst + c * 32, v, inv, a.out_v8, pol);
-        }
+      for (int c = 0; c < HD / 32; ++c) {
+        float v[32];
+        tmem_ld32(trow + C::kOCol + c * 32, v);
+        if (valid) store_half32(dst + c * 32, v, inv, a.out_v8, pol);
       }
-      g += it.ntiles;
-      ++live;
     }
   }
 

@@ -223,6 +223,26 @@ def test_more_items_than_sms_deterministic_and_replayed(shape):
 
 
 @gpu
+@pytest.mark.parametrize("shape", ["hd64_g2", "hd128_g1", "hd256_g6", "hd256_g1"])
+@pytest.mark.parametrize("window", [1, 40, 150])
+def test_many_short_items(shape, window):
+    """Work items of one to four key tiles, hundreds to an SM, in an order that gives every warp
+    items without a tile of its own between others: repeated calls give the same rows."""
+    b = 300
+    ctx = np.arange(b) * 37 % 230 + 20
+    w = case(shape, ctx=ctx, new=np.minimum(ctx, 20 + np.arange(b) % 60), pad=0)
+    rule = Rule(window=window, softcap=9.0)
+    want = attend(w, rule, **ERRORS)
+    d, first = w.to_device(), None
+    for _ in range(8):
+        got, flags = gpu_prefill(w, rule, d=d)
+        assert flags == 0
+        first = got if first is None else first
+        assert np.array_equal(got, first)
+    assert_within(first, *want, True)
+
+
+@gpu
 def test_two_calls_at_once():
     t = torch()
     w = case("hd128_g4")
