@@ -14,8 +14,8 @@
 // scores behind the other tile's weights: 1300 of 2500 cycles a unit). Its order is PV(n),
 // S(n + 2): S(n + 2) goes into the buffer that PV(n) reads, so it follows it in issue order. A
 // softmax that has to rescale O_X waits for the last PV_X.
-// Warps: 0 loads Q, K and V; 1 and 2 issue the MMAs of tile A and B (1 also owns the tensor
-// memory); 3 schedules; 4..7 are tile A's softmax, 8..11 tile B's.
+// Warps: 0 loads K and V; 1 and 2 issue the MMAs of tile A and B (1 also owns the tensor
+// memory); 3 schedules and loads Q; 4..7 are tile A's softmax, 8..11 tile B's.
 #pragma once
 
 #include "early_launch.cuh"
@@ -209,7 +209,10 @@ __global__ void __launch_bounds__(kPrefill2Threads, 1)
     // ================= scheduler =================
     int kv = blockIdx.x, b = blockIdx.y, z = blockIdx.z;
     bool stop = false;
+    int q_loads = 0;
+    const uint64_t pol_q = l2_evict_first_policy();  // each Q tile is read once
     const uint32_t answer = smem_addr(&clc_answer);
+    if (lane == 0) prefetch_tensormap(&tq);
     for (int k = 0;; ++k) {
       // publish item k once every reader has taken item k - 2 from the same entry
       if (k >= 2 && !pipe_wait(bar(kS2ItemEmpty + (k & 1)), ((k >> 1) - 1) & 1, abort_flag, a.err))
@@ -221,6 +224,22 @@ __global__ void __launch_bounds__(kPrefill2Threads, 1)
       if (lane == 0) {
         items[k & 1] = it;
         mbar_arrive(bar(kS2ItemFull + (k & 1)));
+      }
+      __syncwarp();
+      if (it.live) {
+        // both query tiles, once the previous item's last score MMAs have read Q; here rather
+        // than by the producer, whose K and V tiles of the item must not wait for that
+        if (q_loads > 0 && !pipe_wait(bar(kS2QEmpty), (q_loads - 1) & 1, abort_flag, a.err)) break;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(bar(kS2QFull), 2 * C::KB * q_rows * 128);
+#pragma unroll
+          for (int x = 0; x < 2; ++x)
+#pragma unroll
+            for (int kb = 0; kb < C::KB; ++kb)
+              tma_load_3d(q_tile(x) + kb * (C::kRows * 128), &tq, bar(kS2QFull), kb * 64,
+                          it.kv * a.g, it.q0 + (x ? it.tok0_b : it.tok0_a), pol_q);
+        }
+        ++q_loads;
       }
       __syncwarp();
       if (stop) break;
@@ -244,22 +263,20 @@ __global__ void __launch_bounds__(kPrefill2Threads, 1)
       b = y;
       z = zz;
     }
+    if (lane == 0 && q_loads > 0) drain_wait(bar(kS2QFull), (q_loads - 1) & 1, a.err);
+    __syncwarp();
   } else if (warp == 0) {
     // ================= producer: ring item 2t is K of global tile t, 2t + 1 its V =================
     if (lane == 0) {
-      prefetch_tensormap(&tq);
       prefetch_tensormap(&tk);
       prefetch_tensormap(&tv);
     }
-    // L2 policies: every pair of query tiles of a (sequence, K/V head) reads its K/V tiles, so
-    // they stay (evict last); each Q tile is read once (evict first)
+    // every pair of query tiles of a (sequence, K/V head) reads its K/V tiles: they stay in L2
     const uint64_t pol = l2_evict_last_policy();
-    const uint64_t pol_q = l2_evict_first_policy();
     const int rows_per_box = min(a.ps, C::TN);
     const int boxes = C::TN / rows_per_box;
     const uint32_t box_bytes = rows_per_box * 128;
     int next = 0;  // next ring item
-    int q_loads = 0;
     bool ok = true;
     for (int k = 0; ok; ++k) {
       Item it;
@@ -310,28 +327,12 @@ __global__ void __launch_bounds__(kPrefill2Threads, 1)
           page = -1;
         }
         load_tile(&tk, tok, page);
-        if (ok && j == 0) {
-          // both query tiles, once the previous item's last score MMAs have read Q
-          if (q_loads > 0) ok = pipe_wait(bar(kS2QEmpty), (q_loads - 1) & 1, abort_flag, a.err);
-          if (ok && lane == 0) {
-            mbar_arrive_expect_tx(bar(kS2QFull), 2 * C::KB * q_rows * 128);
-#pragma unroll
-            for (int x = 0; x < 2; ++x)
-#pragma unroll
-              for (int kb = 0; kb < C::KB; ++kb)
-                tma_load_3d(q_tile(x) + kb * (C::kRows * 128), &tq, bar(kS2QFull), kb * 64,
-                            it.kv * a.g, it.q0 + (x ? it.tok0_b : it.tok0_a), pol_q);
-          }
-          if (ok) ++q_loads;
-          __syncwarp();
-        }
         if (ok) load_tile(&tv, tok, page);
       }
     }
-    // drain: the last Q load and the newest item of every slot have landed (older items of a
-    // slot were consumed before it was refilled)
+    // drain: the newest item of every slot has landed (older items of a slot were consumed
+    // before it was refilled)
     if (lane == 0) {
-      if (q_loads > 0) drain_wait(bar(kS2QFull), (q_loads - 1) & 1, a.err);
       for (int r = max(0, next - C::kSlots); r < next; ++r)
         drain_wait(bar(kS2Full + r % C::kSlots), (r / C::kSlots) & 1, a.err);
     }
@@ -435,9 +436,12 @@ __global__ void __launch_bounds__(kPrefill2Threads, 1)
               issue_pv(j, hh);
             }
           }
-          if (ok && hh == 0 && j + 1 < it.nt_max) ok = wait_ring(2 * (gt + j) + 2);
-          if (ok && next) issue_s(j + 1, hh);
+          if (ok && next) {
+            if (hh == 0) ok = wait_ring(2 * (gt + j) + 2);
+            if (ok) issue_s(j + 1, hh);
+          }
         }
+        if (ok && !next && j + 1 < it.nt_max) ok = wait_ring(2 * (gt + j) + 2);
         if (!ok) break;
         release(2 * (gt + j) + 1);
         if (j + 1 < it.nt_max) {
