@@ -42,28 +42,29 @@ enum : int {
   kNumBarsS2 = 38
 };
 
-// Geometry of a work item. Its keys go from kv_lo, the first token that some row of
-// the pair sees, to kv_len. Its key tiles are taken last to first, tile j (0 .. nt_max - 1) being
-// the one j before the last: a bias by distance and most attention favour near keys, so a row
-// meets its largest scores first and rarely moves its maximum again (first to last, a steep
-// bias moved it, and rescaled O, on every tile: 7250 cycles a tile against 3600). Query tile X
-// takes part in tiles [from_X, to_X); the pair's other tile may see keys on either side of that.
-// Both spans are non-empty for a tile that has rows, overlap or touch, and cover all tiles.
-// Warp-collective.
+// Geometry of a work item. Its keys go from kv_lo, the first token that some row of the pair
+// sees, to kv_len. Its key tiles are taken last to first, tile j (0 .. nt_max - 1) being the one j
+// before the last: a bias by distance and most attention favour near keys, so a row meets its
+// largest scores first and rarely moves its reference again (first to last, a steep bias moved
+// it, and rescaled O, on every tile: 7250 cycles a tile against 3600). Query tile X takes part in
+// tiles [from_X, to_X), none if it has no rows or they see nothing. `rows` tells that the pair has
+// rows, `live` that some of them sees something; `holes` that tokens between kv_lo and kv_len may
+// be seen by nobody. Warp-collective.
 struct ScoredItem2 : Item2 {
   int kv_lo, prefix, last_tile;  // last_tile: index of the key tile taken first
   int from_a, to_a, from_b, to_b;
+  int rows, holes;
 };
 
-template <int TN>
+template <int TN, bool kFirst>
 __device__ __forceinline__ ScoredItem2 scored_item2_of(const PrefillScoredArgs &a, int kv, int b,
                                                        int pair) {
   ScoredItem2 it;
   it.kv = kv;
   it.b = b;
-  it.live = 0;
+  it.live = it.rows = 0;
   it.stop = 0;
-  it.nt_a = it.nt_b = it.nt_max = 0;
+  it.from_a = it.to_a = it.from_b = it.to_b = it.nt_max = 0;
   const int q0 = __ldg(a.qs + b), q1 = __ldg(a.qs + b + 1), ctx = __ldg(a.ctx + b);
   const int n = q1 - q0;
   it.q0 = q0;
@@ -81,27 +82,29 @@ __device__ __forceinline__ ScoredItem2 scored_item2_of(const PrefillScoredArgs &
   it.tok0_a = 2 * pair * a.qt;
   it.tok0_b = it.tok0_a + a.qt;
   if (it.tok0_a >= n) return it;
+  it.rows = 1;
   it.prefix = prefix_of(a.s, b, ctx);
-  int lo_a, lo_b;
-  seen_range(a.s, q0, ctx - n, it.tok0_a, min(it.tok0_b, n), it.prefix, lo_a, it.max_pos_a);
-  it.max_pos_b = it.max_pos_a;
-  it.kv_lo = lo_b = lo_a;
-  const bool b_rows = it.tok0_b < n;
-  if (b_rows) {
-    seen_range(a.s, q0, ctx - n, it.tok0_b, min(it.tok0_b + a.qt, n), it.prefix, lo_b, it.max_pos_b);
-    it.kv_lo = min(lo_a, lo_b);
+  int lo_a, lo_b = 0, last_a, last_b = -1;
+  bool holes = false;
+  seen_range<kFirst>(a.s, q0, ctx - n, it.tok0_a, min(it.tok0_b, n), it.prefix, lo_a, last_a, holes);
+  if (it.tok0_b < n)
+    seen_range<kFirst>(a.s, q0, ctx - n, it.tok0_b, min(it.tok0_b + a.qt, n), it.prefix, lo_b, last_b,
+               holes);
+  it.holes = holes;
+  const int last = max(last_a, last_b);
+  if (last < 0) return it;
+  it.kv_lo = last_a < 0 ? lo_b : last_b < 0 ? lo_a : min(lo_a, lo_b);
+  it.kv_len = last + 1;
+  it.last_tile = last / TN;
+  if (last_a >= 0) {
+    it.from_a = it.last_tile - last_a / TN;
+    it.to_a = it.last_tile - lo_a / TN + 1;
   }
-  // tile B's rows come after tile A's, so they see at least as far: max_pos_b >= max_pos_a, by
-  // less than a query tile's tokens (<= TN), so that from_a <= 1 <= to_b
-  it.last_tile = it.max_pos_b / TN;
-  it.from_a = it.last_tile - it.max_pos_a / TN;
-  it.from_b = 0;
-  it.to_a = it.last_tile - lo_a / TN + 1;
-  it.to_b = b_rows ? it.last_tile - lo_b / TN + 1 : 0;
-  it.nt_a = it.to_a - it.from_a;
-  it.nt_b = it.to_b;
+  if (last_b >= 0) {
+    it.from_b = it.last_tile - last_b / TN;
+    it.to_b = it.last_tile - lo_b / TN + 1;
+  }
   it.nt_max = max(it.to_a, it.to_b);
-  it.kv_len = it.max_pos_b + 1;
   it.live = 1;
   return it;
 }
@@ -132,7 +135,7 @@ struct ScoredTile2 {
   }
 };
 
-template <int HD>
+template <int HD, bool kFirst>
 __global__ void __launch_bounds__(kPrefill2Threads, 1)
     prefill2_scored_kernel(const __grid_constant__ PrefillScoredArgs a,
                            const __grid_constant__ CUtensorMap tq,
@@ -219,8 +222,8 @@ __global__ void __launch_bounds__(kPrefill2Threads, 1)
         break;
       Item it;
       it.stop = 1;
-      it.live = 0;
-      if (!stop) it = scored_item2_of<C::TN>(a, kv, b, a.n_qtiles - 1 - z);  // grid.z counts pairs
+      it.live = it.rows = 0;
+      if (!stop) it = scored_item2_of<C::TN, kFirst>(a, kv, b, a.n_qtiles - 1 - z);  // grid.z counts pairs
       if (lane == 0) {
         items[k & 1] = it;
         mbar_arrive(bar(kS2ItemFull + (k & 1)));
@@ -285,17 +288,10 @@ __global__ void __launch_bounds__(kPrefill2Threads, 1)
       if (lane == 0) mbar_arrive(bar(kS2ProdStart));
       if (!it.live) continue;
       const int32_t *bt_row = a.bt + static_cast<size_t>(it.b) * a.maxp;
-      // page of this lane's box of tile j, -1 where no row sees a token of it
-      auto page_of = [&](int j) {
+      // whether tile j's box of this lane holds a token between kv_lo and kv_len
+      auto needed = [&](int j) {
         const int tok = tile_token(it, j) + lane * rows_per_box;
-        return (j < it.nt_max && lane < boxes && tok < it.kv_len && tok + rows_per_box > it.kv_lo)
-                   ? __ldg(bt_row + (tok >> a.ps_shift))
-                   : -1;
-      };
-      auto bad_page = [&](int j, int page) {
-        const int tok = tile_token(it, j) + lane * rows_per_box;
-        return lane < boxes && tok < it.kv_len && tok + rows_per_box > it.kv_lo &&
-               (page < 0 || page >= a.num_pages);
+        return j < it.nt_max && lane < boxes && tok < it.kv_len && tok + rows_per_box > it.kv_lo;
       };
       auto load_tile = [&](const CUtensorMap *map, int tok, int page) {
         const int s = next % C::kSlots;
@@ -317,12 +313,25 @@ __global__ void __launch_bounds__(kPrefill2Threads, 1)
         }
         ++next;
       };
+      auto page_of = [&](int j) {
+        const int tok = tile_token(it, j) + lane * rows_per_box;
+        return needed(j) ? __ldg(bt_row + (tok >> a.ps_shift)) : -1;
+      };
       int page_next = page_of(0);
       for (int j = 0; j < it.nt_max && ok; ++j) {
         const int tok = tile_token(it, j) + lane * rows_per_box;
+        bool need = needed(j);
         int page = page_next;
         page_next = page_of(j + 1);
-        if (bad_page(j, page)) {
+        if (kFirst && it.holes) {  // no row may see the box
+          const unsigned seen = seen_word<C::TN>(a.s, it.q0, it.ctx - it.n, it.tok0_a,
+                                                 min(it.tok0_b + a.qt, it.n), it.prefix,
+                                                 tile_token(it, j));
+          const bool any = any_seen(seen, lane * rows_per_box, rows_per_box);
+          need = need && any;
+          if (!need) page = -1;
+        }
+        if (need && (page < 0 || page >= a.num_pages)) {
           atomicOr(a.err, PA_DEVERR_PAGE_ID);
           page = -1;
         }
@@ -389,19 +398,25 @@ __global__ void __launch_bounds__(kPrefill2Threads, 1)
         mma_commit_warp(bar(kS2PV + 2 * x + (p_n & 1)));
         ++p_n;
       };
-      // V rows outside [kv_lo, kv_len) hold cache slots that no row sees (possibly never
-      // written): P is zero there, but 0 * NaN is not, so clear them before the tile's first P.V
-      // (both MMA warps do, with the same zeros).
+      // V rows of tokens that no row sees (outside [kv_lo, kv_len), or in holes) may hold anything:
+      // P is zero there, but 0 * NaN is not, so clear them before the tile's first P.V (both MMA
+      // warps do, with the same zeros).
       auto clear_v = [&](int j) {
         const int first = j == it.nt_max - 1 ? max(it.kv_lo - tile_token(it, j), 0) : 0;
         const int end = j == 0 ? min(it.kv_len - tile_token(it, j), C::TN) : C::TN;
-        const int dead = (first + C::TN - end) * 8;  // 16-byte chunks of a column block
-        if (dead == 0) return;
+        if (first == 0 && end == C::TN && !(kFirst && it.holes)) return;
+        unsigned seen = bits_between(first - 32 * lane, end - 1 - 32 * lane);
+        if (kFirst && it.holes)
+          seen = seen_word<C::TN>(a.s, it.q0, it.ctx - it.n, it.tok0_a,
+                                  min(it.tok0_b + a.qt, it.n), it.prefix, tile_token(it, j));
         uint8_t *vg = sgen + C::kRingOff + ((2 * (gt + j) + 1) % C::kSlots) * C::kSlotBytes;
-        for (int c = lane; c < C::KB * dead; c += 32) {
-          const int kb = c / dead, r = c % dead;
-          const int at = r < first * 8 ? r : end * 8 + r - first * 8;
-          *reinterpret_cast<uint4 *>(vg + kb * (C::TN * 128) + at * 16) = make_uint4(0, 0, 0, 0);
+#pragma unroll 1
+        for (int c = lane; c < C::TN * 8; c += 32) {  // 16-byte chunks of a column block
+          const int r = c >> 3;
+          if (kFirst ? any_seen(seen, r, 1) : r >= first && r < end) continue;
+#pragma unroll
+          for (int kb = 0; kb < C::KB; ++kb)
+            *reinterpret_cast<uint4 *>(vg + kb * (C::TN * 128) + c * 16) = make_uint4(0, 0, 0, 0);
         }
         fence_proxy_async();
         __syncwarp();
@@ -471,13 +486,17 @@ __global__ void __launch_bounds__(kPrefill2Threads, 1)
       ok = take_item(k, it);
       if (!ok || it.stop) break;
       const int from = x ? it.from_b : it.from_a, end = x ? it.to_b : it.to_a;
-      if (!it.live || end == 0) continue;
       const int tok0 = x ? it.tok0_b : it.tok0_a;
+      if (!it.rows || tok0 >= it.n) continue;
       const bool valid = row < q_rows && tok0 + t < it.n;
+      const size_t out_row = (static_cast<size_t>(it.q0 + tok0 + t) * a.qh + it.kv * a.g + h) * HD;
+      if (kFirst && end == 0) {  // no row of the tile sees anything
+        if (valid) store_zero_row(a.out16 + out_row, HD);
+        continue;
+      }
       // rows past the tile's last token repeat it (and are not stored)
       ScoredRow sr = scored_row(a.s, it.q0, it.ctx - it.n, min(tok0 + min(t, a.qt - 1), it.n - 1),
                                 it.kv * a.g + h, it.prefix);
-      const size_t out_row = (static_cast<size_t>(it.q0 + tok0 + t) * a.qh + it.kv * a.g + h) * HD;
       int base = tile_token(it, from) + 64;  // first token of the unit
       for (int u = 2 * from; u < 2 * end; ++u, ++n, base -= 64) {
         ok = pipe_wait(bar(kS2SFull + 2 * x + (n & 1)), (n >> 1) & 1, abort_flag, a.err);

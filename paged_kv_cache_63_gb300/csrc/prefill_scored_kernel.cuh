@@ -27,15 +27,16 @@ constexpr int kScoredSchedWarp = 3;
 // Warp-collective.
 struct ScoredItem1 : Item1 {
   int kv_lo, prefix, last_tile;
+  int rows, holes;  // as in the two-tile kernel
 };
 
-template <int TN>
+template <int TN, bool kFirst>
 __device__ __forceinline__ ScoredItem1 scored_item1_of(const PrefillScoredArgs &a, int kv, int b,
                                                        int qtile) {
   ScoredItem1 it;
   it.kv = kv;
   it.b = b;
-  it.live = 0;
+  it.live = it.rows = 0;
   it.stop = 0;
   it.ntiles = 0;
   const int q0 = __ldg(a.qs + b), q1 = __ldg(a.qs + b + 1), ctx = __ldg(a.ctx + b);
@@ -54,8 +55,13 @@ __device__ __forceinline__ ScoredItem1 scored_item1_of(const PrefillScoredArgs &
   it.tok0 = qtile * a.qt;
   if (it.tok0 >= n) return it;
   it.base_pos = ctx - n + it.tok0;
+  it.rows = 1;
   it.prefix = prefix_of(a.s, b, ctx);
-  seen_range(a.s, q0, ctx - n, it.tok0, min(it.tok0 + a.qt, n), it.prefix, it.kv_lo, it.max_pos);
+  bool holes = false;
+  seen_range<kFirst>(a.s, q0, ctx - n, it.tok0, min(it.tok0 + a.qt, n), it.prefix, it.kv_lo, it.max_pos,
+             holes);
+  it.holes = holes;
+  if (it.max_pos < 0) return it;
   it.kv_len = it.max_pos + 1;
   it.last_tile = it.max_pos / TN;
   it.ntiles = it.last_tile - it.kv_lo / TN + 1;
@@ -90,7 +96,7 @@ struct ScoredTile1 {
   }
 };
 
-template <int HD>
+template <int HD, bool kFirst>
 __global__ void __launch_bounds__(kScoredThreads, 1)
     prefill_scored_kernel(const __grid_constant__ PrefillScoredArgs a,
                           const __grid_constant__ CUtensorMap tq,
@@ -171,8 +177,8 @@ __global__ void __launch_bounds__(kScoredThreads, 1)
         break;
       Item it;
       it.stop = 1;
-      it.live = 0;
-      if (!stop) it = scored_item1_of<C::TN>(a, kv, b, a.n_qtiles - 1 - z);  // longest rows first
+      it.live = it.rows = 0;
+      if (!stop) it = scored_item1_of<C::TN, kFirst>(a, kv, b, a.n_qtiles - 1 - z);  // longest rows first
       if (lane == 0) {
         items[k & 1] = it;
         mbar_arrive(bar(kBarItemFull + (k & 1)));
@@ -237,22 +243,32 @@ __global__ void __launch_bounds__(kScoredThreads, 1)
         ++q_loads;
       }
       const int32_t *bt_row = a.bt + static_cast<size_t>(it.b) * a.maxp;
-      // page of this lane's box of tile j (lanes < boxes); -1 past the last needed token
-      auto needed = [&](int tok) {  // the box at token tok holds a token that some row sees
-        return lane < boxes && tok < it.kv_len && tok + rows_per_box > it.kv_lo;
+      // whether tile j's box of this lane holds a token between kv_lo and kv_len
+      auto needed = [&](int j) {
+        const int tok = tile_token(it, j) + lane * rows_per_box;
+        return j < it.ntiles && lane < boxes && tok < it.kv_len && tok + rows_per_box > it.kv_lo;
       };
       auto page_of = [&](int j) {
         const int tok = tile_token(it, j) + lane * rows_per_box;
-        return (j < it.ntiles && needed(tok)) ? __ldg(bt_row + (tok >> a.ps_shift)) : -1;
+        return needed(j) ? __ldg(bt_row + (tok >> a.ps_shift)) : -1;
       };
       // the block-table read for tile j + 1 is issued before the waits of tile j
       int page_next = page_of(0);
       for (int j = 0; j < it.ntiles && ok; ++j, ++g) {
         const int st = g & 1;
         const int tok = tile_token(it, j) + lane * rows_per_box;
+        bool need = needed(j);
         int page = page_next;
         page_next = page_of(j + 1);
-        if (needed(tok) && (page < 0 || page >= a.num_pages)) {
+        if (kFirst && it.holes) {  // no row may see the box
+          const unsigned seen = seen_word<C::TN>(a.s, it.q0, it.base_pos - it.tok0, it.tok0,
+                                                 min(it.tok0 + a.qt, it.n), it.prefix,
+                                                 tile_token(it, j));
+          const bool any = any_seen(seen, lane * rows_per_box, rows_per_box);
+          need = need && any;
+          if (!need) page = -1;
+        }
+        if (need && (page < 0 || page >= a.num_pages)) {
           if (!is_v) atomicOr(a.err, PA_DEVERR_PAGE_ID);
           page = -1;
         }
@@ -300,8 +316,6 @@ __global__ void __launch_bounds__(kScoredThreads, 1)
       ++q_waits;
       if (!ok) break;
       tc_fence_after();
-      // valid rows of the tile that holds the last needed token
-      const int rows_last = it.kv_len - tile_token(it, 0);
       for (int j = 0; j <= it.ntiles && ok; ++j) {
         if (j < it.ntiles) {
           const int t = g + j, st = t & 1;
@@ -333,27 +347,24 @@ __global__ void __launch_bounds__(kScoredThreads, 1)
           if (ok) ok = pipe_wait(bar(kBarVFull + st), (t >> 1) & 1, abort_flag, a.err);
           if (!ok) break;
           tc_fence_after();
-          // likewise the rows before the first token that some row sees
-          const int rows_first = it.kv_lo - tile_token(it, i);
-          if (i == it.ntiles - 1 && rows_first > 0) {
-            const int per_block = rows_first * 8;
+          // V rows of tokens that no row sees (outside [kv_lo, kv_len), or in holes) may hold
+          // anything; P is zero there, but 0 * NaN is not, so clear them
+          const int first = i == it.ntiles - 1 ? max(it.kv_lo - tile_token(it, i), 0) : 0;
+          const int end = i == 0 ? min(it.kv_len - tile_token(it, i), C::TN) : C::TN;
+          if (first > 0 || end < C::TN || (kFirst && it.holes)) {
+            unsigned seen = bits_between(first - 32 * lane, end - 1 - 32 * lane);
+            if (kFirst && it.holes)
+              seen = seen_word<C::TN>(a.s, it.q0, it.base_pos - it.tok0, it.tok0,
+                                      min(it.tok0 + a.qt, it.n), it.prefix, tile_token(it, i));
             uint8_t *vg = sgen + C::kVOff + st * C::kKVBytes;
-            for (int c = lane; c < C::KB * per_block; c += 32) {
-              const int kb = c / per_block, r = c % per_block;
-              *reinterpret_cast<uint4 *>(vg + kb * (C::TN * 128) + r * 16) = make_uint4(0, 0, 0, 0);
-            }
-            fence_proxy_async();
-            __syncwarp();
-          }
-          if (i == 0 && rows_last < C::TN) {
-            // V rows past the last needed token hold unread cache slots (possibly never
-            // written); P is zero there, but 0 * NaN is not, so clear them.
-            const int per_block = (C::TN - rows_last) * 8;
-            uint8_t *vg = sgen + C::kVOff + st * C::kKVBytes;
-            for (int c = lane; c < C::KB * per_block; c += 32) {
-              const int kb = c / per_block, r = c % per_block;
-              *reinterpret_cast<uint4 *>(vg + kb * (C::TN * 128) + rows_last * 128 + r * 16) =
-                  make_uint4(0, 0, 0, 0);
+#pragma unroll 1
+            for (int c = lane; c < C::TN * 8; c += 32) {  // 16-byte chunks of a column block
+              const int r = c >> 3;
+              if (kFirst ? any_seen(seen, r, 1) : r >= first && r < end) continue;
+#pragma unroll
+              for (int kb = 0; kb < C::KB; ++kb)
+                *reinterpret_cast<uint4 *>(vg + kb * (C::TN * 128) + c * 16) =
+                    make_uint4(0, 0, 0, 0);
             }
             fence_proxy_async();
             __syncwarp();
@@ -392,8 +403,14 @@ __global__ void __launch_bounds__(kScoredThreads, 1)
       Item it;
       ok = take_item(k, it);
       if (!ok || it.stop) break;
-      if (!it.live) continue;
+      if (!it.rows) continue;
       const bool valid = row < q_rows && it.tok0 + t < it.n;
+      const size_t out_row =
+          (static_cast<size_t>(it.q0 + it.tok0 + t) * a.qh + it.kv * a.g + h) * HD;
+      if (kFirst && !it.live) {  // no row sees anything
+        if (valid) store_zero_row(a.out16 + out_row, HD);
+        continue;
+      }
       // rows past the tile's last token repeat it (and are not stored)
       ScoredRow sr = scored_row(a.s, it.q0, it.base_pos - it.tok0,
                                 min(it.tok0 + min(t, a.qt - 1), it.n - 1), it.kv * a.g + h,
@@ -418,13 +435,11 @@ __global__ void __launch_bounds__(kScoredThreads, 1)
       // waits for this warp's next P.
       const float inv = sr.l > 0.f ? 1.f / sr.l : 0.f;
       const uint64_t pol = l2_evict_first_policy();
-      uint16_t *dst =
-          a.out16 + (static_cast<size_t>(it.q0 + it.tok0 + t) * a.qh + it.kv * a.g + h) * HD;
 #pragma unroll
       for (int c = 0; c < HD / 32; ++c) {
         float v[32];
         tmem_ld32(trow + C::kOCol + c * 32, v);
-        if (valid) store_half32(dst + c * 32, v, inv, a.out_v8, pol);
+        if (valid) store_half32(a.out16 + out_row + c * 32, v, inv, a.out_v8, pol);
       }
     }
   }

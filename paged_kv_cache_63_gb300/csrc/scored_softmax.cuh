@@ -224,22 +224,71 @@ __device__ __forceinline__ bool scored_weights(const ScoreArgs &s, float scale_l
   return true;
 }
 
-// The tokens that the new tokens [t0, t1) of sequence b see (t0 < t1; the sequence's query rows
-// start at q0, its new tokens at position p0), as the range its key tiles are taken from:
-// lowest first token and highest last one. A token that sees nothing counts as seeing itself,
-// so that its tile still writes its zero row. Warp-collective; a lane takes every 32nd token.
+// The range [lo, last] of the tokens that the new tokens [t0, t1) of a sequence see (its query
+// rows start at q0, its new tokens at position p0); last = -1 if they see nothing. `holes`
+// becomes true where some of them sees nothing: then tokens inside a range that is joined from
+// several may be seen by nobody (otherwise each sees itself, and what they see is in one piece).
+// kFirst: s.first is given. Warp-collective; a lane takes every 32nd token.
+template <bool kFirst>
 __device__ __forceinline__ void seen_range(const ScoreArgs &s, int q0, int p0, int t0, int t1,
-                                           int prefix, int &lo, int &last) {
-  const int p_last = p0 + t1 - 1;
-  last = p0 + t0 < prefix ? max(p_last, prefix - 1) : p_last;
-  if (!s.first) {
-    lo = min(first_seen(s, 0, p0 + t0), p0 + t0);  // the window's start grows with the position
+                                           int prefix, int &lo, int &last, bool &holes) {
+  if constexpr (!kFirst) {
+    lo = first_seen(s, 0, p0 + t0);  // the window's start grows with the position
+    last = p0 + t0 < prefix ? max(p0 + t1 - 1, prefix - 1) : p0 + t1 - 1;
     return;
   }
-  int mine = 0x7fffffff;
-  for (int t = t0 + (threadIdx.x & 31); t < t1; t += 32)
-    mine = min(mine, min(first_seen(s, static_cast<long long>(q0) + t, p0 + t), p0 + t));
-  lo = __reduce_min_sync(0xffffffffu, mine);
+  int first = 0x7fffffff, end = -1;
+  bool none = false;
+  for (int t = t0 + (threadIdx.x & 31); t < t1; t += 32) {
+    const int from = first_seen(s, static_cast<long long>(q0) + t, p0 + t);
+    const int to = p0 + t < prefix ? prefix - 1 : p0 + t;
+    if (from > to) {
+      none = true;
+    } else {
+      first = min(first, from);
+      end = max(end, to);
+    }
+  }
+  lo = __reduce_min_sync(0xffffffffu, first);
+  last = __reduce_max_sync(0xffffffffu, end);
+  if (__any_sync(0xffffffffu, none)) holes = true;
+}
+
+// Bits l .. r of a word; either may lie outside it.
+__device__ __forceinline__ unsigned bits_between(int l, int r) {
+  l = max(l, 0);
+  r = min(r, 31);
+  return l <= r ? (0xffffffffu >> (31 - r)) & (0xffffffffu << l) : 0u;
+}
+
+// Which of the TN tokens from `base` some of the new tokens [t0, t1) sees: 32 bits in each of the
+// warp's first TN / 32 lanes. Only for work items with holes. Warp-collective.
+template <int TN>
+__device__ __forceinline__ unsigned seen_word(const ScoreArgs &s, int q0, int p0, int t0, int t1,
+                                              int prefix, int base) {
+  const int lane = threadIdx.x & 31;
+  unsigned mine = 0;
+#pragma unroll 1
+  for (int w = 0; w < TN / 32; ++w, base += 32) {
+    unsigned bits = 0;
+#pragma unroll 1
+    for (int t = t0 + lane; t < t1; t += 32) {
+      const int from = first_seen(s, static_cast<long long>(q0) + t, p0 + t);
+      bits |= bits_between(from - base, (p0 + t < prefix ? prefix - 1 : p0 + t) - base);
+    }
+    bits = __reduce_or_sync(0xffffffffu, bits);
+    if (lane == w) mine = bits;
+  }
+  return mine;
+}
+
+// Whether one of the n tokens from `at` on (n a power of two, at a multiple of it) has its bit set
+// in the lanes' words. Warp-collective, with an n that is the same in all lanes.
+__device__ __forceinline__ bool any_seen(unsigned word, int at, int n) {
+  const unsigned words = __ballot_sync(0xffffffffu, word != 0);
+  const unsigned own = __shfl_sync(0xffffffffu, word, (at >> 5) & 31);
+  if (n >= 32) return (words >> ((at >> 5) & 31) & ((1u << (n >> 5)) - 1)) != 0;
+  return (own >> (at & 31) & ((1u << n) - 1)) != 0;
 }
 
 // Length of sequence b's prefix within its context.
@@ -258,6 +307,11 @@ __device__ __forceinline__ ScoredRow scored_row(const ScoreArgs &s, int q0, int 
   r.m = -INFINITY;
   r.l = 0.f;
   return r;
+}
+
+// A row that sees nothing.
+__device__ __forceinline__ void store_zero_row(uint16_t *dst, int n) {
+  for (int i = 0; i < n; i += 8) *reinterpret_cast<uint4 *>(dst + i) = make_uint4(0, 0, 0, 0);
 }
 
 // 32 consecutive fp32 outputs of a row, scaled and written as fp16.

@@ -149,6 +149,44 @@ def test_non_finite_keys_of_unseen_documents(shape):
 
 
 @gpu
+@pytest.mark.parametrize("prefix", [0, 560])
+@pytest.mark.parametrize("shape", ["hd64_g2", "hd128_g4", "hd128_g6", "hd256_g6", "hd256_g1"])
+def test_tokens_nobody_sees_between_seen_ones(shape, prefix):
+    """Rows that see nothing leave their own tokens unseen, between tokens that other rows of the
+    same work item see: their slots hold NaN and Inf, and pages of nothing else have left the
+    table."""
+    w = case(shape, ctx=[700, 411, 130], new=[200, 150, 130], pad=0)
+    first = np.zeros(w.rows, dtype=np.int64)
+    never = 1 << 30
+    first[5:40] = never                       # the first sequence: the old tokens, then two holes
+    first[40:150] = 540 + np.arange(110) // 2
+    first[150:195] = never
+    first[195:200] = 699                      # and rows that see the last token or nothing
+    at = 200
+    for j in range(150):                      # the second: every third row sees itself alone
+        first[at + j] = 411 - 150 + j if j % 3 == 0 else never
+    first[350:420] = never                    # the third: nothing, then from a later token on
+    first[420:] = 75
+    rule = Rule(first=first, softcap=10.0, prefix=np.array([prefix, 0, 0]))
+    want = attend(w, rule, **ERRORS)
+    for b in range(w.batch):
+        n = int(w.ctx[b])
+        seen = np.zeros(n + w.ps, dtype=bool)
+        for row, pos in w.rows_of(b):
+            seen[first[row]:max(pos + 1, int(rule.prefix[b]) if pos < rule.prefix[b] else 0)] = True
+        for t in range(n):
+            if not seen[t]:
+                w.k[w.bt[b, t // w.ps], t % w.ps] = np.nan
+                w.v[w.bt[b, t // w.ps], t % w.ps] = np.inf
+        for page in range(-(-n // w.ps)):
+            if not seen[page * w.ps:(page + 1) * w.ps].any():
+                w.bt[b, page] = -5
+    got, flags = gpu_prefill(w, rule)
+    assert flags == 0
+    assert_within(got, *want, True)
+
+
+@gpu
 @pytest.mark.parametrize("shape", ["hd64_g2", "hd128_g4", "hd256_g6"])
 def test_growing_maxima_and_scores_past_the_polynomial(shape):
     w = case(shape, ctx=[600, 300], new=[500, 300], pad=0)
