@@ -238,6 +238,7 @@ def _rows(where, x, heads, head_dim, stride):
     n, h, d = x.stride()
     rows, nh, nd = x.shape
     if nh != heads or nd != head_dim or d != 1 or (h != head_dim and heads > 1) \
+            or (rows > 1 and n < heads * head_dim) \
             or x.get_device() != (_get_device() if _torch_on_gpu() else 0):
         raise PagedAttnError(1, where)
     # one row has no next one: any stride says the same

@@ -292,6 +292,25 @@ def test_refusals():
     assert append(lib.problem(0, 8, 2, 64, 16, 8, 32), rope, refusal_args()) == 0
 
 
+@gpu
+def test_binding_refuses_rows_that_overlap():
+    """An expanded tensor's row stride is 0, which the library takes for packed rows."""
+    t = torch()
+    prob = lib.problem(1, 8, 2, 64, 16, 8, 32)
+    a = refusal_args()
+    a[7] = 0  # nothing to do, were the rows accepted
+    one = t.zeros(1, 8, 64, device="cuda", dtype=t.float16)
+    a[0] = one.expand(4, 8, 64)
+    assert append(prob, None, a) == 1
+    a[0] = t.zeros(4 * 512, device="cuda", dtype=t.float16).as_strided((4, 8, 64), (448, 64, 1))
+    assert append(prob, None, a) == 1
+    a[0] = one  # a single row has no next one
+    a[2] = one[:, :2].expand(4, 2, 64)
+    assert append(prob, None, a) == 1
+    a[2] = one[:, :2]
+    assert append(prob, None, a) == 0
+
+
 def test_binding_refuses_tensors_it_cannot_pass():
     t = torch()
     prob = lib.problem(1, 8, 2, 64, 16, 8, 32)
