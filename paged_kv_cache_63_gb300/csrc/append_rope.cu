@@ -206,6 +206,7 @@ extern "C" pa_status_t pa_append_rope(const pa_problem_t *problem, const pa_rope
   if ((query && query_stride < q_row) || key_stride < kv_row || value_stride < kv_row)
     return PA_ERR_INVALID_ARG;
   if (query && query_out == query && query_stride != q_row) return PA_ERR_INVALID_ARG;
+  if (rope && rope->reserved != 0) return PA_ERR_INVALID_ARG;
   const int rotary = rope ? rope->rotary_dim : 0;
   if (rotary != 0) {
     if (rotary < 0 || rotary > hd || rope->style < PA_ROPE_HALF ||

@@ -292,6 +292,14 @@ def test_refusals():
     assert append(lib.problem(0, 8, 2, 64, 16, 8, 32), rope, refusal_args()) == 0
 
 
+def test_reserved_field_is_refused():
+    rope = lib.rope(64, "half", GOOD, table_rows=128)
+    rope.reserved = 1
+    assert append(lib.problem(4, 8, 2, 64, 16, 8, 32), rope, refusal_args()) == 1
+    rope.rotary_dim = 0
+    assert append(lib.problem(4, 8, 2, 64, 16, 8, 32), rope, refusal_args()) == 1
+
+
 @gpu
 def test_binding_refuses_rows_that_overlap():
     """An expanded tensor's row stride is 0, which the library takes for packed rows."""
