@@ -832,7 +832,7 @@ extern "C" pa_status_t pa_decode_scored(const pa_problem_t *problem, const pa_sc
     int64_t most = static_cast<int64_t>(problem->max_pages_per_sequence) * problem->page_size;
     int64_t tiles = (most + pl.tile_tokens - 1) / pl.tile_tokens;
     if (a.s.window > 0 && a.s.window < most)  // a window may start anywhere in a tile
-      tiles = std::min<int64_t>(tiles, (a.s.window + 2 * pl.tile_tokens - 2) / pl.tile_tokens);
+      tiles = std::min(tiles, (int64_t{a.s.window} + 2 * pl.tile_tokens - 2) / pl.tile_tokens);
     if (tiles <= 3) {
       if (options) single = *options;
       single.schedule = PA_SCHEDULE_SINGLE;
