@@ -39,7 +39,8 @@ METRIC = "paged decode attention: KV-read GB/s (% of HBM peak) and μs per call"
 DEFAULT_WORKLOAD = "ragged"
 PREFILL_WORKLOADS = ("prefill_gqa4", "prefill_chunked", "prefill_mha", "prefill_gqa6_hd256")
 # the library's other kernels, each timed alone on a full-size workload by --kernel-case
-KERNEL_CASES = ("append", "split_combine", "prefill_hd256")
+KERNEL_CASES = ("append", "append_rope", "split_combine", "decode_scored", "prefill_scored",
+                "prefill_hd256")
 # the other full-size decode workloads, each measured into a block of its own
 OTHER_WORKLOADS = ("gqa4_mid", "mha", "long_gqa6")
 FALLBACK_HBM_GBS = 6800.0
@@ -81,8 +82,10 @@ def parse_args():
                     help="time only the multi-token kernel on its workloads (one JSON line)")
     ap.add_argument("--kernel-case", choices=KERNEL_CASES,
                     help="time one other library kernel alone on a full-size workload (one JSON "
-                         "line): the K/V append on ragged, the fixed split's partial and combine "
-                         "kernels on long_gqa6, or the head_dim-256 multi-token kernel")
+                         "line): the K/V append on ragged, the rotating append of prefill_gqa4's "
+                         "prompts, the fixed split's partial and combine kernels on long_gqa6, "
+                         "decode (gqa4_mid) and multi-token attention (prefill_gqa4) with capped "
+                         "scores in a window of 1024, or the head_dim-256 multi-token kernel")
     ap.add_argument("--splits", type=int, default=64,
                     help="splits per sequence of the split_combine case")
     ap.add_argument("--cpu-seconds", type=float, default=12.0,
@@ -511,6 +514,75 @@ def time_calls(fns, steps, warmup, torch):
     return [sum(e[k].elapsed_time(e[k + 1]) for e in ev) / steps for k in range(len(fns))]
 
 
+def append_rope_case(args, torch, lib, stream):
+    """prefill_gqa4's prompts written into the caches, keys and queries turned by position."""
+    from paged_kv_cache_63_gb300.workloads import make_prefill
+
+    p = make_prefill("prefill_gqa4")
+    w = p.cache
+    t, hd = p.total, w.head_dim
+    gen = torch.Generator(device="cuda").manual_seed(11)
+    # one fused projection's output, as a layer has it
+    qkv = torch.randn((t, w.query_heads + 2 * w.kv_heads, hd), generator=gen, device="cuda",
+                      dtype=torch.float16)
+    q, k, v = qkv.split([w.query_heads, w.kv_heads, w.kv_heads], 1)
+    angle = torch.arange(4096, device="cuda", dtype=torch.float64)[:, None] \
+        * 10000.0 ** -torch.arange(0, 1, 2 / hd, device="cuda", dtype=torch.float64)
+    table = torch.stack([angle.cos(), angle.sin()], 1).float()
+    qs, kc, vc, bt, ctx = [torch.from_numpy(x).cuda() for x in (
+        p.query_start, w.key_cache, w.value_cache, w.block_tables, w.context_lengths)]
+    q_out = torch.empty((t, w.query_heads, hd), device="cuda", dtype=torch.float16)
+    prob, rope = lib.problem_of(w), lib.rope(hd, "half", table)
+    (ms,) = time_calls([lambda: lib.pa_append_rope(prob, rope, q, k, v, qs, t, bt, ctx, q_out, kc,
+                                                   vc, stream=stream)],
+                       args.steps, args.warmup, torch)
+    # rows read and written, and the table's rows that are turned by
+    nbytes = 2 * qkv.numel() * 2 + int(w.context_lengths.max()) * hd * 4
+    return dict(workload="prefill_gqa4", kernel="pa::append_rope_kernel"), ms, "hbm", nbytes
+
+
+def decode_scored_case(args, torch, lib, stream):
+    """gqa4_mid's decode step with scores capped at 30 in a window of 1024 tokens."""
+    from paged_kv_cache_63_gb300.workloads import make_workload
+
+    w, window = make_workload("gqa4_mid"), 1024
+    d, prob = to_device(w, torch), lib.problem_of(w)
+    out = torch.empty_like(d["q"])
+    ws = torch.empty(max(lib.pa_workspace_size(prob), 256), dtype=torch.uint8, device="cuda")
+    score = lib.score(softcap=30.0, window=window, out="fp16")
+    (ms,) = time_calls([lambda: lib.pa_decode_scored(
+        prob, score, d["q"], d["k"], d["v"], d["bt"], d["ctx"], w.scale, out, None, ws,
+        ws.numel(), stream=stream)], args.steps, args.warmup, torch)
+    seen = int(np.minimum(w.context_lengths, window).astype(np.int64).sum())
+    nbytes = seen * w.kv_heads * w.head_dim * 4 + 2 * out.numel() * 2
+    return (dict(workload="gqa4_mid", kernel="pa::decode_scored_kernel, pa::join_scored_kernel",
+                 softcap=30.0, window=window), ms, "hbm", nbytes)
+
+
+def prefill_scored_case(args, torch, lib, stream):
+    """prefill_gqa4's prompts with scores capped at 30 in a window of 1024 tokens."""
+    from paged_kv_cache_63_gb300.workloads import make_prefill
+
+    p, window = make_prefill("prefill_gqa4"), 1024
+    w = p.cache
+    q, qs, k, v, bt, ctx = [torch.from_numpy(x).cuda() for x in (
+        p.query, p.query_start, w.key_cache, w.value_cache, w.block_tables, w.context_lengths)]
+    out, prob = torch.empty_like(q), lib.problem_of(w)
+    score = lib.score(softcap=30.0, window=window, out="fp16")
+    (ms,) = time_calls([lambda: lib.pa_prefill_scored(
+        prob, score, q, qs, p.total, p.max_query_len(), k, v, bt, ctx, w.scale, out,
+        stream=stream)], args.steps, args.warmup, torch)
+    new = p.new_tokens
+    pairs = sum(int(np.minimum(np.arange(c - n, c) + 1, window).sum())
+                for c, n in zip(w.context_lengths.astype(np.int64), new))
+    return (dict(workload="prefill_gqa4", kernel="pa::prefill2_scored_kernel<128>", softcap=30.0,
+                 window=window), ms, "tensor", 4.0 * pairs * w.query_heads * w.head_dim)
+
+
+RULE_CASES = {"append_rope": append_rope_case, "decode_scored": decode_scored_case,
+              "prefill_scored": prefill_scored_case}
+
+
 def run_kernel_case(args):
     """One of the library's other kernels on a full-size workload, timed alone: the command
     its ncu capture runs. Prints one JSON line with microseconds per call and the kernel's
@@ -526,7 +598,19 @@ def run_kernel_case(args):
     hbm, hbm_kind = measured_peak()
     line = {"kernel_case": args.kernel_case, "steps": args.steps, "warmup": args.warmup,
             "l2": L2_FLUSH_NOTE}
-    if args.kernel_case == "append":
+    if args.kernel_case in RULE_CASES:
+        what, ms, bound, amount = RULE_CASES[args.kernel_case](args, torch, lib, stream)
+        tensor = bound == "tensor"
+        peak, kind = measured_tensor_peak() if tensor else measured_peak()
+        rate = amount / (ms * 1e-3) / (1e12 if tensor else 1e9)
+        line.update(what, us_per_call=round(ms * 1e3, 2),
+                    roofline={"bound": bound, "achieved": round(rate, 2), "peak": peak,
+                              "unit": "TFLOP/s" if tensor else "GB/s",
+                              "frac": round(rate / peak, 4),
+                              "peak_source": f"{kind} (" + ("bf16 GEMM burst; fp16 same rate)"
+                                                            if tensor else "HBM copy)"),
+                              ("flops" if tensor else "algorithmic_bytes_per_launch"): amount})
+    elif args.kernel_case == "append":
         # one new K/V row per (sequence, K/V head) of ragged, written at the last cached
         # index (context - 1), whose page every table already holds
         w = make_workload("ragged")
