@@ -401,12 +401,12 @@ typedef struct pa_score_t {
 /* One decode step under a score rule: pa_decode_ex's operation ("[TIL] Optimizing paged
  * attention", sections "Paged Attention" and "V4 (Context-axis parallelism)") with the
  * scores and the seen tokens of `score` (host struct; NULL: no rule, fp32 out), in the
- * plan that pa_plan gives for `options` with three differences: the arithmetic is always the
+ * plan that pa_plan gives for `options` with these differences: the arithmetic is always the
  * tensor-core form (PA_MATH_SIMT: PA_ERR_UNSUPPORTED); a shared unit is always merged by a
  * kernel after the decode kernel (PA_COMBINE_FUSED: PA_ERR_UNSUPPORTED), so that a captured call
  * can be replayed as it is; and PA_SCHEDULE_AUTO means PA_SCHEDULE_SINGLE where the block
- * table's length or the window allows a sequence no more than three tiles. Probabilities are
- * kept to 22 bits and sums in fp32.
+ * table's length or the window allows a sequence no more than three tiles. Where stages is 0 the
+ * rings may be shorter than the plan's. Probabilities are kept to 22 bits and sums in fp32.
  *   out        fp32 or fp16 (score->out_type) [batch][query_heads][head_dim], 16-byte aligned,
  *              fully overwritten
  *   workspace  caller-owned device memory of workspace_bytes >= pa_workspace_size(problem,
