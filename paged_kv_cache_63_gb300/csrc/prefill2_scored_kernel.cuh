@@ -56,7 +56,7 @@ struct ScoredItem2 : Item2 {
   int rows, holes;
 };
 
-template <int TN, bool kFirst>
+template <int TN, int kParts>
 __device__ __forceinline__ ScoredItem2 scored_item2_of(const PrefillScoredArgs &a, int kv, int b,
                                                        int pair) {
   ScoredItem2 it;
@@ -86,9 +86,9 @@ __device__ __forceinline__ ScoredItem2 scored_item2_of(const PrefillScoredArgs &
   it.prefix = prefix_of(a.s, b, ctx);
   int lo_a, lo_b = 0, last_a, last_b = -1;
   bool holes = false;
-  seen_range<kFirst>(a.s, q0, ctx - n, it.tok0_a, min(it.tok0_b, n), it.prefix, lo_a, last_a, holes);
+  seen_range<kParts>(a.s, q0, ctx - n, it.tok0_a, min(it.tok0_b, n), it.prefix, lo_a, last_a, holes);
   if (it.tok0_b < n)
-    seen_range<kFirst>(a.s, q0, ctx - n, it.tok0_b, min(it.tok0_b + a.qt, n), it.prefix, lo_b, last_b,
+    seen_range<kParts>(a.s, q0, ctx - n, it.tok0_b, min(it.tok0_b + a.qt, n), it.prefix, lo_b, last_b,
                holes);
   it.holes = holes;
   const int last = max(last_a, last_b);
@@ -135,7 +135,7 @@ struct ScoredTile2 {
   }
 };
 
-template <int HD, bool kFirst>
+template <int HD, int kParts>
 __global__ void __launch_bounds__(kPrefill2Threads, 1)
     prefill2_scored_kernel(const __grid_constant__ PrefillScoredArgs a,
                            const __grid_constant__ CUtensorMap tq,
@@ -143,6 +143,7 @@ __global__ void __launch_bounds__(kPrefill2Threads, 1)
                            const __grid_constant__ CUtensorMap tv) {
   using C = Prefill2Cfg<HD>;
   using Item = ScoredItem2;
+  constexpr bool kFirst = (kParts & kRuleFirst) != 0;
   constexpr uint32_t kIdescS = idesc_f16(C::kRows, 64, 0, 0);
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t bars[kNumBarsS2];
@@ -223,7 +224,7 @@ __global__ void __launch_bounds__(kPrefill2Threads, 1)
       Item it;
       it.stop = 1;
       it.live = it.rows = 0;
-      if (!stop) it = scored_item2_of<C::TN, kFirst>(a, kv, b, a.n_qtiles - 1 - z);  // grid.z counts pairs
+      if (!stop) it = scored_item2_of<C::TN, kParts>(a, kv, b, a.n_qtiles - 1 - z);  // grid.z counts pairs
       if (lane == 0) {
         items[k & 1] = it;
         mbar_arrive(bar(kS2ItemFull + (k & 1)));
@@ -505,7 +506,7 @@ __global__ void __launch_bounds__(kPrefill2Threads, 1)
         const ScoredTile2<HD> io = {ts + 64u * (n & 1), to,
                                     bar(kS2PV + 2 * x + ((n - 1) & 1)),
                                     static_cast<uint32_t>(((n - 1) >> 1) & 1), abort_flag, a.err};
-        ok = scored_weights(a.s, a.scale_log2, sr, base, u > 2 * from, io);
+        ok = scored_weights<kParts>(a.s, a.scale_log2, sr, base, u > 2 * from, io);
         if (!ok) break;
         tmem_wait_st();
         tc_fence_before();

@@ -42,14 +42,14 @@ cudaError_t allow_smem(Kernel kern, int smem, std::atomic<bool> (&set)[kMaxDevic
 }
 
 // head_dim 64 / 128: two query tiles per CTA (a.n_qtiles counts pairs, grid.z too)
-template <int HD, bool kScored, bool kFirst>
+template <int HD, bool kScored, int kParts>
 cudaError_t launch_prefill2_hd(const PrefillArgsOf<kScored> &a, const PrefillLaunch &l,
                                cudaStream_t stream) {
   static std::atomic<bool> set[kMaxDevicesPrefill];
   constexpr int smem = Prefill2Cfg<HD>::kSmem + 1024;
   void (*kern)(PrefillArgsOf<kScored>, CUtensorMap, CUtensorMap, CUtensorMap);
   if constexpr (kScored)
-    kern = prefill2_scored_kernel<HD, kFirst>;
+    kern = prefill2_scored_kernel<HD, kParts>;
   else
     kern = prefill2_kernel<HD>;
   const cudaError_t e = allow_smem(kern, smem, set);
@@ -60,14 +60,14 @@ cudaError_t launch_prefill2_hd(const PrefillArgsOf<kScored> &a, const PrefillLau
   return cudaGetLastError();
 }
 
-template <int HD, bool kScored, bool kFirst>
+template <int HD, bool kScored, int kParts>
 cudaError_t launch_prefill_hd(const PrefillArgsOf<kScored> &a, const PrefillLaunch &l,
                               cudaStream_t stream) {
   static std::atomic<bool> set[kMaxDevicesPrefill];
   constexpr int smem = PrefillCfg<HD>::kSmem + 1024;
   void (*kern)(PrefillArgsOf<kScored>, CUtensorMap, CUtensorMap, CUtensorMap);
   if constexpr (kScored)
-    kern = prefill_scored_kernel<HD, kFirst>;
+    kern = prefill_scored_kernel<HD, kParts>;
   else
     kern = prefill_kernel<HD>;
   const cudaError_t e = allow_smem(kern, smem, set);
@@ -78,14 +78,14 @@ cudaError_t launch_prefill_hd(const PrefillArgsOf<kScored> &a, const PrefillLaun
   return cudaGetLastError();
 }
 
-template <bool kScored, bool kFirst = false>
+template <bool kScored, int kParts = 0>
 pa_status_t launch_prefill(int head_dim, const PrefillArgsOf<kScored> &a, const PrefillLaunch &l,
                            cudaStream_t stream) {
   cudaError_t e;
   switch (head_dim) {
-    case 64: e = launch_prefill2_hd<64, kScored, kFirst>(a, l, stream); break;
-    case 128: e = launch_prefill2_hd<128, kScored, kFirst>(a, l, stream); break;
-    case 256: e = launch_prefill_hd<256, kScored, kFirst>(a, l, stream); break;
+    case 64: e = launch_prefill2_hd<64, kScored, kParts>(a, l, stream); break;
+    case 128: e = launch_prefill2_hd<128, kScored, kParts>(a, l, stream); break;
+    case 256: e = launch_prefill_hd<256, kScored, kParts>(a, l, stream); break;
     default: return PA_ERR_UNSUPPORTED;
   }
   return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;

@@ -1,6 +1,21 @@
 // prefill_scored.cu -- host entry point of multi-token attention under a score rule.
 #include "prefill_launch.cuh"
 
+namespace pa {
+namespace {
+
+// Launches the kernel compiled for the rule's parts.
+template <int kParts>
+pa_status_t launch_parts(int parts, int head_dim, const PrefillScoredArgs &a,
+                         const PrefillLaunch &l, cudaStream_t stream) {
+  if (parts == kParts) return launch_prefill<true, kParts>(head_dim, a, l, stream);
+  if constexpr (kParts > 0) return launch_parts<kParts - 1>(parts, head_dim, a, l, stream);
+  return PA_ERR_UNSUPPORTED;  // not reached
+}
+
+}  // namespace
+}  // namespace pa
+
 extern "C" pa_status_t pa_prefill_scored(const pa_problem_t *problem, const pa_score_t *score,
                                          const void *query, const int32_t *query_start,
                                          int64_t total_tokens, int32_t max_query_len,
@@ -24,10 +39,8 @@ extern "C" pa_status_t pa_prefill_scored(const pa_problem_t *problem, const pa_s
   // finite dot product (below 2^41) still scores 0 in fp32 next to the maximum
   if (a.scale_log2 == 0.f) a.scale_log2 = 1e-30f;
   a.out16 = static_cast<uint16_t *>(out);
-  const cudaStream_t on = static_cast<cudaStream_t>(stream);
-  // Only with first_tokens may a row see nothing. The code for such rows slows calls that have
-  // none by its size alone: eight prompts of 2048 (head_dim 128, a window of 1024) took 312 us
-  // with it and 281 without, two of 4096 at head_dim 256 443 and 403.
-  return a.s.first ? launch_prefill<true, true>(problem->head_dim, a, l, on)
-                   : launch_prefill<true, false>(problem->head_dim, a, l, on);
+  const int parts = (a.s.cap_in != 0.f ? kRuleCap : 0) | (a.s.slopes ? kRuleSlopes : 0) |
+                    (a.s.first ? kRuleFirst : 0);
+  return launch_parts<kRuleParts - 1>(parts, problem->head_dim, a, l,
+                                      static_cast<cudaStream_t>(stream));
 }

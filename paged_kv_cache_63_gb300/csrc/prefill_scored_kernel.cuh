@@ -30,7 +30,7 @@ struct ScoredItem1 : Item1 {
   int rows, holes;  // as in the two-tile kernel
 };
 
-template <int TN, bool kFirst>
+template <int TN, int kParts>
 __device__ __forceinline__ ScoredItem1 scored_item1_of(const PrefillScoredArgs &a, int kv, int b,
                                                        int qtile) {
   ScoredItem1 it;
@@ -58,7 +58,7 @@ __device__ __forceinline__ ScoredItem1 scored_item1_of(const PrefillScoredArgs &
   it.rows = 1;
   it.prefix = prefix_of(a.s, b, ctx);
   bool holes = false;
-  seen_range<kFirst>(a.s, q0, ctx - n, it.tok0, min(it.tok0 + a.qt, n), it.prefix, it.kv_lo, it.max_pos,
+  seen_range<kParts>(a.s, q0, ctx - n, it.tok0, min(it.tok0 + a.qt, n), it.prefix, it.kv_lo, it.max_pos,
              holes);
   it.holes = holes;
   if (it.max_pos < 0) return it;
@@ -96,7 +96,7 @@ struct ScoredTile1 {
   }
 };
 
-template <int HD, bool kFirst>
+template <int HD, int kParts>
 __global__ void __launch_bounds__(kScoredThreads, 1)
     prefill_scored_kernel(const __grid_constant__ PrefillScoredArgs a,
                           const __grid_constant__ CUtensorMap tq,
@@ -104,6 +104,7 @@ __global__ void __launch_bounds__(kScoredThreads, 1)
                           const __grid_constant__ CUtensorMap tv) {
   using C = PrefillCfg<HD>;
   using Item = ScoredItem1;
+  constexpr bool kFirst = (kParts & kRuleFirst) != 0;
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t bars[kNumBars];
   __shared__ __align__(16) uint4 clc_answer;
@@ -178,7 +179,7 @@ __global__ void __launch_bounds__(kScoredThreads, 1)
       Item it;
       it.stop = 1;
       it.live = it.rows = 0;
-      if (!stop) it = scored_item1_of<C::TN, kFirst>(a, kv, b, a.n_qtiles - 1 - z);  // longest rows first
+      if (!stop) it = scored_item1_of<C::TN, kParts>(a, kv, b, a.n_qtiles - 1 - z);  // longest rows first
       if (lane == 0) {
         items[k & 1] = it;
         mbar_arrive(bar(kBarItemFull + (k & 1)));
@@ -422,7 +423,7 @@ __global__ void __launch_bounds__(kScoredThreads, 1)
         tc_fence_after();
         const ScoredTile1<HD> io = {trow + st * C::TN, trow + C::kOCol, bar(kBarPV + (st ^ 1)),
                                     static_cast<uint32_t>(((g - 1) >> 1) & 1), abort_flag, a.err};
-        ok = scored_weights(a.s, a.scale_log2, sr, tile_token(it, j), j > 0, io);
+        ok = scored_weights<kParts>(a.s, a.scale_log2, sr, tile_token(it, j), j > 0, io);
         if (!ok) break;
         tmem_wait_st();
         tc_fence_before();

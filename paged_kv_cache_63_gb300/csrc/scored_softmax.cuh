@@ -33,6 +33,9 @@ struct PrefillScoredArgs : PrefillArgs {
   uint16_t *out16;  // [total][qh][hd], fp16 bits
 };
 
+// Parts of a rule that a kernel is compiled for.
+enum : int { kRuleCap = 1, kRuleSlopes = 2, kRuleFirst = 4, kRuleParts = 8 };
+
 template <bool kScored>
 using PrefillArgsOf = std::conditional_t<kScored, PrefillScoredArgs, PrefillArgs>;
 
@@ -151,7 +154,7 @@ __device__ __forceinline__ bool settle_row(ScoredRow &row, float top, bool later
 // columns, settle(row, top, later) brings row.m up to date for a largest score `top` (settle_row;
 // `later`: a unit after the row's first), emit(pk) takes the weights as fp16 pairs. False: a wait
 // gave up. A row that has seen nothing yet has m = -inf.
-template <class Io>
+template <int kParts, class Io>
 __device__ __forceinline__ bool scored_weights(const ScoreArgs &s, float scale_log2,
                                                ScoredRow &row, int base, bool later,
                                                const Io &io) {
@@ -169,12 +172,12 @@ __device__ __forceinline__ bool scored_weights(const ScoreArgs &s, float scale_l
   io.load(v);
   float top = -INFINITY;
   bool known = false;  // whether top is the row's largest score already
-  if (s.cap_in != 0.f) {
+  if constexpr (kParts & kRuleCap) {
     // columns nobody sees may widen the extremes, and so send the warp to the exact form
     extremes(v, high, low);
     const float far = fmaxf(fabsf(high), fabsf(low));
     const bool poly = __all_sync(0xffffffffu, far * far <= s.cap_poly_max);
-    if (!masked && !s.slopes) {
+    if (!masked && !(kParts & kRuleSlopes)) {
       // capped scores are monotonic in the raw products
       top = cap_exact(s, scale_log2 >= 0.f ? high : low);
       known = true;
@@ -182,7 +185,7 @@ __device__ __forceinline__ bool scored_weights(const ScoreArgs &s, float scale_l
     cap_scores(v, s, poly);
     mult = 1.f;
   }
-  if (s.slopes) {
+  if constexpr (kParts & kRuleSlopes) {
     const int rel = base - row.pos;
     if (__all_sync(0xffffffffu, rel + 63 <= 0)) {
       add_slope(v, row.slope2, mult);
@@ -228,11 +231,11 @@ __device__ __forceinline__ bool scored_weights(const ScoreArgs &s, float scale_l
 // rows start at q0, its new tokens at position p0); last = -1 if they see nothing. `holes`
 // becomes true where some of them sees nothing: then tokens inside a range that is joined from
 // several may be seen by nobody (otherwise each sees itself, and what they see is in one piece).
-// kFirst: s.first is given. Warp-collective; a lane takes every 32nd token.
-template <bool kFirst>
+// Warp-collective; a lane takes every 32nd token.
+template <int kParts>
 __device__ __forceinline__ void seen_range(const ScoreArgs &s, int q0, int p0, int t0, int t1,
                                            int prefix, int &lo, int &last, bool &holes) {
-  if constexpr (!kFirst) {
+  if constexpr (!(kParts & kRuleFirst)) {
     lo = first_seen(s, 0, p0 + t0);  // the window's start grows with the position
     last = p0 + t0 < prefix ? max(p0 + t1 - 1, prefix - 1) : p0 + t1 - 1;
     return;
