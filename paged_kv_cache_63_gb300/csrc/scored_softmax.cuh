@@ -1,24 +1,23 @@
-// scored_softmax.cuh -- the softmax of one key tile under a score rule, for the multi-token
-// kernels: one query row per thread, the tile's raw dot products in registers.
+// scored_softmax.cuh -- the softmax of one unit of 64 keys under a score rule, for the multi-token
+// kernels: one query row per thread, the unit's raw dot products in registers.
 //
-// A tile's chain bounds the kernel (scores, weights, the two products, the next scores), and in
-// it the instructions per score of one warp and their fetching. So a tile is walked twice, first
-// for the maximum, then for the weights, each part of them written as it stands, by loops short
-// enough for the instruction cache. (One walk with the maximum as it was, checked by the sum as
-// in the causal kernels, has to keep a row's weights until the check; its code spilled -- a
-// spilled word is an L2 access, the shared memory being full -- or outgrew the cache: 6900
-// cycles a tile unrolled, 4750 as a loop of 64 columns, on capped rows in a window.)
+// These instructions bound the kernels: two warps a scheduler run them (one at head_dim 256)
+// next to the products. 64 scores, loaded once and worked on in place, and the packed weights fit
+// the registers; 128 columns spilled, and the shared memory being full a spilled word is an L2
+// access (eight prompts of 2048 in windows of 1024, capped, head_dim 128: 968 us spilling, 264 us
+// so). The code has to fit the instruction cache as well: each part of the rule is written once,
+// and what only some calls need is compiled into kernels of their own.
 //  * tanh is a polynomial on the fp32 pipe in packed pairs wherever a warp's arguments allow:
 //    tanh t = t P(t^2) with P of degree 3, fitted to the least relative error for |t| <= 1/2
 //    (5.8e-7 evaluated in fp32; weighted least squares on Chebyshev nodes, weights iterated
 //    towards the equal-ripple fit), the scale and the cap folded into its coefficients. A score
 //    is then off by at most 0.47 cap * 5.8e-7, 1.4e-5 for a cap of 50, against the 2^-11 by
-//    which the fp16 probability is rounded. A warp with a larger argument in its tile takes
-//    1 - 2 / (1 + e^2t) for it. tanh being monotonic, the first walk needs the extremes of the
-//    raw products only.
+//    which the fp16 probability is rounded. A warp with a larger argument in its unit takes
+//    1 - 2 / (1 + e^2t) for it. tanh being monotonic, the unit's maximum is that of the raw
+//    products, capped, where nothing is masked or biased.
 //  * The bias is linear in the key's column wherever no key of the columns lies past its query.
-//  * The mask is compared per score only in tiles where some row of the warp needs it, and a
-//    tile that none of the warp's rows sees is not computed at all.
+//  * The mask is compared per score only in units where some row of the warp needs it, and a
+//    unit that none of the warp's rows sees is not computed at all.
 #pragma once
 
 #include <type_traits>
@@ -82,23 +81,24 @@ __device__ __forceinline__ float cap_exact(const ScoreArgs &s, float v) {
   return fmaf(-2.f * s.cap_out, fast_rcp(1.f + e), s.cap_out);
 }
 
+// The polynomial: cap_out * tanh(v * cap_in) = v * cap_poly(v), two columns at a time.
+__device__ __forceinline__ float2 cap_poly(const ScoreArgs &s, float2 v) {
+  const float2 z = fmul2(v, v);
+  float2 p = ffma2(make_float2(s.cap_poly[3], s.cap_poly[3]), z,
+                   make_float2(s.cap_poly[2], s.cap_poly[2]));
+  p = ffma2(p, z, make_float2(s.cap_poly[1], s.cap_poly[1]));
+  return ffma2(p, z, make_float2(s.cap_poly[0], s.cap_poly[0]));
+}
+
 // v = cap_out * tanh(v * cap_in), by the polynomial where `poly` (warp-uniform) says so.
 __device__ __forceinline__ void cap_scores(float (&v)[64], const ScoreArgs &s, bool poly) {
   if (__builtin_expect(poly, 1)) {
-    const float2 c0 = make_float2(s.cap_poly[0], s.cap_poly[0]),
-                 c1 = make_float2(s.cap_poly[1], s.cap_poly[1]),
-                 c2 = make_float2(s.cap_poly[2], s.cap_poly[2]),
-                 c3 = make_float2(s.cap_poly[3], s.cap_poly[3]);
 #pragma unroll
     for (int c = 0; c < 64; c += 2) {
       const float2 x = make_float2(v[c], v[c + 1]);
-      const float2 z = fmul2(x, x);
-      float2 p = ffma2(c3, z, c2);
-      p = ffma2(p, z, c1);
-      p = ffma2(p, z, c0);
-      p = fmul2(p, x);
-      v[c] = p.x;
-      v[c + 1] = p.y;
+      const float2 y = fmul2(cap_poly(s, x), x);
+      v[c] = y.x;
+      v[c + 1] = y.y;
     }
   } else {
 #pragma unroll
@@ -118,6 +118,15 @@ __device__ __forceinline__ void add_slope(float (&v)[64], float slope2, float mu
     v[c + 1] = x.y;
     bias = fadd2(bias, step);
   }
+}
+
+// Largest absolute value of 64 columns.
+__device__ __forceinline__ float farthest(const float (&v)[64]) {
+  float mx[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int c = 0; c < 64; c += 2)
+    mx[(c >> 1) & 3] = max3(mx[(c >> 1) & 3], fabsf(v[c]), fabsf(v[c + 1]));
+  return max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
 }
 
 // Extremes of 64 columns.
@@ -149,11 +158,37 @@ __device__ __forceinline__ bool settle_row(ScoredRow &row, float top, bool later
   return true;
 }
 
+// Weights 2^x of 64 columns, arg(c) giving x of columns c and c + 1, as fp16 pairs; row.l grows by
+// their sum. Sixteen arguments are formed before their exponentials are taken.
+template <class Arg>
+__device__ __forceinline__ void weigh(ScoredRow &row, float (&pk)[32], Arg arg) {
+  float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+  for (int e0 = 0; e0 < 32; e0 += 8) {
+    float2 x[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = arg(2 * (e0 + e));
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float2 w = make_float2(prefill_exp2(x[e].x), prefill_exp2(x[e].y));
+      sum[e & 1] = fadd2(sum[e & 1], w);
+      pk[e0 + e] = __uint_as_float(pack_half2(w.x, w.y));
+    }
+  }
+  row.l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+}
+
 // One unit of 64 keys from token `base`: raw dot products become weights relative to row.m,
 // row.l grows by their sum. Warp-collective. `io` gives access to the row: load(v) reads the raw
 // columns, settle(row, top, later) brings row.m up to date for a largest score `top` (settle_row;
 // `later`: a unit after the row's first), emit(pk) takes the weights as fp16 pairs. False: a wait
 // gave up. A row that has seen nothing yet has m = -inf.
+//
+// The largest score is needed only where it may move the reference, and where nothing is masked or
+// biased the farthest raw product bounds it at half the comparisons (|tanh t| <= |t|).
+// Io::kCapWithWeights: the cap of such a unit is taken in the loop of its weights (head_dim 128, two
+// softmax warps a scheduler: 260 us against 304 for the prompts above; at head_dim 256, one warp a
+// scheduler, two capped prompts of 4096 took 387 against 371, so not there).
 template <int kParts, class Io>
 __device__ __forceinline__ bool scored_weights(const ScoreArgs &s, float scale_log2,
                                                ScoredRow &row, int base, bool later,
@@ -161,7 +196,6 @@ __device__ __forceinline__ bool scored_weights(const ScoreArgs &s, float scale_l
   const int lo = row.lo - base, hi = row.hi - base;
   float pk[32];
   if (!__any_sync(0xffffffffu, hi >= 0 && lo < 64 && lo <= hi)) {
-    if (!io.settle(row, -INFINITY, later)) return false;
 #pragma unroll
     for (int e = 0; e < 32; ++e) pk[e] = 0.f;
     io.emit(pk);
@@ -170,20 +204,33 @@ __device__ __forceinline__ bool scored_weights(const ScoreArgs &s, float scale_l
   const bool masked = !__all_sync(0xffffffffu, lo <= 0 && hi >= 63);
   float v[64], mult = scale_log2, offset = 0.f, high, low;
   io.load(v);
-  float top = -INFINITY;
-  bool known = false;  // whether top is the row's largest score already
+  bool settled = false;
   if constexpr (kParts & kRuleCap) {
-    // columns nobody sees may widen the extremes, and so send the warp to the exact form
-    extremes(v, high, low);
-    const float far = fmaxf(fabsf(high), fabsf(low));
+    // columns nobody sees may send the warp to the exact form
+    const float far = farthest(v);
     const bool poly = __all_sync(0xffffffffu, far * far <= s.cap_poly_max);
-    if (!masked && !(kParts & kRuleSlopes)) {
-      // capped scores are monotonic in the raw products
-      top = cap_exact(s, scale_log2 >= 0.f ? high : low);
-      known = true;
+    if (!(kParts & kRuleSlopes) && !masked && poly) {
+      // |tanh t| <= |t|: no score is farther from 0 than the uncapped one
+      if (__any_sync(0xffffffffu, far * fabsf(scale_log2) > row.m + kScoredSlack)) {
+        extremes(v, high, low);  // capped scores are monotonic in the raw products
+        if (!io.settle(row, cap_exact(s, scale_log2 >= 0.f ? high : low), later)) return false;
+      }
+      if constexpr (Io::kCapWithWeights) {
+        const float2 n2 = make_float2(-row.m, -row.m);
+        weigh(row, pk, [&](int c) {
+          const float2 x = make_float2(v[c], v[c + 1]);
+          return ffma2(cap_poly(s, x), x, n2);
+        });
+        io.emit(pk);
+        return true;
+      }
+      settled = true;
     }
     cap_scores(v, s, poly);
     mult = 1.f;
+  } else if (!(kParts & kRuleSlopes) && !masked) {
+    settled = !__any_sync(0xffffffffu,
+                          farthest(v) * fabsf(scale_log2) > row.m + kScoredSlack);
   }
   if constexpr (kParts & kRuleSlopes) {
     const int rel = base - row.pos;
@@ -204,25 +251,14 @@ __device__ __forceinline__ bool scored_weights(const ScoreArgs &s, float scale_l
 #pragma unroll
     for (int c = 0; c < 64; ++c) v[c] = c >= lo && c <= hi ? v[c] : none;
   }
-  if (!known) {
+  if (!settled) {
     extremes(v, high, low);
-    top = fmaf(mult >= 0.f ? high : low, mult, offset);
+    const float top = fmaf(mult >= 0.f ? high : low, mult, offset);
+    if (!io.settle(row, top, later)) return false;
   }
-  if (!io.settle(row, top, later)) return false;
   if (row.m != -INFINITY) offset -= row.m;
   const float2 m2 = make_float2(mult, mult), n2 = make_float2(offset, offset);
-  float rp[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-  for (int e = 0; e < 32; ++e) {
-    const int c = 2 * e;
-    const float2 x = ffma2(make_float2(v[c], v[c + 1]), m2, n2);
-    const float2 w = make_float2(prefill_exp2(x.x), prefill_exp2(x.y));
-    const float2 acc = fadd2(make_float2(rp[c & 2], rp[(c & 2) + 1]), w);
-    rp[c & 2] = acc.x;
-    rp[(c & 2) + 1] = acc.y;
-    pk[e] = __uint_as_float(pack_half2(w.x, w.y));
-  }
-  row.l += (rp[0] + rp[1]) + (rp[2] + rp[3]);
+  weigh(row, pk, [&](int c) { return ffma2(make_float2(v[c], v[c + 1]), m2, n2); });
   io.emit(pk);
   return true;
 }
