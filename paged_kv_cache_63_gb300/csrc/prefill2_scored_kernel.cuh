@@ -42,12 +42,15 @@ enum : int {
   kNumBarsS2 = 38
 };
 
+constexpr int kUnit = 64;  // keys of a unit
+
 // Geometry of a work item. Its keys go from kv_lo, the first token that some row of the pair
 // sees, to kv_len. Its key tiles are taken last to first, tile j (0 .. nt_max - 1) being the one j
 // before the last: a bias by distance and most attention favour near keys, so a row meets its
 // largest scores first and rarely moves its reference again (first to last, a steep bias moved
-// it, and rescaled O, on every tile: 7250 cycles a tile against 3600). Query tile X takes part in
-// tiles [from_X, to_X), none if it has no rows or they see nothing. `rows` tells that the pair has
+// it, and rescaled O, on every tile: 7250 cycles a tile against 3600). A tile is two units of 64
+// keys, taken last to first too, and query tile X takes part in units [from_X, to_X), none if it has
+// no rows or they see nothing. `rows` tells that the pair has
 // rows, `live` that some of them sees something; `holes` that tokens between kv_lo and kv_len may
 // be seen by nobody. Warp-collective.
 struct ScoredItem2 : Item2 {
@@ -97,14 +100,14 @@ __device__ __forceinline__ ScoredItem2 scored_item2_of(const PrefillScoredArgs &
   it.kv_len = last + 1;
   it.last_tile = last / TN;
   if (last_a >= 0) {
-    it.from_a = it.last_tile - last_a / TN;
-    it.to_a = it.last_tile - lo_a / TN + 1;
+    it.from_a = 2 * it.last_tile + 1 - last_a / kUnit;
+    it.to_a = 2 * it.last_tile + 2 - lo_a / kUnit;
   }
   if (last_b >= 0) {
-    it.from_b = it.last_tile - last_b / TN;
-    it.to_b = it.last_tile - lo_b / TN + 1;
+    it.from_b = 2 * it.last_tile + 1 - last_b / kUnit;
+    it.to_b = 2 * it.last_tile + 2 - lo_b / kUnit;
   }
-  it.nt_max = max(it.to_a, it.to_b);
+  it.nt_max = (max(it.to_a, it.to_b) + 1) / 2;
   it.live = 1;
   return it;
 }
@@ -395,7 +398,7 @@ __global__ void __launch_bounds__(kPrefill2Threads, 1)
         for (int ks = 0; ks < 4; ++ks) {
           const uint64_t bd = vd + ((((1 - hh) * 4 + ks) * 2048) >> 4);
           mma_f16_ts_warp(ox, sx + 64u * (p_n & 1) + ks * 8, bd, C::kIdescPV,
-                          (j > from || hh > 0 || ks > 0) ? 1u : 0u);
+                          (2 * j + hh > from || ks > 0) ? 1u : 0u);
         }
         mma_commit_warp(bar(kS2PV + 2 * x + (p_n & 1)));
         ++p_n;
@@ -432,30 +435,29 @@ __global__ void __launch_bounds__(kPrefill2Threads, 1)
       // MMAs were issued earlier by this thread and so run first
       if (ok) ok = wait_ring(2 * gt);
       if (!ok) break;
-      if (from == 0 && to > 0) {
-        issue_s(0, 0);
-        issue_s(0, 1);
-      }
+      if (from == 0 && to > 0) issue_s(0, 0);
+      if (from <= 1 && to > 1) issue_s(0, 1);
       release(2 * gt);
       if (it.nt_max == 1) mma_commit_warp(bar(kS2QEmpty));
       for (int j = 0; j < it.nt_max && ok; ++j) {
-        const bool now = from <= j && j < to;
-        const bool next = j + 1 < it.nt_max && from <= j + 1 && j + 1 < to;
+        // whether some unit of tile j + 1 is this query tile's
+        const bool next = j + 1 < it.nt_max && from < 2 * j + 4 && 2 * j + 2 < to;
         ok = wait_ring(2 * (gt + j) + 1);
         if (!ok) break;
 #pragma unroll
         for (int hh = 0; hh < 2; ++hh) {
-          if (ok && now) {
+          const int u = 2 * j + hh;
+          if (ok && from <= u && u < to) {
             ok = pipe_wait(bar(kS2PFull + 2 * x + (p_n & 1)), (p_n >> 1) & 1, abort_flag, a.err);
             if (ok) {
               tc_fence_after();
-              if (hh == 0) clear_v(j);
+              if (hh == 0 || u == from) clear_v(j);
               issue_pv(j, hh);
             }
           }
           if (ok && next) {
             if (hh == 0) ok = wait_ring(2 * (gt + j) + 2);
-            if (ok) issue_s(j + 1, hh);
+            if (ok && from <= u + 2 && u + 2 < to) issue_s(j + 1, hh);
           }
         }
         if (ok && !next && j + 1 < it.nt_max) ok = wait_ring(2 * (gt + j) + 2);
@@ -499,15 +501,15 @@ __global__ void __launch_bounds__(kPrefill2Threads, 1)
       // rows past the tile's last token repeat it (and are not stored)
       ScoredRow sr = scored_row(a.s, it.q0, it.ctx - it.n, min(tok0 + min(t, a.qt - 1), it.n - 1),
                                 it.kv * a.g + h, it.prefix);
-      int base = tile_token(it, from) + 64;  // first token of the unit
-      for (int u = 2 * from; u < 2 * end; ++u, ++n, base -= 64) {
+      int base = (2 * it.last_tile + 1 - from) * kUnit;  // first token of the unit
+      for (int u = from; u < end; ++u, ++n, base -= kUnit) {
         ok = pipe_wait(bar(kS2SFull + 2 * x + (n & 1)), (n >> 1) & 1, abort_flag, a.err);
         if (!ok) break;
         tc_fence_after();
         const ScoredTile2<HD> io = {ts + 64u * (n & 1), to,
                                     bar(kS2PV + 2 * x + ((n - 1) & 1)),
                                     static_cast<uint32_t>(((n - 1) >> 1) & 1), abort_flag, a.err};
-        ok = scored_weights<kParts>(a.s, a.scale_log2, sr, base, u > 2 * from, io);
+        ok = scored_weights<kParts>(a.s, a.scale_log2, sr, base, u > from, io);
         if (!ok) break;
         tmem_wait_st();
         tc_fence_before();
