@@ -89,10 +89,11 @@ __device__ __forceinline__ ScoredItem2 scored_item2_of(const PrefillScoredArgs &
   it.prefix = prefix_of(a.s, b, ctx);
   int lo_a, lo_b = 0, last_a, last_b = -1;
   bool holes = false;
-  seen_range<kParts>(a.s, q0, ctx - n, it.tok0_a, min(it.tok0_b, n), it.prefix, lo_a, last_a, holes);
+  seen_range<kParts>(a.s, q0, ctx - n, it.tok0_a, min(it.tok0_b, n), it.prefix, lo_a, last_a,
+                     holes);
   if (it.tok0_b < n)
-    seen_range<kParts>(a.s, q0, ctx - n, it.tok0_b, min(it.tok0_b + a.qt, n), it.prefix, lo_b, last_b,
-               holes);
+    seen_range<kParts>(a.s, q0, ctx - n, it.tok0_b, min(it.tok0_b + a.qt, n), it.prefix, lo_b,
+                       last_b, holes);
   it.holes = holes;
   const int last = max(last_a, last_b);
   if (last < 0) return it;
@@ -228,7 +229,8 @@ __global__ void __launch_bounds__(kPrefill2Threads, 1)
       Item it;
       it.stop = 1;
       it.live = it.rows = 0;
-      if (!stop) it = scored_item2_of<C::TN, kParts>(a, kv, b, a.n_qtiles - 1 - z);  // grid.z counts pairs
+      if (!stop)  // grid.z counts pairs
+        it = scored_item2_of<C::TN, kParts>(a, kv, b, a.n_qtiles - 1 - z);
       if (lane == 0) {
         items[k & 1] = it;
         mbar_arrive(bar(kS2ItemFull + (k & 1)));

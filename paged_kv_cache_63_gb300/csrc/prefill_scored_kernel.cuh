@@ -3,13 +3,15 @@
 // of CTAs that have not started, as in prefill_kernel.cuh (work items, K/V stages, score
 // buffers).
 //
-// What differs, beside the keys that an item sees: the weights are a tensor-memory operand of
-// their product (over the first 32 columns of their scores), so no shared memory is written for
-// them and no buffer waited for (472 -> 418 us on two 4096-token prompts of 24 / 4 heads with a
-// prefix and a cap). Q stays in shared memory: as a tensor-memory operand too, copied there by
-// the softmax warps at the start of an item, it took the same prompts to 337 us without a cap
-// (371) but to 438 us with one, where those warps are the bound. Two softmax groups taking turns
-// on the tiles gained nothing: one MMA warp's issue (1200 of 2150 cycles a tile) bound them.
+// What differs, beside the keys that an item sees: Q and the weights are tensor-memory operands
+// of the products, which read shared memory for K and V alone. The weights lie over the first 32
+// columns of their scores, so none are written to shared memory and no buffer is waited for (two
+// 4096-token prompts of 24 / 4 heads with a prefix and a cap: 472 -> 418 us). The softmax warps copy
+// Q there at the start of an item (the same prompts: 373 -> 361 us, without the cap 359 -> 326, with
+// slopes 368 -> 340). The softmax bounds a capped call, one warp a scheduler; a second group of
+// softmax warps taking every other tile gained nothing when it was tried.
+//   TMEM (512 columns): S buffers at 0 and 64, the weights of a tile over the first 32 columns of
+//   its scores; Q at 128 (row = lane, two fp16 a column); O at 256.
 #pragma once
 
 #include "early_launch.cuh"
@@ -17,10 +19,17 @@
 
 namespace pa {
 
+// Barrier slots behind those of the plain kernel.
+enum : int {
+  kS1QReady = kNumBars,  // the item's Q is in tensor memory, its shared copy free (4 arrivals)
+  kNumBarsS1 = kNumBars + 1
+};
+
 // Warps: 0 loads K, 2 Q and V; 1 owns TMEM and issues the MMAs; 3 schedules; 4..7 softmax.
 constexpr int kScoredThreads = 256;
 constexpr int kScoredVWarp = 2;
 constexpr int kScoredSchedWarp = 3;
+constexpr uint32_t kQCol = 128;  // Q's first tensor-memory column
 
 // An item's keys go from kv_lo, the first token that some row sees, to kv_len, and its key tiles
 // are taken last to first (as in prefill2_scored_kernel.cuh): tile j is the one j before last_tile.
@@ -58,8 +67,8 @@ __device__ __forceinline__ ScoredItem1 scored_item1_of(const PrefillScoredArgs &
   it.rows = 1;
   it.prefix = prefix_of(a.s, b, ctx);
   bool holes = false;
-  seen_range<kParts>(a.s, q0, ctx - n, it.tok0, min(it.tok0 + a.qt, n), it.prefix, it.kv_lo, it.max_pos,
-             holes);
+  seen_range<kParts>(a.s, q0, ctx - n, it.tok0, min(it.tok0 + a.qt, n), it.prefix, it.kv_lo,
+                     it.max_pos, holes);
   it.holes = holes;
   if (it.max_pos < 0) return it;
   it.kv_len = it.max_pos + 1;
@@ -107,7 +116,7 @@ __global__ void __launch_bounds__(kScoredThreads, 1)
   using Item = ScoredItem1;
   constexpr bool kFirst = (kParts & kRuleFirst) != 0;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t bars[kNumBars];
+  __shared__ __align__(8) uint64_t bars[kNumBarsS1];
   __shared__ __align__(16) uint4 clc_answer;
   __shared__ Item items[2];
   __shared__ uint32_t tmem_slot;
@@ -125,10 +134,11 @@ __global__ void __launch_bounds__(kScoredThreads, 1)
   auto bar = [&](int i) { return smem_addr(&bars[i]); };
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kNumBars; ++i) {
+    for (int i = 0; i < kNumBarsS1; ++i) {
       uint32_t count = 1;
       if (i == kBarPFull || i == kBarPFull + 1) count = 128;
       if (i == kBarItemEmpty || i == kBarItemEmpty + 1) count = kItemReaders1;
+      if (i == kS1QReady) count = 4;
       mbar_init(bar(i), count);
     }
     abort_word = 0;
@@ -180,7 +190,8 @@ __global__ void __launch_bounds__(kScoredThreads, 1)
       Item it;
       it.stop = 1;
       it.live = it.rows = 0;
-      if (!stop) it = scored_item1_of<C::TN, kParts>(a, kv, b, a.n_qtiles - 1 - z);  // longest rows first
+      if (!stop)  // longest rows first
+        it = scored_item1_of<C::TN, kParts>(a, kv, b, a.n_qtiles - 1 - z);
       if (lane == 0) {
         items[k & 1] = it;
         mbar_arrive(bar(kBarItemFull + (k & 1)));
@@ -232,8 +243,8 @@ __global__ void __launch_bounds__(kScoredThreads, 1)
       if (!is_v && lane == 0) mbar_arrive(bar(kBarProdStart));
       if (!it.live) continue;
       if (is_v) {
-        // Q of this item, once the previous item's last score MMA has read the buffer
-        if (q_loads > 0) ok = pipe_wait(bar(kBarQEmpty), (q_loads - 1) & 1, abort_flag, a.err);
+        // Q of this item, once the previous item's has been copied out
+        if (q_loads > 0) ok = pipe_wait(bar(kS1QReady), (q_loads - 1) & 1, abort_flag, a.err);
         if (!ok) break;
         if (lane == 0) {
           mbar_arrive_expect_tx(bar(kBarQ), C::KB * q_rows * 128);
@@ -314,7 +325,7 @@ __global__ void __launch_bounds__(kScoredThreads, 1)
       ok = take_item(k, it);
       if (!ok || it.stop) break;
       if (!it.live) continue;
-      ok = pipe_wait(bar(kBarQ), q_waits & 1, abort_flag, a.err);
+      ok = pipe_wait(bar(kS1QReady), q_waits & 1, abort_flag, a.err);
       ++q_waits;
       if (!ok) break;
       tc_fence_after();
@@ -329,14 +340,12 @@ __global__ void __launch_bounds__(kScoredThreads, 1)
             // descriptors = base descriptor + step offset / 16 (the empty asm keeps the
             // compiler from hoisting every step's descriptor into registers)
             const uint32_t d = tmem + st * C::TN;
-            uint64_t qd = smem_desc_sw128(sq, 16, 1024);
             uint64_t kd = smem_desc_sw128(k_stage(st), 16, 1024);
-            asm volatile("" : "+l"(qd), "+l"(kd));
+            asm volatile("" : "+l"(kd));
 #pragma unroll
             for (int ks = 0; ks < HD / 16; ++ks) {
-              const uint64_t ad = qd + (((ks >> 2) * (C::kRows * 128) + (ks & 3) * 32) >> 4);
               const uint64_t bd = kd + (((ks >> 2) * (C::TN * 128) + (ks & 3) * 32) >> 4);
-              mma_f16_ss_warp(d, ad, bd, C::kIdescS, ks > 0);
+              mma_f16_ts_warp(d, tmem + kQCol + ks * 8, bd, C::kIdescS, ks > 0);
             }
             mma_commit_warp(bar(kBarSFull + st));
             mma_commit_warp(bar(kBarKEmpty + st));
@@ -399,7 +408,7 @@ __global__ void __launch_bounds__(kScoredThreads, 1)
     const int row = rg * 32 + lane;
     const int t = row / a.g, h = row - t * a.g;
     const uint32_t trow = tmem + (static_cast<uint32_t>(rg * 32) << 16);
-    int g = 0;  // tiles so far
+    int g = 0, live = 0;  // tiles and live items so far
     bool ok = true;
     for (int k = 0; ok; ++k) {
       Item it;
@@ -413,6 +422,29 @@ __global__ void __launch_bounds__(kScoredThreads, 1)
         if (valid) store_zero_row(a.out16 + out_row, HD);
         continue;
       }
+      // Q moves to tensor memory, once the last score MMA of the item before has read the Q there
+      ok = pipe_wait(bar(kBarQ), live & 1, abort_flag, a.err);
+      if (ok && live > 0) ok = pipe_wait(bar(kBarQEmpty), (live - 1) & 1, abort_flag, a.err);
+      if (!ok) break;
+      ++live;
+      tc_fence_after();
+#pragma unroll
+      for (int kb = 0; kb < C::KB; ++kb) {
+        float q[32];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          const uint4 w = lds128(sq + kb * (C::kRows * 128) + row * 128 + ((c ^ (row & 7)) << 4));
+          q[4 * c] = __uint_as_float(w.x);
+          q[4 * c + 1] = __uint_as_float(w.y);
+          q[4 * c + 2] = __uint_as_float(w.z);
+          q[4 * c + 3] = __uint_as_float(w.w);
+        }
+        tmem_st32(trow + kQCol + kb * 32, q);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kS1QReady));
       // rows past the tile's last token repeat it (and are not stored)
       ScoredRow sr = scored_row(a.s, it.q0, it.base_pos - it.tok0,
                                 min(it.tok0 + min(t, a.qt - 1), it.n - 1), it.kv * a.g + h,
