@@ -97,6 +97,20 @@ def test_matches_formula(shape, rule):
 
 
 @gpu
+@pytest.mark.parametrize("parts", range(8))
+@pytest.mark.parametrize("shape", ["hd64_g2", "hd128_g6", "hd256_g6"])
+def test_every_kernel_of_a_rule(shape, parts):
+    """Cap, slopes and first tokens have kernels for each combination of them; windows and prefixes
+    go through all."""
+    w = case(shape, ctx=[150, 70, 3], new=[150, 20, 3], seed=parts)
+    rule = dict(softcap=4.0 if parts & 1 else 0.0,
+                slopes=slopes_of(w.query_heads) if parts & 2 else None,
+                first=documents(w, 25) if parts & 4 else None)
+    check(w, Rule(**rule))
+    check(w, Rule(window=40, prefix=np.array([90, 0, 2]), **rule))
+
+
+@gpu
 @pytest.mark.parametrize("shape", ["hd64_g2", "hd128_g1", "hd256_g1"])
 def test_one_new_token_each(shape):
     w = case(shape, ctx=[1, 2, 128, 129, 400, 257], new=[1] * 6)
