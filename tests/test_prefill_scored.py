@@ -403,6 +403,52 @@ def test_append_prefill_and_decode_steps_together(shape):
         assert_within(o.cpu().numpy(), *attend(now, rule, **ERRORS), True)
 
 
+@gpu
+@pytest.mark.parametrize("head_major", [0, 1])
+def test_pages_past_32_bit_offsets(head_major):
+    """Appended to, and attended from, pages that lie more than 2^31 elements into the caches: the
+    same bits as from a small cache."""
+    t = torch()
+    qh, kvh, hd, ps = 16, 8, 256, 256
+    ctx, rows = [400, 300], 700
+    far = 4300  # pages of 2^19 elements
+    scale, rope_dim = 0.0625, 64
+    g = t.Generator(device="cuda").manual_seed(5)
+    qkv = t.randn(rows, qh + 2 * kvh, hd, generator=g, device="cuda", dtype=t.float16)
+    ang = t.rand(512, rope_dim // 2, generator=g, device="cuda") * 6
+    rope = lib.rope(rope_dim, "interleaved", t.stack([ang.cos(), ang.sin()], 1).contiguous())
+    put = lambda x: t.tensor(x, dtype=t.int32, device="cuda")  # noqa: E731
+    qs, dctx = put([0, 400, 700]), put(ctx)
+    shape = (kvh, ps, hd) if head_major else (ps, kvh, hd)
+    outs = []
+    for pages, table in [(4, [[2, 0], [3, 1]]), (far, [[far - 1, 4097], [4, far - 2]])]:
+        k, v = (t.empty((pages, *shape), dtype=t.float16, device="cuda") for _ in range(2))
+        bt = put(table)
+        prob = lib.problem(2, qh, kvh, hd, ps, 2, pages, head_major)
+        q = t.empty(rows, qh, hd, dtype=t.float16, device="cuda")
+        o, last = t.empty_like(q), t.empty(2, qh, hd, dtype=t.float16, device="cuda")
+        rule = lib.score(softcap=20.0, window=150, out="fp16")
+        lib.pa_append_rope(prob, rope, qkv[:, :qh], qkv[:, qh:qh + kvh], qkv[:, qh + kvh:], qs, rows,
+                           bt, dctx, q, k, v)
+        lib.pa_prefill_scored(prob, rule, q, qs, rows, 400, k, v, bt, dctx, scale, o)
+        n = lib.pa_workspace_size(prob)
+        ws = t.empty(max(n, 256), dtype=t.uint8, device="cuda")
+        lib.pa_decode_scored(prob, rule, q[[399, 699]].contiguous(), k, v, bt, dctx, scale, last,
+                             workspace=ws, workspace_bytes=n)
+        t.cuda.synchronize()
+        assert lib.pa_get_device_error() == 0
+        outs.append([x.cpu().numpy() for x in (q, o, last, k[bt[:, 0].long()])])
+        del k, v
+        t.cuda.empty_cache()
+    for small, large in zip(*outs):
+        assert np.isfinite(small).all()
+        assert np.array_equal(small.view(np.uint16), large.view(np.uint16))
+    # the newest token of each sequence, both ways: two outputs below 8 rounded to fp16 (2^-9 each)
+    # and weights rounded to fp16 (2^-11 of values below 8)
+    a, b = outs[1][1][[399, 699]], outs[1][2]
+    assert np.abs(a).max() < 8 and np.abs(a.astype(np.float64) - b).max() < 2 * 2 ** -9 + 2 ** -8
+
+
 # ---------------------------------------------------------------------------- refusals
 def prefill(prob, score, a, **kw):
     return lib.status_of(lib.pa_prefill_scored, prob, score, *a, **kw)
