@@ -321,7 +321,8 @@ typedef struct pa_rope_t {
  *   query_start  int32 [batch + 1], device, as for pa_prefill
  *   query_out    fp16 [total_tokens][query_heads][head_dim], packed; may be `query` itself
  *                when its rows are packed, and may overlap nothing else
- * Rows before query_start[0] and from query_start[batch] on are left alone, in query_out too.
+ * With total_tokens 0 nothing is done and the rows' addresses may be NULL. Rows before
+ * query_start[0] and from query_start[batch] on are left alone, in query_out too.
  * A sequence with inconsistent offsets is skipped and flagged (PA_DEVERR_QUERY_START), one
  * with a length out of range likewise (PA_DEVERR_CONTEXT). A token whose page id is outside
  * the pool (PA_DEVERR_PAGE_ID) or whose position is outside the table (PA_DEVERR_POSITION) is
@@ -423,7 +424,8 @@ pa_status_t pa_decode_scored(const pa_problem_t *problem, const pa_score_t *scor
  * arguments and checks ("[TIL] Optimizing paged attention", section "Flash Attention" over
  * the paged cache) with the scores and the seen tokens of `score` (host struct, not NULL). The
  * rows of first_tokens are the query's ([total_tokens]; rows of no new token are not read).
- * Key tiles that none of a query tile's tokens sees are skipped.
+ * Key tiles that none of a query tile's tokens sees are skipped. With total_tokens 0 nothing is
+ * done, and query and out may be NULL.
  *   out        fp16 [total_tokens][query_heads][head_dim], 16-byte aligned; rows of new tokens
  *              are written, other rows are left untouched. score->out_type must be PA_OUT_FP16
  *              (PA_ERR_UNSUPPORTED): the probabilities meet V rounded to fp16, so a wider output

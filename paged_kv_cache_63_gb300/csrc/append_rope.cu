@@ -195,8 +195,9 @@ extern "C" pa_status_t pa_append_rope(const pa_problem_t *problem, const pa_rope
   using namespace pa;
   pa_status_t st = check_problem_public(problem);
   if (st != PA_OK) return st;
-  if (!new_key || !new_value || !query_start || !block_tables || !context_lengths || !key_cache ||
-      !value_cache || (query == nullptr) != (query_out == nullptr))
+  if (((!new_key || !new_value) && total_tokens != 0) || !query_start || !block_tables ||
+      !context_lengths || !key_cache || !value_cache ||
+      (query == nullptr) != (query_out == nullptr))
     return PA_ERR_INVALID_ARG;
   if (total_tokens < 0 || total_tokens >= (int64_t(1) << 31)) return PA_ERR_INVALID_ARG;
   const int64_t hd = problem->head_dim;

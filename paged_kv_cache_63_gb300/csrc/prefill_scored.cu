@@ -31,6 +31,10 @@ extern "C" pa_status_t pa_prefill_scored(const pa_problem_t *problem, const pa_s
   st = resolve_score(score, scale, &a.s);
   if (st != PA_OK) return st;
   if (!a.s.out_half) return PA_ERR_UNSUPPORTED;
+  if (total_tokens == 0) {  // no rows, so no addresses of any (an empty tensor's is null)
+    if (!query) query = key_cache;
+    if (!out) out = const_cast<void *>(value_cache);  // not written
+  }
   PrefillLaunch l;
   st = setup_prefill(problem, query, query_start, total_tokens, max_query_len, key_cache,
                      value_cache, block_tables, context_lengths, scale, out, options, &l, &a);

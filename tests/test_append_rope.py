@@ -292,6 +292,16 @@ def test_refusals():
     assert append(lib.problem(0, 8, 2, 64, 16, 8, 32), rope, refusal_args()) == 0
 
 
+def test_no_rows_need_no_addresses():
+    """An empty tensor's address is null."""
+    prob = lib.problem(4, 8, 2, 64, 16, 8, 32)
+    a = refusal_args()
+    a[0] = a[2] = a[4] = a[10] = None
+    assert append(prob, None, a) == 1
+    a[7] = 0
+    assert append(prob, None, a) == 0
+
+
 def test_reserved_field_is_refused():
     rope = lib.rope(64, "half", GOOD, table_rows=128)
     rope.reserved = 1

@@ -479,3 +479,15 @@ def test_refusals():
     a = list(args)
     a[2] = 0
     assert prefill(prob, half, a) == 0
+
+
+def test_no_rows_need_no_addresses():
+    """An empty tensor's address is null."""
+    prob = lib.problem(4, 32, 8, 128, 16, 256, 1024)
+    half = lib.score(softcap=5.0, out="fp16")
+    args = [None, GOOD, 0, 0, GOOD, GOOD, GOOD, GOOD, 0.1, None]
+    assert prefill(prob, half, args) == 0
+    args[2] = args[3] = 1
+    assert prefill(prob, half, args) == 1
+    assert prefill(prob, half, [None, GOOD, 0, 0, None, GOOD, GOOD, GOOD, 0.1, None]) == 1
+    assert prefill(prob, half, [None, GOOD, 0, 0, GOOD, None, GOOD, GOOD, 0.1, None]) == 1
