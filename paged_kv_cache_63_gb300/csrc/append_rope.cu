@@ -195,9 +195,13 @@ extern "C" pa_status_t pa_append_rope(const pa_problem_t *problem, const pa_rope
   using namespace pa;
   pa_status_t st = check_problem_public(problem);
   if (st != PA_OK) return st;
-  if (((!new_key || !new_value) && total_tokens != 0) || !query_start || !block_tables ||
-      !context_lengths || !key_cache || !value_cache ||
-      (query == nullptr) != (query_out == nullptr))
+  if (total_tokens == 0) {  // no rows, so no addresses of any (an empty tensor's is null)
+    query = new_key = new_value = key_cache;
+    query_out = key_cache;
+    query_stride = key_stride = value_stride = 0;
+  }
+  if (!new_key || !new_value || !query_start || !block_tables || !context_lengths || !key_cache ||
+      !value_cache || (query == nullptr) != (query_out == nullptr))
     return PA_ERR_INVALID_ARG;
   if (total_tokens < 0 || total_tokens >= (int64_t(1) << 31)) return PA_ERR_INVALID_ARG;
   const int64_t hd = problem->head_dim;

@@ -32,8 +32,8 @@ extern "C" pa_status_t pa_prefill_scored(const pa_problem_t *problem, const pa_s
   if (st != PA_OK) return st;
   if (!a.s.out_half) return PA_ERR_UNSUPPORTED;
   if (total_tokens == 0) {  // no rows, so no addresses of any (an empty tensor's is null)
-    if (!query) query = key_cache;
-    if (!out) out = const_cast<void *>(value_cache);  // not written
+    query = key_cache;
+    out = const_cast<void *>(value_cache);  // not written
   }
   PrefillLaunch l;
   st = setup_prefill(problem, query, query_start, total_tokens, max_query_len, key_cache,

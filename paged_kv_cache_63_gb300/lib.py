@@ -237,7 +237,8 @@ def _rows(where, x, heads, head_dim, stride):
         return x, stride
     n, h, d = x.stride()
     rows, nh, nd = x.shape
-    if nh != heads or nd != head_dim or d != 1 or (h != head_dim and heads > 1) \
+    # (the strides of an empty tensor say nothing)
+    if nh != heads or nd != head_dim or (rows and (d != 1 or (h != head_dim and heads > 1))) \
             or (rows > 1 and n < heads * head_dim) \
             or x.get_device() != (_get_device() if _torch_on_gpu() else 0):
         raise PagedAttnError(1, where)

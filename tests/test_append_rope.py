@@ -159,6 +159,15 @@ def test_random_ragged_batches():
 
 
 @gpu
+@pytest.mark.parametrize("pad", [0, 2])
+def test_no_new_tokens(pad):
+    """Nothing is written, from empty tensors or from rows of a padded batch alone."""
+    for fused in (True, False):
+        case = Case([0, 0], [40, 3], pad=pad, fused=fused)
+        check(case, *case.run())
+
+
+@gpu
 def test_keys_and_values_alone():
     case = Case([5, 3], [40, 3])
     got, flags = case.run(with_query=False)

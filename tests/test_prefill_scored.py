@@ -97,6 +97,13 @@ def test_matches_formula(shape, rule):
 
 
 @gpu
+@pytest.mark.parametrize("pad", [0, 2])
+def test_no_new_tokens(pad):
+    w = case("hd128_g4", ctx=[40, 0], new=[0, 0], pad=pad)
+    check(w, Rule(softcap=3.0), max_query_len=1)
+
+
+@gpu
 @pytest.mark.parametrize("parts", range(8))
 @pytest.mark.parametrize("shape", ["hd64_g2", "hd128_g6", "hd256_g6"])
 def test_every_kernel_of_a_rule(shape, parts):
