@@ -502,7 +502,7 @@ __global__ void __launch_bounds__(kPrefill2Threads, 1)
       }
       // rows past the tile's last token repeat it (and are not stored)
       ScoredRow sr = scored_row(a.s, it.q0, it.ctx - it.n, min(tok0 + min(t, a.qt - 1), it.n - 1),
-                                it.kv * a.g + h, it.prefix);
+                                it.kv * a.g + h, it.prefix, valid);
       int base = (2 * it.last_tile + 1 - from) * kUnit;  // first token of the unit
       for (int u = from; u < end; ++u, ++n, base -= kUnit) {
         ok = pipe_wait(bar(kS2SFull + 2 * x + (n & 1)), (n >> 1) & 1, abort_flag, a.err);

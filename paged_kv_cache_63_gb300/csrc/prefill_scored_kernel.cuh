@@ -448,7 +448,7 @@ __global__ void __launch_bounds__(kScoredThreads, 1)
       // rows past the tile's last token repeat it (and are not stored)
       ScoredRow sr = scored_row(a.s, it.q0, it.base_pos - it.tok0,
                                 min(it.tok0 + min(t, a.qt - 1), it.n - 1), it.kv * a.g + h,
-                                it.prefix);
+                                it.prefix, valid);
       for (int j = 0; j < it.ntiles; ++j, ++g) {
         const int st = g & 1;
         ok = pipe_wait(bar(kBarSFull + st), (g >> 1) & 1, abort_flag, a.err);

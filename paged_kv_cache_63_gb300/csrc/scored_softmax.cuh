@@ -43,9 +43,11 @@ using PrefillArgsOf = std::conditional_t<kScored, PrefillScoredArgs, PrefillArgs
 constexpr float kScoredSlack = 15.f;  // log2 units
 
 // A query row: its position, the tokens [lo, hi] it sees, its head's slope * log2 e, and the
-// softmax so far (reference maximum in base 2, sum).
+// softmax so far (reference maximum in base 2, sum). `counts` is false for a row of the query tile
+// that is no new token's: its scores may be anything.
 struct ScoredRow {
   int pos, lo, hi;
+  bool counts;
   float slope2, m, l;
 };
 
@@ -206,9 +208,13 @@ __device__ __forceinline__ bool scored_weights(const ScoreArgs &s, float scale_l
   io.load(v);
   bool settled = false;
   if constexpr (kParts & kRuleCap) {
-    // columns nobody sees may send the warp to the exact form
+    // what a row does not see, and rows that do not count, must not choose the warp's form of tanh
+    if (masked) {
+#pragma unroll
+      for (int c = 0; c < 64; ++c) v[c] = c >= lo && c <= hi ? v[c] : 0.f;
+    }
     const float far = farthest(v);
-    const bool poly = __all_sync(0xffffffffu, far * far <= s.cap_poly_max);
+    const bool poly = __all_sync(0xffffffffu, !row.counts || far * far <= s.cap_poly_max);
     if (!(kParts & kRuleSlopes) && !masked && poly) {
       // |tanh t| <= |t|: no score is farther from 0 than the uncapped one
       if (__any_sync(0xffffffffu, far * fabsf(scale_log2) > row.m + kScoredSlack)) {
@@ -337,8 +343,9 @@ __device__ __forceinline__ int prefix_of(const ScoreArgs &s, int b, int ctx) {
 
 // The thread's row: new token t of sequence b (position p0 + t).
 __device__ __forceinline__ ScoredRow scored_row(const ScoreArgs &s, int q0, int p0, int t, int head,
-                                                int prefix) {
+                                                int prefix, bool counts) {
   ScoredRow r;
+  r.counts = counts;
   r.pos = p0 + t;
   r.lo = first_seen(s, static_cast<long long>(q0) + t, r.pos);
   r.hi = r.pos < prefix ? prefix - 1 : r.pos;

@@ -208,6 +208,27 @@ def test_tokens_nobody_sees_between_seen_ones(shape, prefix):
 
 
 @gpu
+@pytest.mark.parametrize("slopes", [False, True])
+@pytest.mark.parametrize("shape", ["hd64_g2", "hd128_g4", "hd128_g6", "hd256_g6"])
+def test_bits_do_not_depend_on_what_is_not_seen(shape, slopes):
+    """Slots outside the contexts, tokens before the window and rows of no new token may hold large
+    values, which would take another form of tanh."""
+    w = case(shape, ctx=[300, 1, 129, 200], new=[170, 1, 60, 31], q_scale=1.0, pad=5)
+    rule = Rule(softcap=20.0, window=100, slopes=slopes_of(w.query_heads) if slopes else None)
+    for b in range(w.batch):
+        w.forget(b, max(0, int(w.ctx[b] - w.new[b]) - rule.window + 1))
+    rows, unseen = int(w.qs[-1]), np.isnan(w.k)
+    outs = []
+    for fill in (0.0, 3000.0, np.nan):
+        w.k[unseen] = fill
+        w.q[rows:] = fill
+        out, flags = gpu_prefill(w, rule)
+        assert flags == 0
+        outs.append(out[:rows].view(np.uint16))
+    assert np.array_equal(outs[0], outs[1]) and np.array_equal(outs[0], outs[2])
+
+
+@gpu
 @pytest.mark.parametrize("shape", ["hd64_g2", "hd128_g4", "hd256_g6"])
 def test_growing_maxima_and_scores_past_the_polynomial(shape):
     w = case(shape, ctx=[600, 300], new=[500, 300], pad=0)
