@@ -120,7 +120,7 @@ struct ScoredTile2 {
   uint32_t ts, to, pv_bar, pv_parity;
   volatile int *abort_flag;
   unsigned *err;
-  static constexpr bool kCapWithWeights = true;
+  static constexpr bool kCapWithWeights = true, kKeysCleared = true;
   __device__ __forceinline__ void load(float (&c)[64]) const { tmem_ld64(ts, c); }
   __device__ __forceinline__ void emit(const float (&pk)[32]) const { tmem_st32(ts, pk); }
   __device__ __forceinline__ bool settle(ScoredRow &row, float top, bool later) const {
@@ -405,10 +405,11 @@ __global__ void __launch_bounds__(kPrefill2Threads, 1)
         mma_commit_warp(bar(kS2PV + 2 * x + (p_n & 1)));
         ++p_n;
       };
-      // V rows of tokens that no row sees (outside [kv_lo, kv_len), or in holes) may hold anything:
-      // P is zero there, but 0 * NaN is not, so clear them before the tile's first P.V (both MMA
-      // warps do, with the same zeros).
-      auto clear_v = [&](int j) {
+      // Rows of tokens that no row of the item sees (outside [kv_lo, kv_len), or in holes) may hold
+      // anything. Of V: P is zero there, but 0 * NaN is not, so they are cleared before the tile's
+      // first P.V. Of K: their scores are masked, but a cap chooses its form by all scores of a warp,
+      // so it must not see them either. Both MMA warps clear, with the same zeros.
+      auto clear_rows = [&](int j, int item) {
         const int first = j == it.nt_max - 1 ? max(it.kv_lo - tile_token(it, j), 0) : 0;
         const int end = j == 0 ? min(it.kv_len - tile_token(it, j), C::TN) : C::TN;
         if (first == 0 && end == C::TN && !(kFirst && it.holes)) return;
@@ -416,17 +417,23 @@ __global__ void __launch_bounds__(kPrefill2Threads, 1)
         if (kFirst && it.holes)
           seen = seen_word<C::TN>(a.s, it.q0, it.ctx - it.n, it.tok0_a,
                                   min(it.tok0_b + a.qt, it.n), it.prefix, tile_token(it, j));
-        uint8_t *vg = sgen + C::kRingOff + ((2 * (gt + j) + 1) % C::kSlots) * C::kSlotBytes;
+        uint8_t *at = sgen + C::kRingOff + (item % C::kSlots) * C::kSlotBytes;
 #pragma unroll 1
         for (int c = lane; c < C::TN * 8; c += 32) {  // 16-byte chunks of a column block
           const int r = c >> 3;
           if (kFirst ? any_seen(seen, r, 1) : r >= first && r < end) continue;
 #pragma unroll
           for (int kb = 0; kb < C::KB; ++kb)
-            *reinterpret_cast<uint4 *>(vg + kb * (C::TN * 128) + c * 16) = make_uint4(0, 0, 0, 0);
+            *reinterpret_cast<uint4 *>(at + kb * (C::TN * 128) + c * 16) = make_uint4(0, 0, 0, 0);
         }
         fence_proxy_async();
         __syncwarp();
+      };
+      // A tile's K has landed (and is cleared) from here on.
+      auto wait_keys = [&](int j) {
+        if (!wait_ring(2 * (gt + j))) return false;
+        if constexpr ((kParts & kRuleCap) != 0) clear_rows(j, 2 * (gt + j));
+        return true;
       };
       // Every ring item is waited for and released by both MMA warps, used or not, so that a
       // slot's phases stay in step with both; a commit after unused items completes at once.
@@ -435,7 +442,7 @@ __global__ void __launch_bounds__(kPrefill2Threads, 1)
       tc_fence_after();
       // the first scores overwrite buffers from which the previous item's last P.V read P: those
       // MMAs were issued earlier by this thread and so run first
-      if (ok) ok = wait_ring(2 * gt);
+      if (ok) ok = wait_keys(0);
       if (!ok) break;
       if (from == 0 && to > 0) issue_s(0, 0);
       if (from <= 1 && to > 1) issue_s(0, 1);
@@ -453,12 +460,12 @@ __global__ void __launch_bounds__(kPrefill2Threads, 1)
             ok = pipe_wait(bar(kS2PFull + 2 * x + (p_n & 1)), (p_n >> 1) & 1, abort_flag, a.err);
             if (ok) {
               tc_fence_after();
-              if (hh == 0 || u == from) clear_v(j);
+              if (hh == 0 || u == from) clear_rows(j, 2 * (gt + j) + 1);
               issue_pv(j, hh);
             }
           }
           if (ok && next) {
-            if (hh == 0) ok = wait_ring(2 * (gt + j) + 2);
+            if (hh == 0) ok = wait_keys(j + 1);
             if (ok && from <= u + 2 && u + 2 < to) issue_s(j + 1, hh);
           }
         }

@@ -85,7 +85,7 @@ struct ScoredTile1 {
   uint32_t ts, to, pv_bar, pv_parity;
   volatile int *abort_flag;
   unsigned *err;
-  static constexpr bool kCapWithWeights = false;
+  static constexpr bool kCapWithWeights = false, kKeysCleared = false;
   __device__ __forceinline__ void load(float (&c)[64]) const { tmem_ld64(ts, c); }
   __device__ __forceinline__ void emit(const float (&pk)[32]) const { tmem_st32(ts, pk); }
   __device__ __forceinline__ bool settle(ScoredRow &row, float top, bool later) const {
