@@ -49,8 +49,8 @@ constexpr int kUnit = 64;  // keys of a unit
 // before the last: a bias by distance and most attention favour near keys, so a row meets its
 // largest scores first and rarely moves its reference again (first to last, a steep bias moved
 // it, and rescaled O, on every tile: 7250 cycles a tile against 3600). A tile is two units of 64
-// keys, taken last to first too, and query tile X takes part in units [from_X, to_X), none if it has
-// no rows or they see nothing. `rows` tells that the pair has
+// keys, taken last to first too, and query tile X takes part in units [from_X, to_X), none if it
+// has no rows or they see nothing. `rows` tells that the pair has
 // rows, `live` that some of them sees something; `holes` that tokens between kv_lo and kv_len may
 // be seen by nobody. Warp-collective.
 struct ScoredItem2 : Item2 {
@@ -407,8 +407,8 @@ __global__ void __launch_bounds__(kPrefill2Threads, 1)
       };
       // Rows of tokens that no row of the item sees (outside [kv_lo, kv_len), or in holes) may hold
       // anything. Of V: P is zero there, but 0 * NaN is not, so they are cleared before the tile's
-      // first P.V. Of K: their scores are masked, but a cap chooses its form by all scores of a warp,
-      // so it must not see them either. Both MMA warps clear, with the same zeros.
+      // first P.V. Of K: their scores are masked, but a cap chooses its form by all scores of a
+      // warp, so it must not see them either. Both MMA warps clear, with the same zeros.
       auto clear_rows = [&](int j, int item) {
         const int first = j == it.nt_max - 1 ? max(it.kv_lo - tile_token(it, j), 0) : 0;
         const int end = j == 0 ? min(it.kv_len - tile_token(it, j), C::TN) : C::TN;

@@ -4,7 +4,7 @@
 // These instructions bound the kernels: two warps a scheduler run them (one at head_dim 256)
 // next to the products. 64 scores, loaded once and worked on in place, and the packed weights fit
 // the registers; 128 columns spilled, and the shared memory being full a spilled word is an L2
-// access (eight prompts of 2048 in windows of 1024, capped, head_dim 128: 968 us spilling, 261 us
+// access (eight prompts of 2048 in windows of 1024, capped, head_dim 128: 968 us spilling, 266 us
 // so). The code has to fit the instruction cache as well: each part of the rule is written once,
 // and what only some calls need is compiled into kernels of their own.
 //  * tanh is a polynomial on the fp32 pipe in packed pairs wherever a warp's arguments allow:
@@ -188,11 +188,12 @@ __device__ __forceinline__ void weigh(ScoredRow &row, float (&pk)[32], Arg arg) 
 //
 // The largest score is needed only where it may move the reference, and where nothing is masked or
 // biased the farthest raw product bounds it at half the comparisons (|tanh t| <= |t|).
-// Io::kCapWithWeights: the cap of such a unit is taken in the loop of its weights (head_dim 128, two
-// softmax warps a scheduler: 260 us against 304 for the prompts above; at head_dim 256, one warp a
-// scheduler, two capped prompts of 4096 took 364 against 361, so not there).
-// Io::kKeysCleared: the scores of tokens that no row sees are 0 (at head_dim 128 the prompts above take
-// 266 us with their keys cleared, 275 with the raw products masked here; at 256 masking is as fast).
+// Io::kCapWithWeights: the cap of such a unit is taken in the loop of its weights (head_dim 128,
+// two softmax warps a scheduler: 260 us against 304 for the prompts above; at head_dim 256, one
+// warp a scheduler, two capped prompts of 4096 took 364 against 361, so not there).
+// Io::kKeysCleared: the scores of tokens that no row sees are 0 (at head_dim 128 the prompts above
+// take 266 us with those keys cleared, 275 with the raw products masked here; at 256 masking costs
+// nothing).
 template <int kParts, class Io>
 __device__ __forceinline__ bool scored_weights(const ScoreArgs &s, float scale_log2,
                                                ScoredRow &row, int base, bool later,
