@@ -8,8 +8,8 @@
 // columns of their scores, so none are written to shared memory and no buffer is waited for (two
 // 4096-token prompts of 24 / 4 heads with a prefix and a cap: 472 -> 418 us). The softmax warps
 // copy Q there at the start of an item (the same prompts: 373 -> 361 us, without the cap 359 ->
-// 326, with slopes 368 -> 340). The softmax bounds a capped call, one warp a scheduler; a second group of
-// softmax warps taking every other tile gained nothing when it was tried.
+// 326, with slopes 368 -> 340). The softmax bounds a capped call, one warp a scheduler; a second
+// group of softmax warps taking every other tile gained nothing while Q was in shared memory.
 //   TMEM (512 columns): S buffers at 0 and 64, the weights of a tile over the first 32 columns of
 //   its scores; Q at 128 (row = lane, two fp16 a column); O at 256.
 #pragma once
