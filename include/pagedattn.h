@@ -386,7 +386,8 @@ typedef enum pa_out_t {
  * values that some query of a call sees must be finite: a non-finite value may also reach the
  * call's other queries of its sequence and K/V head. */
 typedef struct pa_score_t {
-  float softcap;     /* 0: no cap; else positive and finite */
+  float softcap;     /* 0: no cap; else positive and finite, with scale / softcap a normal float
+                        below 2^126 in size (PA_ERR_INVALID_ARG) */
   int32_t window;    /* 0: no window; else >= 1 */
   int32_t out_type;  /* pa_out_t */
   int32_t reserved;  /* 0 */

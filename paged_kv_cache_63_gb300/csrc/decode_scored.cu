@@ -721,21 +721,25 @@ pa_status_t resolve_score(const pa_score_t *score, float scale, ScoreArgs *s) {
   if (score->softcap > 0.f) {
     s->cap_in = static_cast<float>(static_cast<double>(scale) / score->softcap);
     s->cap_out = static_cast<float>(score->softcap * 1.4426950408889634);
-    // a cap so small or large against the scale that the quotient is no normal number
-    if (scale != 0.f && !std::isnormal(s->cap_in)) return PA_ERR_INVALID_ARG;
+    // a cap so small or large against the scale that the quotient is no normal number, or that the
+    // exponential form's multiple of it is none
+    if (scale != 0.f && (!std::isnormal(s->cap_in) || !std::isfinite(4.f * s->cap_in)))
+      return PA_ERR_INVALID_ARG;
     if (!std::isfinite(s->cap_out)) return PA_ERR_INVALID_ARG;
-    // tanh t = t P(t^2) for |t| <= 1/2 (scored_softmax.cuh), as a polynomial of the raw dot
-    // product v = t / cap_in; never taken where a coefficient leaves the normal floats
-    static const double fit[4] = {0.999999463558197, -0.33326318860054016, 0.13190296292304993,
-                                  -0.04440222680568695};
+    // tanh's polynomial as one of the raw dot product v = t / cap_in. Under a large cap the highest
+    // coefficients fall below the normal floats: one that does is left out, for arguments so small
+    // that its term would be below 2^-24 of the sum.
     const double in = static_cast<double>(scale) / score->softcap;
-    double power = in * score->softcap * 1.4426950408889634;
-    s->cap_poly_max = static_cast<float>(0.25 / (in * in));
+    double power = in * score->softcap * 1.4426950408889634, z_max = 0.25;
     for (int k = 0; k < 4; ++k, power *= in * in) {
-      s->cap_poly[k] = static_cast<float>(fit[k] * power);
-      if (!std::isnormal(s->cap_poly[k])) s->cap_poly_max = -1.f;
+      const float c = static_cast<float>(kTanhFit[k] * power);
+      if (std::isnormal(c))
+        s->cap_poly[k] = c;
+      else
+        z_max = k == 0 ? -1. : std::min(z_max, std::pow(0x1p-24 / std::fabs(kTanhFit[k]), 1. / k));
     }
-    if (!std::isnormal(s->cap_poly_max)) s->cap_poly_max = -1.f;
+    s->cap_poly_max = z_max < 0. ? -1.f : static_cast<float>(std::min(z_max / (in * in), 3e38));
+    s->cap_wide = score->softcap > 256.f;
   }
   const uintptr_t ptrs = reinterpret_cast<uintptr_t>(score->slopes) |
                          reinterpret_cast<uintptr_t>(score->first_tokens) |

@@ -122,6 +122,8 @@ struct ScoredTile2 {
   unsigned *err;
   static constexpr bool kCapWithWeights = true, kKeysCleared = true;
   __device__ __forceinline__ void load(float (&c)[64]) const { tmem_ld64(ts, c); }
+  template <class F>
+  __device__ __forceinline__ void rewrite(F f) const { rewrite_columns(ts, f); }
   __device__ __forceinline__ void emit(const float (&pk)[32]) const { tmem_st32(ts, pk); }
   __device__ __forceinline__ bool settle(ScoredRow &row, float top, bool later) const {
     return settle_row(row, top, later, [&](float f) {

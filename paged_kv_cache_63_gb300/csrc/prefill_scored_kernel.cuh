@@ -87,6 +87,8 @@ struct ScoredTile1 {
   unsigned *err;
   static constexpr bool kCapWithWeights = false, kKeysCleared = false;
   __device__ __forceinline__ void load(float (&c)[64]) const { tmem_ld64(ts, c); }
+  template <class F>
+  __device__ __forceinline__ void rewrite(F f) const { rewrite_columns(ts, f); }
   __device__ __forceinline__ void emit(const float (&pk)[32]) const { tmem_st32(ts, pk); }
   __device__ __forceinline__ bool settle(ScoredRow &row, float top, bool later) const {
     return settle_row(row, top, later, [&](float f) {

@@ -11,6 +11,10 @@ namespace pa {
 
 constexpr float kLog2e = 1.4426950408889634f;
 
+// tanh t = t P(t^2) for |t| <= 1/2: the coefficients of P, lowest first (scored_softmax.cuh).
+constexpr double kTanhFit[4] = {0.999999463558197, -0.33326318860054016, 0.13190296292304993,
+                                -0.04440222680568695};
+
 // pa_score_t as the kernels take it.
 struct ScoreArgs {
   const float *slopes;    // [query_heads] or null
@@ -21,6 +25,7 @@ struct ScoreArgs {
   float cap_out;          // softcap * log2 e
   float cap_poly[4];      // cap_out tanh(v cap_in) ~ v (poly[0] + poly[1] v^2 + ...) for
   float cap_poly_max;     // v^2 <= cap_poly_max (multi-token kernels)
+  int cap_wide;           // an error relative to the cap would show in the weights (likewise)
   int window;             // 0: no limit
   int out_half;           // output in fp16
 };

@@ -13,7 +13,12 @@
 //    towards the equal-ripple fit), the scale and the cap folded into its coefficients. A score
 //    is then off by at most 0.47 cap * 5.8e-7, 1.4e-5 for a cap of 50, against the 2^-11 by
 //    which the fp16 probability is rounded. A warp with a larger argument in its unit takes
-//    1 - 2 / (1 + e^2t) for it. tanh being monotonic, the unit's maximum is that of the raw
+//    1 - 2 / (1 + e^2t) for it, whose error of up to 3.6e-7 of the cap stays below a fifth of that
+//    rounding up to a cap of 256. Under larger caps such a unit goes through tensor memory once
+//    more and each score takes the form that is exact for it (eight prompts of 2048 in windows of
+//    1024, head_dim 128: 425 us if every unit does, 365 with the exponential alone, 265 with the
+//    polynomial alone; that code is rolled, because unrolled it slowed every capped call, at
+//    head_dim 64 241 -> 284 us). tanh being monotonic, the unit's maximum is that of the raw
 //    products, capped, where nothing is masked or biased.
 //  * The bias is linear in the key's column wherever no key of the columns lies past its query.
 //  * The mask is compared per score only in units where some row of the warp needs it, and a
@@ -77,8 +82,10 @@ __device__ __forceinline__ float min3(float a, float b, float c) {
   return d;
 }
 
-// cap_out * tanh(v * cap_in); e^2t overflows to infinity and underflows to 0 where tanh is +-1
-__device__ __forceinline__ float cap_exact(const ScoreArgs &s, float v) {
+// cap_out * tanh(v * cap_in) = cap_out (1 - 2 / (1 + e^2t)); e^2t overflows to infinity and underflows
+// to 0 where tanh is +-1. Off by at most 7.2e-7 of the score for |t| >= 1/2, and by 3.6e-7 of the cap
+// below, where the difference cancels.
+__device__ __forceinline__ float cap_exp(const ScoreArgs &s, float v) {
   const float e = prefill_exp2(v * (s.cap_in * (2.f * kLog2e)));
   return fmaf(-2.f * s.cap_out, fast_rcp(1.f + e), s.cap_out);
 }
@@ -104,8 +111,31 @@ __device__ __forceinline__ void cap_scores(float (&v)[64], const ScoreArgs &s, b
     }
   } else {
 #pragma unroll
-    for (int c = 0; c < 64; ++c) v[c] = cap_exact(s, v[c]);
+    for (int c = 0; c < 64; ++c) v[c] = cap_exp(s, v[c]);
   }
+}
+
+// The same score by the form that is exact for it: below |t| = 1/2 the polynomial, not folded, so
+// that it holds under any cap (the largest make t subnormal, which moves a score by 2^-22).
+__device__ __forceinline__ float cap_each(const ScoreArgs &s, float v) {
+  constexpr float p0 = kTanhFit[0], p1 = kTanhFit[1], p2 = kTanhFit[2], p3 = kTanhFit[3];
+  const float t = v * s.cap_in, z = t * t;
+  const float near = s.cap_out * (t * fmaf(fmaf(fmaf(p3, z, p2), z, p1), z, p0));
+  return fabsf(t) <= 0.5f ? near : cap_exp(s, v);
+}
+
+// Replaces 64 columns of tensor memory by f of each. Warp-collective.
+template <class F>
+__device__ __forceinline__ void rewrite_columns(uint32_t ts, F f) {
+#pragma unroll 1
+  for (int c = 0; c < 64; c += 32) {
+    float v[32];
+    tmem_ld32(ts + c, v);
+#pragma unroll
+    for (int e = 0; e < 32; ++e) v[e] = f(v[e]);
+    tmem_st32(ts + c, v);
+  }
+  tmem_wait_st();
 }
 
 // v = v * mult + slope2 * column, by steps of two columns, each off by a rounding (a table of
@@ -182,9 +212,9 @@ __device__ __forceinline__ void weigh(ScoredRow &row, float (&pk)[32], Arg arg) 
 
 // One unit of 64 keys from token `base`: raw dot products become weights relative to row.m,
 // row.l grows by their sum. Warp-collective. `io` gives access to the row: load(v) reads the raw
-// columns, settle(row, top, later) brings row.m up to date for a largest score `top` (settle_row;
-// `later`: a unit after the row's first), emit(pk) takes the weights as fp16 pairs. False: a wait
-// gave up. A row that has seen nothing yet has m = -inf.
+// columns, rewrite(f) replaces each by f of it, settle(row, top, later) brings row.m up to date for
+// a largest score `top` (settle_row; `later`: a unit after the row's first), emit(pk) takes the
+// weights as fp16 pairs. False: a wait gave up. A row that has seen nothing yet has m = -inf.
 //
 // The largest score is needed only where it may move the reference, and where nothing is masked or
 // biased the farthest raw product bounds it at half the comparisons (|tanh t| <= |t|).
@@ -222,7 +252,8 @@ __device__ __forceinline__ bool scored_weights(const ScoreArgs &s, float scale_l
       // |tanh t| <= |t|: no score is farther from 0 than the uncapped one
       if (__any_sync(0xffffffffu, far * fabsf(scale_log2) > row.m + kScoredSlack)) {
         extremes(v, high, low);  // capped scores are monotonic in the raw products
-        if (!io.settle(row, cap_exact(s, scale_log2 >= 0.f ? high : low), later)) return false;
+        const float2 best = scale_log2 >= 0.f ? make_float2(high, high) : make_float2(low, low);
+        if (!io.settle(row, cap_poly(s, best).x * best.x, later)) return false;
       }
       if constexpr (Io::kCapWithWeights) {
         const float2 n2 = make_float2(-row.m, -row.m);
@@ -235,7 +266,12 @@ __device__ __forceinline__ bool scored_weights(const ScoreArgs &s, float scale_l
       }
       settled = true;
     }
-    cap_scores(v, s, poly);
+    if (__builtin_expect(poly || !s.cap_wide, 1)) {
+      cap_scores(v, s, poly);
+    } else {
+      io.rewrite([&](float x) { return cap_each(s, x); });
+      io.load(v);
+    }
     mult = 1.f;
   } else if (!(kParts & kRuleSlopes) && !masked) {
     settled = !__any_sync(0xffffffffu,
