@@ -428,7 +428,8 @@ pa_status_t pa_decode_scored(const pa_problem_t *problem, const pa_score_t *scor
  * Key tiles that none of a query tile's tokens sees are skipped. With total_tokens 0 nothing is
  * done, and query and out may be NULL.
  *   out        fp16 [total_tokens][query_heads][head_dim], 16-byte aligned; rows of new tokens
- *              are written, other rows are left untouched. score->out_type must be PA_OUT_FP16
+ *              are written, other rows are left untouched; a mean that the weights' rounding carries
+              past fp16's largest value is given as that. score->out_type must be PA_OUT_FP16
  *              (PA_ERR_UNSUPPORTED): the probabilities meet V rounded to fp16, so a wider output
  *              would hold no more
  * A prefix reaches past a query only as far as the cache does: the keys of a prefix whose

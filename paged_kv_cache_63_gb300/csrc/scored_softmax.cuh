@@ -399,12 +399,20 @@ __device__ __forceinline__ void store_zero_row(uint16_t *dst, int n) {
   for (int i = 0; i < n; i += 8) *reinterpret_cast<uint4 *>(dst + i) = make_uint4(0, 0, 0, 0);
 }
 
+// Two outputs as fp16. Weights rounded up carry a mean of values next to fp16's largest past it by up
+// to 2^-11 of it, which would round to infinity: it is given as the largest.
+__device__ __forceinline__ uint32_t pack_mean2(float x, float y) {
+  uint32_t r;
+  asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(y), "f"(x));
+  return r;
+}
+
 // 32 consecutive fp32 outputs of a row, scaled and written as fp16.
 __device__ __forceinline__ void store_half32(uint16_t *dst, const float (&o)[32], float inv,
                                              bool v8, uint64_t pol) {
   uint32_t w[16];
 #pragma unroll
-  for (int e = 0; e < 16; ++e) w[e] = pack_half2(o[2 * e] * inv, o[2 * e + 1] * inv);
+  for (int e = 0; e < 16; ++e) w[e] = pack_mean2(o[2 * e] * inv, o[2 * e + 1] * inv);
   if (v8) {
 #pragma unroll
     for (int e = 0; e < 16; e += 8)

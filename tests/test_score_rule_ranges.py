@@ -1,5 +1,5 @@
-"""The score rule over the ranges its fields and the caches allow: caps far above and far below every
-score, rows of very different scores side by side."""
+"""The score rule over the ranges of its fields and the caches: caps far above and far below every
+score, rows of very different scores side by side, cached values next to fp16's largest."""
 
 import numpy as np
 import pytest
@@ -86,3 +86,22 @@ def test_small_scores_beside_large_ones(shape, softcap, biased):
     off = 3.6e-7 * softcap if softcap <= 256 else 0.0
     check_prefill(w, Rule(softcap=softcap, slopes=slopes_of(w.query_heads) if biased else None),
                   probability_error=ERRORS["probability_error"] + off)
+
+
+@gpu
+@pytest.mark.parametrize("shape", KERNELS)
+def test_values_next_to_the_largest_of_fp16(shape):
+    """A mean of finite values is finite: the weights' rounding must not carry it past them."""
+    for w in (chunks(shape, ctx=[64, 40, 3], new=[64, 9, 3]),
+              chunks(shape, ctx=[300], new=[300], q_scale=0.3)):
+        sign = np.where(np.arange(w.head_dim) % 2, -1.0, 1.0)
+        w.v[np.isfinite(w.v)] = 1.0
+        w.v = (w.v * (65504.0 * sign)).astype(np.float16)
+        for rule in (Rule(), Rule(softcap=20.0), Rule(window=3),
+                     Rule(slopes=slopes_of(w.query_heads))):
+            check_prefill(w, rule)
+    step = Cached([64, 40, 3, 300], q_scale=3.0, seed=12, **SHAPES[shape])
+    step.v[np.isfinite(step.v)] = 65504.0
+    got, flags = gpu_decode(step, Rule(softcap=20.0), "fp16")
+    assert flags == 0
+    assert_within(got, *attend(step, Rule(softcap=20.0), P_ERROR, P_FLOOR), True)
