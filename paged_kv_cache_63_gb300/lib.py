@@ -91,6 +91,8 @@ _lock = threading.Lock()
 def load(path: Optional[str] = None):
     """Load (building first if the library is absent and nvcc is available)."""
     global _lib
+    if _lib is not None and path is None:
+        return _lib
     with _lock:
         if _lib is not None and path is None:
             return _lib
@@ -167,11 +169,16 @@ def rope(rotary_dim, style="half", table=None, positions=None, table_rows=None) 
     r = pa_rope_t()
     r.rotary_dim = int(rotary_dim)
     r.style = ROPE_STYLE[style] if isinstance(style, str) else int(style)
-    r.table, r.positions = _addresses("rope", table, positions)
-    if table_rows is None:
-        table_rows = 0 if table is None or isinstance(table, int) else table.shape[0]
-    r.table_rows = int(table_rows)
+    dev = _device()
+    r.table, r.positions = _addresses("rope", dev, (table, _F32, 0), (positions, _I32, 0))
+    rows = 0
+    if table is not None and not isinstance(table, int):
+        rows = table.shape[0]
+        if tuple(table.shape[1:]) != (2, r.rotary_dim // 2) or (table_rows or 0) > rows:
+            raise PagedAttnError(1, "rope")
+    r.table_rows = int(rows if table_rows is None else table_rows)
     r.keep = (table, positions)
+    r.lengths = _lengths(positions)
     return r
 
 
@@ -183,9 +190,11 @@ def score(softcap=0.0, window=0, slopes=None, first_tokens=None, prefix_lengths=
     s = pa_score_t()
     s.softcap, s.window = float(softcap), int(window)
     s.out_type = OUT[out] if isinstance(out, str) else int(out)
-    s.slopes, s.first_tokens, s.prefix_lengths = _addresses("score", slopes, first_tokens,
-                                                            prefix_lengths)
+    dev = _device()
+    s.slopes, s.first_tokens, s.prefix_lengths = _addresses(
+        "score", dev, (slopes, _F32, 0), (first_tokens, _I32, 0), (prefix_lengths, _I32, 0))
     s.keep = (slopes, first_tokens, prefix_lengths)
+    s.lengths = _lengths(slopes, first_tokens, prefix_lengths)
     return s
 
 
@@ -214,22 +223,50 @@ def _torch_on_gpu() -> bool:
     return True
 
 
-def _addresses(where, *xs):
-    """Addresses of tensor arguments, which must be whole and on the current device (an address
-    passes unseen)."""
-    dev, out = None, []
-    for x in xs:
+_F16 = _F32 = _I32 = None  # torch's types, once a call may take tensors
+
+
+def _device() -> int:
+    """The device that a call's tensors must be on; torch's types are known from here on."""
+    global _F16, _F32, _I32
+    if _F16 is None and "torch" in sys.modules:
+        t = sys.modules["torch"]
+        _F16, _F32, _I32 = t.float16, t.float32, t.int32
+    return _get_device() if _raw_stream is not None or _torch_on_gpu() else 0
+
+
+def _addresses(where, dev, *args):
+    """Addresses of tensor arguments (tensor, its type, the least number of its elements; a type of
+    None: of its bytes), which must be whole and on device `dev`. An address passes unseen."""
+    out = []
+    for x, kind, least in args:
         if x is not None and x.__class__ is not int:
-            if dev is None:
-                dev = _get_device() if _torch_on_gpu() else 0
-            if x.get_device() != dev or not x.is_contiguous():
+            if (x.get_device() != dev or not x.is_contiguous()
+                    or (x.nbytes < least if kind is None
+                        else x.dtype is not kind or x.numel() < least)):
                 raise PagedAttnError(1, where)
             x = x.data_ptr()
         out.append(x)
     return out
 
 
-def _rows(where, x, heads, head_dim, stride):
+def _lengths(*xs):
+    """Element counts of the tensors a struct points to (None: absent, or an address), or None if
+    there is none."""
+    n = tuple(None if x is None or isinstance(x, int) else x.numel() for x in xs)
+    return None if n.count(None) == len(n) else n
+
+
+def _check_lengths(where, struct, *least):
+    """Whether the tensors of rope() or score() have the elements that a call reads."""
+    n = getattr(struct, "lengths", None)  # (a struct of the caller's own has none)
+    if n is not None:
+        for have, need in zip(n, least):
+            if have is not None and have < need:
+                raise PagedAttnError(1, where)
+
+
+def _rows(where, dev, x, tokens, heads, head_dim, stride):
     """(address, row stride in elements) of [tokens][heads][head_dim] rows whose tokens may be
     apart, as slices of a fused projection's output are. An address takes ``stride`` as given
     (0: packed)."""
@@ -239,8 +276,8 @@ def _rows(where, x, heads, head_dim, stride):
     rows, nh, nd = x.shape
     # (the strides of an empty tensor say nothing)
     if nh != heads or nd != head_dim or (rows and (d != 1 or (h != head_dim and heads > 1))) \
-            or (rows > 1 and n < heads * head_dim) \
-            or x.get_device() != (_get_device() if _torch_on_gpu() else 0):
+            or (rows > 1 and n < heads * head_dim) or rows < tokens or x.dtype is not _F16 \
+            or x.get_device() != dev:
         raise PagedAttnError(1, where)
     # one row has no next one: any stride says the same
     return x.data_ptr(), n if rows > 1 else 0
@@ -325,11 +362,18 @@ def pa_append_rope(prob, rope, query, new_key, new_value, query_start, total_tok
     new_value may be slices of one fused projection's output (their row strides are taken from
     the tensors); query and query_out may both be None."""
     where, heads, kv_heads, hd = "pa_append_rope", prob.query_heads, prob.kv_heads, prob.head_dim
-    q, qs = _rows(where, query, heads, hd, query_stride)
-    k, ks = _rows(where, new_key, kv_heads, hd, key_stride)
-    v, vs = _rows(where, new_value, kv_heads, hd, value_stride)
-    starts, bt, ctx, q_out, kc, vc = _addresses(where, query_start, block_tables, context_lengths,
-                                                query_out, key_cache, value_cache)
+    dev = _device()
+    q, qs = _rows(where, dev, query, total_tokens, heads, hd, query_stride)
+    k, ks = _rows(where, dev, new_key, total_tokens, kv_heads, hd, key_stride)
+    v, vs = _rows(where, dev, new_value, total_tokens, kv_heads, hd, value_stride)
+    if rope is not None:
+        _check_lengths(where, rope, total_tokens)
+    batch, cache = prob.batch, prob.num_physical_pages * prob.page_size * kv_heads * hd
+    starts, bt, ctx, q_out, kc, vc = _addresses(
+        where, dev, (query_start, _I32, batch + 1),
+        (block_tables, _I32, batch * prob.max_pages_per_sequence), (context_lengths, _I32, batch),
+        (query_out, _F16, total_tokens * heads * hd), (key_cache, _F16, cache),
+        (value_cache, _F16, cache))
     _check(load().pa_append_rope(prob, rope, q, qs, k, ks, v, vs, starts, total_tokens, bt, ctx,
                                  q_out, kc, vc, _stream(stream)), where)
 
@@ -352,20 +396,36 @@ def pa_decode_scored(prob, score, query, key_cache, value_cache, block_tables, c
                      workspace_bytes: int = 0, stream=None):
     """A decode step under a score rule (``score()`` or None); out fp32 or fp16 as the rule says.
     The workspace (pa_workspace_size) needs no initialisation."""
-    q, k, v, bt, ctx, o, ws = _addresses("pa_decode_scored", query, key_cache, value_cache,
-                                         block_tables, context_lengths, out, workspace)
+    where, batch, heads, hd = "pa_decode_scored", prob.batch, prob.query_heads, prob.head_dim
+    dev, half = _device(), False
+    if score is not None:
+        _check_lengths(where, score, heads, batch)
+        half = score.out_type == OUT["fp16"]
+    rows, cache = batch * heads * hd, prob.num_physical_pages * prob.page_size * prob.kv_heads * hd
+    q, k, v, bt, ctx, o, ws = _addresses(
+        where, dev, (query, _F16, rows), (key_cache, _F16, cache), (value_cache, _F16, cache),
+        (block_tables, _I32, batch * prob.max_pages_per_sequence), (context_lengths, _I32, batch),
+        (out, _F16 if half else _F32, rows), (workspace, None, workspace_bytes))
     _check(load().pa_decode_scored(prob, score, q, k, v, bt, ctx, scale, o, opts, ws,
-                                   workspace_bytes, _stream(stream)), "pa_decode_scored")
+                                   workspace_bytes, _stream(stream)), where)
 
 
 def pa_prefill_scored(prob, score, query, query_start, total_tokens, max_query_len, key_cache,
                       value_cache, block_tables, context_lengths, scale, out,
                       opts: Optional[pa_options_t] = None, stream=None):
     """pa_prefill under a score rule (``score(out="fp16", ...)``); fp16 out."""
-    q, qs, k, v, bt, ctx, o = _addresses("pa_prefill_scored", query, query_start, key_cache,
-                                         value_cache, block_tables, context_lengths, out)
+    where, batch, heads, hd = "pa_prefill_scored", prob.batch, prob.query_heads, prob.head_dim
+    dev = _device()
+    if score is not None:
+        _check_lengths(where, score, heads, total_tokens, batch)
+    rows = total_tokens * heads * hd
+    cache = prob.num_physical_pages * prob.page_size * prob.kv_heads * hd
+    q, qs, k, v, bt, ctx, o = _addresses(
+        where, dev, (query, _F16, rows), (query_start, _I32, batch + 1), (key_cache, _F16, cache),
+        (value_cache, _F16, cache), (block_tables, _I32, batch * prob.max_pages_per_sequence),
+        (context_lengths, _I32, batch), (out, _F16, rows))
     _check(load().pa_prefill_scored(prob, score, q, qs, total_tokens, max_query_len, k, v, bt, ctx,
-                                    scale, o, opts, _stream(stream)), "pa_prefill_scored")
+                                    scale, o, opts, _stream(stream)), where)
 
 
 def pa_split_kv_partial(prob, query, key_cache, value_cache, block_tables, context_lengths, scale,
