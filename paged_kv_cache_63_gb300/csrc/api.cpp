@@ -11,6 +11,7 @@
 
 #include "internal.h"
 #include "pagedattn.h"
+#include "row_maps.h"
 
 namespace {
 
@@ -223,33 +224,12 @@ pa_status_t resolve(const pa_problem_t *p, const pa_options_t *o, int sm_count, 
 }
 
 // ---- TMA tensor maps ---------------------------------------------------------------
-typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
-                                  const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
-                                  const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
-  static EncodeTiledFn fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void *p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
-                                         &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeTiledFn>(p);
-  });
-  return fn;
-}
-
 // 3-D map over a cache with a box of rows_per_box rows of one head, 64 elements wide, and
 // 128-byte swizzle. Token-major caches are viewed as [num_pages * page_size rows][kv_heads]
 // [head_dim] (box 64 x 1 x rows), head-major ones as [num_pages * kv_heads][page_size]
 // [head_dim] (box 64 x rows x 1); either way a box lands as rows x 128 bytes.
 pa_status_t encode_cache_map(CUtensorMap *map, const void *base, const pa_problem_t *p,
                              int rows_per_box) {
-  EncodeTiledFn fn = encode_fn();
-  if (!fn) return PA_ERR_CUDA;
   const bool hm = p->cache_layout == PA_LAYOUT_HEAD_MAJOR;
   const cuuint64_t hd = static_cast<cuuint64_t>(p->head_dim);
   cuuint64_t dims[3], strides[2];
@@ -267,11 +247,7 @@ pa_status_t encode_cache_map(CUtensorMap *map, const void *base, const pa_proble
     strides[1] = static_cast<cuuint64_t>(p->kv_heads) * hd * 2;
     box[2] = static_cast<cuuint32_t>(rows_per_box);
   }
-  cuuint32_t estr[3] = {1, 1, 1};
-  CUresult rc = fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void *>(base), dims, strides,
-                   box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return rc == CUDA_SUCCESS ? PA_OK : PA_ERR_CUDA;
+  return encode_map(map, 3, base, dims, strides, box);
 }
 
 }  // namespace
@@ -285,19 +261,13 @@ pa_status_t encode_cache_map_rows(CUtensorMap *map, const void *base, const pa_p
 
 pa_status_t encode_query_map(CUtensorMap *map, const void *query, int64_t total_tokens,
                              int query_heads, int head_dim, int heads_per_box, int tokens_per_box) {
-  EncodeTiledFn fn = encode_fn();
-  if (!fn) return PA_ERR_CUDA;
   const cuuint64_t hd = static_cast<cuuint64_t>(head_dim);
   cuuint64_t dims[3] = {hd, static_cast<cuuint64_t>(query_heads),
                         static_cast<cuuint64_t>(total_tokens > 0 ? total_tokens : 1)};
   cuuint64_t strides[2] = {hd * 2, static_cast<cuuint64_t>(query_heads) * hd * 2};
   cuuint32_t box[3] = {64, static_cast<cuuint32_t>(heads_per_box),
                        static_cast<cuuint32_t>(tokens_per_box)};
-  cuuint32_t estr[3] = {1, 1, 1};
-  CUresult rc = fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void *>(query), dims,
-                   strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return rc == CUDA_SUCCESS ? PA_OK : PA_ERR_CUDA;
+  return encode_map(map, 3, query, dims, strides, box);
 }
 
 pa_status_t check_problem_public(const pa_problem_t *p) { return check_problem(p); }

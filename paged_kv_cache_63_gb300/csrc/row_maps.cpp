@@ -1,11 +1,9 @@
-// row_maps.cpp -- tensor maps that load all 64-column blocks of some rows of one K/V head with
-// one TMA instruction.
-#include <cuda.h>
+// row_maps.cpp -- the library's tensor maps: rows of heads in 64-column blocks.
+#include "row_maps.h"
+
 #include <cuda_runtime.h>
 
 #include <atomic>
-
-#include "row_maps.h"
 
 namespace pa {
 
@@ -34,10 +32,30 @@ EncodeTiledFn encode_tiled() {
 
 }  // namespace
 
-pa_status_t encode_row_map(CUtensorMap *map, const void *cache, const pa_problem_t *p,
-                           int rows_per_box, int blocks_per_box) {
+pa_status_t encode_map(CUtensorMap *map, int rank, const void *base, const cuuint64_t *dims,
+                       const cuuint64_t *strides, const cuuint32_t *box) {
   const EncodeTiledFn fn = encode_tiled();
   if (!fn) return PA_ERR_CUDA;
+  const cuuint32_t steps[4] = {1, 1, 1, 1};
+  auto encode = [&] {
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, static_cast<cuuint32_t>(rank),
+              const_cast<void *>(base), dims, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  };
+  CUresult rc = encode();
+  if (rc != CUDA_SUCCESS) {
+    // The driver wants a context, which a thread has only once a call of the runtime has needed
+    // one: this may be the thread's first.
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaSetDevice(dev) != cudaSuccess) return PA_ERR_CUDA;
+    rc = encode();
+  }
+  return rc == CUDA_SUCCESS ? PA_OK : PA_ERR_CUDA;
+}
+
+pa_status_t encode_row_map(CUtensorMap *map, const void *cache, const pa_problem_t *p,
+                           int rows_per_box, int blocks_per_box) {
   const bool hm = p->cache_layout == PA_LAYOUT_HEAD_MAJOR;
   const cuuint64_t row = static_cast<cuuint64_t>(p->head_dim) * 2;  // bytes of a head's row
   const cuuint64_t pages = p->num_physical_pages, ps = p->page_size, heads = p->kv_heads;
@@ -46,12 +64,7 @@ pa_status_t encode_row_map(CUtensorMap *map, const void *cache, const pa_problem
   const cuuint64_t strides[3] = {hm ? row : heads * row, hm ? ps * row : row, 128};
   const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(rows_per_box), 1,
                              static_cast<cuuint32_t>(blocks_per_box)};
-  const cuuint32_t steps[4] = {1, 1, 1, 1};
-  const CUresult rc =
-      fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, const_cast<void *>(cache), dims, strides, box,
-         steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return rc == CUDA_SUCCESS ? PA_OK : PA_ERR_CUDA;
+  return encode_map(map, 4, cache, dims, strides, box);
 }
 
 }  // namespace pa

@@ -1,4 +1,4 @@
-// row_maps.h -- 4-D tensor maps over a paged cache: (64 columns, rows, heads, column blocks).
+// row_maps.h -- tensor maps; 4-D ones over a paged cache: (64 columns, rows, heads, column blocks).
 #pragma once
 
 #include <cuda.h>
@@ -6,6 +6,11 @@
 #include "pagedattn.h"
 
 namespace pa {
+
+// A tensor map over fp16 with 128-byte swizzle, `rank` (3 or 4) dimensions and a byte stride for
+// each but the first. Works in a thread that has made no CUDA call yet.
+pa_status_t encode_map(CUtensorMap *map, int rank, const void *base, const cuuint64_t *dims,
+                       const cuuint64_t *strides, const cuuint32_t *box);
 
 // A box is rows_per_box rows of one head times blocks_per_box blocks of 64 columns and lands as
 // [blocks][rows][128 bytes], 128-byte swizzled. Coordinates are (0, row, head, block): token-major
