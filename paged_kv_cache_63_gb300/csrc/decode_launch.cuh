@@ -3,27 +3,17 @@
 #pragma once
 
 #include "decode_kernel.cuh"
+#include "early_launch.cuh"
 
 namespace pa {
-
-constexpr int kMaxDevices = 64;
 
 template <int HD, int T, bool MMA, int NH>
 cudaError_t launch_variant(const KernelArgs &a, const CUtensorMap *tk, const CUtensorMap *tv,
                            int ctas, int warps, size_t smem, cudaStream_t stream) {
   auto kern = decode_kernel<HD, T, MMA, NH>;
-  // the opt-in shared-memory size is a per-device function attribute; remember the
-  // largest value set on each device
-  static int smem_set[kMaxDevices] = {0};
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
+  static std::atomic<bool> set[kMaxLaunchDevices];
+  const cudaError_t e = allow_smem(kern, kMaxDecodeSmem, set);
   if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= kMaxDevices || smem_set[dev] < static_cast<int>(smem)) {
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(smem));
-    if (e != cudaSuccess) return e;
-    if (dev >= 0 && dev < kMaxDevices) smem_set[dev] = static_cast<int>(smem);
-  }
   kern<<<ctas, warps * 32, smem, stream>>>(a, *tk, *tv);
   return cudaGetLastError();
 }

@@ -771,19 +771,12 @@ int sm_count() {
 template <int HD, int T>
 cudaError_t launch_scored(const ScoredArgs &a, const CUtensorMap &tk, const CUtensorMap &tv,
                           const pa_plan_t &pl, cudaStream_t stream) {
-  // the opt-in shared-memory size is a per-device attribute of the kernel: raised when needed
-  static std::atomic<int> set[kMaxDev];
+  static std::atomic<bool> set[kMaxLaunchDevices];
   auto kern = decode_scored_kernel<HD, T>;
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
+  const cudaError_t e = allow_smem(kern, kMaxDecodeSmem, set);
   if (e != cudaSuccess) return e;
-  const int smem = static_cast<int>(pl.smem_bytes);
-  if (dev < 0 || dev >= kMaxDev || set[dev].load(std::memory_order_relaxed) < smem) {
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-    if (dev >= 0 && dev < kMaxDev) set[dev].store(smem, std::memory_order_relaxed);
-  }
-  return launch_early(kern, dim3(pl.ctas), pl.warps_per_cta * 32, smem, stream, a, tk, tv);
+  return launch_early(kern, dim3(pl.ctas), pl.warps_per_cta * 32, static_cast<int>(pl.smem_bytes),
+                      stream, a, tk, tv);
 }
 
 template <int HD, int W>

@@ -2,8 +2,6 @@
 // kernel for head_dim 64 and 128, the single-tile kernel for 256, plain or under a score rule.
 #pragma once
 
-#include <atomic>
-
 #include "internal.h"
 #include "pagedattn.h"
 #include "prefill2_scored_kernel.cuh"
@@ -25,27 +23,11 @@ pa_status_t setup_prefill(const pa_problem_t *problem, const void *query,
                           const void *out, const pa_options_t *options, PrefillLaunch *l,
                           PrefillArgs *args);
 
-constexpr int kMaxDevicesPrefill = 64;
-
-// Raises a kernel's shared-memory limit once per device.
-template <typename Kernel>
-cudaError_t allow_smem(Kernel kern, int smem, std::atomic<bool> (&set)[kMaxDevicesPrefill]) {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= kMaxDevicesPrefill || !set[dev].load(std::memory_order_relaxed)) {
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-    if (dev >= 0 && dev < kMaxDevicesPrefill) set[dev].store(true, std::memory_order_relaxed);
-  }
-  return cudaSuccess;
-}
-
 // head_dim 64 / 128: two query tiles per CTA (a.n_qtiles counts pairs, grid.z too)
 template <int HD, bool kScored, int kParts>
 cudaError_t launch_prefill2_hd(const PrefillArgsOf<kScored> &a, const PrefillLaunch &l,
                                cudaStream_t stream) {
-  static std::atomic<bool> set[kMaxDevicesPrefill];
+  static std::atomic<bool> set[kMaxLaunchDevices];
   constexpr int smem = Prefill2Cfg<HD>::kSmem + 1024;
   void (*kern)(PrefillArgsOf<kScored>, CUtensorMap, CUtensorMap, CUtensorMap);
   if constexpr (kScored)
@@ -63,7 +45,7 @@ cudaError_t launch_prefill2_hd(const PrefillArgsOf<kScored> &a, const PrefillLau
 template <int HD, bool kScored, int kParts>
 cudaError_t launch_prefill_hd(const PrefillArgsOf<kScored> &a, const PrefillLaunch &l,
                               cudaStream_t stream) {
-  static std::atomic<bool> set[kMaxDevicesPrefill];
+  static std::atomic<bool> set[kMaxLaunchDevices];
   constexpr int smem = PrefillCfg<HD>::kSmem + 1024;
   void (*kern)(PrefillArgsOf<kScored>, CUtensorMap, CUtensorMap, CUtensorMap);
   if constexpr (kScored)
