@@ -570,14 +570,41 @@ __global__ void __launch_bounds__(kMaxWarpsPerCta * 32, 1)
   finish_unit();
 }
 
+// The unit that is cut where worker w (not the first) starts and at no worker before it: its
+// sequence, group unit and number of contributors, w - 1 the first of them (n = 0: there is none).
+struct Cut {
+  int b, us, n;
+};
+
+// Warp-collective.
+__device__ inline Cut cut_at(const ScoredArgs &sa, int w, int T) {
+  SpanCursor c = {};
+  long long total, nworkers;
+  Cut cut = {0, 0, 0};
+  if (span_balanced_start(sa, w, T, c, total, nworkers) &&
+      c.ug0 < worker_start(w, total, nworkers) && worker_of(c.ug0, total, nworkers) == w - 1) {
+    cut.b = c.b;
+    cut.us = c.us;
+    cut.n = static_cast<int>(worker_of(c.ug0 + span_tiles(c.sp, T) - 1, total, nworkers) - w + 2);
+  }
+  return cut;
+}
+
 // Joins the states of units that several workers share: out = sum_k 2^(m_k - M) acc_k /
 // sum_k 2^(m_k - M) l_k, contributors in their order. W warps take one (unit, head) pair, a
 // CTA of eight warps 8 / W pairs. Its CTAs come up when the decode kernel's have finished their
 // tiles, which had waited for everything before them in the stream: so a warp redoes the split
 // from the inputs before its own wait, and after it the pair costs about one memory round trip.
-template <int HD, int W>
-__global__ void __launch_bounds__(256)
-    join_scored_kernel(const __grid_constant__ ScoredArgs sa, int heads, long long pairs, int T) {
+// kCuts: with more units than workers the CTAs go through the workers' starts, where alone a unit
+// can be cut, instead of all units, `chunks` CTAs to a start: a pass over the batch's lengths for
+// each unit grows with the square of the batch (the call on sequences of 64 tokens, 64/8 heads of
+// 128, that is 1216 workers: 160 of them 24.9 us by units and 22.6 by starts, 512 80 and 42, 4096
+// 2502 and 315). Registers: up to 64 the CTAs come up beside the decode kernel's last ones, 2 us
+// earlier; at head_dim 256 that would spill (four contexts of 100000: 244.4 against 243.7 us).
+template <int HD, int W, bool kCuts>
+__global__ void __launch_bounds__(256, HD == 256 && !kCuts ? 3 : 4)
+    join_scored_kernel(const __grid_constant__ ScoredArgs sa, int heads, long long pairs, int chunks,
+                       int T) {
   constexpr int DPL = HD / 32;
   constexpr int P = 8 / W;
   constexpr int KB = HD >= 256 ? 4 : 8;
@@ -585,36 +612,54 @@ __global__ void __launch_bounds__(256)
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const int sub = warp % W;
-  const long long pair = static_cast<long long>(blockIdx.x) * P + warp / W;
-  const bool valid = pair < pairs;  // warp-uniform
-  const long long unit = valid ? pair / heads : 0;
-  const int h = valid ? static_cast<int>(pair % heads) : 0;
-  const int b = static_cast<int>(unit / a.ups);
-  const int us = static_cast<int>(unit % a.ups);
-  long long all = 0, before = 0;
-  for (int bb = lane; bb < a.batch; bb += 32) {
-    const long long t = span_tiles(load_span(sa, bb), T);
-    all += t;
-    if (bb < b) before += t;
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    all += __shfl_xor_sync(0xffffffffu, all, o);
-    before += __shfl_xor_sync(0xffffffffu, before, o);
-  }
-  const long long total = all * a.upg;
-  const long long nworkers = total < a.workers ? total : a.workers;
-  const int nt = span_tiles(load_span(sa, b), T);
-  long long c0 = 0;
-  int n = 0;
+  long long unit = 0, c0 = 0;
+  int h = 0, n = 0;
   UnitInfo u = {0, 0, 0, 0};
-  if (valid && nt > 0) {
-    const long long ug0 = before * a.upg + static_cast<long long>(us / a.group) * nt;
-    c0 = worker_of(ug0, total, nworkers);
-    n = static_cast<int>(worker_of(ug0 + nt - 1, total, nworkers) - c0 + 1);
-    u = unit_info(a, b, us);
-    // a unit with one worker was finished by it; heads past the unit's own do not exist
-    if (n <= 1 || h >= u.nh) n = 0;
+  if constexpr (kCuts) {
+    __shared__ Cut cut;
+    const int w = blockIdx.x / chunks + 1;
+    const int i = (blockIdx.x - (w - 1) * chunks) * P + warp;  // of the group's units and heads
+    if (warp == 0) {
+      const Cut found = cut_at(sa, w, T);
+      if (lane == 0) cut = found;
+    }
+    __syncthreads();
+    if (cut.n > 0 && i < a.group * heads) {
+      c0 = w - 1;
+      h = i % heads;
+      u = unit_info(a, cut.b, cut.us * a.group + i / heads);
+      unit = static_cast<long long>(u.b) * a.ups + u.us;
+      if (h < u.nh) n = cut.n;
+    }
+  } else {
+    const long long pair = static_cast<long long>(blockIdx.x) * P + warp / W;
+    const bool valid = pair < pairs;  // warp-uniform
+    unit = valid ? pair / heads : 0;
+    h = valid ? static_cast<int>(pair % heads) : 0;
+    const int b = static_cast<int>(unit / a.ups);
+    const int us = static_cast<int>(unit % a.ups);
+    long long all = 0, before = 0;
+    for (int bb = lane; bb < a.batch; bb += 32) {
+      const long long t = span_tiles(load_span(sa, bb), T);
+      all += t;
+      if (bb < b) before += t;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      all += __shfl_xor_sync(0xffffffffu, all, o);
+      before += __shfl_xor_sync(0xffffffffu, before, o);
+    }
+    const long long total = all * a.upg;
+    const long long nworkers = total < a.workers ? total : a.workers;
+    const int nt = span_tiles(load_span(sa, b), T);
+    if (valid && nt > 0) {
+      const long long ug0 = before * a.upg + static_cast<long long>(us / a.group) * nt;
+      c0 = worker_of(ug0, total, nworkers);
+      n = static_cast<int>(worker_of(ug0 + nt - 1, total, nworkers) - c0 + 1);
+      u = unit_info(a, b, us);
+      // a unit with one worker was finished by it; heads past the unit's own do not exist
+      if (n <= 1 || h >= u.nh) n = 0;
+    }
   }
   wait_for_stream();
   if constexpr (W == 1) {
@@ -783,14 +828,21 @@ template <int HD, int W>
 cudaError_t launch_join(const ScoredArgs &a, int units, int heads, int tile, cudaStream_t stream) {
   const long long pairs = static_cast<long long>(units) * heads;
   constexpr int P = 8 / W;
-  return launch_early(join_scored_kernel<HD, W>,
+  return launch_early(join_scored_kernel<HD, W, false>,
                       dim3(static_cast<unsigned>((pairs + P - 1) / P)), 256, 0, stream, a, heads,
-                      pairs, tile);
+                      pairs, 1, tile);
 }
 
 template <int HD>
 cudaError_t launch_join_hd(const ScoredArgs &a, int units, int heads, int warps, int tile,
                            cudaStream_t stream) {
+  if (units > a.k.workers * a.k.group) {  // (warps is 1)
+    const int chunks = (a.k.group * heads + 7) / 8;
+    if (a.k.workers == 1) return cudaSuccess;  // nothing is shared
+    return launch_early(join_scored_kernel<HD, 1, true>,
+                        dim3(static_cast<unsigned>((a.k.workers - 1) * chunks)), 256, 0, stream, a,
+                        heads, 0ll, chunks, tile);
+  }
   switch (warps) {
     case 1: return launch_join<HD, 1>(a, units, heads, tile, stream);
     case 2: return launch_join<HD, 2>(a, units, heads, tile, stream);
