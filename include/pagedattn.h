@@ -324,7 +324,8 @@ typedef struct pa_rope_t {
  * With total_tokens 0 nothing is done and the rows' addresses may be NULL. Rows before
  * query_start[0] and from query_start[batch] on are left alone, in query_out too.
  * A sequence with inconsistent offsets is skipped and flagged (PA_DEVERR_QUERY_START), one
- * with a length out of range likewise (PA_DEVERR_CONTEXT). A token whose page id is outside
+ * with a length out of range likewise (PA_DEVERR_CONTEXT); the others are written, a row that
+ * wrong offsets give to two of them for one. A token whose page id is outside
  * the pool (PA_DEVERR_PAGE_ID) or whose position is outside the table (PA_DEVERR_POSITION) is
  * flagged and nothing of it is written. Two tokens written to the same (page, slot) race.
  * Runs asynchronously on `stream`; allocates nothing, keeps nothing between calls. */

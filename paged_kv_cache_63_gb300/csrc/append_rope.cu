@@ -43,6 +43,25 @@ __device__ __forceinline__ int find_sequence(const int32_t *qs, int batch, int r
   return lo;
 }
 
+// Whether sequence b holds row `row` by offsets and a length that make sense.
+__device__ __forceinline__ bool holds(const RopeArgs &a, int b, int row) {
+  const int q0 = __ldg(a.qs + b), q1 = __ldg(a.qs + b + 1), c = __ldg(a.ctx + b);
+  return q0 >= 0 && q0 <= row && row < q1 && q1 <= a.total && c <= (a.maxp << a.ps_shift) &&
+         q1 - q0 <= c;
+}
+
+// The sequence that holds row `row`, or -1, by a look at every one: one wrong offset sends the
+// search by halves astray for rows of other sequences. Warp-collective.
+__device__ __forceinline__ int look_for_sequence(const RopeArgs &a, int row) {
+#pragma unroll 1
+  for (int b0 = 0; b0 < a.batch; b0 += 32) {
+    const int b = b0 + (threadIdx.x & 31);
+    const unsigned found = __ballot_sync(0xffffffffu, b < a.batch && holds(a, b, row));
+    if (found) return b0 + __ffs(found) - 1;
+  }
+  return -1;
+}
+
 // Turns eight pairs: half style pairs element e of `a` with element e of `b`; interleaved
 // style pairs elements 2e, 2e + 1 of the 16 consecutive elements a, b.
 template <bool kInterleaved>
@@ -89,12 +108,12 @@ __global__ void __launch_bounds__(256) append_rope_kernel(const __grid_constant_
       atomicOr(a.err, PA_DEVERR_QUERY_START);
   }
   const int row = static_cast<int>(blockIdx.x);
-  const int b = find_sequence(a.qs, a.batch, row);
-  if (b < 0) return;
-  const int q0 = __ldg(a.qs + b), q1 = __ldg(a.qs + b + 1), c = __ldg(a.ctx + b);
-  // rows behind the last sequence, and rows of a sequence flagged above
-  if (row >= q1 || q0 < 0 || q1 > a.total || c < 0 || c > (a.maxp << a.ps_shift) || q1 - q0 > c)
-    return;
+  int b = find_sequence(a.qs, a.batch, row);
+  if (b < 0 || !holds(a, b, row)) {
+    // rows behind the last sequence, and rows of a sequence flagged above
+    if (row >= __ldg(a.qs + a.batch) || (b = look_for_sequence(a, row)) < 0) return;
+  }
+  const int q1 = __ldg(a.qs + b + 1), c = __ldg(a.ctx + b);
   const int t = c - q1 + row;
   const int page = __ldg(a.bt + static_cast<long long>(b) * a.maxp + (t >> a.ps_shift));
   const int pos = a.rotary == 0 ? 0 : a.positions ? __ldg(a.positions + row) : t;
