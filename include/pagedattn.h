@@ -382,10 +382,11 @@ typedef enum pa_out_t {
  * the prefix's end, t < min(prefix_lengths[b], context_lengths[b]), instead of to p; the
  * window and the first token bound it as before. A query that sees nothing gives a zero row.
  * The fields of a zeroed struct change nothing: softmax(scale q K) over t <= p, fp32 out.
- * Tokens that no query of a call sees are not read, nor are block-table entries of pages
- * that hold only such tokens (a local layer's freed pages may be anything). Cached keys and
- * values that some query of a call sees must be finite: a non-finite value may also reach the
- * call's other queries of its sequence and K/V head. */
+ * Tokens that no query of a call sees reach no output, whatever their slots hold. Pages that hold
+ * only such tokens are not read, nor are their block-table entries (a local layer's freed pages
+ * may be anything); in a page with a seen token, unseen ones beside it may be loaded with it.
+ * Cached keys and values that some query of a call sees must be finite: a non-finite value may
+ * also reach the call's other queries of its sequence and K/V head. */
 typedef struct pa_score_t {
   float softcap;     /* 0: no cap; else positive and finite, with scale / softcap a normal float
                         below 2^126 in size (PA_ERR_INVALID_ARG) */
@@ -430,7 +431,7 @@ pa_status_t pa_decode_scored(const pa_problem_t *problem, const pa_score_t *scor
  * done, and query and out may be NULL.
  *   out        fp16 [total_tokens][query_heads][head_dim], 16-byte aligned; rows of new tokens
  *              are written, other rows are left untouched; a mean that the weights' rounding carries
-              past fp16's largest value is given as that. score->out_type must be PA_OUT_FP16
+ *              past fp16's largest value is given as that. score->out_type must be PA_OUT_FP16
  *              (PA_ERR_UNSUPPORTED): the probabilities meet V rounded to fp16, so a wider output
  *              would hold no more
  * A prefix reaches past a query only as far as the cache does: the keys of a prefix whose

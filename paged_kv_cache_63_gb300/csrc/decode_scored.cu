@@ -381,6 +381,9 @@ __device__ __forceinline__ void zero_rows_out(const ScoredArgs &a, const UnitInf
   for (int i = lane * 2; i < u.nh * HD; i += 64) store_out2(a.s, a.out, base + i, 0.f, 0.f);
 }
 
+// Eight warps leave a thread 255 registers: enough at head_dim 64 and 128 (156 and 203); at 256,
+// where the output alone takes 64 and the query 32, 112 bytes spill, which the stream hides (0.97
+// of the copy bandwidth).
 template <int HD, int T>
 __global__ void __launch_bounds__(kMaxWarpsPerCta * 32, 1)
     decode_scored_kernel(const __grid_constant__ ScoredArgs sa,

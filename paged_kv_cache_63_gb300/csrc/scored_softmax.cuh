@@ -3,10 +3,11 @@
 //
 // These instructions bound the kernels: two warps a scheduler run them (one at head_dim 256)
 // next to the products. 64 scores, loaded once and worked on in place, and the packed weights fit
-// the registers; 128 columns spilled, and the shared memory being full a spilled word is an L2
-// access (eight prompts of 2048 in windows of 1024, capped, head_dim 128: 968 us spilling, 266 us
-// so). The code has to fit the instruction cache as well: each part of the rule is written once,
-// and what only some calls need is compiled into kernels of their own.
+// the registers but for one to four words of an item's state (4 to 16 bytes a thread at head_dim 64
+// and 128, none at 256); of 128 columns the scores themselves spilled, and the shared memory being
+// full a spilled word is an L2 access (eight prompts of 2048 in windows of 1024, capped, head_dim
+// 128: 968 us so, 265 us with 64). The code has to fit the instruction cache as well: each part of
+// the rule is written once, and what only some calls need is compiled into kernels of their own.
 //  * tanh is a polynomial on the fp32 pipe in packed pairs wherever a warp's arguments allow:
 //    tanh t = t P(t^2) with P of degree 3, fitted to the least relative error for |t| <= 1/2
 //    (5.8e-7 evaluated in fp32; weighted least squares on Chebyshev nodes, weights iterated
@@ -191,7 +192,11 @@ __device__ __forceinline__ bool settle_row(ScoredRow &row, float top, bool later
 }
 
 // Weights 2^x of 64 columns, arg(c) giving x of columns c and c + 1, as fp16 pairs; row.l grows by
-// their sum. Sixteen arguments are formed before their exponentials are taken.
+// their sum, taken in fp32 before the rounding. fp16 because the tensor cores multiply the values'
+// own type: off by half a step, 2^-11 of a weight, which moves an output by 1.2e-4 to 2.0e-4 of its
+// size (rms) next to the 2.1e-4 of its own rounding to fp16. A second fp16 part for the remainder,
+// as the decode step has, would double the output product and take the packing twice. Sixteen
+// arguments are formed before their exponentials are taken.
 template <class Arg>
 __device__ __forceinline__ void weigh(ScoredRow &row, float (&pk)[32], Arg arg) {
   float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
