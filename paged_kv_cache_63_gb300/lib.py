@@ -2,8 +2,9 @@
 
 Every function here forwards to the C entry point of the same name; all compute runs in
 the library's CUDA kernels. Tensor arguments may be torch CUDA tensors or raw device
-addresses (int). There is no fallback: if the shared library is missing or fails to load,
-``load()`` raises.
+addresses (int). pa_append_rope, pa_decode_scored and pa_prefill_scored check the device,
+layout, type and length of tensors first; an address is passed on as it is. There is no
+fallback: if the shared library is missing or fails to load, ``load()`` raises.
 """
 
 from __future__ import annotations
@@ -75,6 +76,7 @@ class pa_rope_t(ctypes.Structure):
     _fields_ = [("rotary_dim", ctypes.c_int32), ("style", ctypes.c_int32),
                 ("table_rows", ctypes.c_int32), ("reserved", ctypes.c_int32),
                 ("table", ctypes.c_void_p), ("positions", ctypes.c_void_p)]
+    lengths = None  # of the tensors pointed to, where rope() was given some
 
 
 class pa_score_t(ctypes.Structure):
@@ -82,6 +84,7 @@ class pa_score_t(ctypes.Structure):
                 ("out_type", ctypes.c_int32), ("reserved", ctypes.c_int32),
                 ("slopes", ctypes.c_void_p), ("first_tokens", ctypes.c_void_p),
                 ("prefix_lengths", ctypes.c_void_p)]
+    lengths = None  # of the tensors pointed to, where score() was given some
 
 
 _lib = None
@@ -259,11 +262,9 @@ def _lengths(*xs):
 
 def _check_lengths(where, struct, *least):
     """Whether the tensors of rope() or score() have the elements that a call reads."""
-    n = getattr(struct, "lengths", None)  # (a struct of the caller's own has none)
-    if n is not None:
-        for have, need in zip(n, least):
-            if have is not None and have < need:
-                raise PagedAttnError(1, where)
+    for have, need in zip(struct.lengths, least):
+        if have is not None and have < need:
+            raise PagedAttnError(1, where)
 
 
 def _rows(where, dev, x, tokens, heads, head_dim, stride):
@@ -283,10 +284,13 @@ def _rows(where, dev, x, tokens, heads, head_dim, stride):
     return x.data_ptr(), n if rows > 1 else 0
 
 
-def _stream(s):
-    """The stream's handle; None: torch's current stream (the default one without torch)."""
+def _stream(s, dev=None):
+    """The stream's handle; None: torch's current stream (the default one without torch), of the
+    current device, which is `dev` where the caller knows it."""
     if s is None:
-        return _raw_stream(_get_device()) if _torch_on_gpu() else None
+        if not _torch_on_gpu():
+            return None
+        return _raw_stream(_get_device() if dev is None else dev)
     if isinstance(s, int):
         return s
     return s.cuda_stream
@@ -366,7 +370,7 @@ def pa_append_rope(prob, rope, query, new_key, new_value, query_start, total_tok
     q, qs = _rows(where, dev, query, total_tokens, heads, hd, query_stride)
     k, ks = _rows(where, dev, new_key, total_tokens, kv_heads, hd, key_stride)
     v, vs = _rows(where, dev, new_value, total_tokens, kv_heads, hd, value_stride)
-    if rope is not None:
+    if rope is not None and rope.lengths:
         _check_lengths(where, rope, total_tokens)
     batch, cache = prob.batch, prob.num_physical_pages * prob.page_size * kv_heads * hd
     starts, bt, ctx, q_out, kc, vc = _addresses(
@@ -375,7 +379,7 @@ def pa_append_rope(prob, rope, query, new_key, new_value, query_start, total_tok
         (query_out, _F16, total_tokens * heads * hd), (key_cache, _F16, cache),
         (value_cache, _F16, cache))
     _check(load().pa_append_rope(prob, rope, q, qs, k, ks, v, vs, starts, total_tokens, bt, ctx,
-                                 q_out, kc, vc, _stream(stream)), where)
+                                 q_out, kc, vc, _stream(stream, dev)), where)
 
 
 def pa_prefill(prob, query, query_start, total_tokens, max_query_len, key_cache, value_cache,
@@ -399,7 +403,8 @@ def pa_decode_scored(prob, score, query, key_cache, value_cache, block_tables, c
     where, batch, heads, hd = "pa_decode_scored", prob.batch, prob.query_heads, prob.head_dim
     dev, half = _device(), False
     if score is not None:
-        _check_lengths(where, score, heads, batch)
+        if score.lengths:
+            _check_lengths(where, score, heads, batch)
         half = score.out_type == OUT["fp16"]
     rows, cache = batch * heads * hd, prob.num_physical_pages * prob.page_size * prob.kv_heads * hd
     q, k, v, bt, ctx, o, ws = _addresses(
@@ -407,7 +412,7 @@ def pa_decode_scored(prob, score, query, key_cache, value_cache, block_tables, c
         (block_tables, _I32, batch * prob.max_pages_per_sequence), (context_lengths, _I32, batch),
         (out, _F16 if half else _F32, rows), (workspace, None, workspace_bytes))
     _check(load().pa_decode_scored(prob, score, q, k, v, bt, ctx, scale, o, opts, ws,
-                                   workspace_bytes, _stream(stream)), where)
+                                   workspace_bytes, _stream(stream, dev)), where)
 
 
 def pa_prefill_scored(prob, score, query, query_start, total_tokens, max_query_len, key_cache,
@@ -416,7 +421,7 @@ def pa_prefill_scored(prob, score, query, query_start, total_tokens, max_query_l
     """pa_prefill under a score rule (``score(out="fp16", ...)``); fp16 out."""
     where, batch, heads, hd = "pa_prefill_scored", prob.batch, prob.query_heads, prob.head_dim
     dev = _device()
-    if score is not None:
+    if score is not None and score.lengths:
         _check_lengths(where, score, heads, total_tokens, batch)
     rows = total_tokens * heads * hd
     cache = prob.num_physical_pages * prob.page_size * prob.kv_heads * hd
@@ -425,7 +430,7 @@ def pa_prefill_scored(prob, score, query, query_start, total_tokens, max_query_l
         (value_cache, _F16, cache), (block_tables, _I32, batch * prob.max_pages_per_sequence),
         (context_lengths, _I32, batch), (out, _F16, rows))
     _check(load().pa_prefill_scored(prob, score, q, qs, total_tokens, max_query_len, k, v, bt, ctx,
-                                    scale, o, opts, _stream(stream)), where)
+                                    scale, o, opts, _stream(stream, dev)), where)
 
 
 def pa_split_kv_partial(prob, query, key_cache, value_cache, block_tables, context_lengths, scale,
