@@ -787,7 +787,7 @@ pa_status_t resolve_score(const pa_score_t *score, float scale, ScoreArgs *s) {
         z_max = k == 0 ? -1. : std::min(z_max, std::pow(0x1p-24 / std::fabs(kTanhFit[k]), 1. / k));
     }
     s->cap_poly_max = z_max < 0. ? -1.f : static_cast<float>(std::min(z_max / (in * in), 3e38));
-    s->cap_wide = score->softcap > 256.f;
+    s->cap_wide = s->cap_in != 0.f && score->softcap > 256.f;
   }
   const uintptr_t ptrs = reinterpret_cast<uintptr_t>(score->slopes) |
                          reinterpret_cast<uintptr_t>(score->first_tokens) |

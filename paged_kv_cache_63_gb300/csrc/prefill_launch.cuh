@@ -73,4 +73,9 @@ pa_status_t launch_prefill(int head_dim, const PrefillArgsOf<kScored> &a, const 
   return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
+// Launches the scored kernel compiled for the parts of a rule with a wide cap
+// (prefill_scored_wide.cu).
+pa_status_t launch_parts_wide(int parts, int head_dim, const PrefillScoredArgs &a,
+                              const PrefillLaunch &l, cudaStream_t stream);
+
 }  // namespace pa

@@ -45,6 +45,7 @@ extern "C" pa_status_t pa_prefill_scored(const pa_problem_t *problem, const pa_s
   a.out16 = static_cast<uint16_t *>(out);
   const int parts = (a.s.cap_in != 0.f ? kRuleCap : 0) | (a.s.slopes ? kRuleSlopes : 0) |
                     (a.s.first ? kRuleFirst : 0);
-  return launch_parts<kRuleParts - 1>(parts, problem->head_dim, a, l,
-                                      static_cast<cudaStream_t>(stream));
+  const cudaStream_t on = static_cast<cudaStream_t>(stream);
+  if (a.s.cap_wide) return launch_parts_wide(parts | kRuleWide, problem->head_dim, a, l, on);
+  return launch_parts<kRuleParts - 1>(parts, problem->head_dim, a, l, on);
 }

@@ -15,11 +15,11 @@
 //    is then off by at most 0.47 cap * 5.8e-7, 1.4e-5 for a cap of 50, against the 2^-11 by
 //    which the fp16 probability is rounded. A warp with a larger argument in its unit takes
 //    1 - 2 / (1 + e^2t) for it, whose error of up to 3.6e-7 of the cap stays below a fifth of that
-//    rounding up to a cap of 256. Under larger caps such a unit goes through tensor memory once
-//    more and each score takes the form that is exact for it (eight prompts of 2048 in windows of
-//    1024, head_dim 128: 425 us if every unit does, 365 with the exponential alone, 265 with the
-//    polynomial alone; that code is rolled, because unrolled it slowed every capped call, at
-//    head_dim 64 241 -> 284 us). tanh being monotonic, the unit's maximum is that of the raw
+//    rounding up to a cap of 256. Larger caps have kernels of their own, in which such a unit goes
+//    through tensor memory once more and each score takes the form that is exact for it (eight
+//    prompts of 2048 in windows of 1024, head_dim 128: 423 us if every unit does, 348 with the
+//    exponential alone, 265 with the polynomial alone; in the same kernels that code cost calls
+//    under small caps up to 4 %). tanh being monotonic, the unit's maximum is that of the raw
 //    products, capped, where nothing is masked or biased.
 //  * The bias is linear in the key's column wherever no key of the columns lies past its query.
 //  * The mask is compared per score only in units where some row of the warp needs it, and a
@@ -38,8 +38,8 @@ struct PrefillScoredArgs : PrefillArgs {
   uint16_t *out16;  // [total][qh][hd], fp16 bits
 };
 
-// Parts of a rule that a kernel is compiled for.
-enum : int { kRuleCap = 1, kRuleSlopes = 2, kRuleFirst = 4, kRuleParts = 8 };
+// Parts of a rule that a kernel is compiled for; kRuleWide (only with kRuleCap): a cap above 256.
+enum : int { kRuleCap = 1, kRuleSlopes = 2, kRuleFirst = 4, kRuleParts = 8, kRuleWide = 8 };
 
 template <bool kScored>
 using PrefillArgsOf = std::conditional_t<kScored, PrefillScoredArgs, PrefillArgs>;
@@ -83,9 +83,9 @@ __device__ __forceinline__ float min3(float a, float b, float c) {
   return d;
 }
 
-// cap_out * tanh(v * cap_in) = cap_out (1 - 2 / (1 + e^2t)); e^2t overflows to infinity and underflows
-// to 0 where tanh is +-1. Off by at most 7.2e-7 of the score for |t| >= 1/2, and by 3.6e-7 of the cap
-// below, where the difference cancels.
+// cap_out * tanh(v * cap_in) = cap_out (1 - 2 / (1 + e^2t)); e^2t overflows to infinity and
+// underflows to 0 where tanh is +-1. Off by at most 7.2e-7 of the score for |t| >= 1/2, and by
+// 3.6e-7 of the cap below, where the difference cancels.
 __device__ __forceinline__ float cap_exp(const ScoreArgs &s, float v) {
   const float e = prefill_exp2(v * (s.cap_in * (2.f * kLog2e)));
   return fmaf(-2.f * s.cap_out, fast_rcp(1.f + e), s.cap_out);
@@ -246,6 +246,7 @@ __device__ __forceinline__ bool scored_weights(const ScoreArgs &s, float scale_l
   io.load(v);
   bool settled = false;
   if constexpr (kParts & kRuleCap) {
+    constexpr bool kWide = (kParts & kRuleWide) != 0;
     // what no row sees, and rows that do not count, must not choose the warp's form of tanh
     if (masked && !Io::kKeysCleared) {
 #pragma unroll
@@ -257,8 +258,10 @@ __device__ __forceinline__ bool scored_weights(const ScoreArgs &s, float scale_l
       // |tanh t| <= |t|: no score is farther from 0 than the uncapped one
       if (__any_sync(0xffffffffu, far * fabsf(scale_log2) > row.m + kScoredSlack)) {
         extremes(v, high, low);  // capped scores are monotonic in the raw products
-        const float2 best = scale_log2 >= 0.f ? make_float2(high, high) : make_float2(low, low);
-        if (!io.settle(row, cap_poly(s, best).x * best.x, later)) return false;
+        const float best = scale_log2 >= 0.f ? high : low;
+        // (the exponential form is near enough for a reference, but not at any cap)
+        const float top = kWide ? cap_poly(s, make_float2(best, best)).x * best : cap_exp(s, best);
+        if (!io.settle(row, top, later)) return false;
       }
       if constexpr (Io::kCapWithWeights) {
         const float2 n2 = make_float2(-row.m, -row.m);
@@ -271,11 +274,11 @@ __device__ __forceinline__ bool scored_weights(const ScoreArgs &s, float scale_l
       }
       settled = true;
     }
-    if (__builtin_expect(poly || !s.cap_wide, 1)) {
-      cap_scores(v, s, poly);
-    } else {
+    if (kWide && !poly) {
       io.rewrite([&](float x) { return cap_each(s, x); });
       io.load(v);
+    } else {
+      cap_scores(v, s, kWide || poly);
     }
     mult = 1.f;
   } else if (!(kParts & kRuleSlopes) && !masked) {
@@ -404,8 +407,8 @@ __device__ __forceinline__ void store_zero_row(uint16_t *dst, int n) {
   for (int i = 0; i < n; i += 8) *reinterpret_cast<uint4 *>(dst + i) = make_uint4(0, 0, 0, 0);
 }
 
-// Two outputs as fp16. Weights rounded up carry a mean of values next to fp16's largest past it by up
-// to 2^-11 of it, which would round to infinity: it is given as the largest.
+// Two outputs as fp16. Weights rounded up carry a mean of values next to fp16's largest past it by
+// up to 2^-11 of it, which would round to infinity: it is given as the largest.
 __device__ __forceinline__ uint32_t pack_mean2(float x, float y) {
   uint32_t r;
   asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(y), "f"(x));
