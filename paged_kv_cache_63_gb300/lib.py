@@ -177,11 +177,12 @@ def rope(rotary_dim, style="half", table=None, positions=None, table_rows=None) 
     rows = 0
     if table is not None and not isinstance(table, int):
         rows = table.shape[0]
-        if tuple(table.shape[1:]) != (2, r.rotary_dim // 2) or (table_rows or 0) > rows:
+        if r.rotary_dim != 0 and (tuple(table.shape[1:]) != (2, r.rotary_dim // 2)
+                                  or (table_rows or 0) > rows):
             raise PagedAttnError(1, "rope")
     r.table_rows = int(rows if table_rows is None else table_rows)
     r.keep = (table, positions)
-    r.lengths = _lengths(positions)
+    r.lengths = _lengths(positions) if r.rotary_dim != 0 else None
     return r
 
 

@@ -104,6 +104,12 @@ def test_rotations():
     assert status("append", lib.rope(32, "half", table, new((TOTAL - 1,), I32))) == 1
 
 
+def test_a_layer_that_does_not_rotate_may_keep_the_others_tensors():
+    """With rotary_dim 0 neither the table nor the positions are read."""
+    table, few = new((8, 2, 16), F32), new((TOTAL - 1,), I32)
+    assert status("append", lib.rope(0, "half", table, few)) in NO_DEVICE
+
+
 @pytest.mark.parametrize("call,rows", [("decode", B), ("prefill", TOTAL)])
 def test_score_rules(call, rows):
     out = "fp16" if call == "prefill" else "fp32"
