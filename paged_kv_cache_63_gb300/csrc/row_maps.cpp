@@ -44,9 +44,8 @@ pa_status_t encode_map(CUtensorMap *map, int rank, const void *base, const cuuin
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   };
   CUresult rc = encode();
-  if (rc != CUDA_SUCCESS) {
-    // The driver wants a context, which a thread has only once a call of the runtime has needed
-    // one: this may be the thread's first.
+  if (rc == CUDA_ERROR_INVALID_CONTEXT) {
+    // a thread has a context only once a call of the runtime has needed one: this may be its first
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || cudaSetDevice(dev) != cudaSuccess) return PA_ERR_CUDA;
     rc = encode();
