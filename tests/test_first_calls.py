@@ -1,6 +1,5 @@
 """A process's first calls, made by several threads at once under different plans."""
 
-import os
 import subprocess
 import sys
 
@@ -69,5 +68,5 @@ print("ok")
 @pytest.mark.parametrize("hd", [64, 128, 256])
 def test_first_calls_at_once(hd, call):
     r = subprocess.run([sys.executable, "-c", PROGRAM, str(hd), call], cwd=ROOT, timeout=300,
-                       env=dict(os.environ, PYTHONPATH=ROOT), capture_output=True, text=True)
+                       capture_output=True, text=True)
     assert r.returncode == 0 and r.stdout.strip() == "ok", r.stdout + r.stderr
