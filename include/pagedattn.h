@@ -443,6 +443,98 @@ pa_status_t pa_prefill_scored(const pa_problem_t *problem, const pa_score_t *sco
                               const int32_t *context_lengths, float scale, void *out,
                               const pa_options_t *options, void *stream);
 
+/* A quantised paged K/V cache: one byte for an element, and one scale for each token and K/V head.
+ * A row x of head_dim elements is held as codes c and a scale 2^e,
+ *     e = the smallest integer of -15 .. 8 with max |x_i| <= 448 * 2^e
+ *     c_i = the e4m3 number nearest to x_i / 2^e (ties to even; at most 448 in size, or 240
+ *           for e = 8)
+ * and stands for the numbers c_i * 2^e, which are finite fp16 numbers: the calls that read a row work
+ * on them exactly. e4m3: sign, 4 bits of exponent (bias 7), 3 of mantissa. A scale is stored as the
+ * byte e + 127 (e8m0). Where a byte that is no such scale, or a NaN code, belongs to a token that no
+ * query of a call sees, it reaches no output. */
+typedef struct pa_quant_cache_t {
+  void *key;            /* device, codes, in the problem's cache_layout, 16-byte aligned */
+  void *value;          /* likewise */
+  uint8_t *key_scale;   /* device, [num_physical_pages][kv_heads][page_size] in either layout,
+                           16-byte aligned */
+  uint8_t *value_scale; /* likewise */
+} pa_quant_cache_t;
+
+/* The norm of queries and keys, head by head, before the rotation (pa_append_quant):
+ *     x_i -> x_i / sqrt(mean_i(x_i^2) + eps) * weight_i */
+typedef struct pa_norm_t {
+  float eps;        /* 1e-30 to 1e30 */
+  int32_t reserved; /* 0 */
+  const float *query_weight; /* device, fp32 [head_dim], 16-byte aligned; NULL: queries as they are */
+  const float *key_weight;   /* likewise for keys */
+} pa_norm_t;
+
+/* Write several new tokens per sequence into a quantised cache: pa_append_rope's operation ("[TIL]
+ * Optimizing paged attention", section "Paged Attention": the K and V of earlier tokens are kept and
+ * reused), arguments and checks, with the norm before the rotation and each key and value row
+ * rounded to the format of pa_quant_cache_t. One call takes a layer's fused projection to what
+ * pa_prefill_quant or pa_decode_quant reads.
+ *   norm         host struct, or NULL: no norm
+ *   rope         as for pa_append_rope
+ *   query_out    fp16, normed and rotated, rounded once
+ *   cache        host struct, not NULL
+ * Each code is the one nearest to the exact normed and rotated value (the arithmetic on keys carries
+ * its rounding errors along). New rows must be finite: with an element that is not, its row of that
+ * head holds anything. */
+pa_status_t pa_append_quant(const pa_problem_t *problem, const pa_norm_t *norm,
+                            const pa_rope_t *rope, const void *query, int64_t query_stride,
+                            const void *new_key, int64_t key_stride, const void *new_value,
+                            int64_t value_stride, const int32_t *query_start,
+                            int64_t total_tokens, const int32_t *block_tables,
+                            const int32_t *context_lengths, void *query_out,
+                            const pa_quant_cache_t *cache, void *stream);
+
+/* Read tokens of a quantised cache back as fp16 rows, exactly: the way out of the format, to move
+ * sequences to a cache of 16 bits or to another holder, or to look at what was written. The tokens
+ * are named as for pa_append_quant, so its arrays read back what it wrote: sequence b's
+ * n_b = query_start[b + 1] - query_start[b] rows are the LAST n_b of its context_lengths[b] tokens
+ * (block-table gather of "[TIL] Optimizing paged attention", section "Baseline").
+ *   key_out, value_out  fp16 [total_tokens][kv_heads][head_dim], packed, 16-byte aligned; one of
+ *                       them may be NULL: not wanted. Rows before query_start[0] and from
+ *                       query_start[batch] on, and those of sequences and pages that are flagged as
+ *                       by pa_append_rope, are left alone
+ * Runs asynchronously on `stream`; allocates nothing. */
+pa_status_t pa_read_quant(const pa_problem_t *problem, const pa_quant_cache_t *cache,
+                          const int32_t *query_start, int64_t total_tokens,
+                          const int32_t *block_tables, const int32_t *context_lengths,
+                          void *key_out, void *value_out, void *stream);
+
+/* Bytes of device workspace that pa_decode_quant needs for `problem` and `options` on the current
+ * device (0 where no sequence is split). */
+pa_status_t pa_quant_workspace_size(const pa_problem_t *problem, const pa_options_t *options,
+                                    size_t *bytes);
+
+/* One decode step over a quantised cache: pa_decode_scored's operation ("[TIL] Optimizing paged
+ * attention", sections "Paged Attention" and "V4 (Context-axis parallelism)"), rule, outputs and
+ * checks on the numbers that the cache stands for, at a little over half the bytes.
+ *   score      as for pa_decode_scored (NULL: no rule, fp32 out)
+ *   options    may be NULL; schedule, workers, stages, warps_per_cta and test_flags are read
+ *              as by pa_decode_ex, the others must be 0 (PA_ERR_UNSUPPORTED)
+ *   workspace  caller-owned device memory of workspace_bytes >= pa_quant_workspace_size(problem,
+ *              options), 256-byte aligned; NULL if that is 0. It needs no initialisation and
+ *              nothing is kept in it between calls; calls that may overlap in time need one
+ *              each. */
+pa_status_t pa_decode_quant(const pa_problem_t *problem, const pa_score_t *score,
+                            const void *query, const pa_quant_cache_t *cache,
+                            const int32_t *block_tables, const int32_t *context_lengths,
+                            float scale, void *out, const pa_options_t *options, void *workspace,
+                            size_t workspace_bytes, void *stream);
+
+/* Attention of several new tokens per sequence over a quantised cache: pa_prefill_scored's operation
+ * ("[TIL] Optimizing paged attention", section "Flash Attention" over the paged cache), arguments,
+ * rule (host struct, not NULL; out_type PA_OUT_FP16) and checks on the numbers that the cache stands
+ * for. The new tokens' keys and values are in the cache (pa_append_quant). */
+pa_status_t pa_prefill_quant(const pa_problem_t *problem, const pa_score_t *score,
+                             const void *query, const int32_t *query_start, int64_t total_tokens,
+                             int32_t max_query_len, const pa_quant_cache_t *cache,
+                             const int32_t *block_tables, const int32_t *context_lengths,
+                             float scale, void *out, const pa_options_t *options, void *stream);
+
 /* Read and clear the device error word of the current device (PA_DEVERR_* bits) after
  * the work queued on `stream` finishes. Synchronises `stream`. The word records the
  * preconditions of "[TIL] Optimizing paged attention", section "Paged Attention" (a

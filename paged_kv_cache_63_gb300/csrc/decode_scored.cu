@@ -23,140 +23,10 @@
 #include <cmath>
 #include <cstring>
 
-#include "decode_kernel.cuh"
-#include "early_launch.cuh"
 #include "row_maps.h"
-#include "score_rule.cuh"
+#include "span_split.cuh"
 
 namespace pa {
-
-struct ScoredArgs {
-  KernelArgs k;  // out, flags, epoch and the fixed-split arrays are unused
-  ScoreArgs s;
-  void *out;  // [batch][query_heads][head_dim], fp32 or fp16
-};
-
-// The tokens [lo, end) that sequence b's query sees.
-struct Span {
-  int lo, end;
-};
-
-__device__ __forceinline__ Span load_span(const ScoredArgs &a, int b) {
-  Span sp;
-  sp.end = load_ctx(a.k, b);
-  sp.lo = sp.end > 0 ? min(first_seen(a.s, b, sp.end - 1), sp.end) : 0;
-  return sp;
-}
-
-// Tiles start at multiples of T, so that a tile's pieces never cross a page.
-__device__ __forceinline__ int span_start(const Span &sp, int T) { return sp.lo & ~(T - 1); }
-
-__device__ __forceinline__ int span_tiles(const Span &sp, int T) {
-  return sp.end > sp.lo ? (sp.end - span_start(sp, T) + T - 1) / T : 0;
-}
-
-// Position of a worker in its token stream.
-struct SpanCursor {
-  int b, us;  // sequence, group unit
-  int tok;    // first token of the current tile
-  Span sp;
-  int left;       // tiles still to visit
-  long long ug0;  // global index of the unit's first tile
-};
-
-__device__ __forceinline__ void advance(const ScoredArgs &a, SpanCursor &c, int T) {
-  c.tok += T;
-  --c.left;
-  if (c.left > 0 && c.tok >= c.sp.end) {
-    c.ug0 += span_tiles(c.sp, T);
-    if (++c.us == a.k.upg) {
-      c.us = 0;
-      do {
-        ++c.b;
-        if (c.b < a.k.batch) c.sp = load_span(a, c.b);
-      } while (c.b < a.k.batch && c.sp.end <= c.sp.lo);
-    }
-    c.tok = span_start(c.sp, T);
-  }
-}
-
-// Total tiles, the workers that get tiles, and the cursor at this worker's first tile; false
-// when it gets none (the split of balanced_start over the spans' tiles).
-__device__ inline bool span_balanced_start(const ScoredArgs &a, int worker, int T, SpanCursor &c,
-                                           long long &total, long long &nworkers) {
-  const int lane = threadIdx.x & 31;
-  const int batch = a.k.batch, upg = a.k.upg;
-  const int blk = (batch + 31) >> 5;
-  const int b0 = min(lane * blk, batch);
-  const int b1 = min(b0 + blk, batch);
-  long long mine = 0;
-#pragma unroll 8
-  for (int b = b0; b < b1; ++b) mine += span_tiles(load_span(a, b), T);
-  long long incl = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += y;
-  }
-  total = __shfl_sync(0xffffffffu, incl, 31) * upg;
-  nworkers = total < a.k.workers ? total : a.k.workers;
-  if (worker >= nworkers) return false;
-  const long long s = worker_start(worker, total, nworkers);
-  const long long e = worker_start(worker + 1, total, nworkers);
-  const int L = __ffs(__ballot_sync(0xffffffffu, incl * upg > s)) - 1;
-  long long run = __shfl_sync(0xffffffffu, incl - mine, L) * upg;
-  const int lb0 = min(L * blk, batch);
-  const int lb1 = min(lb0 + blk, batch);
-  for (int base = lb0; base < lb1; base += 32) {
-    const int b = base + lane;
-    const long long t =
-        b < lb1 ? static_cast<long long>(span_tiles(load_span(a, b), T)) * upg : 0;
-    long long in2 = t;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, in2, o);
-      if (lane >= o) in2 += y;
-    }
-    const long long chunk = __shfl_sync(0xffffffffu, in2, 31);
-    if (s < run + chunk) {
-      const int M = __ffs(__ballot_sync(0xffffffffu, run + in2 > s)) - 1;
-      const long long excl = run + __shfl_sync(0xffffffffu, in2 - t, M);
-      c.b = base + M;
-      c.sp = load_span(a, c.b);
-      const int tb = span_tiles(c.sp, T);
-      const long long inner = s - excl;
-      c.us = static_cast<int>(inner / tb);
-      c.tok = span_start(c.sp, T) + static_cast<int>(inner % tb) * T;
-      c.ug0 = excl + static_cast<long long>(c.us) * tb;
-      c.left = static_cast<int>(e - s);
-      return true;
-    }
-    run += chunk;
-  }
-  return false;
-}
-
-// One elected lane of the converged warp announces the bytes a barrier waits for, or issues a
-// TMA load; the operands are the same in every lane. (In a branch of lane 0 alone the issue of a
-// 16-token tile of head_dim 128 took 1030 of the 2970 cycles that a worker spends on the tile.)
-__device__ __forceinline__ void expect_bytes_warp(uint32_t bar, uint32_t bytes) {
-  asm volatile(
-      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
-      "@e mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}" ::"r"(bar),
-      "r"(bytes)
-      : "memory");
-}
-
-__device__ __forceinline__ void tma_rows_warp(uint32_t dst, const CUtensorMap *map, uint32_t bar,
-                                              int row, int head, int block, uint64_t policy) {
-  asm volatile(
-      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
-      "@e cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
-      ".L2::cache_hint [%0], [%1, {%3, %4, %5, %6}], [%2], %7;\n\t}" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(0), "r"(row), "r"(head), "r"(block),
-      "l"(policy)
-      : "memory");
-}
 
 // Issue the TMA loads of the tile at cursor c into a stage (warp-uniform). Pieces (min(page
 // size, T) rows) that hold no seen token are not loaded. A tile of one piece is one load each
@@ -214,22 +84,7 @@ __device__ __forceinline__ void issue_span_tile(const ScoredArgs &sa, const CUte
   }
 }
 
-// D(16x8, fp32) = A(16x16, fp16) B(16x8, fp16) + D.
-__device__ __forceinline__ void mma_rows16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                           uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-      "{%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-// Running state of a unit; a lane's row (head) is lane / 4. Probabilities are 2^(x - m): the
-// reference m follows the row's maximum so that it lies kLift below it when set, and moves
-// only when a score passes m + kLift + kRescaleSlack. They stay within 2^15 (fp16 holds them),
-// and a probability 2^-31 of the largest still has a nonzero fp16 value.
-constexpr float kLift = 7.f;
-
+// Running state of a unit; a lane's row (head) is lane / 4.
 template <int HD>
 struct SpanState {
   float m, lsum;
@@ -371,14 +226,6 @@ __device__ __forceinline__ void span_tile(SpanState<HD> &st, const MmaLane<HD, T
     st.o[2 * dt + 1][0] += d1[0] + d1[2];
     st.o[2 * dt + 1][1] += d1[1] + d1[3];
   }
-}
-
-// Zero the output rows of a unit that sees nothing.
-template <int HD>
-__device__ __forceinline__ void zero_rows_out(const ScoredArgs &a, const UnitInfo &u) {
-  const int lane = threadIdx.x & 31;
-  const long long base = (static_cast<long long>(u.b) * a.k.qh + u.h0) * HD;
-  for (int i = lane * 2; i < u.nh * HD; i += 64) store_out2(a.s, a.out, base + i, 0.f, 0.f);
 }
 
 // Eight warps leave a thread 255 registers: enough at head_dim 64 and 128 (156 and 203); at 256,
@@ -803,19 +650,6 @@ pa_status_t resolve_score(const pa_score_t *score, float scale, ScoreArgs *s) {
 
 namespace {
 
-constexpr int kMaxDev = 64;
-
-// SM count of the current device, looked up once; 0 on failure.
-int sm_count() {
-  static std::atomic<int> known[kMaxDev];
-  int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDev) return 0;
-  n = known[dev].load(std::memory_order_relaxed);
-  if (n == 0 && cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess)
-    known[dev].store(n, std::memory_order_relaxed);
-  return n;
-}
-
 template <int HD, int T>
 cudaError_t launch_scored(const ScoredArgs &a, const CUtensorMap &tk, const CUtensorMap &tv,
                           const pa_plan_t &pl, cudaStream_t stream) {
@@ -856,6 +690,64 @@ cudaError_t launch_join_hd(const ScoredArgs &a, int units, int heads, int warps,
 
 }  // namespace
 
+int device_sm_count() {
+  static std::atomic<int> known[kMaxLaunchDevices];
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxLaunchDevices) return 0;
+  n = known[dev].load(std::memory_order_relaxed);
+  if (n == 0 && cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess)
+    known[dev].store(n, std::memory_order_relaxed);
+  return n;
+}
+
+pa_status_t fill_scored_args(const pa_problem_t *problem, const pa_plan_t &pl, const void *query,
+                             const int32_t *block_tables, const int32_t *context_lengths,
+                             float scale, void *out, void *workspace, ScoredArgs *a) {
+  const int g = problem->query_heads / problem->kv_heads;
+  KernelArgs &k = a->k;
+  k.q = static_cast<const uint16_t *>(query);
+  k.bt = block_tables;
+  k.ctx = context_lengths;
+  k.err = device_error_word();
+  if (!k.err) return PA_ERR_CUDA;
+  k.batch = problem->batch;
+  k.qh = problem->query_heads;
+  k.kvh = problem->kv_heads;
+  k.hd = problem->head_dim;
+  k.ps = problem->page_size;
+  while ((1 << k.ps_shift) < k.ps) ++k.ps_shift;
+  k.maxp = problem->max_pages_per_sequence;
+  k.num_pages = problem->num_physical_pages;
+  k.layout = problem->cache_layout;
+  k.g = g;
+  k.sub = (g + kMaxHeads - 1) / kMaxHeads;
+  k.nh_unit = (g + k.sub - 1) / k.sub;
+  k.ups = k.kvh * k.sub;
+  k.group = pl.group;
+  k.upg = k.ups / k.group;
+  k.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
+  k.mode = pl.schedule == PA_SCHEDULE_SINGLE ? MODE_SINGLE : MODE_BALANCED;
+  k.workers = pl.workers / pl.group;
+  k.stages = pl.stages;
+  a->out = out;
+  if (k.mode == MODE_BALANCED) {
+    const int64_t slots = static_cast<int64_t>(pl.units) + pl.workers;
+    char *base = static_cast<char *>(workspace);
+    k.ws_ml = reinterpret_cast<float *>(base);
+    k.ws_acc = reinterpret_cast<float *>(base + (slots * kMaxHeads * 2 * 4 + 255) / 256 * 256);
+  }
+  return PA_OK;
+}
+
+cudaError_t launch_join_states(const ScoredArgs &a, int units, int heads, int warps, int tile,
+                               cudaStream_t stream) {
+  switch (a.k.hd) {
+    case 64: return launch_join_hd<64>(a, units, heads, warps, tile, stream);
+    case 128: return launch_join_hd<128>(a, units, heads, warps, tile, stream);
+    default: return launch_join_hd<256>(a, units, heads, warps, tile, stream);
+  }
+}
+
 }  // namespace pa
 
 extern "C" pa_status_t pa_decode_scored(const pa_problem_t *problem, const pa_score_t *score,
@@ -895,7 +787,7 @@ extern "C" pa_status_t pa_decode_scored(const pa_problem_t *problem, const pa_sc
   int smem_optin = 0;
   st = current_device_smem(&smem_optin);
   if (st != PA_OK) return st;
-  st = pa_plan(problem, options, sm_count(), &pl);
+  st = pa_plan(problem, options, device_sm_count(), &pl);
   if (st != PA_OK) return st;
   // At head_dim 128 a warp with one tile on the way beside the one it works on is faster than
   // with two (32 heads of their own over 2048 tokens, 64 sequences: 191 against 202 us; 8 K/V
@@ -920,41 +812,12 @@ extern "C" pa_status_t pa_decode_scored(const pa_problem_t *problem, const pa_sc
   if (st != PA_OK) return st;
   st = encode_row_map(&tv, value_cache, problem, rows, blocks);
   if (st != PA_OK) return st;
-  const int g = problem->query_heads / problem->kv_heads;
+  st = fill_scored_args(problem, pl, query, block_tables, context_lengths, scale, out, workspace,
+                        &a);
+  if (st != PA_OK) return st;
   KernelArgs &k = a.k;
-  k.q = static_cast<const uint16_t *>(query);
-  k.bt = block_tables;
-  k.ctx = context_lengths;
-  k.err = device_error_word();
-  if (!k.err) return PA_ERR_CUDA;
-  k.batch = problem->batch;
-  k.qh = problem->query_heads;
-  k.kvh = problem->kv_heads;
-  k.hd = hd;
-  k.ps = problem->page_size;
-  while ((1 << k.ps_shift) < k.ps) ++k.ps_shift;
-  k.maxp = problem->max_pages_per_sequence;
-  k.num_pages = problem->num_physical_pages;
-  k.layout = problem->cache_layout;
-  k.g = g;
-  k.sub = (g + kMaxHeads - 1) / kMaxHeads;
-  k.nh_unit = (g + k.sub - 1) / k.sub;
-  k.ups = k.kvh * k.sub;
-  k.group = pl.group;
-  k.upg = k.ups / k.group;
-  k.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
-  k.mode = pl.schedule == PA_SCHEDULE_SINGLE ? MODE_SINGLE : MODE_BALANCED;
-  k.workers = pl.workers / pl.group;
-  k.stages = pl.stages;
   k.warp_smem = warp_smem_bytes(hd, 1, kMaxHeads, pl.stages, pl.tile_tokens);
   if (options && (options->test_flags & PA_TEST_EXPIRE_WAITS)) k.tx_extra = 16;
-  a.out = out;
-  if (k.mode == MODE_BALANCED) {
-    const int64_t slots = static_cast<int64_t>(pl.units) + pl.workers;
-    char *base = static_cast<char *>(workspace);
-    k.ws_ml = reinterpret_cast<float *>(base);
-    k.ws_acc = reinterpret_cast<float *>(base + (slots * kMaxHeads * 2 * 4 + 255) / 256 * 256);
-  }
 
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e = cudaErrorInvalidValue;
@@ -968,12 +831,8 @@ extern "C" pa_status_t pa_decode_scored(const pa_problem_t *problem, const pa_sc
     e = launch_scored<256, 16>(a, tk, tv, pl, s);
   if (e != cudaSuccess) return PA_ERR_CUDA;
   if (k.mode == MODE_BALANCED) {
-    const int warps = combine_warps_per_pair(pl.units, pl.workers);
-    switch (hd) {
-      case 64: e = launch_join_hd<64>(a, pl.units, k.nh_unit, warps, pl.tile_tokens, s); break;
-      case 128: e = launch_join_hd<128>(a, pl.units, k.nh_unit, warps, pl.tile_tokens, s); break;
-      default: e = launch_join_hd<256>(a, pl.units, k.nh_unit, warps, pl.tile_tokens, s); break;
-    }
+    e = launch_join_states(a, pl.units, k.nh_unit, combine_warps_per_pair(pl.units, pl.workers),
+                           pl.tile_tokens, s);
     if (e != cudaSuccess) return PA_ERR_CUDA;
   }
   return PA_OK;

@@ -146,6 +146,8 @@ pa_status_t encode_cache_map_rows(CUtensorMap *map, const void *base, const pa_p
 pa_status_t encode_query_map(CUtensorMap *map, const void *query, int64_t total_tokens,
                              int query_heads, int head_dim, int heads_per_box, int tokens_per_box);
 pa_status_t check_problem_public(const pa_problem_t *p);
+// Addresses of a quantised cache (append_quant.cu).
+pa_status_t check_quant_cache(const pa_quant_cache_t *cache);
 // The current device's opt-in shared memory per block; PA_ERR_NO_DEVICE unless sm_103.
 pa_status_t current_device_smem(int *smem_optin);
 

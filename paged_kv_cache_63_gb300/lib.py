@@ -2,9 +2,9 @@
 
 Every function here forwards to the C entry point of the same name; all compute runs in
 the library's CUDA kernels. Tensor arguments may be torch CUDA tensors or raw device
-addresses (int). pa_append_rope, pa_decode_scored and pa_prefill_scored check the device,
-layout, type and length of tensors first; an address is passed on as it is. There is no
-fallback: if the shared library is missing or fails to load, ``load()`` raises.
+addresses (int). pa_append_rope, pa_decode_scored, pa_prefill_scored and the calls on a
+quantised cache check the device, layout, type and length of tensors first; an address is passed
+on as it is. There is no fallback: if the shared library is missing or fails to load, ``load()`` raises.
 """
 
 from __future__ import annotations
@@ -37,7 +37,8 @@ ROPE_STYLE = {"half": 0, "interleaved": 1}
 # Every entry point include/pagedattn.h declares.
 EXPORTS = ("pa_plan", "pa_workspace_size", "pa_workspace_init", "pa_decode", "pa_decode_ex",
            "pa_decode_noalloc", "pa_append_kv", "pa_append_rope", "pa_prefill",
-           "pa_decode_scored", "pa_prefill_scored",
+           "pa_decode_scored", "pa_prefill_scored", "pa_append_quant", "pa_read_quant",
+           "pa_quant_workspace_size", "pa_decode_quant", "pa_prefill_quant",
            "pa_split_kv_partial", "pa_split_kv_combine", "pa_get_device_error",
            "pa_status_string", "pa_version")
 
@@ -87,6 +88,19 @@ class pa_score_t(ctypes.Structure):
     lengths = None  # of the tensors pointed to, where score() was given some
 
 
+class pa_norm_t(ctypes.Structure):
+    _fields_ = [("eps", ctypes.c_float), ("reserved", ctypes.c_int32),
+                ("query_weight", ctypes.c_void_p), ("key_weight", ctypes.c_void_p)]
+    lengths = None  # of the tensors pointed to, where norm() was given some
+
+
+class pa_quant_cache_t(ctypes.Structure):
+    _fields_ = [("key", ctypes.c_void_p), ("value", ctypes.c_void_p),
+                ("key_scale", ctypes.c_void_p), ("value_scale", ctypes.c_void_p)]
+    lengths = None  # of the tensors pointed to, where quant_cache() was given some
+    device = None   # they are on this device
+
+
 _lib = None
 _lock = threading.Lock()
 
@@ -122,6 +136,16 @@ def load(path: Optional[str] = None):
                                          P(pa_options_t), vp, ctypes.c_size_t, vp]
         lib.pa_prefill_scored.argtypes = [P(pa_problem_t), P(pa_score_t), vp, vp, i64, i32, vp, vp,
                                           vp, vp, f32, vp, P(pa_options_t), vp]
+        lib.pa_append_quant.argtypes = [P(pa_problem_t), P(pa_norm_t), P(pa_rope_t), vp, i64, vp, i64,
+                                        vp, i64, vp, i64, vp, vp, vp, P(pa_quant_cache_t), vp]
+        lib.pa_read_quant.argtypes = [P(pa_problem_t), P(pa_quant_cache_t), vp, i64, vp, vp, vp, vp,
+                                      vp]
+        lib.pa_quant_workspace_size.argtypes = [P(pa_problem_t), P(pa_options_t),
+                                                P(ctypes.c_size_t)]
+        lib.pa_decode_quant.argtypes = [P(pa_problem_t), P(pa_score_t), vp, P(pa_quant_cache_t), vp,
+                                        vp, f32, vp, P(pa_options_t), vp, ctypes.c_size_t, vp]
+        lib.pa_prefill_quant.argtypes = [P(pa_problem_t), P(pa_score_t), vp, vp, i64, i32,
+                                         P(pa_quant_cache_t), vp, vp, f32, vp, P(pa_options_t), vp]
         lib.pa_prefill.argtypes = [P(pa_problem_t), vp, vp, ctypes.c_int64, i32, vp, vp, vp, vp,
                                    f32, vp, P(pa_options_t), vp]
         lib.pa_split_kv_partial.argtypes = [P(pa_problem_t), vp, vp, vp, vp, vp, f32, i32, i32, vp,
@@ -200,6 +224,46 @@ def score(softcap=0.0, window=0, slopes=None, first_tokens=None, prefix_lengths=
     s.keep = (slopes, first_tokens, prefix_lengths)
     s.lengths = _lengths(slopes, first_tokens, prefix_lengths)
     return s
+
+
+def norm(eps=1e-6, query_weight=None, key_weight=None) -> pa_norm_t:
+    """pa_norm_t: the norm of queries and keys in pa_append_quant. Weights are fp32 [head_dim], or
+    None: those rows are not normed. The struct keeps the tensors it points to."""
+    n = pa_norm_t()
+    n.eps = float(eps)
+    n.query_weight, n.key_weight = _addresses("norm", _device(), (query_weight, _F32, 0),
+                                              (key_weight, _F32, 0))
+    n.keep = (query_weight, key_weight)
+    n.lengths = _lengths(query_weight, key_weight)
+    return n
+
+
+def quant_cache(key, value, key_scale, value_scale) -> pa_quant_cache_t:
+    """pa_quant_cache_t: codes in the problem's layout (uint8 or float8_e4m3fn tensors) and scale
+    bytes [num_physical_pages][kv_heads][page_size] (uint8 or float8_e8m0fnu). The struct keeps
+    the tensors it points to."""
+    c = pa_quant_cache_t()
+    dev = _device()
+    for x in (key, value, key_scale, value_scale):
+        if x is not None and not isinstance(x, int) and x.element_size() != 1:
+            raise PagedAttnError(1, "quant_cache")
+    c.key, c.value, c.key_scale, c.value_scale = _addresses(
+        "quant_cache", dev, (key, None, 0), (value, None, 0), (key_scale, None, 0),
+        (value_scale, None, 0))
+    c.keep = (key, value, key_scale, value_scale)
+    c.lengths = _lengths(*c.keep)
+    c.device = dev
+    return c
+
+
+def _check_quant_cache(where, cache, prob, dev):
+    """Whether the tensors of quant_cache() hold the problem's cache, on the call's device."""
+    if cache is not None and cache.lengths:
+        rows = prob.num_physical_pages * prob.page_size * prob.kv_heads
+        n = rows * prob.head_dim
+        if cache.device != dev:
+            raise PagedAttnError(1, where)
+        _check_lengths(where, cache, n, n, rows, rows)
 
 
 def _ptr(x):
@@ -432,6 +496,89 @@ def pa_prefill_scored(prob, score, query, query_start, total_tokens, max_query_l
         (context_lengths, _I32, batch), (out, _F16, rows))
     _check(load().pa_prefill_scored(prob, score, q, qs, total_tokens, max_query_len, k, v, bt, ctx,
                                     scale, o, opts, _stream(stream, dev)), where)
+
+
+def pa_append_quant(prob, norm, rope, query, new_key, new_value, query_start, total_tokens,
+                    block_tables, context_lengths, query_out, cache, query_stride=0, key_stride=0,
+                    value_stride=0, stream=None):
+    """pa_append_rope into a quantised cache (``quant_cache()``), with queries and keys normed head
+    by head first (``norm()`` or None)."""
+    where, heads, kv_heads, hd = "pa_append_quant", prob.query_heads, prob.kv_heads, prob.head_dim
+    dev = _device()
+    q, qs = _rows(where, dev, query, total_tokens, heads, hd, query_stride)
+    k, ks = _rows(where, dev, new_key, total_tokens, kv_heads, hd, key_stride)
+    v, vs = _rows(where, dev, new_value, total_tokens, kv_heads, hd, value_stride)
+    if rope is not None and rope.lengths:
+        _check_lengths(where, rope, total_tokens)
+    if norm is not None and norm.lengths:
+        _check_lengths(where, norm, hd, hd)
+    _check_quant_cache(where, cache, prob, dev)
+    batch = prob.batch
+    starts, bt, ctx, q_out = _addresses(
+        where, dev, (query_start, _I32, batch + 1),
+        (block_tables, _I32, batch * prob.max_pages_per_sequence), (context_lengths, _I32, batch),
+        (query_out, _F16, total_tokens * heads * hd))
+    _check(load().pa_append_quant(prob, norm, rope, q, qs, k, ks, v, vs, starts, total_tokens, bt,
+                                  ctx, q_out, cache, _stream(stream, dev)), where)
+
+
+def pa_read_quant(prob, cache, query_start, total_tokens, block_tables, context_lengths, key_out,
+                  value_out, stream=None):
+    """Each sequence's last n_b tokens of a quantised cache as fp16 rows [total_tokens][kv_heads]
+    [head_dim]; key_out or value_out may be None."""
+    where, batch, dev = "pa_read_quant", prob.batch, _device()
+    _check_quant_cache(where, cache, prob, dev)
+    rows = total_tokens * prob.kv_heads * prob.head_dim
+    starts, bt, ctx, k, v = _addresses(
+        where, dev, (query_start, _I32, batch + 1),
+        (block_tables, _I32, batch * prob.max_pages_per_sequence), (context_lengths, _I32, batch),
+        (key_out, _F16, rows), (value_out, _F16, rows))
+    _check(load().pa_read_quant(prob, cache, starts, total_tokens, bt, ctx, k, v,
+                                _stream(stream, dev)), where)
+
+
+def pa_quant_workspace_size(prob: pa_problem_t, opts: Optional[pa_options_t] = None) -> int:
+    n = ctypes.c_size_t(0)
+    _check(load().pa_quant_workspace_size(prob, opts, ctypes.byref(n)), "pa_quant_workspace_size")
+    return int(n.value)
+
+
+def pa_decode_quant(prob, score, query, cache, block_tables, context_lengths, scale, out,
+                    opts: Optional[pa_options_t] = None, workspace=None, workspace_bytes: int = 0,
+                    stream=None):
+    """pa_decode_scored over a quantised cache; the workspace is pa_quant_workspace_size's."""
+    where, batch, heads, hd = "pa_decode_quant", prob.batch, prob.query_heads, prob.head_dim
+    dev, half = _device(), False
+    if score is not None:
+        if score.lengths:
+            _check_lengths(where, score, heads, batch)
+        half = score.out_type == OUT["fp16"]
+    _check_quant_cache(where, cache, prob, dev)
+    rows = batch * heads * hd
+    q, bt, ctx, o, ws = _addresses(
+        where, dev, (query, _F16, rows),
+        (block_tables, _I32, batch * prob.max_pages_per_sequence), (context_lengths, _I32, batch),
+        (out, _F16 if half else _F32, rows), (workspace, None, workspace_bytes))
+    _check(load().pa_decode_quant(prob, score, q, cache, bt, ctx, scale, o, opts, ws,
+                                  workspace_bytes, _stream(stream, dev)), where)
+
+
+def pa_prefill_quant(prob, score, query, query_start, total_tokens, max_query_len, cache,
+                     block_tables, context_lengths, scale, out,
+                     opts: Optional[pa_options_t] = None, stream=None):
+    """pa_prefill_scored over a quantised cache; fp16 out."""
+    where, batch, heads, hd = "pa_prefill_quant", prob.batch, prob.query_heads, prob.head_dim
+    dev = _device()
+    if score is not None and score.lengths:
+        _check_lengths(where, score, heads, total_tokens, batch)
+    _check_quant_cache(where, cache, prob, dev)
+    rows = total_tokens * heads * hd
+    q, qs, bt, ctx, o = _addresses(
+        where, dev, (query, _F16, rows), (query_start, _I32, batch + 1),
+        (block_tables, _I32, batch * prob.max_pages_per_sequence), (context_lengths, _I32, batch),
+        (out, _F16, rows))
+    _check(load().pa_prefill_quant(prob, score, q, qs, total_tokens, max_query_len, cache, bt, ctx,
+                                   scale, o, opts, _stream(stream, dev)), where)
 
 
 def pa_split_kv_partial(prob, query, key_cache, value_cache, block_tables, context_lengths, scale,
