@@ -227,27 +227,32 @@ pa_status_t resolve(const pa_problem_t *p, const pa_options_t *o, int sm_count, 
 // 3-D map over a cache with a box of rows_per_box rows of one head, 64 elements wide, and
 // 128-byte swizzle. Token-major caches are viewed as [num_pages * page_size rows][kv_heads]
 // [head_dim] (box 64 x 1 x rows), head-major ones as [num_pages * kv_heads][page_size]
-// [head_dim] (box 64 x rows x 1); either way a box lands as rows x 128 bytes.
+// [head_dim] (box 64 x rows x 1); either way a box lands as rows x 128 bytes. `codes`: one-byte
+// elements in boxes 128 wide (64 bytes a row at head_dim 64).
 pa_status_t encode_cache_map(CUtensorMap *map, const void *base, const pa_problem_t *p,
-                             int rows_per_box) {
+                             int rows_per_box, bool codes = false) {
   const bool hm = p->cache_layout == PA_LAYOUT_HEAD_MAJOR;
   const cuuint64_t hd = static_cast<cuuint64_t>(p->head_dim);
+  const cuuint64_t row = codes ? hd : hd * 2;  // bytes of a head's row
   cuuint64_t dims[3], strides[2];
-  cuuint32_t box[3] = {64, 1, 1};
+  cuuint32_t box[3] = {codes && hd > 64 ? 128u : 64u, 1, 1};
   dims[0] = hd;
-  strides[0] = hd * 2;
+  strides[0] = row;
   if (hm) {
     dims[1] = static_cast<cuuint64_t>(p->page_size);
     dims[2] = static_cast<cuuint64_t>(p->num_physical_pages) * p->kv_heads;
-    strides[1] = static_cast<cuuint64_t>(p->page_size) * hd * 2;
+    strides[1] = static_cast<cuuint64_t>(p->page_size) * row;
     box[1] = static_cast<cuuint32_t>(rows_per_box);
   } else {
     dims[1] = static_cast<cuuint64_t>(p->kv_heads);
     dims[2] = static_cast<cuuint64_t>(p->num_physical_pages) * p->page_size;
-    strides[1] = static_cast<cuuint64_t>(p->kv_heads) * hd * 2;
+    strides[1] = static_cast<cuuint64_t>(p->kv_heads) * row;
     box[2] = static_cast<cuuint32_t>(rows_per_box);
   }
-  return encode_map(map, 3, base, dims, strides, box);
+  return encode_map(map, 3, base, dims, strides, box,
+                    !codes     ? MapKind::kHalf
+                    : hd == 64 ? MapKind::kBytes64
+                               : MapKind::kBytes128);
 }
 
 }  // namespace
@@ -255,8 +260,8 @@ pa_status_t encode_cache_map(CUtensorMap *map, const void *base, const pa_proble
 namespace pa {
 
 pa_status_t encode_cache_map_rows(CUtensorMap *map, const void *base, const pa_problem_t *p,
-                                  int rows_per_box) {
-  return encode_cache_map(map, base, p, rows_per_box);
+                                  int rows_per_box, bool codes) {
+  return encode_cache_map(map, base, p, rows_per_box, codes);
 }
 
 pa_status_t encode_query_map(CUtensorMap *map, const void *query, int64_t total_tokens,

@@ -17,7 +17,7 @@ pa_status_t setup_prefill(const pa_problem_t *problem, const void *query,
                           const void *key_cache, const void *value_cache,
                           const int32_t *block_tables, const int32_t *context_lengths, float scale,
                           const void *out, const pa_options_t *options, PrefillLaunch *l,
-                          PrefillArgs *args) {
+                          PrefillArgs *args, bool codes) {
   l->grid = dim3(0, 0, 0);
   pa_status_t st = check_problem_public(problem);
   if (st != PA_OK) return st;
@@ -75,9 +75,9 @@ pa_status_t setup_prefill(const pa_problem_t *problem, const void *query,
   const int rows = a.ps < tn ? a.ps : tn;
   st = encode_query_map(&l->tq, query, total_tokens, a.qh, hd, g, qt);
   if (st != PA_OK) return st;
-  st = encode_cache_map_rows(&l->tk, key_cache, problem, rows);
+  st = encode_cache_map_rows(&l->tk, key_cache, problem, rows, codes);
   if (st != PA_OK) return st;
-  st = encode_cache_map_rows(&l->tv, value_cache, problem, rows);
+  st = encode_cache_map_rows(&l->tv, value_cache, problem, rows, codes);
   if (st != PA_OK) return st;
 
   if (hd != 256) a.n_qtiles = (a.n_qtiles + 1) / 2;  // pairs of query tiles

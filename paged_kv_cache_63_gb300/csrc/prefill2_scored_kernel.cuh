@@ -18,6 +18,7 @@
 // memory); 3 schedules and loads Q; 4..7 are tile A's softmax, 8..11 tile B's.
 #pragma once
 
+#include "code_tiles.cuh"
 #include "early_launch.cuh"
 #include "prefill2_kernel.cuh"
 #include "scored_softmax.cuh"
@@ -39,7 +40,10 @@ enum : int {
   kS2Clc = 21,        // the answer to a cancellation request landed
   kS2Full = 22,       // +slot
   kS2Empty = 30,      // +slot (2 arrivals: both MMA warps are done with it)
-  kNumBarsS2 = 38
+  kNumBarsS2 = 38,
+  kS2Codes = 38,      // +slot, of a quantised cache: a tile's codes and scales landed (33 arrivals:
+                      // the announced bytes, and each lane's copies of scales)
+  kNumBarsQ2 = 46
 };
 
 constexpr int kUnit = 64;  // keys of a unit
@@ -142,9 +146,23 @@ struct ScoredTile2 {
   }
 };
 
-template <int HD, int kParts>
-__global__ void __launch_bounds__(kPrefill2Threads, 1)
-    prefill2_scored_kernel(const __grid_constant__ PrefillScoredArgs a,
+// Over a quantised cache a fourth warpgroup converts the tiles: warps 12 and 13 those of K, 14 and 15
+// those of V, half a tile each (head_dim 64: 12 and 14 whole ones, code_tiles.cuh). (With K's by
+// warp 0 and V's by warp 3 beside their other work, and the softmax's registers as they are, a tile
+// took warp 0 9000 cycles, 4900 of them conversion and 3500 loading, and 512 new tokens of 16
+// contexts 768 us.)
+template <int HD>
+constexpr int kConverters2 = HD == 64 ? 1 : 2;  // warps to a tile
+constexpr int kQuantThreads2 = 512;
+constexpr uint32_t kQuantRoleRegs2 = 72, kQuantConvertRegs2 = 56, kQuantSoftmaxRegs2 = 192;
+static_assert(kQuantRoleRegs2 + kQuantConvertRegs2 + 2 * kQuantSoftmaxRegs2 <= 4 * 128,
+              "register split exceeds the launch allocation");
+
+// kQuant: the caches are quantised (code_tiles.cuh). A slot's barrier kS2Full then stands for the
+// converted tile.
+template <int HD, int kParts, bool kQuant = false>
+__global__ void __launch_bounds__(kQuant ? kQuantThreads2 : kPrefill2Threads, 1)
+    prefill2_scored_kernel(const __grid_constant__ ScoredArgsOf<kQuant> a,
                            const __grid_constant__ CUtensorMap tq,
                            const __grid_constant__ CUtensorMap tk,
                            const __grid_constant__ CUtensorMap tv) {
@@ -153,7 +171,9 @@ __global__ void __launch_bounds__(kPrefill2Threads, 1)
   constexpr bool kFirst = (kParts & kRuleFirst) != 0;
   constexpr uint32_t kIdescS = idesc_f16(C::kRows, 64, 0, 0);
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t bars[kNumBarsS2];
+  constexpr int kBars = kQuant ? kNumBarsQ2 : kNumBarsS2;
+  constexpr int kThreads = kQuant ? kQuantThreads2 : kPrefill2Threads;
+  __shared__ __align__(8) uint64_t bars[kBars];
   __shared__ __align__(16) uint4 clc_answer;
   __shared__ Item items[2];
   __shared__ uint32_t tmem_slot;
@@ -170,11 +190,16 @@ __global__ void __launch_bounds__(kPrefill2Threads, 1)
   auto bar = [&](int i) { return smem_addr(&bars[i]); };
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kNumBarsS2; ++i) {
+    for (int i = 0; i < kBars; ++i) {
       uint32_t count = 1;
       if (i >= kS2PFull && i < kS2PFull + 4) count = 128;
-      if (i == kS2ItemEmpty || i == kS2ItemEmpty + 1) count = kItemReaders;
+      if (i == kS2ItemEmpty || i == kS2ItemEmpty + 1)
+        count = kItemReaders + (kQuant ? 2 * kConverters2<HD> : 0);
       if (i == kS2QEmpty || i >= kS2Empty) count = 2;
+      if constexpr (kQuant) {
+        if (i >= kS2Full && i < kS2Empty) count = kConverters2<HD>;
+        if (i >= kS2Codes) count = 33;
+      }
       mbar_init(bar(i), count);
     }
     abort_word = 0;
@@ -183,7 +208,7 @@ __global__ void __launch_bounds__(kPrefill2Threads, 1)
   // MMA rows past q_rows (g not dividing 128) are never written by the Q loads: zero once
   if (q_rows < C::kRows) {
     const int per_block = (C::kRows - q_rows) * 8;
-    for (int i = threadIdx.x; i < 2 * C::KB * per_block; i += kPrefill2Threads) {
+    for (int i = threadIdx.x; i < 2 * C::KB * per_block; i += kThreads) {
       const int x = i / (C::KB * per_block), r = i % (C::KB * per_block);
       const int kb = r / per_block, c = r % per_block;
       *reinterpret_cast<uint4 *>(sgen + C::kQOff + x * C::kQBytes + kb * (C::kRows * 128) +
@@ -215,7 +240,11 @@ __global__ void __launch_bounds__(kPrefill2Threads, 1)
 
   // registers: the softmax warpgroups hold a 128-column score row per thread; each role
   // changes its own allocation inside its branch so the compiler sees one limit per region
-  if (warp < 4) regs_decrease<kPrefill2SmallRegs>();
+  if (warp < 4) regs_decrease<kQuant ? kQuantRoleRegs2 : kPrefill2SmallRegs>();
+  // of a quantised cache: the scales of each slot's tile
+  using Codes = CodeTile<HD, C::TN>;
+  __shared__ __align__(16) uint8_t scale_rows[kQuant ? C::kSlots : 1][C::TN];
+  auto scales_of = [&](int s) { return smem_addr(scale_rows[kQuant ? s : 0]); };
   if (warp == 3) {
     // ================= scheduler =================
     int kv = blockIdx.x, b = blockIdx.y, z = blockIdx.z;
@@ -287,7 +316,9 @@ __global__ void __launch_bounds__(kPrefill2Threads, 1)
     const uint64_t pol = l2_evict_last_policy();
     const int rows_per_box = min(a.ps, C::TN);
     const int boxes = C::TN / rows_per_box;
-    const uint32_t box_bytes = rows_per_box * 128;
+    const uint32_t box_bytes = rows_per_box * (kQuant ? Codes::kBlock : 128);
+    constexpr int kBlocks = kQuant ? Codes::kBlocks : C::KB;  // column blocks of a tile as loaded
+    constexpr int kFull = kQuant ? kS2Codes : kS2Full;
     int next = 0;  // next ring item
     bool ok = true;
     for (int k = 0; ok; ++k) {
@@ -302,7 +333,7 @@ __global__ void __launch_bounds__(kPrefill2Threads, 1)
         const int tok = tile_token(it, j) + lane * rows_per_box;
         return j < it.nt_max && lane < boxes && tok < it.kv_len && tok + rows_per_box > it.kv_lo;
       };
-      auto load_tile = [&](const CUtensorMap *map, int tok, int page) {
+      auto load_tile = [&](const CUtensorMap *map, bool is_v, int tok, int page) {
         const int s = next % C::kSlots;
         const uint32_t issue = __ballot_sync(0xffffffffu, page >= 0);
         const int slot_in_page = tok & (a.ps - 1);
@@ -312,14 +343,19 @@ __global__ void __launch_bounds__(kPrefill2Threads, 1)
         if (next >= C::kSlots)
           ok = pipe_wait(bar(kS2Empty + s), ((next / C::kSlots) - 1) & 1, abort_flag, a.err);
         if (!ok) return;
-        if (lane == 0) mbar_arrive_expect_tx(bar(kS2Full + s), __popc(issue) * box_bytes * C::KB);
+        if (lane == 0) mbar_arrive_expect_tx(bar(kFull + s), __popc(issue) * box_bytes * kBlocks);
         __syncwarp();
         if (page >= 0) {
 #pragma unroll
-          for (int kb = 0; kb < C::KB; ++kb)
-            tma_load_3d(slot_addr(s) + kb * (C::TN * 128) + lane * box_bytes, map,
-                        bar(kS2Full + s), kb * 64, y, z, pol);
+          for (int kb = 0; kb < kBlocks; ++kb)
+            tma_load_3d(slot_addr(s) + (kQuant ? Codes::kOff : 0) + kb * (C::TN * 128) +
+                            lane * box_bytes,
+                        map, bar(kFull + s), kb * 64, y, z, pol);
         }
+        if constexpr (kQuant)
+          load_scales<C::TN>(scales_of(s), is_v ? a.v_scale : a.k_scale,
+                             tok - lane * rows_per_box, page, rows_per_box, it.kv, a.kvh, a.ps,
+                             bar(kFull + s));
         ++next;
       };
       auto page_of = [&](int j) {
@@ -344,15 +380,15 @@ __global__ void __launch_bounds__(kPrefill2Threads, 1)
           atomicOr(a.err, PA_DEVERR_PAGE_ID);
           page = -1;
         }
-        load_tile(&tk, tok, page);
-        if (ok) load_tile(&tv, tok, page);
+        load_tile(&tk, false, tok, page);
+        if (ok) load_tile(&tv, true, tok, page);
       }
     }
     // drain: the newest item of every slot has landed (older items of a slot were consumed
     // before it was refilled)
     if (lane == 0) {
       for (int r = max(0, next - C::kSlots); r < next; ++r)
-        drain_wait(bar(kS2Full + r % C::kSlots), (r / C::kSlots) & 1, a.err);
+        drain_wait(bar(kFull + r % C::kSlots), (r / C::kSlots) & 1, a.err);
     }
     __syncwarp();
   } else if (warp < 3) {
@@ -484,8 +520,8 @@ __global__ void __launch_bounds__(kPrefill2Threads, 1)
     mma_commit_warp(bar(kS2Done + x));
     if (lane == 0) drain_wait(bar(kS2Done + x), 0, a.err);
     __syncwarp();
-  } else if (warp >= 4) {
-    regs_increase<kPrefill2BigRegs>();
+  } else if (warp < 12) {
+    regs_increase<kQuant ? kQuantSoftmaxRegs2 : kPrefill2BigRegs>();
     // ================= softmax: tile x = (warp - 4) / 4, one query row per thread =================
     const int x = (warp - 4) >> 2;
     const int rg = warp & 3;
@@ -540,6 +576,26 @@ __global__ void __launch_bounds__(kPrefill2Threads, 1)
         float o[32];
         tmem_ld32(to + c * 32, o);
         if (valid) store_half32(a.out16 + out_row + c * 32, o, inv, a.out_v8, pol);
+      }
+    }
+  } else if constexpr (kQuant) {
+    // ================= converters =================
+    regs_decrease<kQuantConvertRegs2>();
+    constexpr int kRows = C::TN / kConverters2<HD>;
+    const int is_v = warp >= 14, part = warp & 1;
+    int gt = 0;  // tiles so far
+    bool ok = part < kConverters2<HD>;
+    for (int k = 0; ok; ++k) {
+      Item it;
+      ok = take_item(k, it);
+      if (!ok || it.stop) break;
+      if (!it.live) continue;
+      for (int j = 0; j < it.nt_max; ++j, ++gt) {
+        const int r = 2 * gt + is_v, s = r % C::kSlots;
+        ok = pipe_wait(bar(kS2Codes + s), (r / C::kSlots) & 1, abort_flag, a.err);
+        if (!ok) break;
+        convert_rows<HD, C::TN, kRows>(slot_addr(s), scales_of(s), part * kRows);
+        if (lane == 0) mbar_arrive(bar(kS2Full + s));
       }
     }
   }

@@ -14,6 +14,7 @@
 //   its scores; Q at 128 (row = lane, two fp16 a column); O at 256.
 #pragma once
 
+#include "code_tiles.cuh"
 #include "early_launch.cuh"
 #include "scored_softmax.cuh"
 
@@ -22,7 +23,10 @@ namespace pa {
 // Barrier slots behind those of the plain kernel.
 enum : int {
   kS1QReady = kNumBars,  // the item's Q is in tensor memory, its shared copy free (4 arrivals)
-  kNumBarsS1 = kNumBars + 1
+  kNumBarsS1 = kNumBars + 1,
+  kS1KCodes = kNumBarsS1,     // +stage, of a quantised cache: a tile's codes and scales landed
+  kS1VCodes = kS1KCodes + 2,  // (33 arrivals, as in the two-tile kernel)
+  kNumBarsQ1 = kS1VCodes + 2
 };
 
 // Warps: 0 loads K, 2 Q and V; 1 owns TMEM and issues the MMAs; 3 schedules; 4..7 softmax.
@@ -30,6 +34,13 @@ constexpr int kScoredThreads = 256;
 constexpr int kScoredVWarp = 2;
 constexpr int kScoredSchedWarp = 3;
 constexpr uint32_t kQCol = 128;  // Q's first tensor-memory column
+
+// Over a quantised cache warps 8 and 9 convert the tiles of K, 10 and 11 those of V, half a tile
+// each. The launch holds 384 * 168 registers; the softmax warps take more than that share.
+constexpr int kQuantThreads = 384;
+constexpr uint32_t kQuantRoleRegs = 104, kQuantSoftmaxRegs = 232, kQuantConvertRegs = 104;
+static_assert(kQuantRoleRegs + kQuantSoftmaxRegs + kQuantConvertRegs <= 3 * 168,
+              "register split exceeds the launch allocation");
 
 // An item's keys go from kv_lo, the first token that some row sees, to kv_len, and its key tiles
 // are taken last to first (as in prefill2_scored_kernel.cuh): tile j is the one j before last_tile.
@@ -108,9 +119,11 @@ struct ScoredTile1 {
   }
 };
 
-template <int HD, int kParts>
-__global__ void __launch_bounds__(kScoredThreads, 1)
-    prefill_scored_kernel(const __grid_constant__ PrefillScoredArgs a,
+// kQuant: the caches are quantised (code_tiles.cuh); a stage's full barrier then stands for the
+// converted tile.
+template <int HD, int kParts, bool kQuant = false>
+__global__ void __launch_bounds__(kQuant ? kQuantThreads : kScoredThreads, 1)
+    prefill_scored_kernel(const __grid_constant__ ScoredArgsOf<kQuant> a,
                           const __grid_constant__ CUtensorMap tq,
                           const __grid_constant__ CUtensorMap tk,
                           const __grid_constant__ CUtensorMap tv) {
@@ -118,7 +131,9 @@ __global__ void __launch_bounds__(kScoredThreads, 1)
   using Item = ScoredItem1;
   constexpr bool kFirst = (kParts & kRuleFirst) != 0;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t bars[kNumBarsS1];
+  constexpr int kBars = kQuant ? kNumBarsQ1 : kNumBarsS1;
+  constexpr int kThreads = kQuant ? kQuantThreads : kScoredThreads;
+  __shared__ __align__(8) uint64_t bars[kBars];
   __shared__ __align__(16) uint4 clc_answer;
   __shared__ Item items[2];
   __shared__ uint32_t tmem_slot;
@@ -136,11 +151,15 @@ __global__ void __launch_bounds__(kScoredThreads, 1)
   auto bar = [&](int i) { return smem_addr(&bars[i]); };
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kNumBarsS1; ++i) {
+    for (int i = 0; i < kBars; ++i) {
       uint32_t count = 1;
       if (i == kBarPFull || i == kBarPFull + 1) count = 128;
-      if (i == kBarItemEmpty || i == kBarItemEmpty + 1) count = kItemReaders1;
+      if (i == kBarItemEmpty || i == kBarItemEmpty + 1) count = kItemReaders1 + (kQuant ? 4 : 0);
       if (i == kS1QReady) count = 4;
+      if constexpr (kQuant) {
+        if (i == kBarKFull || i == kBarKFull + 1 || i == kBarVFull || i == kBarVFull + 1) count = 2;
+        if (i >= kS1KCodes) count = 33;
+      }
       mbar_init(bar(i), count);
     }
     abort_word = 0;
@@ -150,7 +169,7 @@ __global__ void __launch_bounds__(kScoredThreads, 1)
   // finite.
   if (q_rows < C::kRows) {
     const int per_block = (C::kRows - q_rows) * 8;  // 16-byte chunks
-    for (int i = threadIdx.x; i < C::KB * per_block; i += kScoredThreads) {
+    for (int i = threadIdx.x; i < C::KB * per_block; i += kThreads) {
       const int kb = i / per_block, c = i % per_block;
       *reinterpret_cast<uint4 *>(sgen + C::kQOff + kb * (C::kRows * 128) + q_rows * 128 + c * 16) =
           make_uint4(0, 0, 0, 0);
@@ -179,8 +198,15 @@ __global__ void __launch_bounds__(kScoredThreads, 1)
     return true;
   };
 
+  // of a quantised cache: the scales of the stages of K, then of V
+  __shared__ __align__(16) uint8_t scale_rows[kQuant ? 4 : 1][C::TN];
+  auto scales_of = [&](int stage) { return smem_addr(scale_rows[kQuant ? stage : 0]); };
+
   // K/V tiles, S and P buffers and their barrier phases are numbered across the work items
   // a CTA runs: tile t (global) uses stage / buffer t & 1 and phase (t >> 1) & 1.
+  if constexpr (kQuant) {
+    if (warp < 4) regs_decrease<kQuantRoleRegs>();
+  }
   if (warp == kScoredSchedWarp) {
     // ================= scheduler: one request per item (as in prefill2_kernel) =================
     int kv = blockIdx.x, b = blockIdx.y, z = blockIdx.z;
@@ -229,12 +255,16 @@ __global__ void __launch_bounds__(kScoredThreads, 1)
     const CUtensorMap *map = is_v ? &tv : &tk;
     // every query tile of the (sequence, K/V head) reads these K/V tiles: keep them in L2
     const uint64_t pol = l2_evict_last_policy();
-    const int full = is_v ? kBarVFull : kBarKFull;
+    const int full = kQuant ? (is_v ? kS1VCodes : kS1KCodes) : is_v ? kBarVFull : kBarKFull;
     const int empty = is_v ? kBarVEmpty : kBarKEmpty;
     const uint32_t stage0 = is_v ? v_stage(0) : k_stage(0);
     const int rows_per_box = min(a.ps, C::TN);
     const int boxes = C::TN / rows_per_box;
     const uint32_t box_bytes = rows_per_box * 128;
+    using Codes = CodeTile<HD, C::TN>;
+    constexpr int kBlocks = kQuant ? Codes::kBlocks : C::KB;  // column blocks of a tile as loaded
+    constexpr int kColumns = kQuant ? Codes::kBlock : 64;     // of a block
+    constexpr uint32_t kLandAt = kQuant ? Codes::kOff : 0;    // in the stage
     int g = 0;  // global index of the next tile
     int q_loads = 0;
     bool ok = true;
@@ -299,14 +329,18 @@ __global__ void __launch_bounds__(kScoredThreads, 1)
         }
         if (g >= 2) ok = pipe_wait(bar(empty + st), ((g >> 1) - 1) & 1, abort_flag, a.err);
         if (!ok) break;
-        if (lane == 0) mbar_arrive_expect_tx(bar(full + st), __popc(issue) * box_bytes * C::KB);
+        if (lane == 0) mbar_arrive_expect_tx(bar(full + st), __popc(issue) * box_bytes * kBlocks);
         __syncwarp();
         if (page >= 0) {
 #pragma unroll
-          for (int kb = 0; kb < C::KB; ++kb)
-            tma_load_3d(stage0 + st * C::kKVBytes + kb * (C::TN * 128) + lane * box_bytes, map,
-                        bar(full + st), kb * 64, y, z, pol);
+          for (int kb = 0; kb < kBlocks; ++kb)
+            tma_load_3d(stage0 + st * C::kKVBytes + kLandAt + kb * (C::TN * 128) + lane * box_bytes,
+                        map, bar(full + st), kb * kColumns, y, z, pol);
         }
+        if constexpr (kQuant)
+          load_scales<C::TN>(scales_of((is_v ? 2 : 0) + st), is_v ? a.v_scale : a.k_scale,
+                             tile_token(it, j), page, rows_per_box, it.kv, a.kvh, a.ps,
+                             bar(full + st));
       }
     }
     // drain: the last load issued into each stage, and the last Q, have landed before the CTA
@@ -404,7 +438,8 @@ __global__ void __launch_bounds__(kScoredThreads, 1)
     mma_commit_warp(bar(kBarDone));
     if (lane == 0) drain_wait(bar(kBarDone), 0, a.err);
     __syncwarp();
-  } else {
+  } else if (warp < 8) {
+    if constexpr (kQuant) regs_increase<kQuantSoftmaxRegs>();
     // ================= softmax: one query row per thread =================
     const int rg = warp & 3;
     const int row = rg * 32 + lane;
@@ -476,6 +511,27 @@ __global__ void __launch_bounds__(kScoredThreads, 1)
         float v[32];
         tmem_ld32(trow + C::kOCol + c * 32, v);
         if (valid) store_half32(a.out16 + out_row + c * 32, v, inv, a.out_v8, pol);
+      }
+    }
+  } else if constexpr (kQuant) {
+    // ================= converters =================
+    regs_decrease<kQuantConvertRegs>();
+    const bool is_v = warp >= 10;
+    const int half = C::TN / 2;
+    int g = 0;  // global index of the next tile
+    bool ok = true;
+    for (int k = 0; ok; ++k) {
+      Item it;
+      ok = take_item(k, it);
+      if (!ok || it.stop) break;
+      if (!it.live) continue;
+      for (int j = 0; j < it.ntiles; ++j, ++g) {
+        const int st = g & 1;
+        ok = pipe_wait(bar((is_v ? kS1VCodes : kS1KCodes) + st), (g >> 1) & 1, abort_flag, a.err);
+        if (!ok) break;
+        convert_rows<HD, C::TN, half>(is_v ? v_stage(st) : k_stage(st),
+                                      scales_of((is_v ? 2 : 0) + st), (warp & 1) * half);
+        if (lane == 0) mbar_arrive(bar((is_v ? kBarVFull : kBarKFull) + st));
       }
     }
   }

@@ -38,6 +38,13 @@ struct PrefillScoredArgs : PrefillArgs {
   uint16_t *out16;  // [total][qh][hd], fp16 bits
 };
 
+struct PrefillQuantArgs : PrefillScoredArgs {
+  const uint8_t *k_scale, *v_scale;
+};
+
+template <bool kQuant>
+using ScoredArgsOf = std::conditional_t<kQuant, PrefillQuantArgs, PrefillScoredArgs>;
+
 // Parts of a rule that a kernel is compiled for; kRuleWide (only with kRuleCap): a cap above 256.
 enum : int { kRuleCap = 1, kRuleSlopes = 2, kRuleFirst = 4, kRuleParts = 8, kRuleWide = 8 };
 
