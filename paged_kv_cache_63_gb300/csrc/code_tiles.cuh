@@ -1,12 +1,13 @@
 // code_tiles.cuh -- tiles of a quantised cache on their way to the tensor cores of the multi-token
 // kernels: the loads of codes and scales, and the conversion to fp16 operands.
 //
-// A K or V tile lands as codes in the upper half of the slot that its fp16 form fills, so the ring is
-// no larger than one of fp16 tiles. A converting warp rewrites it in place: for head_dim 128 and 256
-// a row's codes lie where the same row's upper columns go, and all lanes of a warp have read a row
-// before one writes it; for head_dim 64 (where codes are packed more densely than rows of fp16) a
-// row's fp16 never reaches codes of later rows, so one warp converts in ascending order. Each element
-// is one exact conversion and one exact product with the row's power of two.
+// A K or V tile lands as codes in the slot that its fp16 form fills, so the ring is no larger than one
+// of fp16 tiles, and converting warps rewrite it in place. A block of 128 columns lies where its upper
+// 64 go in fp16: a row's codes are then overwritten by that row alone, which all lanes of a warp have
+// read before one writes it, and blocks and rows are independent. At head_dim 64, where rows of codes
+// are packed more densely than rows of fp16, the codes fill the slot's upper half; a row's fp16 never
+// reaches codes of later rows, so one warp converts in ascending order. Each element is one exact
+// conversion and one exact product with the row's power of two.
 #pragma once
 
 #include "prefill_kernel.cuh"
@@ -19,7 +20,8 @@ template <int HD, int TN>
 struct CodeTile {
   static constexpr int kBlock = HD < 128 ? HD : 128;
   static constexpr int kBlocks = HD / kBlock;
-  static constexpr int kOff = TN * HD;
+  static constexpr int kOff = HD < 128 ? TN * HD : TN * 128;  // of the first block
+  static constexpr int kStep = 2 * TN * 128;                  // from block to block
 };
 
 // The scales of a tile's TN tokens from token `tok` on, eight to a lane, into shared memory at `dst`.
@@ -41,59 +43,69 @@ __device__ __forceinline__ void load_scales(uint32_t dst, const uint8_t *scales,
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 
-// Rewrites rows [row0, row0 + kRows) of a tile from codes to fp16, K-major in column blocks of 64,
-// 128-byte swizzled. A lane takes 16 codes at a time; the lanes of a quarter warp take even chunks of
-// one row and odd places of the next, so that no load or store meets a bank twice. Warp-collective.
+// Rewrites rows [row0, row0 + kRows) of a column block from codes to fp16, K-major in blocks of 64,
+// 128-byte swizzled; `at` is the slot, plus the block's number times CodeTile::kStep. A lane takes 16
+// codes at a time; the lanes of a quarter warp take even chunks of one row and odd places of the
+// next, so that no load or store meets a bank twice. The integer pipe, half rate, takes most of it (a
+// conversion 2.2 cycles of a scheduler, one of a word's upper half 3.8), and the loop is kept short
+// for the instruction cache, which it shares with the softmax: 512 new tokens of 16 contexts at
+// head_dim 128 took 428 us with the waits of all roles written out at each place, 355 with short
+// ones (prefill_kernel.cuh, pipe_wait). Warp-collective.
 template <int HD, int TN, int kRows>
-__device__ __forceinline__ void convert_rows(uint32_t slot, uint32_t scales, int row0) {
+__device__ __forceinline__ void convert_rows(uint32_t at, uint32_t scales, int row0) {
   using C = CodeTile<HD, TN>;
-  constexpr int kAtOnce = HD == 64 ? 8 : 4;  // rows of an iteration
-  constexpr int U = 4;                       // iterations whose loads are issued together
-  static_assert(kRows % (kAtOnce * U) == 0, "rows of a converter");
+  constexpr int kAtOnce = HD == 64 ? 8 : 4;  // rows that a warp's lanes cover
+  constexpr int kSteps = kRows / (2 * kAtOnce);
   const int lane = threadIdx.x & 31;
   const int i = lane & 7, q = lane >> 3;
-  int r, c;  // row within the iteration, chunk of 16 codes within the column block
+  int r, c;  // row within the first kAtOnce, chunk of 16 codes within the column block
+  uint32_t from;
   if constexpr (HD == 64) {
     r = 2 * q + (i >> 2);
     c = i & 3;
+    from = at + C::kOff + (row0 + r) * 64 + ((c ^ ((r >> 1) & 3)) << 4);
   } else {
     r = 2 * (q >> 1) + (i >> 2);
     c = (i & 3) + 4 * ((i >> 2) ^ (q & 1));
+    from = at + C::kOff + (row0 + r) * 128 + ((c ^ r) << 4);
   }
-#pragma unroll 1
-  for (int base = row0; base < row0 + kRows; base += kAtOnce * U) {
+  // two chunks of fp16, side by side before the swizzle; the second four rows of eight have the
+  // swizzle's bit 2 the other way
+  constexpr uint32_t kFlip = HD == 64 ? 0 : 64;
+  uint32_t to = at + (c >> 2) * (TN * 128) + (row0 + r) * 128 + (((2 * (c & 3)) ^ (r & 7)) << 4);
+  uint32_t scale = scales + row0 + r;
+  uint4 w0, w1;
+  uint32_t e0, e1;
+  auto load = [&]() {
+    w0 = lds128_at<0>(from);
+    w1 = lds128_at<kAtOnce * C::kBlock>(from ^ kFlip);
+    e0 = lds8_at<0>(scale);
+    e1 = lds8_at<kAtOnce>(scale);
+  };
+  auto store = [&](auto off, const uint4 &w, uint32_t e, uint32_t flip) {
+    const uint32_t f = half2_of_scale(e);
+    const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+    uint32_t o[8];
 #pragma unroll
-    for (int blk = 0; blk < C::kBlocks; ++blk) {
-      uint4 w[U];
-      uint32_t f[U];
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int row = base + u * kAtOnce + r;
-        const uint32_t at = HD == 64 ? row * 64 + ((c ^ ((row >> 1) & 3)) << 4)
-                                     : blk * (TN * 128) + row * 128 + ((c ^ (row & 7)) << 4);
-        w[u] = lds128(slot + C::kOff + at);
-        uint16_t e;
-        asm volatile("ld.shared.u8 %0, [%1];" : "=h"(e) : "r"(scales + row));
-        f[u] = half2_of_scales(e, e);
-      }
-      __syncwarp();
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int row = base + u * kAtOnce + r;
-        const uint32_t v[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
-        uint32_t o[8];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          o[2 * k] = mul_half2(half2_of_low(v[k]), f[u]);
-          o[2 * k + 1] = mul_half2(half2_of_high(v[k]), f[u]);
-        }
-        const uint32_t to = slot + (2 * blk + (c >> 2)) * (TN * 128) + row * 128;
-        const int ch = 2 * (c & 3);
-        sts128(to + ((ch ^ (row & 7)) << 4), make_uint4(o[0], o[1], o[2], o[3]));
-        sts128(to + (((ch + 1) ^ (row & 7)) << 4), make_uint4(o[4], o[5], o[6], o[7]));
-      }
-      __syncwarp();
+    for (int n = 0; n < 4; ++n) {
+      o[2 * n] = mul_half2(half2_of_low(v[n]), f);
+      o[2 * n + 1] = mul_half2(half2_of_high(v[n]), f);
     }
+    sts128_at<decltype(off)::value>(to ^ flip, make_uint4(o[0], o[1], o[2], o[3]));
+    sts128_at<decltype(off)::value>(to ^ (flip + 16), make_uint4(o[4], o[5], o[6], o[7]));
+  };
+  load();
+#pragma unroll 1
+  for (int m = 0; m < kSteps; ++m) {
+    const uint4 v0 = w0, v1 = w1;
+    const uint32_t f0 = e0, f1 = e1;
+    from += 2 * kAtOnce * C::kBlock;
+    scale += 2 * kAtOnce;
+    if (m + 1 < kSteps) load();  // rows that nothing has overwritten yet
+    __syncwarp();
+    store(Const<0>{}, v0, f0, 0);
+    store(Const<kAtOnce * 128>{}, v1, f1, kFlip);
+    to += 2 * kAtOnce * 128;
   }
   // the tensor cores read the slot through the asynchronous proxy
   fence_proxy_async();

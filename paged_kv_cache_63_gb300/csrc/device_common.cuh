@@ -105,6 +105,64 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr) {
   return v;
 }
 
+// Forms with a constant offset, which the instruction takes: no address is computed for it.
+template <int kOff>
+__device__ __forceinline__ uint4 lds128_at(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4+%5];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr), "n"(kOff));
+  return v;
+}
+
+template <int kOff>
+__device__ __forceinline__ uint32_t lds8_at(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.u8 %0, [%1+%2];" : "=r"(v) : "r"(addr), "n"(kOff));
+  return v;
+}
+
+template <int kOff>
+__device__ __forceinline__ uint32_t lds16_at(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.u16 %0, [%1+%2];" : "=r"(v) : "r"(addr), "n"(kOff));
+  return v;
+}
+
+template <int kOff>
+__device__ __forceinline__ void sts128_at(uint32_t addr, uint4 v) {
+  asm volatile("st.shared.v4.b32 [%0+%5], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y),
+               "r"(v.z), "r"(v.w), "n"(kOff)
+               : "memory");
+}
+
+template <int kOff>
+__device__ __forceinline__ void ldsm_x4_at(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4+%5];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr), "n"(kOff));
+}
+
+template <int kOff>
+__device__ __forceinline__ void ldsm_x4_trans_at(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4+%5];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr), "n"(kOff));
+}
+
+// f(0), f(1), ... f(N - 1) with the index as a constant (decltype(i)::value).
+template <int kI>
+struct Const {
+  static constexpr int value = kI;
+};
+template <int N, int kI = 0, class F>
+__device__ __forceinline__ void unrolled(F f) {
+  if constexpr (kI < N) {
+    f(Const<kI>{});
+    unrolled<N, kI + 1>(f);
+  }
+}
+
 __device__ __forceinline__ uint2 lds64(uint32_t addr) {
   uint2 v;
   asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));

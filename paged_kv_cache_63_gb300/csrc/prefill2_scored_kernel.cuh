@@ -349,7 +349,7 @@ __global__ void __launch_bounds__(kQuant ? kQuantThreads2 : kPrefill2Threads, 1)
 #pragma unroll
           for (int kb = 0; kb < kBlocks; ++kb)
             tma_load_3d(slot_addr(s) + (kQuant ? Codes::kOff : 0) + kb * (C::TN * 128) +
-                            lane * box_bytes,
+                            lane * box_bytes,  // (codes: one block)
                         map, bar(kFull + s), kb * 64, y, z, pol);
         }
         if constexpr (kQuant)

@@ -159,33 +159,35 @@ __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
-// Warp-collective bounded wait that also gives up when another role has aborted.
+// mbarrier.try_wait that suspends the warp for up to 50 us (a hint) before it answers no.
+__device__ __forceinline__ bool mbar_try_wait_long(uint32_t bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 50000;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return done != 0;
+}
+
+// Warp-collective bounded wait that also gives up when another role has aborted. Written short: it
+// stands at some thirty places of a kernel, whose roles share one instruction cache.
 __device__ __forceinline__ bool pipe_wait(uint32_t bar, uint32_t parity, volatile int *abort_flag,
                                           unsigned *err) {
   bool ok = mbar_try_wait(bar, parity);
-  bool expired = false;
   if (!ok) {
     const uint64_t t0 = global_ns();
-    for (uint32_t i = 1;; ++i) {
-      if (mbar_try_wait(bar, parity)) {
-        ok = true;
-        break;
-      }
-      if ((i & 31u) == 0) {
-        if (*abort_flag) break;
-        if (global_ns() - t0 > kWaitLimitNs) {
-          expired = true;
-          break;
-        }
-      }
-    }
+    uint64_t t;
+    do {
+      ok = mbar_try_wait_long(bar, parity);
+      t = global_ns() - t0;
+    } while (!ok && !*abort_flag && t <= kWaitLimitNs);
+    if (!ok && t > kWaitLimitNs) atomicOr(err, PA_DEVERR_TIMEOUT);
   }
   ok = __all_sync(0xffffffffu, ok);
-  expired = __any_sync(0xffffffffu, expired);
-  if (!ok && (threadIdx.x & 31) == 0) {
-    if (expired) atomicOr(err, PA_DEVERR_TIMEOUT);
-    *abort_flag = 1;
-  }
+  if (!ok) *abort_flag = 1;
   return ok;
 }
 

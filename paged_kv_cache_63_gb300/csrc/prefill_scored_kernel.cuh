@@ -35,8 +35,8 @@ constexpr int kScoredVWarp = 2;
 constexpr int kScoredSchedWarp = 3;
 constexpr uint32_t kQCol = 128;  // Q's first tensor-memory column
 
-// Over a quantised cache warps 8 and 9 convert the tiles of K, 10 and 11 those of V, half a tile
-// each. The launch holds 384 * 168 registers; the softmax warps take more than that share.
+// Over a quantised cache warps 8 and 9 convert the tiles of K, 10 and 11 those of V, a block of 128
+// columns each. The launch holds 384 * 168 registers; the softmax warps take more than that share.
 constexpr int kQuantThreads = 384;
 constexpr uint32_t kQuantRoleRegs = 104, kQuantSoftmaxRegs = 232, kQuantConvertRegs = 104;
 static_assert(kQuantRoleRegs + kQuantSoftmaxRegs + kQuantConvertRegs <= 3 * 168,
@@ -265,6 +265,7 @@ __global__ void __launch_bounds__(kQuant ? kQuantThreads : kScoredThreads, 1)
     constexpr int kBlocks = kQuant ? Codes::kBlocks : C::KB;  // column blocks of a tile as loaded
     constexpr int kColumns = kQuant ? Codes::kBlock : 64;     // of a block
     constexpr uint32_t kLandAt = kQuant ? Codes::kOff : 0;    // in the stage
+    constexpr uint32_t kApart = kQuant ? Codes::kStep : C::TN * 128;
     int g = 0;  // global index of the next tile
     int q_loads = 0;
     bool ok = true;
@@ -334,8 +335,8 @@ __global__ void __launch_bounds__(kQuant ? kQuantThreads : kScoredThreads, 1)
         if (page >= 0) {
 #pragma unroll
           for (int kb = 0; kb < kBlocks; ++kb)
-            tma_load_3d(stage0 + st * C::kKVBytes + kLandAt + kb * (C::TN * 128) + lane * box_bytes,
-                        map, bar(full + st), kb * kColumns, y, z, pol);
+            tma_load_3d(stage0 + st * C::kKVBytes + kLandAt + kb * kApart + lane * box_bytes, map,
+                        bar(full + st), kb * kColumns, y, z, pol);
         }
         if constexpr (kQuant)
           load_scales<C::TN>(scales_of((is_v ? 2 : 0) + st), is_v ? a.v_scale : a.k_scale,
@@ -517,7 +518,6 @@ __global__ void __launch_bounds__(kQuant ? kQuantThreads : kScoredThreads, 1)
     // ================= converters =================
     regs_decrease<kQuantConvertRegs>();
     const bool is_v = warp >= 10;
-    const int half = C::TN / 2;
     int g = 0;  // global index of the next tile
     bool ok = true;
     for (int k = 0; ok; ++k) {
@@ -529,8 +529,9 @@ __global__ void __launch_bounds__(kQuant ? kQuantThreads : kScoredThreads, 1)
         const int st = g & 1;
         ok = pipe_wait(bar((is_v ? kS1VCodes : kS1KCodes) + st), (g >> 1) & 1, abort_flag, a.err);
         if (!ok) break;
-        convert_rows<HD, C::TN, half>(is_v ? v_stage(st) : k_stage(st),
-                                      scales_of((is_v ? 2 : 0) + st), (warp & 1) * half);
+        convert_rows<HD, C::TN, C::TN>(
+            (is_v ? v_stage(st) : k_stage(st)) + (warp & 1) * CodeTile<HD, C::TN>::kStep,
+            scales_of((is_v ? 2 : 0) + st), 0);
         if (lane == 0) mbar_arrive(bar((is_v ? kBarVFull : kBarKFull) + st));
       }
     }

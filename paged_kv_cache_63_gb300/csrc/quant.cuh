@@ -77,6 +77,12 @@ __device__ __forceinline__ uint32_t mul_half2(uint32_t a, uint32_t b) {
   return r;
 }
 
+// 2^e of a scale byte, as an fp16 pair; anything for a byte that is no scale.
+__device__ __forceinline__ uint32_t half2_of_scale(uint32_t b) {
+  const float x = __uint_as_float(b << 23);
+  return pack_half2(x, x);
+}
+
 // 2^e of two scale bytes, as an fp16 pair. Bytes that no row was written with (tokens that nobody
 // sees) give a finite factor too.
 __device__ __forceinline__ uint32_t half2_of_scales(uint32_t b0, uint32_t b1) {
