@@ -9,17 +9,22 @@
 //
 // The work is laid out as in decode_scored.cu (span_split.cuh): a warp is a worker with a ring of
 // K/V tiles loaded by TMA, the tiles of all units are cut into equal ranges, and the states of units
-// that workers share are joined by the same kernel. A tile is twice the tokens in the same bytes.
-//  * Codes stay bytes until they are operands: ldmatrix brings four codes of a token to a lane, and
-//    the products run over the head's elements in the order in which they come. A word of four keys
-//    converts to the two words that m16n8k16 takes for B (the query's fragments are loaded in the
-//    same order); a word of two tokens by two elements of V (ldmatrix.trans on pairs of codes)
-//    becomes a word for the even and one for the odd elements. The conversion is exact, one
-//    instruction a pair.
-//  * A key's scale multiplies its score in fp32; a value's scale, a power of two, its fp16 elements
-//    (exact, quant.cuh). Scales come by 8-byte asynchronous copies that arrive on the tile's
-//    barrier: a page may hold fewer of them than the 16 bytes of a TMA copy.
-//  * Probabilities keep 22 bits and sums are fp32, as in decode_scored.cu.
+// that workers share are joined by the same kernel. A tile is twice the tokens in the same bytes, and
+// the instructions a tile takes decide how near the kernel comes to the memory:
+//  * Scores are products of 16 tokens by 8 heads, outputs of 16 elements by 8 heads (m16n8k16), so
+//    that all rows of an instruction carry work. Codes are converted to fp16, exactly, as they become
+//    operands: a word of four keys' elements is two words of the first product (the queries are held
+//    in the same order). Values' bytes are transposed by ldmatrix, so that a lane holds four tokens of
+//    one element, and the tokens are dealt to the rows of both products so that these are the ones
+//    whose weights the lane has. (Products of the codes themselves, the query split into three e4m3
+//    numbers, took 168 us for 64 sequences of 1500 seen tokens with 32 heads of their own: the
+//    compiler converts both operands for each product.)
+//  * A key's scale multiplies its score in fp32; a value's scale multiplies its probability, relative
+//    to the tile's largest, whose own power of two multiplies the tile's output. Scales come by
+//    8-byte asynchronous copies that arrive on the tile's barrier: a page may hold fewer of them than
+//    the 16 bytes of a TMA copy.
+//  * Probabilities keep 22 bits (two fp16 numbers, a product each) and sums are fp32, as in
+//    decode_scored.cu.
 #include <algorithm>
 #include <atomic>
 #include <cmath>
@@ -35,12 +40,19 @@ struct QuantDecodeArgs : ScoredArgs {
   const uint8_t *k_scale, *v_scale;
 };
 
+// Warps of a CTA, one CTA to a multiprocessor: the tiles in flight, two to a warp, are those of
+// decode_scored.cu's eight warps, but a warp's chain of loads, products and shuffles is long for the
+// half tile of bytes it brings (eight warps: 162 us against 134 for 64 sequences of 1500 seen tokens,
+// 32 heads of 128 of their own; sixteen with tiles of 16 tokens, which the registers allow: 178).
+constexpr int kQuantWarps = 12;
+
 template <int HD, int T>
 struct CodeGeom {
   static constexpr int kBlock = HD < 128 ? HD : 128;  // bytes of a column block's row
   static constexpr int kHalfBytes = T * HD;           // the K (or V) part of a stage
   static constexpr int kStageBytes = 2 * kHalfBytes;
   static constexpr int kScaleBytes = 2 * T;           // a stage's scales: K's, then V's
+  static constexpr int kShift = T == 16 ? 4 : T == 32 ? 5 : 6;
   // byte offset of 16-byte chunk `chunk` of tile row `row` (row_maps.h, encode_code_map)
   static __device__ __forceinline__ uint32_t at(int row, int chunk) {
     if constexpr (HD < 128)
@@ -61,14 +73,35 @@ __device__ __forceinline__ void arrive_after_copies(uint32_t bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 
-__device__ __forceinline__ uint32_t lds16(uint32_t addr) {
-  uint16_t v;
-  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr));
-  return v;
+// D(16x8, fp32) = A(16x16, fp16) B(16x8, fp16) + D; fresh: + 0.
+__device__ __forceinline__ void mma_halves(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                           uint32_t b1, bool fresh) {
+  if (fresh)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%10, %10, %10, %10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Issue the loads of the tile at cursor c into a stage (warp-uniform), as issue_span_tile does. The
-// barrier takes 33 arrivals: the announcement of the bytes, and each lane's copies of scales.
+// Two 16x16 matrices of bytes, transposed: of each, r[2 m] has column lane / 4 and r[2 m + 1] column
+// 8 + lane / 4 in rows 4 (lane % 4) .. + 3, lowest byte first. Lanes 0..15 give the rows' addresses
+// of the first matrix, 16..31 of the second.
+template <int kOff>
+__device__ __forceinline__ void ldsm_bytes_trans(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0, %1, %2, %3}, [%4+%5];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr), "n"(kOff));
+}
+
+// Issue the loads of the tile at cursor c into a stage. Pieces (min(page size, T) rows) that hold no
+// seen token are not loaded; lane p looks at piece p. The barrier takes 33 arrivals: the announcement
+// of the bytes, and each lane's copies of scales. Warp-collective. (Written as loops: what all warps
+// run has to fit the instruction cache.)
 template <int HD, int T>
 __device__ __forceinline__ void issue_code_tile(const QuantDecodeArgs &qa, const CUtensorMap *tk,
                                                 const CUtensorMap *tv, const SpanCursor &c, int kv,
@@ -76,98 +109,84 @@ __device__ __forceinline__ void issue_code_tile(const QuantDecodeArgs &qa, const
                                                 uint32_t bar, uint64_t pol, uint32_t extra_tx) {
   using G = CodeGeom<HD, T>;
   const KernelArgs &a = qa.k;
-  constexpr int kMaxPieces = T / 8;
   const int lane = threadIdx.x & 31;
-  const int R = a.ps < T ? a.ps : T;
+  const int shift = min(a.ps_shift, G::kShift);  // of a piece's rows
   const int npages = (c.sp.end + a.ps - 1) >> a.ps_shift;
   const bool hm = a.layout == PA_LAYOUT_HEAD_MAJOR;
-  int page_of_lane = -1;  // the page of the eight scales that this lane copies
-  auto place = [&](int tok, int &page, int &row, int &head) {  // false: id outside the pool
-    page = bt_page(a, w, c.b, tok >> a.ps_shift, npages);
-    const int slot = tok & (a.ps - 1);
-    row = hm ? slot : (page << a.ps_shift) + slot;
-    head = hm ? page * a.kvh + kv : kv;
-    if (page >= 0 && page < a.num_pages) return true;
-    if (lane == 0) atomicOr(a.err, PA_DEVERR_PAGE_ID);
-    return false;
-  };
-  if (R == T) {
-    int page, row, head;
-    const bool good = place(c.tok, page, row, head);
-    expect_bytes_warp(bar, (good ? G::kStageBytes : 0u) + extra_tx);
-    if (good) {
-      page_of_lane = page;
-      tma_rows_warp(stage, tk, bar, row, head, 0, pol);
-      tma_rows_warp(stage + G::kHalfBytes, tv, bar, row, head, 0, pol);
-    }
-  } else {
-    int row[kMaxPieces], head[kMaxPieces];  // row < 0 marks a piece not loaded
-    uint32_t bytes = 0;
-#pragma unroll
-    for (int p = 0; p < kMaxPieces; ++p) {
-      const int tok = c.tok + p * R;
-      int page;
-      head[p] = 0;
-      if (p * R < T && tok < c.sp.end && tok + R > c.sp.lo && place(tok, page, row[p], head[p])) {
-        bytes += static_cast<uint32_t>(R * HD * 2);
-        if ((lane & 15) * 8 >> a.ps_shift == p) page_of_lane = page;
-      } else {
-        row[p] = -1;
-      }
-    }
-    expect_bytes_warp(bar, bytes + extra_tx);
-#pragma unroll
-    for (int p = 0; p < kMaxPieces; ++p) {
-      if (row[p] < 0) continue;
-#pragma unroll
-      for (int blk = 0; blk < HD / G::kBlock; ++blk) {
-        const uint32_t dst = stage + blk * (T * G::kBlock) + p * R * G::kBlock;
-        tma_rows_warp(dst, tk, bar, row[p], head[p], blk, pol);
-        tma_rows_warp(dst + G::kHalfBytes, tv, bar, row[p], head[p], blk, pol);
+  const int lp0 = c.tok >> a.ps_shift;
+  bt_page(a, w, c.b, lp0, npages);  // the window is over the tile's first page from here on
+  const int tok = c.tok + (lane << shift);
+  const int at = min((tok >> a.ps_shift) - w.base, 63);
+  const int p0 = __shfl_sync(0xffffffffu, w.cur, at & 31);
+  const int p1 = __shfl_sync(0xffffffffu, w.nxt, at & 31);
+  int page = at < 32 ? p0 : p1;
+  const bool needed = lane < T >> shift && tok < c.sp.end && tok + (1 << shift) > c.sp.lo;
+  const bool good = needed && page >= 0 && page < a.num_pages;
+  if (needed && !good) atomicOr(a.err, PA_DEVERR_PAGE_ID);
+  page = good ? page : -1;
+  unsigned pieces = __ballot_sync(0xffffffffu, good);
+  expect_bytes_warp(bar, (__popc(pieces) << shift) * (HD * 2) + extra_tx);
+#pragma unroll 1
+  for (; pieces; pieces &= pieces - 1) {
+    const int p = __ffs(pieces) - 1;
+    const int pg = __shfl_sync(0xffffffffu, page, p);
+    const int slot = (c.tok + (p << shift)) & (a.ps - 1);
+    const int row = hm ? slot : (pg << a.ps_shift) + slot;
+    const int head = hm ? pg * a.kvh + kv : kv;
+    const uint32_t dst = stage + (p << shift) * G::kBlock;
+    tma_rows_warp(dst, tk, bar, row, head, 0, pol);
+    tma_rows_warp(dst + G::kHalfBytes, tv, bar, row, head, 0, pol);
+    if constexpr (HD > 128) {
+      if (shift < G::kShift) {  // a whole tile's box has both column blocks
+        tma_rows_warp(dst + T * G::kBlock, tk, bar, row, head, 1, pol);
+        tma_rows_warp(dst + T * G::kBlock + G::kHalfBytes, tv, bar, row, head, 1, pol);
       }
     }
   }
   const int i = (lane & 15) * 8;  // token of the tile
+  const int pg = __shfl_sync(0xffffffffu, page, (i >> shift) & 31);
   if (i < T) {
     const bool is_v = lane >= 16;
-    const int page = max(page_of_lane, 0);
     const uint8_t *src = (is_v ? qa.v_scale : qa.k_scale) +
-                         scale_place(page, kv, (c.tok + i) & (a.ps - 1), a.kvh, a.ps);
-    copy8_async(scales + (is_v ? T : 0) + i, src, page_of_lane >= 0 ? 8u : 0u);
+                         scale_place(max(pg, 0), kv, (c.tok + i) & (a.ps - 1), a.kvh, a.ps);
+    copy8_async(scales + (is_v ? T : 0) + i, src, pg >= 0 ? 8u : 0u);
   }
   arrive_after_copies(bar);
 }
 
-// Running state of a unit (as SpanState of decode_scored.cu). A lane's row (head) is lane / 4; it
-// holds elements 16 k + 4 (lane % 4) .. + 3 of the query and of the output.
+// Running state of a unit (as SpanState of decode_scored.cu). Lane l has heads 2 (l % 4) and the next
+// in its scores and outputs, and of the queries elements 4 (l % 4) .. + 3 of each 16 of head l / 4.
 template <int HD>
 struct CodeState {
-  float m, lsum;
-  float slope2;
-  float o[HD / 16][4];
-  uint32_t qa[HD / 16][2];
+  float m[2], lsum[2];
+  float slope2[2];
+  float o[HD / 16][4];  // elements 16 k + l / 4 (two heads), + 8 (two heads)
+  uint32_t q[HD / 16][2];
 };
 
 template <int HD>
 __device__ __forceinline__ void code_begin(CodeState<HD> &st, const ScoredArgs &a, int b, int h0,
                                            int nh) {
   const int lane = threadIdx.x & 31;
-  const int h = lane >> 2;
+  const int h = lane >> 2, pair = 2 * (lane & 3);
   const uint2 *src = reinterpret_cast<const uint2 *>(
       a.k.q + (static_cast<long long>(b) * a.k.qh + h0 + h) * HD);
 #pragma unroll
-  for (int ks = 0; ks < HD / 16; ++ks) {
-    const uint2 q = h < nh ? __ldg(src + ks * 4 + (lane & 3)) : make_uint2(0u, 0u);
-    st.qa[ks][0] = q.x;
-    st.qa[ks][1] = q.y;
+  for (int k = 0; k < HD / 16; ++k) {
+    const uint2 q = h < nh ? __ldg(src + k * 4 + (lane & 3)) : make_uint2(0u, 0u);
+    st.q[k][0] = q.x;
+    st.q[k][1] = q.y;
   }
-  st.slope2 = a.s.slopes && h < nh ? __ldg(a.s.slopes + h0 + h) * kLog2e : 0.f;
-  st.m = -INFINITY;
-  st.lsum = 0.f;
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    st.slope2[j] = a.s.slopes && pair + j < nh ? __ldg(a.s.slopes + h0 + pair + j) * kLog2e : 0.f;
+    st.m[j] = -INFINITY;
+    st.lsum[j] = 0.f;
+  }
 #pragma unroll
   for (int k = 0; k < HD / 16; ++k)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) st.o[k][j] = 0.f;
+    for (int i = 0; i < 4; ++i) st.o[k][i] = 0.f;
 }
 
 // Zero V rows [from, to) of a stage: a zero probability must not meet a NaN code.
@@ -179,130 +198,204 @@ __device__ __forceinline__ void zero_code_rows(uint32_t stv, int from, int to) {
     sts128(stv + CodeGeom<HD, T>::at(from + i / (HD / 16), i % (HD / 16)), make_uint4(0, 0, 0, 0));
 }
 
+// Addresses of a lane's rows in a stage. Tokens are dealt in groups of 16: rows 0..7 of the scores are
+// tokens 0..7, rows 8..15 tokens 12..15, 8..11, so that after the transposition lane l has weights of
+// tokens 2 c, 2 c + 1 and 8 + (2 c + 4) % 8, + 1 (c = l % 4), and these four are rows 4 c .. 4 c + 3 of
+// the values' matrix. (With the second eight in order, eight rows of a load would meet four banks.)
 template <int HD, int T>
-__device__ __forceinline__ void code_tile(CodeState<HD> &st, uint32_t stage, uint32_t scales,
-                                          const SpanCursor &c, const ScoredArgs &a) {
-  using G = CodeGeom<HD, T>;
-  constexpr int NT = T / 8;
-  const int lane = threadIdx.x & 31;
-  const int mi = lane >> 3, rr = lane & 7, col = 2 * (lane & 3);
-  const int tok0 = c.tok;
-
-  // S[h][t], eight tokens at a time, 64 elements a load; two chains
-  float x[NT][2];
+struct CodeLane {
+  uint32_t k[HD < 128 ? 2 : 4];  // 32-element quarter of a column block
+  uint32_t v[HD < 128 ? 2 : 4];
+  __device__ __forceinline__ void init() {
+    using G = CodeGeom<HD, T>;
+    const int lane = threadIdx.x & 31;
+    const int mi = lane >> 3, rr = lane & 7;
+    const int i = lane & 15, c = 2 * (i >> 2) + (i & 1);
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    float s[2][2] = {};
-#pragma unroll
-    for (int cq = 0; cq < HD / 64; ++cq) {
-      uint32_t w[4];
-      ldsm_x4(stage + G::at(rr, (cq & 1) * 4 + mi) + (cq >> 1) * (T * 128) + nt * 8 * G::kBlock,
-              w[0], w[1], w[2], w[3]);
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        mma_rows8(s[i & 1][0], s[i & 1][1], st.qa[cq * 4 + i][0], st.qa[cq * 4 + i][1],
-                  half2_of_low(w[i]), half2_of_high(w[i]));
+    for (int d = 0; d < (HD < 128 ? 2 : 4); ++d) {
+      // matrices: rows 0..7 and 8..15 of the first 16 elements, then of the second
+      k[d] = G::at(mi & 1 ? 8 + ((rr + 4) & 7) : rr, 2 * d + (mi >> 1));
+      v[d] = G::kHalfBytes + G::at(i & 2 ? 8 + ((c + 4) & 7) : c, 2 * d + (lane >> 4));
     }
-    // a scale that no written row has belongs to a token that is masked below
-    const uint32_t f = lds16(scales + nt * 8 + col);
-    x[nt][0] = (s[0][0] + s[1][0]) * __uint_as_float(f << 23 & 0x7f800000u);
-    x[nt][1] = (s[0][1] + s[1][1]) * __uint_as_float(f << 15 & 0x7f800000u);
   }
+};
 
-  // the score rule, in base-2 units; the row's scores live in lanes lane & ~3 .. lane | 3
-  const bool partial = tok0 < c.sp.lo || c.sp.end - tok0 < T;
-  const float away0 = static_cast<float>(tok0 + col - (c.sp.end - 1));
-  float mt = -INFINITY;
+// An 8x8 matrix of 16-bit elements, transposed: a lane gives row l / 4, columns 2 (l % 4), + 1.
+__device__ __forceinline__ uint32_t transposed(uint32_t x) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+
+template <int HD, int T>
+__device__ __forceinline__ void code_tile(CodeState<HD> &st, const CodeLane<HD, T> &ln,
+                                          uint32_t stage, uint32_t scales, const SpanCursor &c,
+                                          const ScoredArgs &a) {
+  using G = CodeGeom<HD, T>;
+  constexpr int NG = T / 16;  // groups of 16 tokens
+  constexpr int kQuarters = HD < 128 ? 2 : 4;
+  const int lane = threadIdx.x & 31;
+  // the lane's tokens of a group: 16 g + row[i]
+  const int row[2] = {lane >> 2, 8 + (((lane >> 2) + 4) & 7)};
+  const int tok0 = c.tok;
+  const uint32_t sa = scales + row[0], sb = scales + row[1];
+
+  // x[g][i][j]: token 16 g + row[i], head 2 (lane % 4) + j, in two chains (even and odd steps)
+  float x[NG][2][2];
+  unrolled<NG>([&](auto g) {
+    constexpr int gi = decltype(g)::value;
+    float d[2][4];
+    unrolled<HD / 32>([&](auto q) {
+      constexpr int ks = decltype(q)::value;
+      uint32_t w[4];
+      ldsm_x4_at<(ks / kQuarters) * (T * 128) + gi * 16 * G::kBlock>(stage + ln.k[ks % kQuarters],
+                                                                     w);
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
+      for (int n = 0; n < 2; ++n) {
+        const uint32_t k[4] = {half2_of_low(w[2 * n]), half2_of_low(w[2 * n + 1]),
+                               half2_of_high(w[2 * n]), half2_of_high(w[2 * n + 1])};
+        mma_halves(d[n], k, st.q[2 * ks + n][0], st.q[2 * ks + n][1], ks == 0);
+      }
+    });
+    // a scale that no written row has belongs to a token that is masked below
+    const float f[2] = {__uint_as_float(lds8_at<gi * 16>(sa) << 23),
+                        __uint_as_float(lds8_at<gi * 16>(sb) << 23)};
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) x[gi][i][j] = (d[0][2 * i + j] + d[1][2 * i + j]) * f[i];
+  });
+
+  // the score rule, in base-2 units
+  const bool partial = tok0 < c.sp.lo || c.sp.end - tok0 < T;
+  auto seen = [&](int g, int i) {
+    const int t = tok0 + g * 16 + row[i];
+    return t >= c.sp.lo && t < c.sp.end;
+  };
+  auto each = [&](auto f) {  // f(score, group, i, j)
+#pragma unroll
+    for (int g = 0; g < NG; ++g)
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) f(x[g][i][j], g, i, j);
+  };
+  if (a.s.cap_in != 0.f)
+    each([&](float &y, int, int, int) { y = a.s.cap_out * tanhf(y * a.s.cap_in); });
+  else
+    each([&](float &y, int, int, int) { y *= a.k.scale_log2; });
+  if (a.s.slopes)
+    each([&](float &y, int g, int i, int j) {
+      y = fmaf(st.slope2[j], static_cast<float>(tok0 + g * 16 + row[i] - (c.sp.end - 1)), y);
+    });
+  if (partial) each([&](float &y, int g, int i, int) { y = seen(g, i) ? y : -INFINITY; });
+  float top[2] = {-INFINITY, -INFINITY};
+  each([&](float &y, int, int, int j) { top[j] = fmaxf(top[j], y); });
+#pragma unroll
+  for (int o = 4; o < 32; o <<= 1)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) top[j] = fmaxf(top[j], __shfl_xor_sync(0xffffffffu, top[j], o));
+  if (__any_sync(0xffffffffu, top[0] > st.m[0] + (kLift + kRescaleSlack) ||
+                                  top[1] > st.m[1] + (kLift + kRescaleSlack))) {
+    float alpha[2];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      float y = x[nt][j];
-      y = a.s.cap_in != 0.f ? a.s.cap_out * tanhf(y * a.s.cap_in) : y * a.k.scale_log2;
-      if (a.s.slopes) y = fmaf(st.slope2, away0 + static_cast<float>(nt * 8 + j), y);
-      if (partial) {
-        const int tok = tok0 + nt * 8 + col + j;
-        y = tok >= c.sp.lo && tok < c.sp.end ? y : -INFINITY;
-      }
-      x[nt][j] = y;
-      mt = fmaxf(mt, y);
+      const float mn = fmaxf(st.m[j], top[j] - kLift);
+      alpha[j] = mn == -INFINITY ? 1.f : fast_exp2(st.m[j] - mn);
+      st.m[j] = mn;
+      st.lsum[j] *= alpha[j];
     }
-  mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 1));
-  mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 2));
-  if (__any_sync(0xffffffffu, mt > st.m + (kLift + kRescaleSlack))) {
-    const float mn = fmaxf(st.m, mt - kLift);
-    const float alpha = mn == -INFINITY ? 1.f : fast_exp2(st.m - mn);
-    st.m = mn;
-    st.lsum *= alpha;
 #pragma unroll
     for (int k = 0; k < HD / 16; ++k)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) st.o[k][j] *= alpha;
+      for (int i = 0; i < 4; ++i) st.o[k][i] *= alpha[i & 1];
   }
-  const float m = st.m == -INFINITY ? 0.f : st.m;  // no score above -inf yet
-  float psum = 0.f;
-  uint32_t hi[NT], lo[NT];
+  float m[2];  // no score above -inf yet: 0
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    const float p0 = fast_exp2(x[nt][0] - m);
-    const float p1 = fast_exp2(x[nt][1] - m);
-    hi[nt] = pack_half2(p0, p1);
-    const float2 r = half2_bits_to_float2(hi[nt]);
-    lo[nt] = pack_half2(p0 - r.x, p1 - r.y);
-    psum += p0 + p1;
-  }
-  st.lsum += psum;
+  for (int j = 0; j < 2; ++j) m[j] = st.m[j] == -INFINITY ? 0.f : st.m[j];
 
-  uint32_t vf[NT];  // the values' scales
+  // the values' scales, and the tile's largest of a value that is seen
+  uint32_t vbyte[NG][2];
+  unrolled<NG>([&](auto g) {
+    constexpr int gi = decltype(g)::value;
+    vbyte[gi][0] = lds8_at<T + gi * 16>(sa);
+    vbyte[gi][1] = lds8_at<T + gi * 16>(sb);
+  });
+  if (partial) {
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    const uint32_t f = lds16(scales + T + nt * 8 + col);
-    vf[nt] = half2_of_scales(f & 0xffu, f >> 8);
+    for (int g = 0; g < NG; ++g)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) vbyte[g][i] = seen(g, i) ? vbyte[g][i] : 0u;
   }
+  uint32_t most = 0;
+#pragma unroll
+  for (int g = 0; g < NG; ++g) most = max(most, max(vbyte[g][0], vbyte[g][1]));
+  most = min(__reduce_max_sync(0xffffffffu, most), 254u);
+  const float out_scale = __uint_as_float(most << 23);
+  // 2^(b - most) as float bits: (b - most + 127) << 23. Bytes of written rows lie within 23 of each
+  // other; a byte of 0 (a token that is not seen) gives a finite number, which its probability of 0
+  // meets.
+  const uint32_t bias = (127u - most) << 23;
+
+  // Weights relative to the tile's scale: at most the probability, so they hold as fp16; the row sum
+  // takes the probability.
+  uint32_t hi[NG][2], lo[NG][2];
+#pragma unroll
+  for (int g = 0; g < NG; ++g)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float f = __uint_as_float((vbyte[g][i] << 23) + bias);
+      float p0 = fast_exp2(x[g][i][0] - m[0]);
+      float p1 = fast_exp2(x[g][i][1] - m[1]);
+      st.lsum[0] += p0;
+      st.lsum[1] += p1;
+      p0 *= f;
+      p1 *= f;
+      const uint32_t h = pack_half2(p0, p1);
+      const float2 r = half2_bits_to_float2(h);
+      hi[g][i] = transposed(h);
+      lo[g][i] = transposed(pack_half2(p0 - r.x, p1 - r.y));
+    }
+
   if (partial) {
     const uint32_t stv = stage + G::kHalfBytes;
     if (tok0 < c.sp.lo) zero_code_rows<HD, T>(stv, 0, c.sp.lo - tok0);
     if (c.sp.end - tok0 < T) zero_code_rows<HD, T>(stv, c.sp.end - tok0, T);
     __syncwarp();
   }
+  unrolled<HD / 32>([&](auto db) {
+    constexpr int D = decltype(db)::value;
+    float d[2][4];  // 16 elements each
+    unrolled<NG>([&](auto g) {
+      constexpr int gi = decltype(g)::value;
+      uint32_t w[4];
+      ldsm_bytes_trans<(D / kQuarters) * (T * 128) + gi * 16 * G::kBlock>(
+          stage + ln.v[D % kQuarters], w);
 #pragma unroll
-  for (int cp = 0; cp < HD / 32; ++cp) {  // 32 elements: two chunks of 16
-    float d[2][2][4] = {};                // [chunk][even, odd elements]
-#pragma unroll
-    for (int ch = 0; ch < NT / 2; ++ch) {
-      uint32_t w[4];  // chunk 0 tokens 0..7, 8..15, chunk 1 likewise
-      ldsm_x4_trans(stage + G::kHalfBytes + G::at((mi & 1) * 8 + rr, (2 * cp & 7) + (mi >> 1)) +
-                        (cp >> 2) * (T * 128) + ch * 16 * G::kBlock,
-                    w[0], w[1], w[2], w[3]);
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const uint32_t u = __byte_perm(w[2 * k], 0, 0x3120), z = __byte_perm(w[2 * k + 1], 0, 0x3120);
-        mma_rows16(d[k][0], hi[2 * ch], lo[2 * ch], hi[2 * ch + 1], lo[2 * ch + 1],
-                   mul_half2(half2_of_low(u), vf[2 * ch]), mul_half2(half2_of_low(z), vf[2 * ch + 1]));
-        mma_rows16(d[k][1], hi[2 * ch], lo[2 * ch], hi[2 * ch + 1], lo[2 * ch + 1],
-                   mul_half2(half2_of_high(u), vf[2 * ch]),
-                   mul_half2(half2_of_high(z), vf[2 * ch + 1]));
+      for (int n = 0; n < 2; ++n) {
+        const uint32_t v[4] = {half2_of_low(w[2 * n]), half2_of_low(w[2 * n + 1]),
+                               half2_of_high(w[2 * n]), half2_of_high(w[2 * n + 1])};
+        mma_halves(d[n], v, hi[gi][0], hi[gi][1], gi == 0);
+        mma_halves(d[n], v, lo[gi][0], lo[gi][1], false);
       }
-    }
+    });
 #pragma unroll
-    for (int k = 0; k < 2; ++k)
+    for (int n = 0; n < 2; ++n)
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        st.o[2 * cp + k][j] += d[k][j][0] + d[k][j][2];
-        st.o[2 * cp + k][2 + j] += d[k][j][1] + d[k][j][3];
-      }
-  }
+      for (int i = 0; i < 4; ++i)
+        st.o[2 * D + n][i] = fmaf(d[n][i], out_scale, st.o[2 * D + n][i]);
+  });
 }
 
 template <int HD, int T>
-__global__ void __launch_bounds__(kMaxWarpsPerCta * 32, 1)
+__global__ void __launch_bounds__(kQuantWarps * 32, 1)
     decode_quant_kernel(const __grid_constant__ QuantDecodeArgs sa,
                         const __grid_constant__ CUtensorMap tk,
                         const __grid_constant__ CUtensorMap tv) {
   using G = CodeGeom<HD, T>;
   const KernelArgs &a = sa.k;
   extern __shared__ uint8_t dsm[];
-  __shared__ __align__(8) uint64_t bars[kMaxWarpsPerCta * kMaxStages];
+  __shared__ __align__(8) uint64_t bars[kQuantWarps * kMaxStages];
   const int lane = threadIdx.x & 31;
   const int warp = threadIdx.x >> 5;
   const int worker = (blockIdx.x * (blockDim.x >> 5) + warp) / a.group;
@@ -399,9 +492,9 @@ __global__ void __launch_bounds__(kMaxWarpsPerCta * 32, 1)
     ++flying;
     advance(sa, ic, T);
   };
-  while (flying < S - 1 && ic.left > 0) issue();
-
   CodeState<HD> st = {};
+  CodeLane<HD, T> lane_addr;
+  lane_addr.init();
   UnitInfo cur;
   cur.b = -1;
   cur.us = -1;
@@ -411,53 +504,67 @@ __global__ void __launch_bounds__(kMaxWarpsPerCta * 32, 1)
   bool aborted = false;
 
   auto finish_unit = [&]() {
-    float l = st.lsum;
-    l += __shfl_xor_sync(0xffffffffu, l, 1);
-    l += __shfl_xor_sync(0xffffffffu, l, 2);
-    const int h = lane >> 2;
     bool whole = true;
     const long long unit = static_cast<long long>(cur.b) * a.ups + cur.us;
     if (a.mode == MODE_BALANCED)
       whole = worker_of(cur_ug0, total, nworkers) ==
               worker_of(cur_ug0 + cur_tiles - 1, total, nworkers);
-    if (h >= cur.nh) return;
-    if (whole) {
-      const float inv = l > 0.f ? 1.f / l : 0.f;
-      const long long at =
-          (static_cast<long long>(cur.b) * a.qh + cur.h0 + h) * HD + 4 * (lane & 3);
+    const int element = lane >> 2;
+    float sum[2] = {st.lsum[0], st.lsum[1]};
 #pragma unroll
-      for (int k = 0; k < HD / 16; ++k) {
-        store_out2(sa.s, sa.out, at + k * 16, st.o[k][0] * inv, st.o[k][1] * inv);
-        store_out2(sa.s, sa.out, at + k * 16 + 2, st.o[k][2] * inv, st.o[k][3] * inv);
-      }
-      return;
+    for (int o = 4; o < 32; o <<= 1) {
+      sum[0] += __shfl_xor_sync(0xffffffffu, sum[0], o);
+      sum[1] += __shfl_xor_sync(0xffffffffu, sum[1], o);
     }
-    // partial state relative to the row's reference, for the joining kernel
-    const long long slot = slot_of(unit, worker, a.group) * kMaxHeads + h;
-    if ((lane & 3) == 0)
-      *reinterpret_cast<float2 *>(a.ws_ml + slot * 2) = make_float2(st.m, l);
-    float *dst = a.ws_acc + slot * HD + 4 * (lane & 3);
 #pragma unroll
-    for (int k = 0; k < HD / 16; ++k)
-      *reinterpret_cast<float4 *>(dst + k * 16) =
-          make_float4(st.o[k][0], st.o[k][1], st.o[k][2], st.o[k][3]);
+    for (int j = 0; j < 2; ++j) {
+      const int h = 2 * (lane & 3) + j;
+      const float l = sum[j];
+      if (h >= cur.nh) break;
+      if (whole) {
+        const float inv = l > 0.f ? 1.f / l : 0.f;
+        const long long at = (static_cast<long long>(cur.b) * a.qh + cur.h0 + h) * HD + element;
+#pragma unroll
+        for (int k = 0; k < HD / 16; ++k) {
+          store_out1(sa.s, sa.out, at + k * 16, st.o[k][j] * inv);
+          store_out1(sa.s, sa.out, at + k * 16 + 8, st.o[k][2 + j] * inv);
+        }
+      } else {
+        // partial state relative to the head's reference, for the joining kernel
+        const long long slot = slot_of(unit, worker, a.group) * kMaxHeads + h;
+        if (element == 0)
+          *reinterpret_cast<float2 *>(a.ws_ml + slot * 2) = make_float2(st.m[j], l);
+        float *dst = a.ws_acc + slot * HD + element;
+#pragma unroll
+        for (int k = 0; k < HD / 16; ++k) {
+          dst[k * 16] = st.o[k][j];
+          dst[k * 16 + 8] = st.o[k][2 + j];
+        }
+      }
+    }
   };
 
-  // ---- main loop: refill the slot freed last iteration, wait for the next tile, compute
-  while (c.left > 0) {
-    if (c.b != cur.b || c.us * a.group + member != cur.us) {
-      if (cur.b >= 0) finish_unit();
+  // ---- main loop: fill the ring, wait for the next tile, compute
+  for (;;) {
+    const bool done = c.left <= 0;
+    // the joining kernel may come up now (it waits for this grid before it reads any state)
+    if (done) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const bool change = done || c.b != cur.b || c.us * a.group + member != cur.us;
+    if (change && cur.b >= 0) finish_unit();
+    if (done) break;
+#pragma unroll 1
+    while (flying < S && ic.left > 0) issue();
+    if (change) {
       cur = unit_info(a, c.b, c.us * a.group + member);
       cur_ug0 = c.ug0;
       cur_tiles = span_tiles(c.sp, T);
       code_begin<HD>(st, sa, cur.b, cur.h0, cur.nh);
     }
-    if (ic.left > 0) issue();
     if (!mbar_wait(bar0 + 8 * cs, cphase, a.err)) {
       aborted = true;
       break;
     }
-    code_tile<HD, T>(st, wbase + cs * G::kStageBytes, wscales + cs * G::kScaleBytes, c, sa);
+    code_tile<HD, T>(st, lane_addr, wbase + cs * G::kStageBytes, wscales + cs * G::kScaleBytes, c, sa);
     fence_proxy_async();
     __syncwarp();
     if (++cs == S) {
@@ -467,8 +574,6 @@ __global__ void __launch_bounds__(kMaxWarpsPerCta * 32, 1)
     --flying;
     advance(sa, c, T);
   }
-  // the joining kernel may come up now (it waits for this grid before it reads any state)
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (aborted) {
     // let the copies still in flight land before the shared memory is given up
     for (; flying > 0; --flying) {
@@ -478,14 +583,14 @@ __global__ void __launch_bounds__(kMaxWarpsPerCta * 32, 1)
         cphase ^= 1u;
       }
     }
-    return;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   }
-  finish_unit();
 }
 
 namespace {
 
-constexpr int kQuantStages = 3;
+
+constexpr int kQuantStages = 2;
 
 int quant_tile(int head_dim) { return head_dim == 64 ? 64 : head_dim == 128 ? 32 : 16; }
 
@@ -503,7 +608,7 @@ pa_status_t quant_plan(const pa_problem_t *p, const pa_options_t *o, int sm_coun
   const int g = p->query_heads / p->kv_heads;
   const int sub = (g + kMaxHeads - 1) / kMaxHeads;
   pl->tile_tokens = quant_tile(p->head_dim);
-  pl->warps_per_cta = o && o->warps_per_cta ? o->warps_per_cta : kMaxWarpsPerCta;
+  pl->warps_per_cta = o && o->warps_per_cta ? o->warps_per_cta : kQuantWarps;
   pl->stages = o && o->stages ? o->stages : kQuantStages;
   pl->smem_bytes = quant_smem(p->head_dim, pl->warps_per_cta, pl->stages);
   if (pl->smem_bytes > kMaxDecodeSmem) return PA_ERR_UNSUPPORTED;

@@ -46,6 +46,14 @@ __device__ __forceinline__ void store_out2(const ScoreArgs &s, void *out, long l
     *reinterpret_cast<float2 *>(static_cast<float *>(out) + i) = make_float2(x, y);
 }
 
+// Element i of the output.
+__device__ __forceinline__ void store_out1(const ScoreArgs &s, void *out, long long i, float x) {
+  if (s.out_half)
+    static_cast<uint16_t *>(out)[i] = __half_as_ushort(__float2half_rn(x));
+  else
+    static_cast<float *>(out)[i] = x;
+}
+
 // Host: checks `score` (null: none of it) and fills the kernels' form of it (decode_scored.cu).
 pa_status_t resolve_score(const pa_score_t *score, float scale, ScoreArgs *s);
 
