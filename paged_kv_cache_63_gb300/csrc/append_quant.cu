@@ -4,11 +4,13 @@
 //
 // Mathematics: a query or key row x becomes x / sqrt(mean(x^2) + eps) * w, its pairs (x, y) then
 // (x c - y s, x s + y c); a query is rounded once to fp16, a key or value row to the codes of
-// quant.cuh. Queries are computed in fp32. Keys are computed in pairs of fp32 (value and error, 2^-44
-// or so) and each code is the one nearest to the exact value: in plain fp32 one key element in some
-// 2^19 lies near enough to the border of two codes to fall on the wrong side.
+// quant.cuh, each the nearest to the exact value. Everything is computed in fp32 with a bound of the
+// error; where that leaves a key's code or its row's scale open (one key element in some 2^14), the
+// warp computes its keys again in pairs of fp32 (a value and its error, 2^-44 or so).
 // Bound: HBM. A token reads (query_heads + 2 kv_heads) * head_dim fp16 and writes query_heads *
 // head_dim fp16 and 2 kv_heads * (head_dim + 1) bytes.
+#include <algorithm>
+#include <atomic>
 #include <cmath>
 
 #include "early_launch.cuh"
@@ -21,6 +23,7 @@ struct AppendQuantArgs : RopeArgs {
   const float *q_weight, *k_weight;  // either may be null: its rows are not normed
   float eps;
   uint8_t *k_scale, *v_scale;
+  int rows;  // of a CTA
 };
 
 // A sum of two floats: the value and what rounding it left.
@@ -80,6 +83,37 @@ __device__ __forceinline__ Pair turned(Pair a, float c, Pair b, float s) {
   return r;
 }
 
+// Two floats at a time.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 ra, rb, rd;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+      "mul.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+      : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 ra, rb, rc, rd;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+      "mov.b64 rc, {%6, %7};\n\tfma.rn.f32x2 rd, ra, rb, rc;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+      : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+// Largest magnitude of 16 values.
+__device__ __forceinline__ float top16(const float (&v)[16]) {
+  float t = max3(fabsf(v[0]), fabsf(v[1]), fabsf(v[2]));
+#pragma unroll
+  for (int e = 3; e < 15; e += 2) t = max3(t, fabsf(v[e]), fabsf(v[e + 1]));
+  return fmaxf(t, fabsf(v[15]));
+}
+
 // Places of an item's 16 elements: element e of the first chunk pairs with element e of the second
 // (half style), or 2 e with 2 e + 1 of the 16 (interleaved).
 template <bool kInterleaved>
@@ -97,6 +131,41 @@ __device__ __forceinline__ void floats16(const uint4 &x, const uint4 &y, float (
   }
 }
 
+// Turns an item's eight pairs.
+template <bool kInterleaved>
+__device__ __forceinline__ void turn16(float (&v)[16], const float (&cs)[8], const float (&sn)[8]) {
+  if constexpr (kInterleaved) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float p = v[2 * e], q = v[2 * e + 1];
+      v[2 * e] = p * cs[e] - q * sn[e];
+      v[2 * e + 1] = p * sn[e] + q * cs[e];
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; e += 2) {
+      const float2 p = make_float2(v[e], v[e + 1]), q = make_float2(v[8 + e], v[9 + e]);
+      const float2 c = make_float2(cs[e], cs[e + 1]), s = make_float2(sn[e], sn[e + 1]);
+      const float2 f = fma2(make_float2(-q.x, -q.y), s, mul2(p, c)), g = fma2(p, s, mul2(q, c));
+      v[e] = f.x;
+      v[e + 1] = f.y;
+      v[8 + e] = g.x;
+      v[9 + e] = g.y;
+    }
+  }
+}
+
+// v *= r * w.
+__device__ __forceinline__ void scale16(float (&v)[16], float r, const float (&w)[16]) {
+#pragma unroll
+  for (int e = 0; e < 16; e += 2) {
+    const float2 x = mul2(make_float2(v[e], v[e + 1]),
+                          mul2(make_float2(r, r), make_float2(w[e], w[e + 1])));
+    v[e] = x.x;
+    v[e + 1] = x.y;
+  }
+}
+
 // 16 norm weights of an item's chunks.
 __device__ __forceinline__ void weights16(const float *w, int off_x, int off_y, float (&v)[16]) {
 #pragma unroll
@@ -109,146 +178,449 @@ __device__ __forceinline__ void weights16(const float *w, int off_x, int off_y, 
   }
 }
 
-// One CTA per row of the packed batch, items and their pairing as in append_rope_kernel: HD / 16
-// neighbouring lanes share a head's row, so its mean square and its largest element take two to
-// four shuffles.
-template <int HD, bool kInterleaved, bool kNorm>
-__global__ void __launch_bounds__(256)
-    append_quant_kernel(const __grid_constant__ AppendQuantArgs a) {
-  constexpr int IPR = HD / 16;  // items per head row
-  wait_for_stream();
-  check_sequences(a);
-  const int row = static_cast<int>(blockIdx.x);
-  const int b = sequence_of_row(a, row);
-  if (b < 0) return;
-  int t, page, pos;
-  if (!place_of_row(a, b, row, t, page, pos)) return;
-  const int slot = t & (a.ps - 1);
-  const int i = threadIdx.x % IPR;
-  const bool turns = i < a.rotary >> 4;
-  float cs[8], sn[8];
+// Inverse root mean square of a head's row, from the squares of a lane's 16 elements (those of fp16
+// numbers are exact in fp32); HD / 16 neighbouring lanes share the row. Warp-collective.
+template <int HD>
+__device__ __forceinline__ Pair inverse_rms(const float (&v)[16], float eps) {
+  Pair s = {0.f, 0.f};
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    cs[e] = 1.f;
-    sn[e] = 0.f;
+  for (int e = 0; e < 16; ++e) {
+    const Pair t = sum(s.h, v[e] * v[e]);
+    s.h = t.h;
+    s.l += t.l;
   }
-  if (turns) load_angles(a, pos, i, cs, sn);
-  const int nq = a.q ? a.qh : 0;
-  const int heads = nq + 2 * a.kvh;
-  const int step = blockDim.x / IPR;
-  // a warp's lanes walk together, so that those past the last head take part in the shuffles
-  const int first = (threadIdx.x & ~31) / IPR, mine = (threadIdx.x & 31) / IPR;
-  for (int h0 = first; h0 < heads; h0 += step) {
-    const int h = h0 + mine;
-    const bool live = h < heads;
-    const bool is_q = h < nq, is_k = !is_q && h < nq + a.kvh;
-    const bool apart = !kInterleaved && turns && (is_q || is_k);
-    const int off_x = apart ? i * 8 : i * 16;
-    const int off_y = apart ? i * 8 + a.rotary / 2 : i * 16 + 8;
-    const uint16_t *src;
-    if (is_q)
-      src = a.q + row * a.q_stride + static_cast<long long>(h) * HD;
-    else if (is_k)
-      src = a.k + row * a.k_stride + static_cast<long long>(h - nq) * HD;
-    else
-      src = a.v + row * a.v_stride + static_cast<long long>(h - nq - a.kvh) * HD;
-    uint4 x = make_uint4(0, 0, 0, 0), y = x;
-    if (live) {  // plain loads: query_out may be the query buffer itself
-      x = *reinterpret_cast<const uint4 *>(src + off_x);
-      y = *reinterpret_cast<const uint4 *>(src + off_y);
-    }
-    float v[16];
-    floats16(x, y, v);
-    const float *weight = kNorm && live ? (is_q ? a.q_weight : is_k ? a.k_weight : nullptr) : nullptr;
-    Pair norm = {1.f, 0.f};
+#pragma unroll
+  for (int o = 1; o < HD / 16; o <<= 1) {
+    const Pair t = sum(s.h, __shfl_xor_sync(0xffffffffu, s.h, o));
+    s.l = t.l + (s.l + __shfl_xor_sync(0xffffffffu, s.l, o));
+    s.h = t.h;
+  }
+  Pair m = sum(s.h * (1.f / HD), eps);
+  m.l += s.l * (1.f / HD);
+  return inverse_root(m);
+}
+
+// A lane's 16 elements (x, y) of key rows, normed and turned in pairs of fp32, each rounded to odd:
+// rounding them again to codes gives the codes nearest to the exact values; elements of value rows stay
+// as they are. Gives the codes and the row's exponent. A call of its own: what it needs of registers
+// would halve the warps of the kernel, which takes this way for few rows. Warp-collective.
+template <int HD, bool kInterleaved, bool kNorm>
+__device__ __noinline__ int exact_codes(uint4 x, uint4 y, const float *weight, float eps, bool is_k,
+                                        int off_x, int off_y, const float *angles, int sines,
+                                        uint32_t *codes) {
+  float v[16];
+  floats16(x, y, v);
+  Pair norm = {1.f, 0.f};
+  if constexpr (kNorm) norm = inverse_rms<HD>(v, eps);
+  if (is_k) {
     float w[16];
-    if constexpr (kNorm) {
-      Pair s = {0.f, 0.f};
+    const bool normed = kNorm && weight;
+    if (normed) weights16(weight, off_x, off_y, w);
 #pragma unroll
-      for (int e = 0; e < 16; ++e) {  // a square of an fp16 number is exact in fp32
-        const Pair t = sum(s.h, v[e] * v[e]);
-        s.h = t.h;
-        s.l += t.l;
+    for (int e = 0; e < 8; ++e) {
+      float &p = v[first_of_pair<kInterleaved>(e)], &q = v[second_of_pair<kInterleaved>(e)];
+      Pair u = {p, 0.f}, z = {q, 0.f};
+      if (normed) {
+        u = product(p, w[first_of_pair<kInterleaved>(e)]);
+        z = product(q, w[second_of_pair<kInterleaved>(e)]);
       }
-#pragma unroll
-      for (int o = 1; o < IPR; o <<= 1) {
-        const Pair t = sum(s.h, __shfl_xor_sync(0xffffffffu, s.h, o));
-        s.l = t.l + (s.l + __shfl_xor_sync(0xffffffffu, s.l, o));
-        s.h = t.h;
+      const float c = angles ? angles[e] : 1.f, s = angles ? angles[sines + e] : 0.f;
+      Pair f = turned(u, c, z, s);
+      Pair g = turned(u, s, z, -c);
+      if (normed) {
+        f = times(f, norm);
+        g = times(g, norm);
       }
-      if (weight) {
-        weights16(weight, off_x, off_y, w);
-        Pair m = sum(s.h * (1.f / HD), a.eps);
-        m.l += s.l * (1.f / HD);
-        norm = inverse_root(m);
-      }
+      p = to_odd(f);
+      q = to_odd(g);
     }
-    if (is_q) {
-      if (weight) {
+  }
+  float top = top16(v);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) v[e] *= norm.h * w[e];
-      }
-      if (turns) {
+  for (int o = 1; o < HD / 16; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  const int e = row_exponent(top);
+  uint32_t c[4];
+  codes16(v, e, c);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          float &p = v[first_of_pair<kInterleaved>(e)], &q = v[second_of_pair<kInterleaved>(e)];
-          const float p0 = p, q0 = q;
-          p = p0 * cs[e] - q0 * sn[e];
-          q = p0 * sn[e] + q0 * cs[e];
-        }
-      }
-      if (live) {
-        uint16_t *dst = a.q_out + (static_cast<long long>(row) * a.qh + h) * HD;
-        uint32_t o[8];
+  for (int k = 0; k < 4; ++k) codes[k] = c[k];
+  return e;
+}
+
+// Inverse root mean square of a head's row in fp32, off by at most 10 * 2^-24 of itself: 13
+// additions, halved by the root, two roundings, and the two units of rsqrtf. Warp-collective.
+template <int HD>
+__device__ __forceinline__ float row_rsqrt(const float (&v)[16], float eps) {
+  float2 s2 = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) o[e] = pack_half2(v[2 * e], v[2 * e + 1]);
-        *reinterpret_cast<uint4 *>(dst + off_x) = make_uint4(o[0], o[1], o[2], o[3]);
-        *reinterpret_cast<uint4 *>(dst + off_y) = make_uint4(o[4], o[5], o[6], o[7]);
-      }
+  for (int e = 0; e < 16; e += 2) {
+    const float2 x = make_float2(v[e], v[e + 1]);
+    s2 = fma2(x, x, s2);
+  }
+  float s = s2.x + s2.y;
+#pragma unroll
+  for (int o = 1; o < HD / 16; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  return rsqrtf(fmaf(s, 1.f / HD, eps));
+}
+
+// A query's item: normed and turned in fp32, rounded to fp16. Warp-collective.
+template <int HD, bool kInterleaved, bool kNorm>
+__device__ __forceinline__ void query_item(uint4 &x, uint4 &y, const float *weight, float eps,
+                                           int off_x, int off_y, bool turns, const float (&cs)[8],
+                                           const float (&sn)[8]) {
+  float v[16];
+  floats16(x, y, v);
+  if constexpr (kNorm) {
+    if (weight) {
+      const float r = row_rsqrt<HD>(v, eps);
+      float w[16];
+      weights16(weight, off_x, off_y, w);
+      scale16(v, r, w);
     }
-    if (__all_sync(0xffffffffu, is_q)) continue;
+  }
+  if (turns) turn16<kInterleaved>(v, cs, sn);
+  uint32_t o[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) o[e] = pack_half2(v[2 * e], v[2 * e + 1]);
+  x = make_uint4(o[0], o[1], o[2], o[3]);
+  y = make_uint4(o[4], o[5], o[6], o[7]);
+}
+
+__device__ __forceinline__ void copy16_async(uint32_t dst, const void *src, bool live) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(live ? 16u : 0u)
+               : "memory");
+}
+
+// What a thread knows of its place in a row: its item, the offsets of its two chunks in query and key
+// rows, the angles of its pairs, and what a key's error is bounded by: a turned element of a pair (x, y)
+// is off by at most (|x| + |y|) * bound, for 16 roundings of 2^-24 at the most, of products with cosines
+// and sines of up to bound / 2^-19.
+struct Item {
+  int i, off_x, off_y;
+  bool turns, apart;
+  float cs[8], sn[8], bound;
+
+  __device__ __forceinline__ Item(const AppendQuantArgs &a, int index, bool interleaved) {
+    i = index;
+    turns = i < a.rotary >> 4;
+    apart = !interleaved && turns;
+    off_x = apart ? i * 8 : i * 16;
+    off_y = apart ? i * 8 + a.rotary / 2 : i * 16 + 8;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      cs[e] = 1.f;
+      sn[e] = 0.f;
+    }
+  }
+  __device__ __forceinline__ void bounds() {
+    float steep = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) steep = max3(steep, fabsf(cs[e]), fabsf(sn[e]));
+    bound = steep * 0x1p-19f;
+  }
+};
+
+// Key or value head n (values after all keys; dead where there is none) of the token at (page, slot):
+// its codes and its scale. `angles`: the cosines of the thread's pairs, sines rotary / 2 further.
+// Warp-collective.
+template <int HD, bool kInterleaved, bool kNorm>
+__device__ __forceinline__ void write_kv(const AppendQuantArgs &a, const Item &it, uint4 kx, uint4 ky,
+                                         int n, bool live, int page, int slot,
+                                         const float *angles) {
+  constexpr int IPR = HD / 16;
+  const int i = it.i, off_x = it.off_x, off_y = it.off_y;
+  const bool turns = it.turns, apart = it.apart, is_k = n < a.kvh;
+  const float bound = it.bound;
+  const bool normed = kNorm && is_k && a.k_weight;
+  float v[16], err[8];  // values; their pairs' error bounds
+  floats16(kx, ky, v);
+  float far = 0.f, top;
+  int e;
+  uint32_t c[4];
+  if (__any_sync(0xffffffffu, is_k)) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) err[k] = 0.f;
+    float inv = 1.f;
+    if constexpr (kNorm) inv = row_rsqrt<HD>(v, a.eps);
     if (is_k) {
+      if (normed) {
+        float w[16];
+        weights16(a.k_weight, off_x, off_y, w);
+        scale16(v, inv, w);
+      }
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        float &p = v[first_of_pair<kInterleaved>(e)], &q = v[second_of_pair<kInterleaved>(e)];
-        Pair u = {p, 0.f}, z = {q, 0.f};
-        if (weight) {
-          u = product(p, w[first_of_pair<kInterleaved>(e)]);
-          z = product(q, w[second_of_pair<kInterleaved>(e)]);
+      for (int k = 0; k < 8; ++k) {
+        err[k] = fabsf(v[first_of_pair<kInterleaved>(k)]) + fabsf(v[second_of_pair<kInterleaved>(k)]);
+        far = fmaxf(far, err[k]);
+      }
+      turn16<kInterleaved>(v, it.cs, it.sn);
+    }
+    top = top16(v);
+#pragma unroll
+    for (int o = 1; o < IPR; o <<= 1) {
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      far = fmaxf(far, __shfl_xor_sync(0xffffffffu, far, o));
+    }
+    e = row_exponent(top);
+    // (the largest exponent, which clamps, is left to the careful way too)
+    bool open = row_exponent(fmaf(far, bound, top)) != row_exponent(fmaf(far, -bound, top)) ||
+                e == kMaxExp;
+    uint32_t low[4];
+    float hi[16], lo[16];
+    const float f = __uint_as_float(static_cast<uint32_t>(127 - e) << 23), d = f * bound;
+    const float2 f2 = make_float2(f, f);
+    if constexpr (kInterleaved) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float2 x = make_float2(v[2 * k], v[2 * k + 1]);
+        const float z = err[k] * d;
+        const float2 h = fma2(x, f2, make_float2(z, z)), l = fma2(x, f2, make_float2(-z, -z));
+        hi[2 * k] = h.x;
+        hi[2 * k + 1] = h.y;
+        lo[2 * k] = l.x;
+        lo[2 * k + 1] = l.y;
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; k += 2) {
+        const float2 z = mul2(make_float2(err[k], err[k + 1]), make_float2(d, d));
+        const float2 m = make_float2(-z.x, -z.y);
+#pragma unroll
+        for (int half = 0; half < 16; half += 8) {
+          const float2 x = make_float2(v[half + k], v[half + k + 1]);
+          const float2 h = fma2(x, f2, z), l = fma2(x, f2, m);
+          hi[half + k] = h.x;
+          hi[half + k + 1] = h.y;
+          lo[half + k] = l.x;
+          lo[half + k + 1] = l.y;
         }
-        Pair f = turned(u, cs[e], z, sn[e]);
-        Pair g = turned(u, sn[e], z, -cs[e]);
-        if (weight) {
-          f = times(f, norm);
-          g = times(g, norm);
-        }
-        p = to_odd(f);
-        q = to_odd(g);
       }
     }
-    float top = 0.f;
+    pack_codes(hi, c);
+    pack_codes(lo, low);
+    open = open || ((c[0] ^ low[0]) | (c[1] ^ low[1]) | (c[2] ^ low[2]) | (c[3] ^ low[3])) != 0;
+    if (__any_sync(0xffffffffu, open)) {
+      uint32_t codes[4];
+      e = exact_codes<HD, kInterleaved, kNorm>(kx, ky, a.k_weight, a.eps, is_k, off_x, off_y,
+                                               turns ? angles : nullptr, a.rotary / 2, codes);
 #pragma unroll
-    for (int e = 0; e < 16; ++e) top = fmaxf(top, fabsf(v[e]));
+      for (int k = 0; k < 4; ++k) c[k] = codes[k];
+    }
+  } else {
+    top = top16(v);
 #pragma unroll
     for (int o = 1; o < IPR; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    if (!is_q && live) {
-      const int e = row_exponent(top);
-      uint32_t c[4];
-      codes16(v, e, c);
-      const int kv = is_k ? h - nq : h - nq - a.kvh;
-      const long long at = a.layout == PA_LAYOUT_HEAD_MAJOR
-                               ? (static_cast<long long>(page) * a.kvh + kv) * a.ps + slot
-                               : (static_cast<long long>(page) * a.ps + slot) * a.kvh + kv;
-      uint8_t *dst = static_cast<uint8_t *>(is_k ? a.k_cache : a.v_cache) + at * HD;
-      if (apart) {
-        *reinterpret_cast<uint2 *>(dst + off_x) = make_uint2(c[0], c[1]);
-        *reinterpret_cast<uint2 *>(dst + off_y) = make_uint2(c[2], c[3]);
-      } else {
-        *reinterpret_cast<uint4 *>(dst + off_x) = make_uint4(c[0], c[1], c[2], c[3]);
+    e = row_exponent(top);
+    codes16(v, e, c);
+  }
+  if (live) {
+    const int kv = is_k ? n : n - a.kvh;
+    const long long at = a.layout == PA_LAYOUT_HEAD_MAJOR
+                             ? (static_cast<long long>(page) * a.kvh + kv) * a.ps + slot
+                             : (static_cast<long long>(page) * a.ps + slot) * a.kvh + kv;
+    uint8_t *dst = static_cast<uint8_t *>(is_k ? a.k_cache : a.v_cache) + at * HD;
+    if (is_k && apart) {
+      *reinterpret_cast<uint2 *>(dst + off_x) = make_uint2(c[0], c[1]);
+      *reinterpret_cast<uint2 *>(dst + off_y) = make_uint2(c[2], c[3]);
+    } else {
+      *reinterpret_cast<uint4 *>(dst + i * 16) = make_uint4(c[0], c[1], c[2], c[3]);
+    }
+    if (i == 0)
+      (is_k ? a.k_scale : a.v_scale)[scale_place(page, kv, slot, a.kvh, a.ps)] =
+          static_cast<uint8_t>(e + kScaleBias);
+  }
+}
+
+// Few rows: a CTA takes one, all its warps look up its place, and a thread asks for its first query and
+// its first key or value item before that: no address of them depends on the sequence that the row is
+// of.
+template <int HD, bool kInterleaved, bool kNorm>
+__global__ void __launch_bounds__(256, 3)
+    append_quant_kernel(const __grid_constant__ AppendQuantArgs a) {
+  constexpr int IPR = HD / 16;
+  wait_for_stream();
+  const long long row = blockIdx.x;
+  Item it(a, threadIdx.x % IPR, kInterleaved);
+  const int nq = a.q ? a.qh : 0, nkv = 2 * a.kvh;
+  const int step = blockDim.x / IPR, slot0 = threadIdx.x / IPR;
+  auto load_q = [&](int h, uint4 &x, uint4 &y) {  // plain: query_out may be the query buffer itself
+    if (h >= nq) return;
+    const uint16_t *src = a.q + row * a.q_stride + static_cast<long long>(h) * HD;
+    x = *reinterpret_cast<const uint4 *>(src + it.off_x);
+    y = *reinterpret_cast<const uint4 *>(src + it.off_y);
+  };
+  auto load_kv = [&](int n, uint4 &x, uint4 &y) {
+    if (n >= nkv) return;
+    const bool is_k = n < a.kvh;
+    const uint16_t *src =
+        is_k ? a.k + row * a.k_stride + n * HD : a.v + row * a.v_stride + (n - a.kvh) * HD;
+    x = __ldg(reinterpret_cast<const uint4 *>(src + (is_k ? it.off_x : it.i * 16)));
+    y = __ldg(reinterpret_cast<const uint4 *>(src + (is_k ? it.off_y : it.i * 16 + 8)));
+  };
+  uint4 qx = make_uint4(0, 0, 0, 0), qy = qx, kx = qx, ky = qx;
+  load_q(slot0, qx, qy);
+  load_kv(slot0, kx, ky);
+
+  check_sequences(a);
+  const int b = sequence_of_row(a, static_cast<int>(row));
+  if (b < 0) return;
+  int t, page, pos;
+  if (!place_of_row(a, b, static_cast<int>(row), t, page, pos, threadIdx.x == 0)) return;
+  if (it.turns) load_angles(a, pos, it.i, it.cs, it.sn);
+  it.bounds();
+
+  // a warp's lanes walk together, so that those past the last head take part in the shuffles
+  const int first = (threadIdx.x & ~31) / IPR;
+#pragma unroll 1
+  for (int w0 = first, h = slot0; w0 < nq; w0 += step, h += step) {
+    if (w0 != first) load_q(h, qx, qy);
+    query_item<HD, kInterleaved, kNorm>(qx, qy, a.q_weight, a.eps, it.off_x, it.off_y, it.turns,
+                                        it.cs, it.sn);
+    if (h < nq) {
+      uint16_t *dst = a.q_out + (row * a.qh + h) * HD;
+      *reinterpret_cast<uint4 *>(dst + it.off_x) = qx;
+      *reinterpret_cast<uint4 *>(dst + it.off_y) = qy;
+    }
+  }
+  const float *turn = a.table + static_cast<long long>(pos) * a.rotary + it.i * 8;
+#pragma unroll 1
+  for (int w0 = first, n = slot0; w0 < nkv; w0 += step, n += step) {
+    if (w0 != first) load_kv(n, kx, ky);
+    write_kv<HD, kInterleaved, kNorm>(a, it, kx, ky, n, n < nkv, page, t & (a.ps - 1), turn);
+  }
+}
+
+constexpr int kRowsAtMost = 8;    // rows of a CTA
+constexpr int kQueriesAtOnce = 2; // query heads of a thread
+constexpr int kChunks = 2 * kQueriesAtOnce + 2;
+
+// Many rows: a CTA takes a.rows neighbouring rows of the packed batch. Its warps first look up the places of one
+// row each. A head row is HD / 16 items of two 16-byte chunks, paired as in append_rope_kernel; a
+// thread keeps its item index and walks query heads two at a time, then key and value heads. What a
+// thread needs of the next row it has copied to shared memory meanwhile, each thread for itself.
+template <int HD, bool kInterleaved, bool kNorm>
+__global__ void __launch_bounds__(256, 2)
+    append_quant_rows_kernel(const __grid_constant__ AppendQuantArgs a) {
+  constexpr int IPR = HD / 16;  // items per head row
+  // [2 rows][kChunks][threads], then the rows' table rows [a.rows][rotary]
+  extern __shared__ __align__(16) uint4 chunks[];
+  __shared__ int places[kRowsAtMost][3];
+  wait_for_stream();
+  const long long row0 = static_cast<long long>(blockIdx.x) * a.rows;
+  const int rows = static_cast<int>(min(static_cast<long long>(a.rows), a.total - row0));
+  Item it(a, threadIdx.x % IPR, kInterleaved);
+  const int i = it.i, off_x = it.off_x, off_y = it.off_y;
+  const int nq = a.q ? a.qh : 0, nkv = 2 * a.kvh;
+  const int step = blockDim.x / IPR, slot0 = threadIdx.x / IPR;
+  const int warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+
+  // plain loads of query rows: query_out may be the query buffer itself
+  auto kv_row = [&](long long row, int n) {
+    return n < a.kvh ? a.k + row * a.k_stride + n * HD
+                     : a.v + row * a.v_stride + (n - a.kvh) * HD;
+  };
+  auto q_row = [&](long long row, int h) {
+    return a.q + row * a.q_stride + static_cast<long long>(h) * HD;
+  };
+  // What the thread reads of the next row: its query items (u), its key or value item.
+  const bool kv_live = slot0 < nkv, kv_is_k = slot0 < a.kvh;
+  const uint16_t *next_q = nq > 0 ? q_row(row0, min(slot0, nq - 1)) : a.k;
+  const uint16_t *next_kv = kv_live ? kv_row(row0, slot0) : a.k;
+  const long long kv_stride = kv_is_k ? a.k_stride : a.v_stride;
+  const int kv_x = kv_is_k ? off_x : i * 16, kv_y = kv_is_k ? off_y : i * 16 + 8;
+  auto prefetch = [&](int r) {
+    const uint32_t at = smem_addr(chunks + (r & 1) * kChunks * blockDim.x + threadIdx.x);
+    const uint32_t next = blockDim.x * 16;
+#pragma unroll
+    for (int u = 0; u < kQueriesAtOnce; ++u) {
+      const bool live = slot0 + u * step < nq;
+      const uint16_t *src = live ? next_q + u * step * HD : a.k;
+      copy16_async(at + 2 * u * next, src + off_x, live);
+      copy16_async(at + (2 * u + 1) * next, src + off_y, live);
+    }
+    copy16_async(at + 2 * kQueriesAtOnce * next, next_kv + kv_x, kv_live);
+    copy16_async(at + (2 * kQueriesAtOnce + 1) * next, next_kv + kv_y, kv_live);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    next_q += a.q_stride;
+    next_kv += kv_stride;
+  };
+  prefetch(0);
+
+  check_sequences(a);
+  for (int r = warp; r < rows; r += warps) {
+    const int row = static_cast<int>(row0) + r;
+    int t = 0, page = -1, pos = 0;
+    const int b = sequence_of_row(a, row);
+    if (b >= 0 && !place_of_row(a, b, row, t, page, pos, (threadIdx.x & 31) == 0)) page = -1;
+    if ((threadIdx.x & 31) == 0) {
+      places[r][0] = t;
+      places[r][1] = page;
+      places[r][2] = pos;
+    }
+  }
+  __syncthreads();
+  float *angles = reinterpret_cast<float *>(chunks + 2 * kChunks * blockDim.x);
+  {
+    const int per_row = a.rotary >> 2;  // copies of 16 bytes
+    for (int n = threadIdx.x; n < rows * per_row; n += blockDim.x) {
+      const int r = n / per_row, c = n - r * per_row;
+      if (places[r][1] >= 0)
+        copy16_async(smem_addr(angles + r * a.rotary + c * 4),
+                     a.table + static_cast<long long>(places[r][2]) * a.rotary + c * 4, true);
+    }
+    asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
+  }
+  __syncthreads();
+
+  // a warp's lanes walk together, so that those past the last head take part in the shuffles
+  const int first = (threadIdx.x & ~31) / IPR;
+#pragma unroll 1
+  for (int r = 0; r < rows; ++r) {
+    const long long row = row0 + r;
+    const int t = places[r][0], page = places[r][1];
+    const float *turn = angles + r * a.rotary + i * 8;
+    if (it.turns) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        it.cs[e] = turn[e];
+        it.sn[e] = turn[a.rotary / 2 + e];
       }
-      if (i == 0)
-        (is_k ? a.k_scale : a.v_scale)[scale_place(page, kv, slot, a.kvh, a.ps)] =
-            static_cast<uint8_t>(e + kScaleBias);
+    }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    const uint4 *mine = chunks + (r & 1) * kChunks * blockDim.x + threadIdx.x;
+    if (r + 1 < rows) prefetch(r + 1);
+    if (page < 0) continue;  // the CTA's, as places are
+    it.bounds();
+
+#pragma unroll 1
+    for (int w0 = first, h0 = slot0; w0 < nq; w0 += kQueriesAtOnce * step, h0 += kQueriesAtOnce * step) {
+#pragma unroll
+      for (int u = 0; u < kQueriesAtOnce; ++u) {
+        const int h = h0 + u * step;
+        uint4 x = mine[2 * u * blockDim.x], y = mine[(2 * u + 1) * blockDim.x];
+        if (w0 != first && h < nq) {
+          x = *reinterpret_cast<const uint4 *>(q_row(row, h) + off_x);
+          y = *reinterpret_cast<const uint4 *>(q_row(row, h) + off_y);
+        }
+        query_item<HD, kInterleaved, kNorm>(x, y, a.q_weight, a.eps, off_x, off_y, it.turns, it.cs,
+                                            it.sn);
+        if (h < nq) {
+          uint16_t *dst = a.q_out + (row * a.qh + h) * HD;
+          *reinterpret_cast<uint4 *>(dst + off_x) = x;
+          *reinterpret_cast<uint4 *>(dst + off_y) = y;
+        }
+      }
+    }
+
+    const int slot = t & (a.ps - 1);
+#pragma unroll 1
+    for (int w0 = first, n = slot0; w0 < nkv; w0 += step, n += step) {
+      uint4 x = mine[2 * kQueriesAtOnce * blockDim.x], y = mine[(2 * kQueriesAtOnce + 1) * blockDim.x];
+      if (w0 != first && n < nkv) {
+        x = __ldg(reinterpret_cast<const uint4 *>(kv_row(row, n) + (n < a.kvh ? off_x : i * 16)));
+        y = __ldg(reinterpret_cast<const uint4 *>(kv_row(row, n) + (n < a.kvh ? off_y : i * 16 + 8)));
+      }
+      write_kv<HD, kInterleaved, kNorm>(a, it, x, y, n, n < nkv, page, slot, turn);
     }
   }
 }
@@ -324,21 +696,42 @@ __global__ void __launch_bounds__(kReadRows * 32)
 
 namespace {
 
+constexpr long long kManyRows = 8192;
+
 bool off_by(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) != 0; }
+
+template <int HD, bool kInterleaved, bool kNorm>
+cudaError_t launch_append_quant_as(const AppendQuantArgs &a, cudaStream_t stream) {
+  constexpr int IPR = HD / 16;
+  const int nq = a.q ? a.qh : 0, nkv = 2 * a.kvh;
+  // What a CTA of several rows saves in instructions it pays in warps, of which its registers leave
+  // few: worth it once the rows keep all multiprocessors busy for several rounds (eight prompts of 2048
+  // tokens, 32/8 heads of 128: 85 against 125 us; 3300 rows of 24/4 heads of 256: 49 against 35).
+  if (a.total < kManyRows) {
+    const int threads = std::min(256, (std::max(nq, nkv) * IPR + 31) / 32 * 32);
+    return launch_early(append_quant_kernel<HD, kInterleaved, kNorm>,
+                        dim3(static_cast<unsigned>(a.total)), threads, 0, stream, a);
+  }
+  const int slots = std::max((nq + kQueriesAtOnce - 1) / kQueriesAtOnce, nkv);
+  const int threads = std::min(256, (slots * IPR + 31) / 32 * 32);
+  AppendQuantArgs b = a;
+  b.rows = kRowsAtMost;
+  static std::atomic<bool> set[kMaxLaunchDevices];
+  auto kern = append_quant_rows_kernel<HD, kInterleaved, kNorm>;
+  const cudaError_t e =
+      allow_smem(kern, 2 * kChunks * 256 * 16 + kRowsAtMost * HD * 4, set);
+  if (e != cudaSuccess) return e;
+  return launch_early(kern, dim3(static_cast<unsigned>((a.total + b.rows - 1) / b.rows)), threads,
+                      2 * kChunks * threads * 16 + b.rows * a.rotary * 4, stream, b);
+}
 
 template <int HD>
 cudaError_t launch_append_quant(const AppendQuantArgs &a, cudaStream_t stream) {
-  constexpr int IPR = HD / 16;
-  const int heads = (a.q ? a.qh : 0) + 2 * a.kvh;
-  const int want = heads * IPR;
-  const int threads = want >= 256 ? 256 : (want + 31) / 32 * 32;
-  void (*kern)(AppendQuantArgs);
   if (a.q_weight || a.k_weight)
-    kern = a.interleaved ? append_quant_kernel<HD, true, true> : append_quant_kernel<HD, false, true>;
-  else
-    kern =
-        a.interleaved ? append_quant_kernel<HD, true, false> : append_quant_kernel<HD, false, false>;
-  return launch_early(kern, dim3(static_cast<unsigned>(a.total)), threads, 0, stream, a);
+    return a.interleaved ? launch_append_quant_as<HD, true, true>(a, stream)
+                         : launch_append_quant_as<HD, false, true>(a, stream);
+  return a.interleaved ? launch_append_quant_as<HD, true, false>(a, stream)
+                       : launch_append_quant_as<HD, false, false>(a, stream);
 }
 
 }  // namespace

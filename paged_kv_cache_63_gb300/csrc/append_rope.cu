@@ -53,7 +53,7 @@ __global__ void __launch_bounds__(256) append_rope_kernel(const __grid_constant_
   const int b = sequence_of_row(a, row);
   if (b < 0) return;
   int t, page, pos;
-  if (!place_of_row(a, b, row, t, page, pos)) return;
+  if (!place_of_row(a, b, row, t, page, pos, threadIdx.x == 0)) return;
   const int slot = t & (a.ps - 1);
   const int i = threadIdx.x % IPR;
   const int turned = a.rotary >> 4;  // items that turn

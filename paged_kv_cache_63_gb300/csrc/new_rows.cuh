@@ -84,10 +84,10 @@ __device__ __forceinline__ int sequence_of_row(const NewRowsArgs &a, int row) {
   return look_for_sequence(a, row);
 }
 
-// Token index, page and rotation position of row `row` of sequence b; false (flagged): nothing of it
-// is to be written.
+// Token index, page and rotation position of row `row` of sequence b; false (flagged by the threads
+// that `tells`): nothing of it is to be written.
 __device__ __forceinline__ bool place_of_row(const RopeArgs &a, int b, int row, int &t, int &page,
-                                             int &pos) {
+                                             int &pos, bool tells) {
   const int q1 = __ldg(a.qs + b + 1), c = __ldg(a.ctx + b);
   t = c - q1 + row;
   page = __ldg(a.bt + static_cast<long long>(b) * a.maxp + (t >> a.ps_shift));
@@ -95,7 +95,7 @@ __device__ __forceinline__ bool place_of_row(const RopeArgs &a, int b, int row, 
   const bool bad_page = page < 0 || page >= a.num_pages;
   const bool bad_pos = a.rotary > 0 && (pos < 0 || pos >= a.table_rows);
   if (!bad_page && !bad_pos) return true;
-  if (threadIdx.x == 0)
+  if (tells)
     atomicOr(a.err, (bad_page ? PA_DEVERR_PAGE_ID : 0u) | (bad_pos ? PA_DEVERR_POSITION : 0u));
   return false;
 }

@@ -35,6 +35,12 @@ __device__ __forceinline__ uint32_t code2(float x, float y) {
   return c;
 }
 
+__device__ __forceinline__ void pack_codes(const float (&y)[16], uint32_t (&w)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    w[i] = code2(y[4 * i], y[4 * i + 1]) | code2(y[4 * i + 2], y[4 * i + 3]) << 16;
+}
+
 // 16 values of a row as codes, four to a word.
 __device__ __forceinline__ void codes16(const float (&x)[16], int e, uint32_t (&w)[4]) {
   const float f = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
@@ -49,9 +55,7 @@ __device__ __forceinline__ void codes16(const float (&x)[16], int e, uint32_t (&
           : "+f"(y[i])
           : "f"(240.f), "f"(-240.f));
   }
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    w[i] = code2(y[4 * i], y[4 * i + 1]) | code2(y[4 * i + 2], y[4 * i + 3]) << 16;
+  pack_codes(y, w);
 }
 
 // Codes to fp16: the low and the high two of a word.
