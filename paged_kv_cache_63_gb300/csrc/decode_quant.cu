@@ -325,7 +325,7 @@ __device__ __forceinline__ void code_tile(CodeState<HD> &st, const CodeLane<HD, 
 #pragma unroll
     for (int g = 0; g < NG; ++g)
 #pragma unroll
-      for (int i = 0; i < 2; ++i) vbyte[g][i] = seen(g, i) ? vbyte[g][i] : 0u;
+      for (int i = 0; i < 2; ++i) vbyte[g][i] = seen(g, i) ? vbyte[g][i] : kSmallestByte;
   }
   uint32_t most = 0;
 #pragma unroll
@@ -333,8 +333,8 @@ __device__ __forceinline__ void code_tile(CodeState<HD> &st, const CodeLane<HD, 
   most = min(__reduce_max_sync(0xffffffffu, most), 254u);
   const float out_scale = __uint_as_float(most << 23);
   // 2^(b - most) as float bits: (b - most + 127) << 23. Bytes of written rows lie within 23 of each
-  // other; a byte of 0 (a token that is not seen) gives a finite number, which its probability of 0
-  // meets.
+  // other, and a token that is not seen has the smallest, so that its probability of 0 meets a finite
+  // number.
   const uint32_t bias = (127u - most) << 23;
 
   // Weights relative to the tile's scale: at most the probability, so they hold as fp16; the row sum
@@ -602,7 +602,12 @@ int quant_smem(int head_dim, int warps, int stages) {
 // What pa_decode_quant launches, in pa_plan's terms. `score`: null, or the resolved rule.
 pa_status_t quant_plan(const pa_problem_t *p, const pa_options_t *o, int sm_count,
                        const ScoreArgs *score, pa_plan_t *pl) {
-  pa_status_t st = pa_plan(p, o, sm_count, pl);  // its checks, and the split into units
+  if (o && (o->stages < 0 || o->stages > kMaxStages || o->warps_per_cta < 0 ||
+            o->warps_per_cta > kMaxWarpsPerCta))
+    return PA_ERR_INVALID_ARG;
+  pa_options_t rest = o ? *o : pa_options_t{};
+  rest.stages = rest.warps_per_cta = 0;  // what they take of shared memory is another here
+  pa_status_t st = pa_plan(p, &rest, sm_count, pl);  // its checks, and the split into units
   if (st != PA_OK) return st;
   if (o && (o->math || o->combine || o->tile_tokens)) return PA_ERR_UNSUPPORTED;
   const int g = p->query_heads / p->kv_heads;
