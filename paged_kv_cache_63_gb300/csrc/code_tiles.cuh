@@ -55,7 +55,10 @@ template <int HD, int TN, int kRows>
 __device__ __forceinline__ void convert_rows(uint32_t at, uint32_t scales, int row0) {
   using C = CodeTile<HD, TN>;
   constexpr int kAtOnce = HD == 64 ? 8 : 4;  // rows that a warp's lanes cover
-  constexpr int kSteps = kRows / (2 * kAtOnce);
+  // Two steps to a turn, but one at head_dim 256, where the instruction cache misses most (572 us
+  // against 597 for two capped prompts of 4096; at 128 two take 357 us, one 361, for the chunks above)
+  constexpr bool kTwo = HD < 256;
+  constexpr int kSteps = kRows / (kTwo ? 2 * kAtOnce : kAtOnce);
   const int lane = threadIdx.x & 31;
   const int i = lane & 7, q = lane >> 3;
   int r, c;  // row within the first kAtOnce, chunk of 16 codes within the column block
@@ -74,13 +77,13 @@ __device__ __forceinline__ void convert_rows(uint32_t at, uint32_t scales, int r
   constexpr uint32_t kFlip = HD == 64 ? 0 : 64;
   uint32_t to = at + (c >> 2) * (TN * 128) + (row0 + r) * 128 + (((2 * (c & 3)) ^ (r & 7)) << 4);
   uint32_t scale = scales + row0 + r;
-  uint4 w0, w1;
-  uint32_t e0, e1;
+  uint4 w0, w1 = {};
+  uint32_t e0, e1 = 0;
   auto load = [&]() {
     w0 = lds128_at<0>(from);
-    w1 = lds128_at<kAtOnce * C::kBlock>(from ^ kFlip);
+    if constexpr (kTwo) w1 = lds128_at<kAtOnce * C::kBlock>(from ^ kFlip);
     e0 = lds8_at<0>(scale);
-    e1 = lds8_at<kAtOnce>(scale);
+    if constexpr (kTwo) e1 = lds8_at<kAtOnce>(scale);
   };
   auto store = [&](auto off, const uint4 &w, uint32_t e, uint32_t flip) {
     const uint32_t f = half2_of_scale(e);
@@ -99,13 +102,22 @@ __device__ __forceinline__ void convert_rows(uint32_t at, uint32_t scales, int r
   for (int m = 0; m < kSteps; ++m) {
     const uint4 v0 = w0, v1 = w1;
     const uint32_t f0 = e0, f1 = e1;
-    from += 2 * kAtOnce * C::kBlock;
-    scale += 2 * kAtOnce;
+    if constexpr (kTwo) {
+      from += 2 * kAtOnce * C::kBlock;
+      scale += 2 * kAtOnce;
+    } else {
+      from = (from ^ kFlip) + kAtOnce * C::kBlock;
+      scale += kAtOnce;
+    }
     if (m + 1 < kSteps) load();  // rows that nothing has overwritten yet
     __syncwarp();
     store(Const<0>{}, v0, f0, 0);
-    store(Const<kAtOnce * 128>{}, v1, f1, kFlip);
-    to += 2 * kAtOnce * 128;
+    if constexpr (kTwo) {
+      store(Const<kAtOnce * 128>{}, v1, f1, kFlip);
+      to += 2 * kAtOnce * 128;
+    } else {
+      to = (to ^ kFlip) + kAtOnce * 128;
+    }
   }
   // the tensor cores read the slot through the asynchronous proxy
   fence_proxy_async();

@@ -138,7 +138,11 @@ struct ScoredTile2 {
         float o[32];
         tmem_ld32(to + c * 32, o);
 #pragma unroll
-        for (int e = 0; e < 32; ++e) o[e] *= f;
+        for (int e = 0; e < 32; e += 2) {
+          const float2 x = fmul2(make_float2(o[e], o[e + 1]), make_float2(f, f));
+          o[e] = x.x;
+          o[e + 1] = x.y;
+        }
         tmem_st32(to + c * 32, o);
       }
       return true;

@@ -111,7 +111,11 @@ struct ScoredTile1 {
         float v[32];
         tmem_ld32(to + c * 32, v);
 #pragma unroll
-        for (int e = 0; e < 32; ++e) v[e] *= f;
+        for (int e = 0; e < 32; e += 2) {
+          const float2 x = fmul2(make_float2(v[e], v[e + 1]), make_float2(f, f));
+          v[e] = x.x;
+          v[e + 1] = x.y;
+        }
         tmem_st32(to + c * 32, v);
       }
       return true;
@@ -281,7 +285,7 @@ __global__ void __launch_bounds__(kQuant ? kQuantThreads : kScoredThreads, 1)
         if (!ok) break;
         if (lane == 0) {
           mbar_arrive_expect_tx(bar(kBarQ), C::KB * q_rows * 128);
-#pragma unroll
+#pragma unroll(kQuant ? 1 : C::KB)
           for (int kb = 0; kb < C::KB; ++kb)
             tma_load_3d(sq + kb * (C::kRows * 128), &tq, bar(kBarQ), kb * 64, it.kv * a.g,
                         it.q0 + it.tok0, l2_evict_first_policy());  // read once
@@ -333,7 +337,7 @@ __global__ void __launch_bounds__(kQuant ? kQuantThreads : kScoredThreads, 1)
         if (lane == 0) mbar_arrive_expect_tx(bar(full + st), __popc(issue) * box_bytes * kBlocks);
         __syncwarp();
         if (page >= 0) {
-#pragma unroll
+#pragma unroll(kQuant ? 1 : kBlocks)
           for (int kb = 0; kb < kBlocks; ++kb)
             tma_load_3d(stage0 + st * C::kKVBytes + kLandAt + kb * kApart + lane * box_bytes, map,
                         bar(full + st), kb * kColumns, y, z, pol);
@@ -379,7 +383,10 @@ __global__ void __launch_bounds__(kQuant ? kQuantThreads : kScoredThreads, 1)
             const uint32_t d = tmem + st * C::TN;
             uint64_t kd = smem_desc_sw128(k_stage(st), 16, 1024);
             asm volatile("" : "+l"(kd));
-#pragma unroll
+            // (with converter warps beside it the shared instruction cache is short: 552 us against
+            // 572 written out for two capped prompts of 4096 over a quantised cache; without, the
+            // six heads of prefill_gqa6_hd256 take 302 us written out, 346 in loops)
+#pragma unroll(kQuant ? 4 : HD / 16)
             for (int ks = 0; ks < HD / 16; ++ks) {
               const uint64_t bd = kd + (((ks >> 2) * (C::TN * 128) + (ks & 3) * 32) >> 4);
               mma_f16_ts_warp(d, tmem + kQCol + ks * 8, bd, C::kIdescS, ks > 0);
@@ -422,7 +429,7 @@ __global__ void __launch_bounds__(kQuant ? kQuantThreads : kScoredThreads, 1)
             // had read the previous item's O
             uint64_t vd = smem_desc_sw128(v_stage(st), C::TN * 128, 1024);
             asm volatile("" : "+l"(vd));
-#pragma unroll
+#pragma unroll(kQuant ? 2 : C::TN / 16)
             for (int ks = 0; ks < C::TN / 16; ++ks) {
               const uint64_t bd = vd + ((ks * 2048) >> 4);
               mma_f16_ts_warp(tmem + C::kOCol, tmem + st * C::TN + ks * 8, bd, C::kIdescPV,
@@ -466,7 +473,7 @@ __global__ void __launch_bounds__(kQuant ? kQuantThreads : kScoredThreads, 1)
       if (!ok) break;
       ++live;
       tc_fence_after();
-#pragma unroll
+#pragma unroll 1
       for (int kb = 0; kb < C::KB; ++kb) {
         float q[32];
 #pragma unroll
@@ -507,7 +514,7 @@ __global__ void __launch_bounds__(kQuant ? kQuantThreads : kScoredThreads, 1)
       // waits for this warp's next P.
       const float inv = sr.l > 0.f ? 1.f / sr.l : 0.f;
       const uint64_t pol = l2_evict_first_policy();
-#pragma unroll
+#pragma unroll 1
       for (int c = 0; c < HD / 32; ++c) {
         float v[32];
         tmem_ld32(trow + C::kOCol + c * 32, v);

@@ -251,7 +251,10 @@ __device__ __forceinline__ bool scored_weights(const ScoreArgs &s, float scale_l
   const bool masked = !__all_sync(0xffffffffu, lo <= 0 && hi >= 63);
   float v[64], mult = scale_log2, offset = 0.f, high, low;
   io.load(v);
-  bool settled = false;
+  // `settled`: the largest score need not be looked for any more; `moves`: it is `top`, and may move
+  // the reference (one place that does it: the code is long)
+  bool settled = false, moves = false;
+  float top = -INFINITY;
   if constexpr (kParts & kRuleCap) {
     constexpr bool kWide = (kParts & kRuleWide) != 0;
     // what no row sees, and rows that do not count, must not choose the warp's form of tanh
@@ -267,10 +270,11 @@ __device__ __forceinline__ bool scored_weights(const ScoreArgs &s, float scale_l
         extremes(v, high, low);  // capped scores are monotonic in the raw products
         const float best = scale_log2 >= 0.f ? high : low;
         // (the exponential form is near enough for a reference, but not at any cap)
-        const float top = kWide ? cap_poly(s, make_float2(best, best)).x * best : cap_exp(s, best);
-        if (!io.settle(row, top, later)) return false;
+        top = kWide ? cap_poly(s, make_float2(best, best)).x * best : cap_exp(s, best);
+        moves = true;
       }
       if constexpr (Io::kCapWithWeights) {
+        if (moves && !io.settle(row, top, later)) return false;
         const float2 n2 = make_float2(-row.m, -row.m);
         weigh(row, pk, [&](int c) {
           const float2 x = make_float2(v[c], v[c + 1]);
@@ -313,9 +317,10 @@ __device__ __forceinline__ bool scored_weights(const ScoreArgs &s, float scale_l
   }
   if (!settled) {
     extremes(v, high, low);
-    const float top = fmaf(mult >= 0.f ? high : low, mult, offset);
-    if (!io.settle(row, top, later)) return false;
+    top = fmaf(mult >= 0.f ? high : low, mult, offset);
+    moves = true;
   }
+  if (moves && !io.settle(row, top, later)) return false;
   if (row.m != -INFINITY) offset -= row.m;
   const float2 m2 = make_float2(mult, mult), n2 = make_float2(offset, offset);
   weigh(row, pk, [&](int c) { return ffma2(make_float2(v[c], v[c + 1]), m2, n2); });
