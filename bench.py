@@ -40,7 +40,7 @@ DEFAULT_WORKLOAD = "ragged"
 PREFILL_WORKLOADS = ("prefill_gqa4", "prefill_chunked", "prefill_mha", "prefill_gqa6_hd256")
 # the library's other kernels, each timed alone on a full-size workload by --kernel-case
 KERNEL_CASES = ("append", "append_rope", "split_combine", "decode_scored", "prefill_scored",
-                "prefill_hd256")
+                "prefill_hd256", "append_quant", "read_quant", "decode_quant", "prefill_quant")
 # the other full-size decode workloads, each measured into a block of its own
 OTHER_WORKLOADS = ("gqa4_mid", "mha", "long_gqa6")
 FALLBACK_HBM_GBS = 6800.0
@@ -579,8 +579,98 @@ def prefill_scored_case(args, torch, lib, stream):
                  window=window), ms, "tensor", 4.0 * pairs * w.query_heads * w.head_dim)
 
 
+def quantised(w, torch, lib):
+    """A quantised cache of w's shape, and a call that writes every token of w's contexts into it."""
+    total = int(w.context_lengths.sum())
+    gen = torch.Generator(device="cuda").manual_seed(12)
+    rows = torch.randn((total, 2 * w.kv_heads, w.head_dim), generator=gen, device="cuda",
+                       dtype=torch.float16)
+    codes = [torch.zeros(w.key_cache.shape, device="cuda", dtype=torch.uint8) for _ in range(2)]
+    scales = [torch.zeros((w.num_physical_pages, w.kv_heads, w.page_size), device="cuda",
+                          dtype=torch.uint8) for _ in range(2)]
+    cache = lib.quant_cache(*codes, *scales)
+    qs, bt, ctx = [torch.from_numpy(np.ascontiguousarray(x, dtype=np.int32)).cuda() for x in (
+        np.concatenate([[0], np.cumsum(w.context_lengths)]), w.block_tables, w.context_lengths)]
+    lib.pa_append_quant(lib.problem_of(w), None, None, None, rows[:, :w.kv_heads],
+                        rows[:, w.kv_heads:], qs, total, bt, ctx, None, cache)
+    return cache, qs, total, bt, ctx
+
+
+def append_quant_case(args, torch, lib, stream):
+    """prefill_gqa4's prompts into a quantised cache, keys and queries normed and turned."""
+    from paged_kv_cache_63_gb300.workloads import make_prefill
+
+    w = make_prefill("prefill_gqa4").cache
+    cache, qs, total, bt, ctx = quantised(w, torch, lib)
+    hd, qh, kvh = w.head_dim, w.query_heads, w.kv_heads
+    qkv = torch.randn((total, qh + 2 * kvh, hd), device="cuda", dtype=torch.float16)
+    angle = torch.arange(4096, device="cuda", dtype=torch.float64)[:, None] \
+        * 10000.0 ** -torch.arange(0, 1, 2 / hd, device="cuda", dtype=torch.float64)
+    rope = lib.rope(hd, "half", torch.stack([angle.cos(), angle.sin()], 1).float())
+    norm = lib.norm(1e-6, *(1 + 0.1 * torch.randn((2, hd), device="cuda")).unbind())
+    q_out = torch.empty((total, qh, hd), device="cuda", dtype=torch.float16)
+    q, k, v = qkv.split([qh, kvh, kvh], 1)
+    (ms,) = time_calls([lambda: lib.pa_append_quant(
+        lib.problem_of(w), norm, rope, q, k, v, qs, total, bt, ctx, q_out, cache, stream=stream)],
+        args.steps, args.warmup, torch)
+    nbytes = total * ((2 * qh + 2 * kvh) * hd * 2 + 2 * kvh * (hd + 1)) \
+        + int(w.context_lengths.max()) * hd * 4
+    return dict(workload="prefill_gqa4", kernel="pa::append_quant_rows_kernel"), ms, "hbm", nbytes
+
+
+def read_quant_case(args, torch, lib, stream):
+    """prefill_gqa4's contexts read back from a quantised cache as fp16 rows."""
+    from paged_kv_cache_63_gb300.workloads import make_prefill
+
+    w = make_prefill("prefill_gqa4").cache
+    cache, qs, total, bt, ctx = quantised(w, torch, lib)
+    k, v = [torch.empty((total, w.kv_heads, w.head_dim), device="cuda", dtype=torch.float16)
+            for _ in range(2)]
+    (ms,) = time_calls([lambda: lib.pa_read_quant(lib.problem_of(w), cache, qs, total, bt, ctx, k,
+                                                  v, stream=stream)],
+                       args.steps, args.warmup, torch)
+    nbytes = total * 2 * w.kv_heads * (3 * w.head_dim + 1)
+    return dict(workload="prefill_gqa4", kernel="pa::read_quant_kernel"), ms, "hbm", nbytes
+
+
+def decode_quant_case(args, torch, lib, stream):
+    """gqa4_mid's decode step over a quantised cache, no rule."""
+    from paged_kv_cache_63_gb300.workloads import make_workload
+
+    w = make_workload("gqa4_mid")
+    cache, _, total, bt, ctx = quantised(w, torch, lib)
+    q, prob = torch.from_numpy(w.query).cuda(), lib.problem_of(w)
+    out = torch.empty(q.shape, device="cuda")
+    ws = torch.empty(max(lib.pa_quant_workspace_size(prob), 256), dtype=torch.uint8, device="cuda")
+    (ms,) = time_calls([lambda: lib.pa_decode_quant(prob, None, q, cache, bt, ctx, w.scale, out,
+                                                    None, ws, ws.numel(), stream=stream)],
+                       args.steps, args.warmup, torch)
+    nbytes = total * 2 * w.kv_heads * (w.head_dim + 1) + out.numel() * 6
+    return (dict(workload="gqa4_mid", kernel="pa::decode_quant_kernel, pa::join_scored_kernel"), ms,
+            "hbm", nbytes)
+
+
+def prefill_quant_case(args, torch, lib, stream):
+    """prefill_gqa4's prompts over a quantised cache, no rule."""
+    from paged_kv_cache_63_gb300.workloads import make_prefill
+
+    p = make_prefill("prefill_gqa4")
+    w = p.cache
+    cache, _, _, bt, ctx = quantised(w, torch, lib)
+    q, qs = [torch.from_numpy(x).cuda() for x in (p.query, p.query_start)]
+    out, score = torch.empty_like(q), lib.score(out="fp16")
+    (ms,) = time_calls([lambda: lib.pa_prefill_quant(
+        lib.problem_of(w), score, q, qs, p.total, p.max_query_len(), cache, bt, ctx, w.scale, out,
+        stream=stream)], args.steps, args.warmup, torch)
+    flops = 4.0 * p.causal_pairs() * w.query_heads * w.head_dim
+    return (dict(workload="prefill_gqa4", kernel="pa::prefill2_scored_kernel<128> (codes)"), ms,
+            "tensor", flops)
+
+
 RULE_CASES = {"append_rope": append_rope_case, "decode_scored": decode_scored_case,
-              "prefill_scored": prefill_scored_case}
+              "prefill_scored": prefill_scored_case, "append_quant": append_quant_case,
+              "read_quant": read_quant_case, "decode_quant": decode_quant_case,
+              "prefill_quant": prefill_quant_case}
 
 
 def run_kernel_case(args):
