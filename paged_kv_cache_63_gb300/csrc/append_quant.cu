@@ -633,7 +633,8 @@ struct ReadQuantArgs : NewRowsArgs {
 constexpr int kReadRows = 8;  // rows of a CTA: one for each of its warps to place
 
 // A CTA places eight rows, a warp each, and then all its threads stream their heads: an item is 16
-// codes and 32 bytes of fp16. Bound: HBM, a byte read for two written.
+// codes and 32 bytes of fp16. Bound: HBM, a byte read for two written: 473 MB of 32 sequences (8 heads of
+// 128) in 75.9 us, 0.93 of the copy bandwidth.
 template <int HD>
 __global__ void __launch_bounds__(kReadRows * 32)
     read_quant_kernel(const __grid_constant__ ReadQuantArgs a) {

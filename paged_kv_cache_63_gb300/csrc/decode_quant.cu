@@ -25,6 +25,8 @@
 //    the 16 bytes of a TMA copy.
 //  * Probabilities keep 22 bits (two fp16 numbers, a product each) and sums are fp32, as in
 //    decode_scored.cu.
+// 64 sequences of 1500 seen tokens, 32 heads of 128 of their own: 133.5 us, 0.89 of the copy bandwidth;
+// four contexts of 100000, 24 / 4 heads of 256: 135.3 us, 0.91.
 #include <algorithm>
 #include <atomic>
 #include <cmath>

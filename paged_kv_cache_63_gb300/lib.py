@@ -3,8 +3,9 @@
 Every function here forwards to the C entry point of the same name; all compute runs in
 the library's CUDA kernels. Tensor arguments may be torch CUDA tensors or raw device
 addresses (int). pa_append_rope, pa_decode_scored, pa_prefill_scored and the calls on a
-quantised cache check the device, layout, type and length of tensors first; an address is passed
-on as it is. There is no fallback: if the shared library is missing or fails to load, ``load()`` raises.
+quantised cache check the device, layout, type and length of tensors first; an address is
+passed on as it is. There is no fallback: if the shared library is missing or fails to load,
+``load()`` raises.
 """
 
 from __future__ import annotations
