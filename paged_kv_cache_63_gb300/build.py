@@ -18,7 +18,7 @@ LIB = os.path.join(BUILD, "libpagedattn.so")
 SOURCES = ["api.cpp", "row_maps.cpp", "launch.cu", "noalloc.cu", "append.cu", "append_rope.cu",
            "prefill.cu", "prefill_scored.cu", "prefill_scored_wide.cu", "decode_scored.cu",
            "append_quant.cu", "decode_quant.cu", "prefill_quant.cu", "prefill_quant_wide.cu",
-           "decode_hd64.cu", "decode_hd128.cu", "decode_hd256.cu"]
+           "prefill_few_quant.cu", "decode_hd64.cu", "decode_hd128.cu", "decode_hd256.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -1,4 +1,5 @@
 // prefill_quant.cu -- host entry point of multi-token attention over a quantised cache.
+#include "prefill_few_quant.h"
 #include "prefill_launch.cuh"
 
 namespace pa {
@@ -46,6 +47,9 @@ extern "C" pa_status_t pa_prefill_quant(const pa_problem_t *problem, const pa_sc
   // a masked score is an infinity times the scale, so the scale is never 0 (as in pa_prefill_scored)
   if (a.scale_log2 == 0.f) a.scale_log2 = 1e-30f;
   a.out16 = static_cast<uint16_t *>(out);
+  if (few_rows(problem, a.s, max_query_len))
+    return launch_few_quant(problem, a, query, max_query_len, cache,
+                            static_cast<cudaStream_t>(stream));
   const int parts = (a.s.cap_in != 0.f ? kRuleCap : 0) | (a.s.slopes ? kRuleSlopes : 0) |
                     (a.s.first ? kRuleFirst : 0);
   const cudaStream_t on = static_cast<cudaStream_t>(stream);
