@@ -615,7 +615,7 @@ def append_quant_case(args, torch, lib, stream):
         args.steps, args.warmup, torch)
     nbytes = total * ((2 * qh + 2 * kvh) * hd * 2 + 2 * kvh * (hd + 1)) \
         + int(w.context_lengths.max()) * hd * 4
-    return dict(workload="prefill_gqa4", kernel="pa::append_quant_rows_kernel"), ms, "hbm", nbytes
+    return dict(workload="prefill_gqa4", kernel="pa::append_quant_kernel"), ms, "hbm", nbytes
 
 
 def read_quant_case(args, torch, lib, stream):

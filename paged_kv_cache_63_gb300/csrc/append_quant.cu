@@ -10,7 +10,6 @@
 // Bound: HBM. A token reads (query_heads + 2 kv_heads) * head_dim fp16 and writes query_heads *
 // head_dim fp16 and 2 kv_heads * (head_dim + 1) bytes.
 #include <algorithm>
-#include <atomic>
 #include <cmath>
 
 #include "early_launch.cuh"
@@ -23,7 +22,6 @@ struct AppendQuantArgs : RopeArgs {
   const float *q_weight, *k_weight;  // either may be null: its rows are not normed
   float eps;
   uint8_t *k_scale, *v_scale;
-  int rows;  // of a CTA
 };
 
 // A sum of two floats: the value and what rounding it left.
@@ -285,12 +283,6 @@ __device__ __forceinline__ void query_item(uint4 &x, uint4 &y, const float *weig
   y = make_uint4(o[4], o[5], o[6], o[7]);
 }
 
-__device__ __forceinline__ void copy16_async(uint32_t dst, const void *src, bool live) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-               "r"(live ? 16u : 0u)
-               : "memory");
-}
-
 // What a thread knows of its place in a row: its item, the offsets of its two chunks in query and key
 // rows, the angles of its pairs, and what a key's error is bounded by: a turned element of a pair (x, y)
 // is off by at most (|x| + |y|) * bound, for 16 roundings of 2^-24 at the most, of products with cosines
@@ -319,6 +311,8 @@ struct Item {
     bound = steep * 0x1p-19f;
   }
 };
+
+constexpr int kThreadsPerSm = 768;  // what the kernel's registers leave room for
 
 // Key or value head n (values after all keys; dead where there is none) of the token at (page, slot):
 // its codes and its scale. `angles`: the cosines of the thread's pairs, sines rotary / 2 further.
@@ -431,11 +425,17 @@ __device__ __forceinline__ void write_kv(const AppendQuantArgs &a, const Item &i
   }
 }
 
-// Few rows: a CTA takes one, all its warps look up its place, and a thread asks for its first query and
-// its first key or value item before that: no address of them depends on the sequence that the row is
-// of.
-template <int HD, bool kInterleaved, bool kNorm>
-__global__ void __launch_bounds__(256, 3)
+// A CTA takes one row. A head row is HD / 16 items of two 16-byte chunks, paired as in append_rope_kernel;
+// a thread keeps its item index and walks query heads, then key and value heads, and asks for the next
+// item before it works on one. All warps look up the row's place, and the first query and key or value
+// item are asked for before that: no address of them depends on the sequence that the row is of. That
+// chain of offsets, length, page and angles is half of a row's time, so the rows in flight count: CTAs of
+// 64 threads, twelve a multiprocessor, unless the rows are so few that all of them are in flight as CTAs
+// of 256 (launch_append_quant_as). Rows that share a CTA, prefetched through shared memory, saved
+// instructions and cost warps: 83.6 us against 78.4 for eight prompts of 2048 tokens, 32/8 heads of 128.
+// That is 0.70 of the copy bandwidth; the instructions of norm, rotation, error bound and rounding set it.
+template <int HD, bool kInterleaved, bool kNorm, int kThreads>
+__global__ void __launch_bounds__(kThreads, kThreadsPerSm / kThreads)
     append_quant_kernel(const __grid_constant__ AppendQuantArgs a) {
   constexpr int IPR = HD / 16;
   wait_for_stream();
@@ -473,155 +473,22 @@ __global__ void __launch_bounds__(256, 3)
   const int first = (threadIdx.x & ~31) / IPR;
 #pragma unroll 1
   for (int w0 = first, h = slot0; w0 < nq; w0 += step, h += step) {
-    if (w0 != first) load_q(h, qx, qy);
-    query_item<HD, kInterleaved, kNorm>(qx, qy, a.q_weight, a.eps, it.off_x, it.off_y, it.turns,
-                                        it.cs, it.sn);
+    uint4 x = qx, y = qy;
+    load_q(h + step, qx, qy);
+    query_item<HD, kInterleaved, kNorm>(x, y, a.q_weight, a.eps, it.off_x, it.off_y, it.turns, it.cs,
+                                        it.sn);
     if (h < nq) {
       uint16_t *dst = a.q_out + (row * a.qh + h) * HD;
-      *reinterpret_cast<uint4 *>(dst + it.off_x) = qx;
-      *reinterpret_cast<uint4 *>(dst + it.off_y) = qy;
+      *reinterpret_cast<uint4 *>(dst + it.off_x) = x;
+      *reinterpret_cast<uint4 *>(dst + it.off_y) = y;
     }
   }
   const float *turn = a.table + static_cast<long long>(pos) * a.rotary + it.i * 8;
 #pragma unroll 1
   for (int w0 = first, n = slot0; w0 < nkv; w0 += step, n += step) {
-    if (w0 != first) load_kv(n, kx, ky);
-    write_kv<HD, kInterleaved, kNorm>(a, it, kx, ky, n, n < nkv, page, t & (a.ps - 1), turn);
-  }
-}
-
-constexpr int kRowsAtMost = 8;    // rows of a CTA
-constexpr int kQueriesAtOnce = 2; // query heads of a thread
-constexpr int kChunks = 2 * kQueriesAtOnce + 2;
-
-// Many rows: a CTA takes a.rows neighbouring rows of the packed batch. Its warps first look up the places of one
-// row each. A head row is HD / 16 items of two 16-byte chunks, paired as in append_rope_kernel; a
-// thread keeps its item index and walks query heads two at a time, then key and value heads. What a
-// thread needs of the next row it has copied to shared memory meanwhile, each thread for itself.
-template <int HD, bool kInterleaved, bool kNorm>
-__global__ void __launch_bounds__(256, 2)
-    append_quant_rows_kernel(const __grid_constant__ AppendQuantArgs a) {
-  constexpr int IPR = HD / 16;  // items per head row
-  // [2 rows][kChunks][threads], then the rows' table rows [a.rows][rotary]
-  extern __shared__ __align__(16) uint4 chunks[];
-  __shared__ int places[kRowsAtMost][3];
-  wait_for_stream();
-  const long long row0 = static_cast<long long>(blockIdx.x) * a.rows;
-  const int rows = static_cast<int>(min(static_cast<long long>(a.rows), a.total - row0));
-  Item it(a, threadIdx.x % IPR, kInterleaved);
-  const int i = it.i, off_x = it.off_x, off_y = it.off_y;
-  const int nq = a.q ? a.qh : 0, nkv = 2 * a.kvh;
-  const int step = blockDim.x / IPR, slot0 = threadIdx.x / IPR;
-  const int warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-
-  // plain loads of query rows: query_out may be the query buffer itself
-  auto kv_row = [&](long long row, int n) {
-    return n < a.kvh ? a.k + row * a.k_stride + n * HD
-                     : a.v + row * a.v_stride + (n - a.kvh) * HD;
-  };
-  auto q_row = [&](long long row, int h) {
-    return a.q + row * a.q_stride + static_cast<long long>(h) * HD;
-  };
-  // What the thread reads of the next row: its query items (u), its key or value item.
-  const bool kv_live = slot0 < nkv, kv_is_k = slot0 < a.kvh;
-  const uint16_t *next_q = nq > 0 ? q_row(row0, min(slot0, nq - 1)) : a.k;
-  const uint16_t *next_kv = kv_live ? kv_row(row0, slot0) : a.k;
-  const long long kv_stride = kv_is_k ? a.k_stride : a.v_stride;
-  const int kv_x = kv_is_k ? off_x : i * 16, kv_y = kv_is_k ? off_y : i * 16 + 8;
-  auto prefetch = [&](int r) {
-    const uint32_t at = smem_addr(chunks + (r & 1) * kChunks * blockDim.x + threadIdx.x);
-    const uint32_t next = blockDim.x * 16;
-#pragma unroll
-    for (int u = 0; u < kQueriesAtOnce; ++u) {
-      const bool live = slot0 + u * step < nq;
-      const uint16_t *src = live ? next_q + u * step * HD : a.k;
-      copy16_async(at + 2 * u * next, src + off_x, live);
-      copy16_async(at + (2 * u + 1) * next, src + off_y, live);
-    }
-    copy16_async(at + 2 * kQueriesAtOnce * next, next_kv + kv_x, kv_live);
-    copy16_async(at + (2 * kQueriesAtOnce + 1) * next, next_kv + kv_y, kv_live);
-    asm volatile("cp.async.commit_group;" ::: "memory");
-    next_q += a.q_stride;
-    next_kv += kv_stride;
-  };
-  prefetch(0);
-
-  check_sequences(a);
-  for (int r = warp; r < rows; r += warps) {
-    const int row = static_cast<int>(row0) + r;
-    int t = 0, page = -1, pos = 0;
-    const int b = sequence_of_row(a, row);
-    if (b >= 0 && !place_of_row(a, b, row, t, page, pos, (threadIdx.x & 31) == 0)) page = -1;
-    if ((threadIdx.x & 31) == 0) {
-      places[r][0] = t;
-      places[r][1] = page;
-      places[r][2] = pos;
-    }
-  }
-  __syncthreads();
-  float *angles = reinterpret_cast<float *>(chunks + 2 * kChunks * blockDim.x);
-  {
-    const int per_row = a.rotary >> 2;  // copies of 16 bytes
-    for (int n = threadIdx.x; n < rows * per_row; n += blockDim.x) {
-      const int r = n / per_row, c = n - r * per_row;
-      if (places[r][1] >= 0)
-        copy16_async(smem_addr(angles + r * a.rotary + c * 4),
-                     a.table + static_cast<long long>(places[r][2]) * a.rotary + c * 4, true);
-    }
-    asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
-  }
-  __syncthreads();
-
-  // a warp's lanes walk together, so that those past the last head take part in the shuffles
-  const int first = (threadIdx.x & ~31) / IPR;
-#pragma unroll 1
-  for (int r = 0; r < rows; ++r) {
-    const long long row = row0 + r;
-    const int t = places[r][0], page = places[r][1];
-    const float *turn = angles + r * a.rotary + i * 8;
-    if (it.turns) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        it.cs[e] = turn[e];
-        it.sn[e] = turn[a.rotary / 2 + e];
-      }
-    }
-    asm volatile("cp.async.wait_group 0;" ::: "memory");
-    const uint4 *mine = chunks + (r & 1) * kChunks * blockDim.x + threadIdx.x;
-    if (r + 1 < rows) prefetch(r + 1);
-    if (page < 0) continue;  // the CTA's, as places are
-    it.bounds();
-
-#pragma unroll 1
-    for (int w0 = first, h0 = slot0; w0 < nq; w0 += kQueriesAtOnce * step, h0 += kQueriesAtOnce * step) {
-#pragma unroll
-      for (int u = 0; u < kQueriesAtOnce; ++u) {
-        const int h = h0 + u * step;
-        uint4 x = mine[2 * u * blockDim.x], y = mine[(2 * u + 1) * blockDim.x];
-        if (w0 != first && h < nq) {
-          x = *reinterpret_cast<const uint4 *>(q_row(row, h) + off_x);
-          y = *reinterpret_cast<const uint4 *>(q_row(row, h) + off_y);
-        }
-        query_item<HD, kInterleaved, kNorm>(x, y, a.q_weight, a.eps, off_x, off_y, it.turns, it.cs,
-                                            it.sn);
-        if (h < nq) {
-          uint16_t *dst = a.q_out + (row * a.qh + h) * HD;
-          *reinterpret_cast<uint4 *>(dst + off_x) = x;
-          *reinterpret_cast<uint4 *>(dst + off_y) = y;
-        }
-      }
-    }
-
-    const int slot = t & (a.ps - 1);
-#pragma unroll 1
-    for (int w0 = first, n = slot0; w0 < nkv; w0 += step, n += step) {
-      uint4 x = mine[2 * kQueriesAtOnce * blockDim.x], y = mine[(2 * kQueriesAtOnce + 1) * blockDim.x];
-      if (w0 != first && n < nkv) {
-        x = __ldg(reinterpret_cast<const uint4 *>(kv_row(row, n) + (n < a.kvh ? off_x : i * 16)));
-        y = __ldg(reinterpret_cast<const uint4 *>(kv_row(row, n) + (n < a.kvh ? off_y : i * 16 + 8)));
-      }
-      write_kv<HD, kInterleaved, kNorm>(a, it, x, y, n, n < nkv, page, slot, turn);
-    }
+    const uint4 x = kx, y = ky;
+    load_kv(n + step, kx, ky);
+    write_kv<HD, kInterleaved, kNorm>(a, it, x, y, n, n < nkv, page, t & (a.ps - 1), turn);
   }
 }
 
@@ -697,33 +564,24 @@ __global__ void __launch_bounds__(kReadRows * 32)
 
 namespace {
 
-constexpr long long kManyRows = 8192;
-
 bool off_by(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) != 0; }
 
+template <int HD, bool kInterleaved, bool kNorm, int kThreads>
+cudaError_t launch_append_quant_threads(const AppendQuantArgs &a, cudaStream_t stream) {
+  constexpr int IPR = HD / 16;
+  const int heads = std::max(a.q ? a.qh : 0, 2 * a.kvh);
+  const int threads = std::min(kThreads, (heads * IPR + 31) / 32 * 32);
+  return launch_early(append_quant_kernel<HD, kInterleaved, kNorm, kThreads>,
+                      dim3(static_cast<unsigned>(a.total)), threads, 0, stream, a);
+}
+
+// 256 rows of 64/8 heads of 128: 6.7 us with CTAs of 256 threads, 7.9 of 64; 1000 rows of 32/8 heads: 13.5
+// and 9.2; 3300 rows of 24/4 heads of 256: 30.0 and 20.3.
 template <int HD, bool kInterleaved, bool kNorm>
 cudaError_t launch_append_quant_as(const AppendQuantArgs &a, cudaStream_t stream) {
-  constexpr int IPR = HD / 16;
-  const int nq = a.q ? a.qh : 0, nkv = 2 * a.kvh;
-  // What a CTA of several rows saves in instructions it pays in warps, of which its registers leave
-  // few: worth it once the rows keep all multiprocessors busy for several rounds (eight prompts of 2048
-  // tokens, 32/8 heads of 128: 85 against 125 us; 3300 rows of 24/4 heads of 256: 49 against 35).
-  if (a.total < kManyRows) {
-    const int threads = std::min(256, (std::max(nq, nkv) * IPR + 31) / 32 * 32);
-    return launch_early(append_quant_kernel<HD, kInterleaved, kNorm>,
-                        dim3(static_cast<unsigned>(a.total)), threads, 0, stream, a);
-  }
-  const int slots = std::max((nq + kQueriesAtOnce - 1) / kQueriesAtOnce, nkv);
-  const int threads = std::min(256, (slots * IPR + 31) / 32 * 32);
-  AppendQuantArgs b = a;
-  b.rows = kRowsAtMost;
-  static std::atomic<bool> set[kMaxLaunchDevices];
-  auto kern = append_quant_rows_kernel<HD, kInterleaved, kNorm>;
-  const cudaError_t e =
-      allow_smem(kern, 2 * kChunks * 256 * 16 + kRowsAtMost * HD * 4, set);
-  if (e != cudaSuccess) return e;
-  return launch_early(kern, dim3(static_cast<unsigned>((a.total + b.rows - 1) / b.rows)), threads,
-                      2 * kChunks * threads * 16 + b.rows * a.rotary * 4, stream, b);
+  return a.total <= static_cast<long long>(device_sm_count()) * (kThreadsPerSm / 256)
+             ? launch_append_quant_threads<HD, kInterleaved, kNorm, 256>(a, stream)
+             : launch_append_quant_threads<HD, kInterleaved, kNorm, 64>(a, stream);
 }
 
 template <int HD>

@@ -152,6 +152,9 @@ pa_status_t check_quant_cache(const pa_quant_cache_t *cache);
 // The current device's opt-in shared memory per block; PA_ERR_NO_DEVICE unless sm_103.
 pa_status_t current_device_smem(int *smem_optin);
 
+// SM count of the current device, looked up once; 0 on failure (decode_scored.cu).
+int device_sm_count();
+
 // One decode step: validation, plan, workspace checks, tensor maps and launches.
 pa_status_t decode_into(const pa_problem_t *p, const void *q, const void *k, const void *v,
                         const int32_t *bt, const int32_t *ctx, float scale, float *out,

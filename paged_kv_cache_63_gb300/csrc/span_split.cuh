@@ -160,9 +160,6 @@ __device__ __forceinline__ void zero_rows_out(const ScoredArgs &a, const UnitInf
   for (int i = lane * 2; i < u.nh * HD; i += 64) store_out2(a.s, a.out, base + i, 0.f, 0.f);
 }
 
-// Host: SM count of the current device, looked up once; 0 on failure (decode_scored.cu).
-int device_sm_count();
-
 // Host: the arguments of a decode call under a plan, but the rule, the rings' size and the test hook
 // (decode_scored.cu). `a` comes in zeroed but for its rule.
 pa_status_t fill_scored_args(const pa_problem_t *problem, const pa_plan_t &pl, const void *query,

@@ -177,8 +177,7 @@ def test_one_kind_of_rows_normed(norm, hd):
     (0, 64, 2, 1, 8, False), (1, 64, 14, 2, 16, True), (0, 128, 3, 3, 16, False),
     (1, 256, 2, 1, 64, False), (0, 256, 1, 1, 32, True)])
 def test_many_rows(head_major, hd, qh, kvh, ps, interleaved):
-    """Enough rows for several to a CTA, ragged, so that a CTA's rows are of several sequences, rows of
-    a padded batch among the last."""
+    """Many rows, ragged, rows of a padded batch among the last."""
     rng = np.random.default_rng(3)
     ctx = rng.integers(1, 300, 56)
     new = np.minimum(ctx, rng.integers(0, 300, 56))
