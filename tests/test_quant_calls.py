@@ -32,7 +32,7 @@ def entry_points(w):
     rope = lib.rope(hd, "half", t.from_numpy(table_of(int(w.ctx.max()), hd)).cuda())
     norm = lib.norm(1e-6, t.ones(hd, device="cuda"), t.ones(hd, device="cuda"))
     score = lib.score(softcap=5.0, out="fp16")
-    q_out, dec, pre = half(b, qh), half(b, qh), half(b, qh)
+    q_out, dec, pre, many = (half(b, qh) for _ in range(4))
     k, v = half(b, kvh), half(b, kvh)
     return {
         "append": (lambda: lib.pa_append_quant(prob, norm, rope, d["q"], *kv, qs, b, d["bt"], d["ctx"],
@@ -42,6 +42,9 @@ def entry_points(w):
                                                w.scale, dec, workspace=ws, workspace_bytes=n), [dec]),
         "prefill": (lambda: lib.pa_prefill_quant(prob, score, d["q"], qs, b, 1, d["cache"], d["bt"],
                                                  d["ctx"], w.scale, pre), [pre]),
+        # (a grid for many rows)
+        "prefill_many": (lambda: lib.pa_prefill_quant(prob, score, d["q"], qs, b, 2500, d["cache"],
+                                                      d["bt"], d["ctx"], w.scale, many), [many]),
     }
 
 
@@ -94,8 +97,8 @@ d, dr, prob = w.to_device(), device_rule(rule, "fp32"), w.prob()
 half = device_rule(rule, "fp16")
 qs = t.arange(4, dtype=t.int32, device="cuda")
 work = []
-for plan in [dict(stages=s, warps_per_cta=n) for s in (1, 2) for n in (0, 1, 4)] + ["prefill"] * 2:
-    opts = None if plan == "prefill" else lib.options(schedule="balanced", **plan)
+for plan in [dict(stages=s, warps_per_cta=n) for s in (1, 2) for n in (0, 1, 4)] + [None] * 4:
+    opts = None if plan is None else lib.options(schedule="balanced", **plan)
     n = lib.pa_quant_workspace_size(prob, opts)
     out = t.full((3, 8, hd), float("nan"), device="cuda")
     work.append((opts, t.zeros(n, dtype=t.uint8, device="cuda"), n, t.cuda.Stream(),
@@ -109,8 +112,10 @@ def call(opts, ws, n, stream, out):
     try:
         for _ in range(3):
             if opts is None:
-                lib.pa_prefill_quant(prob, half, d["q"], qs, 3, 1, d["cache"], d["bt"], d["ctx"],
-                                     w.scale, out, stream=stream.cuda_stream)
+                # the kernel for few rows, and those for many
+                for most in (1, 2500):
+                    lib.pa_prefill_quant(prob, half, d["q"], qs, 3, most, d["cache"], d["bt"],
+                                         d["ctx"], w.scale, out, stream=stream.cuda_stream)
             else:
                 lib.pa_decode_quant(prob, dr, d["q"], d["cache"], d["bt"], d["ctx"], w.scale, out,
                                     opts, ws, n, stream=stream.cuda_stream)
