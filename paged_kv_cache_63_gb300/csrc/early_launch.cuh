@@ -6,6 +6,7 @@
 #include <cuda_runtime.h>
 
 #include <atomic>
+#include <utility>
 
 namespace pa {
 
@@ -34,22 +35,33 @@ cudaError_t allow_smem(Kernel kern, int smem, std::atomic<bool> (&set)[kMaxLaunc
   return cudaSuccess;
 }
 
+// `cluster` neighbouring blocks along x form a cluster.
 template <typename... Params, typename... Args>
-cudaError_t launch_early(void (*kernel)(Params...), dim3 grid, int threads, int smem,
-                         cudaStream_t stream, Args &&...args) {
+cudaError_t launch_early_in_clusters(unsigned cluster, void (*kernel)(Params...), dim3 grid,
+                                     int threads, int smem, cudaStream_t stream, Args &&...args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
   cfg.dynamicSmemBytes = static_cast<size_t>(smem);
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
   if (e != cudaSuccess) cudaGetLastError();  // reported here, not by a later call
   return e;
+}
+
+template <typename... Params, typename... Args>
+cudaError_t launch_early(void (*kernel)(Params...), dim3 grid, int threads, int smem,
+                         cudaStream_t stream, Args &&...args) {
+  return launch_early_in_clusters(1, kernel, grid, threads, smem, stream,
+                                  std::forward<Args>(args)...);
 }
 
 }  // namespace pa

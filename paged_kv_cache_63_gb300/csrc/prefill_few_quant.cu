@@ -6,9 +6,11 @@
 // heads a hundred rows are padding, and 8 sequences with 8 K/V heads are work for 64 of 152
 // multiprocessors. Here a CTA takes eight rows of a sequence and K/V head, its twelve warps a twelfth of
 // the keys each, by the decode step's walk (code_walk.cuh) with a mask for each row, and their states are
-// joined in shared memory. K and V are read once for each eight rows, from L2 after the first. Bound: the
-// walk's chain of loads and products, about 1 us a tile and warp. Eight sequences of up to 4096 tokens, 2
-// to 7 of them new, 32/8 heads of 128: 22.6 us against 42.4.
+// joined in shared memory; where such CTAs leave multiprocessors idle, up to eight of them form a cluster
+// that shares the keys and joins through its shared memories. K and V are read once for each eight rows,
+// from L2 after the first. Bound: the walk's chain of loads and products, about 1 us a tile and warp. Eight
+// sequences of up to 4096 tokens, 2 to 7 of them new, 32/8 heads of 128: 22.0 us against 42.4; one of
+// 100000, one new token: 68 against 1200.
 #include <algorithm>
 #include <atomic>
 #include <climits>
@@ -22,7 +24,23 @@ namespace pa {
 struct FewArgs : QuantDecodeArgs {
   const int32_t *qs;
   long long total;
+  int parts;  // CTAs of a cluster, which share the keys of its eight rows
 };
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+
+// A float of shared memory of the cluster's block `rank`, at the place that `p` has in this block's.
+__device__ __forceinline__ float load_of_block(const float *p, int rank) {
+  float x;
+  asm volatile("{\n\t.reg .u32 a;\n\tmapa.shared::cluster.u32 a, %1, %2;\n\t"
+               "ld.shared::cluster.f32 %0, [a];\n\t}"
+               : "=f"(x)
+               : "r"(smem_addr(p)), "r"(rank)
+               : "memory");
+  return x;
+}
 
 // What the lane's two rows (2 (l % 4) and the next) see; lo_max and end_min are over all eight rows.
 struct FewRows {
@@ -48,8 +66,10 @@ __global__ void __launch_bounds__(kQuantWarps * 32, 1)
   extern __shared__ uint8_t dsm[];
   __shared__ __align__(8) uint64_t bars[kQuantWarps * S];
   __shared__ float part[kQuantWarps][kMaxHeads][2];
+  __shared__ float joined[kMaxHeads * HD], joined_ml[kMaxHeads][2];  // of a cluster's block
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int kv = blockIdx.x, b = blockIdx.z;
+  const int kv = blockIdx.x / fa.parts, b = blockIdx.z;
+  const int rank = blockIdx.x - kv * fa.parts;  // in the cluster
   const uint32_t base = (smem_addr(dsm) + kSmemAlign - 1) & ~static_cast<uint32_t>(kSmemAlign - 1);
   const uint32_t ring = base + warp * S * G::kStageBytes;
   const uint32_t scales = base + kQuantWarps * S * G::kStageBytes + warp * S * G::kScaleBytes;
@@ -119,13 +139,14 @@ __global__ void __launch_bounds__(kQuantWarps * 32, 1)
   rs.end_min = __reduce_min_sync(0xffffffffu, rs.end_min);
 
   // ---- the warp's tiles
-  const int tiles = span_tiles(c.sp, T);
-  const int from = static_cast<int>(static_cast<long long>(tiles) * warp / kQuantWarps);
+  const long long tiles = span_tiles(c.sp, T);
+  const int walks = fa.parts * kQuantWarps, walk = rank * kQuantWarps + warp;
+  const int from = static_cast<int>(tiles * walk / walks);
   c.b = b;
   c.us = 0;
   c.ug0 = 0;
   c.tok = span_start(c.sp, T) + from * T;
-  c.left = static_cast<int>(static_cast<long long>(tiles) * (warp + 1) / kQuantWarps) - from;
+  c.left = static_cast<int>(tiles * (walk + 1) / walks) - from;
   SpanCursor ic = c;
   BtWindow win;
   win.b = -1;
@@ -194,7 +215,14 @@ __global__ void __launch_bounds__(kQuantWarps * 32, 1)
   }
   __syncthreads();
   const int live = min(kMaxHeads, rows - row0);
-  for (int at = threadIdx.x; at < live * HD; at += kQuantWarps * 32) {
+  constexpr int kThreads = kQuantWarps * 32;
+  auto store = [&](int at, float o, float l) {
+    const int r = row0 + at / HD;
+    store_out1(fa.s, fa.out,
+               (static_cast<long long>(q0 + r / a.g) * a.qh + kv * a.g + r % a.g) * HD + at % HD,
+               l > 0.f ? o / l : 0.f);
+  };
+  for (int at = threadIdx.x; at < live * HD; at += kThreads) {
     const int i = at / HD, element = at % HD;
     float m = -INFINITY;
 #pragma unroll
@@ -207,11 +235,30 @@ __global__ void __launch_bounds__(kQuantWarps * 32, 1)
       l = fmaf(part[w][i][1], f, l);
       o = fmaf(states[w * kState + i * kRow + element], f, o);
     }
-    const int r = row0 + i;
-    store_out1(fa.s, fa.out,
-               (static_cast<long long>(q0 + r / a.g) * a.qh + kv * a.g + r % a.g) * HD + element,
-               l > 0.f ? o / l : 0.f);
+    if (fa.parts == 1) {
+      store(at, o, l);
+    } else {
+      joined[at] = o;
+      if (element == 0) {
+        joined_ml[i][0] = m;
+        joined_ml[i][1] = l;
+      }
+    }
   }
+  if (fa.parts == 1) return;
+  cluster_sync();  // every block of the cluster gets here: they have the same rows
+  for (int at = threadIdx.x + rank * kThreads; at < live * HD; at += fa.parts * kThreads) {
+    const float *ml = joined_ml[at / HD];
+    float m = -INFINITY, l = 0.f, o = 0.f;
+    for (int p = 0; p < fa.parts; ++p) m = fmaxf(m, load_of_block(ml, p));
+    for (int p = 0; p < fa.parts; ++p) {
+      const float mp = load_of_block(ml, p), f = mp == -INFINITY ? 0.f : fast_exp2(mp - m);
+      l = fmaf(load_of_block(ml + 1, p), f, l);
+      o = fmaf(load_of_block(joined + at, p), f, o);
+    }
+    store(at, o, l);
+  }
+  cluster_sync();  // no block leaves while others read its memory
 }
 
 namespace {
@@ -224,7 +271,8 @@ cudaError_t launch_few(const FewArgs &a, const CUtensorMap &tk, const CUtensorMa
   const int smem = quant_smem(HD, kQuantWarps, kQuantStages);
   const cudaError_t e = allow_smem(kern, smem, set);
   if (e != cudaSuccess) return e;
-  return launch_early(kern, grid, kQuantWarps * 32, smem, stream, a, tk, tv);
+  return launch_early_in_clusters(static_cast<unsigned>(a.parts), kern, grid, kQuantWarps * 32, smem,
+                                  stream, a, tk, tv);
 }
 
 }  // namespace
@@ -283,7 +331,18 @@ pa_status_t launch_few_quant(const pa_problem_t *problem, const PrefillQuantArgs
   st = encode_code_map(&tv, cache->value, problem, rows, blocks);
   if (st != PA_OK) return st;
   const long long rows_most = static_cast<long long>(max_query_len) * p.g;
-  const dim3 grid(p.kvh, static_cast<unsigned>((rows_most + kMaxHeads - 1) / kMaxHeads), p.batch);
+  const long long groups = (rows_most + kMaxHeads - 1) / kMaxHeads;
+  const long long ctas = groups * p.kvh * p.batch;
+  // Multiprocessors left idle share the keys, where the tables hold 32 tiles and more: one sequence of
+  // 4000 tokens, 32/8 heads of 128, 1, 2, 4, 8 blocks to a cluster: 23.4, 16.1, 10.9, 9.1 us; of 1000: 8.8,
+  // 8.6, 7.0, 6.9; of 300 (not shared) 5.5, 7.1, 6.9, 6.9. Clusters of 8 only on half of the
+  // multiprocessors: 16 of them do not run at once, and two sequences took 22 against 17 us at head_dim 256.
+  const int sms = device_sm_count();
+  const long long most = static_cast<long long>(p.maxp) << p.ps_shift;
+  a.parts = 1;
+  if (most >= 32 * quant_tile(problem->head_dim))
+    while (a.parts < 8 && (a.parts < 4 ? 2 : 4) * a.parts * ctas <= sms) a.parts *= 2;
+  const dim3 grid(static_cast<unsigned>(p.kvh * a.parts), static_cast<unsigned>(groups), p.batch);
   cudaError_t e;
   switch (hd) {
     case 64: e = launch_few<64, 64>(a, tk, tv, grid, stream); break;

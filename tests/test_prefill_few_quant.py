@@ -79,6 +79,60 @@ def test_more_tokens_of_one_sequence(shape):
 
 
 @gpu
+@pytest.mark.parametrize("new", [1, 9, 30, 70, 150])
+@pytest.mark.parametrize("shape", ["hd64_g1", "hd128_g3", "hd128_g32", "hd256_g6", "hd256_g1"])
+def test_keys_shared_by_a_cluster(shape, new):
+    """One long context, so that the blocks of a cluster (two to eight of them, fewer with more rows)
+    share its keys; alone, and beside a short one, for which most of them have none."""
+    for ctx in ([2500], [2300, 5]):
+        n = [min(new, x) for x in ctx]
+        w = QuantCached(ctx, n, q_scale=3.0, seed=2, head_major=new % 2, pad=2, **SHAPES[shape])
+        if not few(w, Rule(), max(n)):
+            continue
+        check(w, Rule())
+        check(w, Rule(window=700, softcap=9.0, slopes=slopes_of(w.query_heads)))
+        for b in range(w.batch):
+            w.forget(b, max(0, int(w.ctx[b] - w.new[b]) - 64 + 1))
+        got, flags = gpu_prefill(w, Rule(window=64))
+        assert flags == 0
+        # (the formula does not read what the window hides)
+        assert_within(got, *formula(w, Rule(window=64)), True)
+
+
+@gpu
+@pytest.mark.parametrize("shape", ["hd64_g1", "hd128_g3", "hd256_g1"])
+def test_clusters_replayed_expired_and_at_once(shape):
+    t = torch()
+    w = QuantCached([3000], [4], seed=6, **SHAPES[shape])
+    want = formula(w, Rule())
+    d, dr = w.to_device(), device_rule(Rule(), "fp16")
+    outs = [t.zeros(w.rows, w.query_heads, w.head_dim, device="cuda", dtype=t.float16)
+            for _ in range(3)]
+    streams = [t.cuda.Stream() for _ in outs]
+    t.cuda.synchronize()
+    for _ in range(5):
+        for o, s in zip(outs, streams):
+            lib.pa_prefill_quant(w.prob(), dr, d["q"], d["qs"], w.rows, 4, d["cache"], d["bt"], d["ctx"],
+                                 w.scale, o, stream=s)
+    t.cuda.synchronize()
+    first = outs[0].cpu().numpy()
+    assert_within(first, *want, True)
+    assert all(np.array_equal(o.cpu().numpy(), first) for o in outs)
+    _, flags = gpu_prefill(w, Rule(), lib.options(test_flags=lib.PA_TEST_EXPIRE_WAITS))
+    assert flags == lib.PA_DEVERR_TIMEOUT
+    g = t.cuda.CUDAGraph()
+    with t.cuda.graph(g):
+        lib.pa_prefill_quant(w.prob(), dr, d["q"], d["qs"], w.rows, 4, d["cache"], d["bt"], d["ctx"],
+                             w.scale, outs[1])
+    for _ in range(3):
+        outs[1].zero_()
+        g.replay()
+        t.cuda.synchronize()
+        assert np.array_equal(outs[1].cpu().numpy(), first)
+    assert lib.pa_get_device_error() == 0
+
+
+@gpu
 @pytest.mark.parametrize("shape", ["hd64_g1", "hd128_g4"])
 def test_many_sequences_of_few_rows(shape):
     rng = np.random.default_rng(6)
