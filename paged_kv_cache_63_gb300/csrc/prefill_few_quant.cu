@@ -277,13 +277,13 @@ cudaError_t launch_few(const FewArgs &a, const CUtensorMap &tk, const CUtensorMa
 
 }  // namespace
 
-// A CTA here takes about half the time of a work item of 128 rows there, so this kernel is taken while its
-// CTAs are at most twice the larger of the other's items and the multiprocessors. Measured here | there, us,
-// on contexts of 4000, 32/8 heads of 128: one sequence, 1 to 32 new tokens 24 | 54 to 59, 64 of them 46 | 70;
-// eight sequences, 8 tokens 46 | 58, 16 (past the rule) 90 | 58; up to 600 tokens of 64 sequences, 4 new 44 | 47,
-// 8 (past it) 80 | 47; head_dim 256, 24/4 heads, two sequences, 42 new 88 | 91. On contexts of 100 the two
-// are within 3 us. First tokens may leave tokens that no row sees between others, which only the other
-// kernels clear.
+// A CTA here takes about half the time of a work item of 128 rows there, so this kernel is taken while
+// its CTAs are at most twice the larger of the other's items and the multiprocessors. Measured here |
+// there (no clusters), us, on contexts of 4000, 32/8 heads of 128: one sequence, 1 to 32 new tokens 24 |
+// 54 to 59, 64 of them 46 | 70; eight sequences, 8 tokens 46 | 58, 16 (past the rule) 90 | 58; 64
+// sequences of up to 600 tokens, 4 new 44 | 47, 8 (past it) 80 | 47; head_dim 256, 24/4 heads, two
+// sequences, 42 new 88 | 91. On contexts of 100 the two are within 3 us. First tokens may leave tokens
+// that no row sees between others, which only the other kernels clear.
 bool few_rows(const pa_problem_t *p, const ScoreArgs &s, int max_query_len) {
   if (s.first) return false;
   const long long rows = static_cast<long long>(max_query_len) * (p->query_heads / p->kv_heads);
@@ -334,9 +334,9 @@ pa_status_t launch_few_quant(const pa_problem_t *problem, const PrefillQuantArgs
   const long long groups = (rows_most + kMaxHeads - 1) / kMaxHeads;
   const long long ctas = groups * p.kvh * p.batch;
   // Multiprocessors left idle share the keys, where the tables hold 32 tiles and more: one sequence of
-  // 4000 tokens, 32/8 heads of 128, 1, 2, 4, 8 blocks to a cluster: 23.4, 16.1, 10.9, 9.1 us; of 1000: 8.8,
-  // 8.6, 7.0, 6.9; of 300 (not shared) 5.5, 7.1, 6.9, 6.9. Clusters of 8 only on half of the
-  // multiprocessors: 16 of them do not run at once, and two sequences took 22 against 17 us at head_dim 256.
+  // 4000 tokens, 32/8 heads of 128, 1, 2, 4, 8 blocks to a cluster: 23.4, 16.1, 10.9, 9.1 us; of 1000:
+  // 8.8, 8.6, 7.0, 6.9; of 300 (not shared) 5.5, 7.1, 6.9, 6.9. Clusters of 8 only on half of the
+  // multiprocessors: 16 of them do not run at once (head_dim 256, four sequences of 4000: 22 against 17).
   const int sms = device_sm_count();
   const long long most = static_cast<long long>(p.maxp) << p.ps_shift;
   a.parts = 1;
