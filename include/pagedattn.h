@@ -528,7 +528,9 @@ pa_status_t pa_decode_quant(const pa_problem_t *problem, const pa_score_t *score
 /* Attention of several new tokens per sequence over a quantised cache: pa_prefill_scored's operation
  * ("[TIL] Optimizing paged attention", section "Flash Attention" over the paged cache), arguments,
  * rule (host struct, not NULL; out_type PA_OUT_FP16) and checks on the numbers that the cache stands
- * for. The new tokens' keys and values are in the cache (pa_append_quant). */
+ * for. The new tokens' keys and values are in the cache (pa_append_quant). A call with few rows (drafted
+ * tokens, say) runs several times faster than one with many; max_query_len tells, so it should be near
+ * the largest n_b. */
 pa_status_t pa_prefill_quant(const pa_problem_t *problem, const pa_score_t *score,
                              const void *query, const int32_t *query_start, int64_t total_tokens,
                              int32_t max_query_len, const pa_quant_cache_t *cache,
