@@ -177,6 +177,64 @@ __device__ __forceinline__ uint32_t transposed(uint32_t x) {
   return r;
 }
 
+// A tile's weights carry its values' scales, relative to the smallest that is seen, where these lie
+// within 2^kScaleSpan: probabilities stay within 2^(kLift + kCodeSlack), weights within 2^15, and a
+// weight keeps all bits of its probability. In other tiles the codes take their scales as they become
+// operands, at four products of fp16 pairs for two of the tensor cores. 64 sequences of 1500 seen
+// tokens, 32 heads of 128 of their own, cap: 134 us, 143 with the codes scaled in every tile; 32
+// sequences of up to 4096, 32/8 heads: 32.6 and 34.3. (All weights relative to the tile's largest scale:
+// 133 and 31.6, but they lost a bit for each power of two that they lay below it.)
+constexpr uint32_t kScaleSpan = 3;
+constexpr float kCodeSlack = 8.f - kScaleSpan;
+
+// A tile's outputs, from the weights of its tokens. kScaled: the codes take their scales here, in a
+// product that fp16 holds exactly; else the weights have them, relative to out_scale.
+template <int HD, int T, bool kScaled>
+__device__ __forceinline__ void code_values(CodeState<HD> &st, const CodeLane<HD, T> &ln,
+                                            uint32_t stage, uint32_t scales,
+                                            const uint32_t (&hi)[T / 16][2],
+                                            const uint32_t (&lo)[T / 16][2], float out_scale) {
+  using G = CodeGeom<HD, T>;
+  constexpr int NG = T / 16, kQuarters = HD < 128 ? 2 : 4;
+  uint32_t vs[NG][2];  // scales of the four tokens whose weights the lane has
+  if constexpr (kScaled) {
+    const int c = 2 * (threadIdx.x & 3);
+    unrolled<NG>([&](auto g) {
+      constexpr int gi = decltype(g)::value;
+      const uint32_t b0 = lds16_at<T + gi * 16>(scales + c);
+      const uint32_t b1 = lds16_at<T + gi * 16>(scales + 8 + ((c + 4) & 7));
+      vs[gi][0] = half2_of_scales(b0 & 255, b0 >> 8);
+      vs[gi][1] = half2_of_scales(b1 & 255, b1 >> 8);
+    });
+  }
+  unrolled<HD / 32>([&](auto db) {
+    constexpr int D = decltype(db)::value;
+    float d[2][4];  // 16 elements each
+    unrolled<NG>([&](auto g) {
+      constexpr int gi = decltype(g)::value;
+      uint32_t w[4];
+      ldsm_bytes_trans<(D / kQuarters) * (T * 128) + gi * 16 * G::kBlock>(
+          stage + ln.v[D % kQuarters], w);
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+        uint32_t v[4] = {half2_of_low(w[2 * n]), half2_of_low(w[2 * n + 1]),
+                         half2_of_high(w[2 * n]), half2_of_high(w[2 * n + 1])};
+        if constexpr (kScaled) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[i] = mul_half2(v[i], vs[gi][i >> 1]);
+        }
+        mma_halves(d[n], v, hi[gi][0], hi[gi][1], gi == 0);
+        mma_halves(d[n], v, lo[gi][0], lo[gi][1], false);
+      }
+    });
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        st.o[2 * D + n][i] = fmaf(d[n][i], out_scale, st.o[2 * D + n][i]);
+  });
+}
+
 // One tile: scores, rule, weights, outputs. c.sp is what some head sees; `rows` knows of each of the
 // lane's two heads what it sees and where its query is.
 template <int HD, int T, class Rows>
@@ -191,6 +249,27 @@ __device__ __forceinline__ void code_tile(CodeState<HD> &st, const CodeLane<HD, 
   const int row[2] = {lane >> 2, 8 + (((lane >> 2) + 4) & 7)};
   const int tok0 = c.tok;
   const uint32_t sa = scales + row[0], sb = scales + row[1];
+
+  // the smallest and the largest scale of the values that are seen
+  uint32_t least, most;
+  {
+    const int t = lane & (T > 32 ? 31 : T - 1);
+    least = most = lds8_at<T>(scales + t);
+    if (tok0 + t < c.sp.lo || tok0 + t >= c.sp.end) {
+      least = 255;
+      most = 0;
+    }
+    if constexpr (T > 32) {
+      const uint32_t v = lds8_at<T + 32>(scales + t);
+      if (tok0 + t + 32 >= c.sp.lo && tok0 + t + 32 < c.sp.end) {
+        least = min(least, v);
+        most = max(most, v);
+      }
+    }
+    least = __reduce_min_sync(0xffffffffu, least);
+    most = __reduce_max_sync(0xffffffffu, most);
+  }
+  const bool apart = most > least + kScaleSpan;
 
   // x[g][i][j]: token 16 g + row[i], head 2 (lane % 4) + j, in two chains (even and odd steps)
   float x[NG][2][2];
@@ -250,8 +329,8 @@ __device__ __forceinline__ void code_tile(CodeState<HD> &st, const CodeLane<HD, 
   for (int o = 4; o < 32; o <<= 1)
 #pragma unroll
     for (int j = 0; j < 2; ++j) top[j] = fmaxf(top[j], __shfl_xor_sync(0xffffffffu, top[j], o));
-  if (__any_sync(0xffffffffu, top[0] > st.m[0] + (kLift + kRescaleSlack) ||
-                                  top[1] > st.m[1] + (kLift + kRescaleSlack))) {
+  if (__any_sync(0xffffffffu, top[0] > st.m[0] + (kLift + kCodeSlack) ||
+                                  top[1] > st.m[1] + (kLift + kCodeSlack))) {
     float alpha[2];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
@@ -269,31 +348,30 @@ __device__ __forceinline__ void code_tile(CodeState<HD> &st, const CodeLane<HD, 
 #pragma unroll
   for (int j = 0; j < 2; ++j) m[j] = st.m[j] == -INFINITY ? 0.f : st.m[j];
 
-  // the values' scales, and the tile's largest of a value that is seen
   uint32_t vbyte[NG][2];
   unrolled<NG>([&](auto g) {
     constexpr int gi = decltype(g)::value;
     vbyte[gi][0] = lds8_at<T + gi * 16>(sa);
     vbyte[gi][1] = lds8_at<T + gi * 16>(sb);
   });
-  if (partial) {
+  auto each_byte = [&](auto f) {
 #pragma unroll
     for (int g = 0; g < NG; ++g)
 #pragma unroll
-      for (int i = 0; i < 2; ++i) vbyte[g][i] = seen(g, i) ? vbyte[g][i] : kSmallestByte;
+      for (int i = 0; i < 2; ++i) f(vbyte[g][i], g, i);
+  };
+  // (a token that is not seen gets a finite factor, which its probability of 0 meets)
+  if (partial) each_byte([&](uint32_t &v, int g, int i) { v = seen(g, i) ? v : least; });
+  if (apart) {
+    each_byte([&](uint32_t &v, int, int) { v = 127u; });
+    least = 127u;
   }
-  uint32_t most = 0;
-#pragma unroll
-  for (int g = 0; g < NG; ++g) most = max(most, max(vbyte[g][0], vbyte[g][1]));
-  most = min(__reduce_max_sync(0xffffffffu, most), 254u);
-  const float out_scale = __uint_as_float(most << 23);
-  // 2^(b - most) as float bits: (b - most + 127) << 23. Bytes of written rows lie within 23 of each
-  // other, and a token that is not seen has the smallest, so that its probability of 0 meets a finite
-  // number.
-  const uint32_t bias = (127u - most) << 23;
+  const float out_scale = __uint_as_float(least << 23);
+  // 2^(b - least) as float bits: (b - least + 127) << 23
+  const uint32_t bias = (127u - least) << 23;
 
-  // Weights relative to the tile's scale: at most the probability, so they hold as fp16; the row sum
-  // takes the probability.
+  // Weights relative to the tile's scale: from the probability to 2^kScaleSpan of it, so they hold as
+  // fp16 and keep all its bits; the row sum takes the probability.
   uint32_t hi[NG][2], lo[NG][2];
 #pragma unroll
   for (int g = 0; g < NG; ++g)
@@ -318,28 +396,10 @@ __device__ __forceinline__ void code_tile(CodeState<HD> &st, const CodeLane<HD, 
     if (c.sp.end - tok0 < T) zero_code_rows<HD, T>(stv, c.sp.end - tok0, T);
     __syncwarp();
   }
-  unrolled<HD / 32>([&](auto db) {
-    constexpr int D = decltype(db)::value;
-    float d[2][4];  // 16 elements each
-    unrolled<NG>([&](auto g) {
-      constexpr int gi = decltype(g)::value;
-      uint32_t w[4];
-      ldsm_bytes_trans<(D / kQuarters) * (T * 128) + gi * 16 * G::kBlock>(
-          stage + ln.v[D % kQuarters], w);
-#pragma unroll
-      for (int n = 0; n < 2; ++n) {
-        const uint32_t v[4] = {half2_of_low(w[2 * n]), half2_of_low(w[2 * n + 1]),
-                               half2_of_high(w[2 * n]), half2_of_high(w[2 * n + 1])};
-        mma_halves(d[n], v, hi[gi][0], hi[gi][1], gi == 0);
-        mma_halves(d[n], v, lo[gi][0], lo[gi][1], false);
-      }
-    });
-#pragma unroll
-    for (int n = 0; n < 2; ++n)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        st.o[2 * D + n][i] = fmaf(d[n][i], out_scale, st.o[2 * D + n][i]);
-  });
+  if (apart)
+    code_values<HD, T, true>(st, ln, stage, scales, hi, lo, out_scale);
+  else
+    code_values<HD, T, false>(st, ln, stage, scales, hi, lo, out_scale);
 }
 
 // A decode step's heads: all of one query, which sees [lo, end) from its last token.

@@ -20,13 +20,13 @@
 //    numbers, took 168 us for 64 sequences of 1500 seen tokens with 32 heads of their own: the
 //    compiler converts both operands for each product.)
 //  * A key's scale multiplies its score in fp32; a value's scale multiplies its probability, relative
-//    to the tile's largest, whose own power of two multiplies the tile's output. Scales come by
-//    8-byte asynchronous copies that arrive on the tile's barrier: a page may hold fewer of them than
-//    the 16 bytes of a TMA copy.
+//    to the tile's smallest, whose own power of two multiplies the tile's output, or its codes where a
+//    tile's scales lie far apart (code_walk.cuh, kScaleSpan). Scales come by 8-byte asynchronous copies
+//    that arrive on the tile's barrier: a page may hold fewer of them than the 16 bytes of a TMA copy.
 //  * Probabilities keep 22 bits (two fp16 numbers, a product each) and sums are fp32, as in
 //    decode_scored.cu.
-// 64 sequences of 1500 seen tokens, 32 heads of 128 of their own: 133.5 us, 0.89 of the copy bandwidth;
-// four contexts of 100000, 24 / 4 heads of 256: 135.3 us, 0.91.
+// 64 sequences of 1500 seen tokens, 32 heads of 128 of their own: 134.2 us, 0.88 of the copy bandwidth;
+// four contexts of 100000, 24 / 4 heads of 256: 137 us, 0.90.
 #include <algorithm>
 #include <atomic>
 #include <cmath>

@@ -15,7 +15,6 @@ namespace pa {
 
 constexpr int kScaleBias = 127;  // a scale's byte is e + 127
 constexpr int kMinExp = -15, kMaxExp = 8;
-constexpr uint32_t kSmallestByte = kScaleBias + kMinExp;
 
 // Place of the scale of (page, K/V head, slot): [page][kv_head][slot] whatever the codes' layout, so
 // that a head's scales of a page lie side by side.
