@@ -5,8 +5,9 @@
 // Mathematics: a query or key row x becomes x / sqrt(mean(x^2) + eps) * w, its pairs (x, y) then
 // (x c - y s, x s + y c); a query is rounded once to fp16, a key or value row to the codes of
 // quant.cuh, each the nearest to the exact value. Everything is computed in fp32 with a bound of the
-// error; where that leaves a key's code or its row's scale open (one key element in some 2^14), the
-// warp computes its keys again in pairs of fp32 (a value and its error, 2^-44 or so).
+// error; where that leaves a key's code or its row's scale open, the warp computes its keys again in
+// pairs of fp32 (a value and its error, 2^-44 or so). Of normal keys one normed or turned element in
+// 2^11.5 is left open, so 15 warps of a hundred compute twice; keys that are neither are exact.
 // Bound: HBM. A token reads (query_heads + 2 kv_heads) * head_dim fp16 and writes query_heads *
 // head_dim fp16 and 2 kv_heads * (head_dim + 1) bytes.
 #include <algorithm>
@@ -199,8 +200,8 @@ __device__ __forceinline__ Pair inverse_rms(const float (&v)[16], float eps) {
 }
 
 // A lane's 16 elements (x, y) of key rows, normed and turned in pairs of fp32, each rounded to odd:
-// rounding them again to codes gives the codes nearest to the exact values; elements of value rows stay
-// as they are. Gives the codes and the row's exponent. A call of its own: what it needs of registers
+// rounding them again to codes gives the codes nearest to the exact values; elements of value rows, and
+// of keys that are neither normed nor turned here, stay as they are. Gives the codes and the row's exponent. A call of its own: what it needs of registers
 // would halve the warps of the kernel, which takes this way for few rows. Warp-collective.
 template <int HD, bool kInterleaved, bool kNorm>
 __device__ __noinline__ int exact_codes(uint4 x, uint4 y, const float *weight, float eps, bool is_k,
@@ -210,9 +211,9 @@ __device__ __noinline__ int exact_codes(uint4 x, uint4 y, const float *weight, f
   floats16(x, y, v);
   Pair norm = {1.f, 0.f};
   if constexpr (kNorm) norm = inverse_rms<HD>(v, eps);
-  if (is_k) {
+  const bool normed = kNorm && weight;
+  if (is_k && (normed || angles)) {
     float w[16];
-    const bool normed = kNorm && weight;
     if (normed) weights16(weight, off_x, off_y, w);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
@@ -284,9 +285,9 @@ __device__ __forceinline__ void query_item(uint4 &x, uint4 &y, const float *weig
 }
 
 // What a thread knows of its place in a row: its item, the offsets of its two chunks in query and key
-// rows, the angles of its pairs, and what a key's error is bounded by: a turned element of a pair (x, y)
-// is off by at most (|x| + |y|) * bound, for 16 roundings of 2^-24 at the most, of products with cosines
-// and sines of up to bound / 2^-19.
+// rows, the angles of its pairs, and what a key's error is bounded by: an element of a pair (x, y) is off
+// by at most (|x| + |y|) * bound / 2, for 16 roundings of 2^-24 at the most, of products with cosines and
+// sines of up to bound / 2^-19. (Elements that are neither normed nor turned have no error.)
 struct Item {
   int i, off_x, off_y;
   bool turns, apart;
@@ -324,8 +325,10 @@ __device__ __forceinline__ void write_kv(const AppendQuantArgs &a, const Item &i
   constexpr int IPR = HD / 16;
   const int i = it.i, off_x = it.off_x, off_y = it.off_y;
   const bool turns = it.turns, apart = it.apart, is_k = n < a.kvh;
-  const float bound = it.bound;
   const bool normed = kNorm && is_k && a.k_weight;
+  // fp16 numbers as they came lie between two codes (one in 128) or do not, but are not open: left so,
+  // they sent 95 of a hundred warps the careful way, a quarter of heads of 256 turned, none normed
+  const float bound = turns || normed ? it.bound : 0.f;
   float v[16], err[8];  // values; their pairs' error bounds
   floats16(kx, ky, v);
   float far = 0.f, top;
@@ -347,7 +350,7 @@ __device__ __forceinline__ void write_kv(const AppendQuantArgs &a, const Item &i
         err[k] = fabsf(v[first_of_pair<kInterleaved>(k)]) + fabsf(v[second_of_pair<kInterleaved>(k)]);
         far = fmaxf(far, err[k]);
       }
-      turn16<kInterleaved>(v, it.cs, it.sn);
+      if (turns) turn16<kInterleaved>(v, it.cs, it.sn);
     }
     top = top16(v);
 #pragma unroll
