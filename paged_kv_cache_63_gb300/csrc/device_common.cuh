@@ -143,13 +143,6 @@ __device__ __forceinline__ void ldsm_x4_at(uint32_t addr, uint32_t (&r)[4]) {
                : "r"(addr), "n"(kOff));
 }
 
-template <int kOff>
-__device__ __forceinline__ void ldsm_x4_trans_at(uint32_t addr, uint32_t (&r)[4]) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4+%5];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr), "n"(kOff));
-}
-
 // f(0), f(1), ... f(N - 1) with the index as a constant (decltype(i)::value).
 template <int kI>
 struct Const {
