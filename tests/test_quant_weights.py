@@ -7,7 +7,7 @@ import pytest
 
 from tests.gpu_util import torch
 from tests.quant_reference import QuantCached, quantise
-from tests.scored_reference import Rule, assert_within, attend, seen
+from tests.scored_reference import Rule, assert_within, attend, seen, slopes_of
 from tests.test_decode_quant import SHAPES, gpu_decode, redo
 from tests.test_prefill_quant import few, gpu_prefill
 
@@ -29,6 +29,10 @@ def formula(w, rule):
             lo, end = seen(rule, b, row, pos, int(w.ctx[b]))
             for h in range(w.query_heads if lo < end else 0):
                 s = w.scale * (keys[lo:end, h // g] @ w.q[row, h].astype(np.float64))
+                if rule.softcap:
+                    s = rule.softcap * np.tanh(s / rule.softcap)
+                if rule.slopes is not None:
+                    s = s - float(rule.slopes[h]) * np.abs(pos - np.arange(lo, end))
                 p = np.exp(s - s.max())
                 off = np.minimum(p, FLOOR) / p.sum()
                 bound[row, h] += off @ np.abs(values[lo:end, h // g]) + off.sum() * np.abs(out[row, h])
@@ -74,9 +78,10 @@ def make(shape, ctx, heavy, apart, new=None):
 def test_decode_weights_beside_large_scales(shape, apart):
     for ctx, heavy in (([40, 7, 200], [3, 5]), ([129, 65], [0, 17, 33, 34, 35]), ([33, 600], [6])):
         w = make(shape, ctx, heavy, apart)
-        got, flags = gpu_decode(w, Rule())
-        assert flags == 0
-        assert_within(got, *formula(w, Rule()), False)
+        for rule in (Rule(), Rule(softcap=50.0, slopes=0.001 * slopes_of(w.query_heads))):
+            got, flags = gpu_decode(w, rule)
+            assert flags == 0
+            assert_within(got, *formula(w, rule), False)
 
 
 @gpu
