@@ -465,7 +465,8 @@ typedef struct pa_quant_cache_t {
 typedef struct pa_norm_t {
   float eps;        /* 1e-30 to 1e30 */
   int32_t reserved; /* 0 */
-  const float *query_weight; /* device, fp32 [head_dim], 16-byte aligned; NULL: queries as they are */
+  const float *query_weight; /* device, fp32 [head_dim], of at most 1e20 in size, 16-byte aligned;
+                                NULL: queries as they are */
   const float *key_weight;   /* likewise for keys */
 } pa_norm_t;
 
@@ -530,7 +531,9 @@ pa_status_t pa_decode_quant(const pa_problem_t *problem, const pa_score_t *score
  * rule (host struct, not NULL; out_type PA_OUT_FP16) and checks on the numbers that the cache stands
  * for. The new tokens' keys and values are in the cache (pa_append_quant). A call with few rows (drafted
  * tokens, say) runs several times faster than one with many; max_query_len tells, so it should be near
- * the largest n_b. */
+ * the largest n_b. The two ways sum in different orders, and the one for many rows rounds weights to fp16
+ * (as pa_prefill_scored, whose bits it gives): which is taken depends on the problem, max_query_len and
+ * whether there are first_tokens, so a call with another max_query_len may give other last bits. */
 pa_status_t pa_prefill_quant(const pa_problem_t *problem, const pa_score_t *score,
                              const void *query, const int32_t *query_start, int64_t total_tokens,
                              int32_t max_query_len, const pa_quant_cache_t *cache,

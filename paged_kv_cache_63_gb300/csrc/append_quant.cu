@@ -435,8 +435,8 @@ __device__ __forceinline__ void write_kv(const AppendQuantArgs &a, const Item &i
 // chain of offsets, length, page and angles is half of a row's time, so the rows in flight count: CTAs of
 // 64 threads, twelve a multiprocessor, unless the rows are so few that all of them are in flight as CTAs
 // of 256 (launch_append_quant_as). Rows that share a CTA, prefetched through shared memory, saved
-// instructions and cost warps: 83.6 us against 78.4 for eight prompts of 2048 tokens, 32/8 heads of 128.
-// That is 0.70 of the copy bandwidth; the instructions of norm, rotation, error bound and rounding set it.
+// instructions and cost warps: 83.6 us against 78.4 then for eight prompts of 2048 tokens, 32/8 heads of
+// 128, now 79.3 to 80. That is 0.69 of the copy bandwidth; the instructions of norm, rotation, error bound and rounding set it.
 template <int HD, bool kInterleaved, bool kNorm, int kThreads>
 __global__ void __launch_bounds__(kThreads, kThreadsPerSm / kThreads)
     append_quant_kernel(const __grid_constant__ AppendQuantArgs a) {
@@ -578,8 +578,9 @@ cudaError_t launch_append_quant_threads(const AppendQuantArgs &a, cudaStream_t s
                       dim3(static_cast<unsigned>(a.total)), threads, 0, stream, a);
 }
 
-// 256 rows of 64/8 heads of 128: 6.7 us with CTAs of 256 threads, 7.9 of 64; 1000 rows of 32/8 heads: 13.5
-// and 9.2; 3300 rows of 24/4 heads of 256: 30.0 and 20.3.
+// Captured calls, with CTAs of 256 threads and of 64: 256 rows of 64/8 heads of 128 6.7 and 7.9 us; 456
+// rows of 32/8 heads 6.9 and 7.1, 600 (past the rule) 9.5 and 7.5, 1000 12.1 and 9.3; 3300 rows of 24/4
+// heads of 256, a quarter turned and nothing normed, 26.7 and 18.5.
 template <int HD, bool kInterleaved, bool kNorm>
 cudaError_t launch_append_quant_as(const AppendQuantArgs &a, cudaStream_t stream) {
   return a.total <= static_cast<long long>(device_sm_count()) * (kThreadsPerSm / 256)

@@ -8,8 +8,10 @@
 // the keys each, by the decode step's walk (code_walk.cuh) with a mask for each row, and their states are
 // joined in shared memory; where such CTAs leave multiprocessors idle, up to eight of them form a cluster
 // that shares the keys and joins through its shared memories. K and V are read once for each eight rows,
-// from L2 after the first. Bound: the walk's chain of loads and products, about 1 us a tile and warp. Eight
-// sequences of up to 4096 tokens, 2 to 7 of them new, 32/8 heads of 128: 22.0 us against 42.4; one of
+// from L2 after the first (CTAs of the same keys run side by side: loads marked to stay in L2, as in
+// prefill2_scored_kernel.cuh, took 959.6 us against 959.7 for 64 new tokens of 100000, 32/8 heads of
+// 128, and 23.4 against 23.0 for the eight sequences below). Bound: the walk's chain of loads and products, about 1 us a tile and warp. Eight
+// sequences of up to 4096 tokens, 2 to 7 of them new, 32/8 heads of 128: 23.0 us against 42.4; one of
 // 100000, one new token: 68 against 1200.
 #include <algorithm>
 #include <atomic>
@@ -280,9 +282,9 @@ cudaError_t launch_few(const FewArgs &a, const CUtensorMap &tk, const CUtensorMa
 // A CTA here takes about half the time of a work item of 128 rows there, so this kernel is taken while
 // its CTAs are at most twice the larger of the other's items and the multiprocessors. Measured here |
 // there (no clusters), us, on contexts of 4000, 32/8 heads of 128: one sequence, 1 to 32 new tokens 24 |
-// 54 to 59, 64 of them 46 | 70; eight sequences, 8 tokens 46 | 58, 16 (past the rule) 90 | 58; 64
+// 54 to 59, 64 of them 47 | 70; eight sequences, 8 tokens 47 | 58, 16 (past the rule) 90 | 58; 64
 // sequences of up to 600 tokens, 4 new 44 | 47, 8 (past it) 80 | 47; head_dim 256, 24/4 heads, two
-// sequences, 42 new 88 | 91. On contexts of 100 the two are within 3 us. First tokens may leave tokens
+// sequences, 42 new 90 | 91. On contexts of 100 the two are within 3 us. First tokens may leave tokens
 // that no row sees between others, which only the other kernels clear.
 bool few_rows(const pa_problem_t *p, const ScoreArgs &s, int max_query_len) {
   if (s.first) return false;
